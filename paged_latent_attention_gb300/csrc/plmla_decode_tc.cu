@@ -69,10 +69,9 @@
 // the workspace status word and a CTA-wide abort flag, the producer waits (with
 // its own bound) for the copies it issued, each MMA thread waits for its MMAs,
 // and TMEM is freed before the CTA exits.
-#include <cuda.h>
 #include <math.h>
 
-#include "plmla_internal.cuh"
+#include "plmla_ptx.cuh"
 
 namespace plmla {
 namespace {
@@ -86,8 +85,6 @@ constexpr int kVHalf = 64 * 64 * 2;             // one 64 x 64 half of a bf16 V 
 constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;                     // S^T buffers from column 256 on
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;
-constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr int kMaxDynSmem = 232448;
 constexpr int kMaxK = 8, kMaxV = 8;             // ring slots (K, V) at most
 
@@ -174,343 +171,6 @@ constexpr int kBarPvIssued = 352;                // [4] P^T V of tile g issued, 
 // the bytes (measured best for each).
 template <bool F8>
 constexpr int kLead = F8 ? 3 : 2;
-
-// ---------------------------------------------------------------------------
-// PTX wrappers
-// ---------------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ unsigned long long global_ns()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Slow path of wait_bounded.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                       int32_t *status, int32_t code)
-{
-    const unsigned long long t0 = global_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if ((it & 63u) == 0u) {
-            if (*abort_flag)
-                return false;
-            if (global_ns() - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                atomicExch(status, code);
-                return false;
-            }
-        }
-    }
-}
-
-// Wait for the phase of `bar` with the given parity to complete.  Gives up
-// (returns false) when another thread of the CTA aborted, or after
-// kWaitLimitNs, in which case it raises the abort flag and the status word.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
-                                             volatile int *abort_flag, int32_t *status,
-                                             int32_t code)
-{
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status, code);
-}
-
-// Wait used while tearing down: only time-bounded.
-__device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity)
-{
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (global_ns() - t0 > kDrainLimitNs)
-            return;
-    }
-}
-
-// A 3-D tiled TMA load into shared memory, completing on an mbarrier, with an
-// L2 eviction-priority policy (from createpolicy).
-__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                                 int c2, uint32_t bar, uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-// The hinted load delivered to the same shared-memory offset of every CTA in
-// `cta_mask` (thread-block cluster), completing on the barrier at the same
-// offset in each of them.
-__device__ __forceinline__ void tma_load_3d_mc(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                               int c2, uint32_t bar, uint16_t cta_mask,
-                                               uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "h"(cta_mask),
-        "l"(policy)
-        : "memory");
-}
-
-// A KV load into the ring slot at `dst`: to this CTA alone (CL = 1) or to all
-// CL CTAs of the cluster.
-template <int CL>
-__device__ __forceinline__ void kv_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
-                                        uint32_t bar, uint64_t policy)
-{
-    if constexpr (CL == 1)
-        tma_load_3d_hint(dst, map, c0, c1, c2, bar, policy);
-    else
-        tma_load_3d_mc(dst, map, c0, c1, c2, bar, (uint16_t)((1u << CL) - 1u), policy);
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// All threads of all CTAs of the cluster (release / acquire).
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Prefetch one box of a tiled tensor into L2 (no shared memory, no barrier).
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint64_t l2_policy_evict_last()
-{
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-
-__device__ __forceinline__ uint64_t l2_policy_evict_first()
-{
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                            uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async()
-{
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Shared-memory matrix descriptor (tcgen05): start, leading/stride byte offsets
-// (16-byte units), descriptor version 1, swizzle layout in bits 61..63.
-constexpr uint32_t kSw128 = 2, kSw64 = 4, kSw32 = 6;
-
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout)
-{
-    uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)layout << 61;
-    return d;
-}
-
-// Instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major)
-{
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
-           ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-           ((uint32_t)(M >> 4) << 24);
-}
-
-// Instruction descriptor, kind::f8f6f4: fp32 accumulate, E4M3 A and B.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major)
-{
-    return (1u << 4) | (0u << 7) | (0u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
-           ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-           ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-template <bool F8>
-__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                    uint32_t accumulate)
-{
-    if constexpr (F8)
-        mma_e4m3(d_tmem, a, b, idesc, accumulate);
-    else
-        mma_bf16(d_tmem, a, b, idesc, accumulate);
-}
-
-template <bool F8>
-__host__ __device__ constexpr uint32_t idesc_for(int M, int N, bool a_mn_major, bool b_mn_major)
-{
-    return F8 ? idesc_e4m3(M, N, a_mn_major, b_mn_major)
-              : idesc_bf16(M, N, a_mn_major, b_mn_major);
-}
-
-// Swizzle mode of a K- or MN-major operand whose rows are `row_bytes` wide.
-__host__ __device__ constexpr uint32_t layout_for_row(int row_bytes)
-{
-    return row_bytes == 128 ? kSw128 : (row_bytes == 64 ? kSw64 : kSw32);
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-// Arrive on the barrier at offset `bar` of every CTA of the cluster once this
-// thread's MMAs so far have completed (CL = 1: this CTA's barrier).
-template <int CL>
-__device__ __forceinline__ void mma_commit_all(uint32_t bar)
-{
-    if constexpr (CL == 1) {
-        mma_commit(bar);
-    } else {
-        const uint16_t mask = (uint16_t)((1u << CL) - 1u);
-        asm volatile(
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"(mask)
-            : "memory");
-    }
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]));
-}
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Load C consecutive fp32 TMEM columns of this thread's lane (C = 8, 16 or 32).
-template <int C>
-__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, float (&v)[C])
-{
-    if constexpr (C % 16 == 0) {
-#pragma unroll
-        for (int b = 0; b < C / 16; ++b) {
-            uint32_t r[16];
-            tmem_ld16(taddr + 16 * b, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                v[16 * b + e] = __uint_as_float(r[e]);
-        }
-    } else {
-        static_assert(C == 8, "column count");
-        uint32_t r[8];
-        tmem_ld8(taddr, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = __uint_as_float(r[e]);
-    }
-}
 
 // Multiply C consecutive fp32 TMEM columns of this thread's lane by alpha[col].
 template <int C>
@@ -688,13 +348,6 @@ __device__ __forceinline__ bool shift_and_test(float (&x)[NG], uint32_t m_addr)
         }
     }
     return vmax > F::tau;
-}
-
-__device__ __forceinline__ float ld_shared_f32(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
 }
 
 // Q^T of one segment's query rows (row qrow on): bf16 nine 64-column blocks;
@@ -1555,40 +1208,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 // ---------------------------------------------------------------------------
 // host side: tensor maps and launch
 // ---------------------------------------------------------------------------
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    if (fn == nullptr) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
-
-bool make_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, int rank,
-              const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
-              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
-{
-    EncodeTiledFn fn = encode_fn();
-    if (fn == nullptr)
-        return false;
-    const cuuint32_t estr[3] = {1, 1, 1};
-    // out-of-range elements (the E4M3 rope block's columns past 576) read as zero
-    return fn(map, dtype, rank, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // Tensor maps over the slab (K items, V items, and the V tail boxes), kept for
 // the last slab seen by this host thread: they depend only on the slab's
