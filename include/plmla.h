@@ -559,6 +559,204 @@ plmla_status mla_kv_append_fp8(const void *latent_new, const void *rope_new, voi
                                const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
                                int32_t *status, void *stream);
 
+/*
+ * Rotary positions.  Pair i of a head's `dim` rotated elements at position p is
+ * turned by the angle a = p f_i:
+ *
+ *   (x, y) -> magnitude * (x cos a - y sin a, x sin a + y cos a)
+ *
+ * where the pair is (x[i], x[i + dim/2]) in the half layout and
+ * (x[2i], x[2i + 1]) in the interleaved one.  The frequencies are passed as
+ * turns[i] = f_i / (2 pi) in units of 2^-64 turns: the kernels multiply them by
+ * the position in 64-bit integers, which wraps modulo whole turns, so the angle
+ * is exact for every int32 position (negative ones turn backwards).
+ */
+enum { PLMLA_ROPE_HALF = 0, PLMLA_ROPE_INTERLEAVED = 1 };
+enum { PLMLA_ROPE_PLAIN = 0, PLMLA_ROPE_LINEAR = 1, PLMLA_ROPE_BY_PARTS = 2 };
+enum { PLMLA_BF16 = 0, PLMLA_FP16 = 1, PLMLA_FP32 = 2 };
+
+/*
+ * mla_rope_turns -- the frequency table, on the host: f_i = base^(-2 i / dim) and
+ *   PLMLA_ROPE_PLAIN     f_i
+ *   PLMLA_ROPE_LINEAR    f_i / factor
+ *   PLMLA_ROPE_BY_PARTS  (1 - g_i) f_i / factor + g_i f_i, with
+ *                        g_i = clamp((t_i - low) / (high - low), 0, 1) and
+ *                        t_i = original_len f_i / (2 pi), the turns of pair i over
+ *                        the original context (Peng et al., YaRN, 2023, section 3.2)
+ *
+ * dim    even, 2 .. 1024;  base finite and > 1;  factor finite and >= 1;
+ *        by parts: original_len > 0, 0 <= low < high
+ * turns  HOST array of dim / 2, written; copy it to the device for the calls below
+ */
+plmla_status mla_rope_turns(int32_t dim, double base, int32_t scaling, double factor,
+                            double original_len, double low, double high, uint64_t *turns);
+
+/*
+ * mla_rope -- rotate heads of `dim` elements.  x and out are given by their first
+ * element and the strides, in elements, from token to token and from head to
+ * head; the elements of a head are contiguous.  A rotated part of a wider head
+ * (the last 64 of 192, say) is x + its offset with the wider head's strides.
+ *
+ * positions    int32 [tokens], device
+ * turns        uint64 [dim / 2], device (mla_rope_turns)
+ * magnitude    finite factor of the rotated pairs (1, or a scaled rotation's)
+ * tokens       >= 0;  heads 1 .. 65535;  dim even, 2 .. 1024
+ * dtype        PLMLA_BF16, PLMLA_FP16 or PLMLA_FP32 elements; computed in fp32 and
+ *              rounded once
+ * layout       PLMLA_ROPE_HALF or PLMLA_ROPE_INTERLEAVED
+ * inverse      nonzero: the angle is negated (and the magnitude kept): the
+ *              transposed map, so the gradient of the forward call
+ * out          may be x with the same strides (in place); must not overlap it
+ *              otherwise.  Heads of out must not overlap each other.
+ * Rows in 16-byte accesses where addresses and strides (and dim / 2) allow, else
+ * element by element.
+ */
+plmla_status mla_rope(const void *x, int64_t tok_stride, int64_t head_stride,
+                      const int32_t *positions, const uint64_t *turns, float magnitude,
+                      int64_t tokens, int32_t heads, int32_t dim, int32_t dtype, int32_t layout,
+                      int32_t inverse, void *out, int64_t out_tok_stride, int64_t out_head_stride,
+                      void *stream);
+
+/*
+ * mla_kv_append_rope -- mla_kv_append of rope keys that are not rotated yet: row
+ * r * n_new + j is turned by its position on the way into its page, and in the
+ * same launch the query heads of the same tokens can be rotated for mla_decode.
+ *
+ * positions    int32 [num_reqs * n_new], device, or NULL: the token's index in its
+ *              history, seq_lens[r] - n_new + j.  A history that lost tokens
+ *              (mla_kv_compact) needs its true positions here.
+ * turns, magnitude, layout   as in mla_rope, dim = 64
+ * q            NULL, or bf16 query heads [num_reqs * n_new, num_heads] of 64
+ *              elements at the given strides (q_tok_stride, q_head_stride in
+ *              elements); num_heads 1 .. 65535, ignored without q
+ * q_out        bf16 [num_reqs * n_new, num_heads, 64], contiguous, 16-byte
+ *              aligned, written when q is given: mla_decode's q_rope.  Must not
+ *              overlap q.
+ * Other arguments, the skipped rows, the status word and errors as mla_kv_append.
+ * The rotated key is computed in fp32 and rounded once.
+ */
+plmla_status mla_kv_append_rope(const void *latent_new, const void *rope_new, void *slab_base,
+                                int64_t num_pages, int64_t page_stride_elems,
+                                const int32_t *page_table, int64_t page_table_ld,
+                                const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+                                const int32_t *positions, const uint64_t *turns, float magnitude,
+                                int32_t layout, const void *q, int64_t q_tok_stride,
+                                int64_t q_head_stride, int32_t num_heads, void *q_out,
+                                int32_t *status, void *stream);
+
+/* mla_kv_append_rope into E4M3 pages (see mla_kv_append_fp8): the rotated fp32
+ * value is divided by kv_scale and rounded once, to E4M3. */
+plmla_status mla_kv_append_rope_fp8(const void *latent_new, const void *rope_new, void *slab_base,
+                                    int64_t num_pages, int64_t page_stride_elems, float kv_scale,
+                                    const int32_t *page_table, int64_t page_table_ld,
+                                    const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+                                    const int32_t *positions, const uint64_t *turns,
+                                    float magnitude, int32_t layout, const void *q,
+                                    int64_t q_tok_stride, int64_t q_head_stride, int32_t num_heads,
+                                    void *q_out, int32_t *status, void *stream);
+
+/*
+ * mla_attention_mass -- add to every cached token the attention weight that this
+ * step's query rows gave it, for eviction by accumulated weight:
+ *
+ *   mass[r, t] <- decay * mass[r, t]
+ *                 + sum_{j, h: t < L_r - (n_q - 1 - j)} exp(s_{r,j,h,t} - lse[r,j,h])
+ *
+ * for t < L_r = seq_lens[r], with mla_decode's scores s and the lse it returned
+ * (rows given lse = -inf add nothing).  Columns at and past L_r are neither read
+ * nor written, and what the pages hold there is never used.  Several layers that
+ * share a page table accumulate into one mass, a call each.
+ *
+ * lse          fp32 [num_reqs * n_q, num_heads], natural log
+ * mass         fp32, row r at mass + r * mass_ld, of mass_cols columns (mass_cols
+ *              <= mass_ld, so that a view of a wider buffer works)
+ * decay        finite; 0 overwrites (the old values are not read)
+ * status       optional device int32, as in mla_kv_append: set to 33 if a history
+ *              needs a page column past page_table_ld or a page ID outside the
+ *              pool, to 34 if it is longer than mass_cols -- such tokens are left as
+ *              they are --, or to 1 .. 12 if a pipeline wait gave up after its time
+ *              bound (mass is then incomplete)
+ * Other arguments as in mla_decode (num_reqs 1 .. 1024, n_q 1 .. 256, num_heads a
+ * multiple of 16 up to 128).  One kernel; no atomics: the same inputs give the
+ * same bits.
+ */
+plmla_status mla_attention_mass(const void *q_nope_absorbed, const void *q_rope, const float *lse,
+                                const void *slab_base, int64_t num_pages,
+                                int64_t page_stride_elems, const int32_t *page_table,
+                                int64_t page_table_ld, const int32_t *seq_lens, int32_t num_reqs,
+                                int32_t n_q_per_req, int32_t num_heads, float scale, float decay,
+                                float *mass, int64_t mass_ld, int64_t mass_cols, int32_t *status,
+                                void *stream);
+
+/*
+ * mla_attention_mass_fp8 -- mla_attention_mass over E4M3 pages (see
+ * mla_decode_fp8: kv_scale, page strides in bytes).  The workspace, of at least
+ * mla_mass_workspace_size_fp8(...) bytes and 256-byte aligned, holds the query
+ * rows in two E4M3 parts; its contents on entry are irrelevant.
+ */
+size_t mla_mass_workspace_size_fp8(int32_t num_reqs, int32_t n_q, int32_t num_heads);
+plmla_status mla_attention_mass_fp8(const void *q_nope_absorbed, const void *q_rope,
+                                    const float *lse, const void *slab_base, int64_t num_pages,
+                                    int64_t page_stride_elems, float kv_scale,
+                                    const int32_t *page_table, int64_t page_table_ld,
+                                    const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req,
+                                    int32_t num_heads, float scale, float decay, float *mass,
+                                    int64_t mass_ld, int64_t mass_cols, void *workspace,
+                                    size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * mla_evict_select -- the tokens of each history that stay within a budget: the
+ * first `sink`, the last `recent`, and of the others the heaviest by mass until
+ * `keep` are chosen; equal masses go to the lower index, NaN counts below every
+ * number and -0 as 0.  A history of at most `keep` tokens stays whole.
+ *
+ * mass         fp32, row r at mass + r * mass_ld, of mass_cols columns; a longer
+ *              history is taken as mass_cols long
+ * seq_lens     int32 [num_reqs], device; num_reqs 1 .. 1024
+ * keep         1 .. 2^31 - 1, sink >= 0, recent >= 0, sink + recent <= keep
+ * kept         int32, row r at kept + r * kept_ld (kept_ld >= min(keep, mass_cols)):
+ *              min(keep, L_r) indices in ascending order; later entries are not
+ *              written
+ * kept_lens    int32 [num_reqs], written: min(keep, L_r)
+ * One kernel, deterministic.
+ */
+plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
+                              const int32_t *seq_lens, int32_t num_reqs, int32_t keep,
+                              int32_t sink, int32_t recent, int32_t *kept, int64_t kept_ld,
+                              int32_t *kept_lens, void *stream);
+
+/*
+ * mla_kv_compact -- copy the kept token rows of each history into fresh pages, for
+ * every layer: row i of request r's new history is its token kept[r, i].  The
+ * rows keep their rotation (their positions), only their places change; the old
+ * pages are left as they are, so shared prefixes stay valid.
+ *
+ * slab_base    HOST array of num_layers (1 .. 1024) device pointers, 16-byte
+ *              aligned, each a pool as in mla_decode; elem_bytes 2 (bf16) or 1
+ *              (E4M3), page_stride_elems as there
+ * page_table, page_table_ld, seq_lens   the histories as they are
+ * out_table    int32, row r at out_table + r * out_table_ld: the pages of the new
+ *              histories, ceil(kept_lens[r] / 1536) of them.  They must be distinct
+ *              and none may be read by this call (a page of any page_table row
+ *              that a kept index reaches); the same table is refused.
+ * kept, kept_ld, kept_lens   as mla_evict_select writes them; entries from
+ *              min(kept_lens[r], kept_cols) on are not used; kept_cols 0 .. kept_ld
+ * mass         NULL, or fp32 rows of mass_cols columns (row stride mass_ld) whose
+ *              kept entries are copied to mass_out[r, i] (row stride mass_out_ld >=
+ *              kept_cols); the two must not overlap.  An index past mass_cols
+ *              leaves its mass_out entry as it is.
+ * status       optional device int32, as in mla_kv_append: set to 33 if an index or
+ *              a page is out of range; such rows are skipped
+ */
+plmla_status mla_kv_compact(int32_t num_layers, void *const *slab_base, int32_t elem_bytes,
+                            int64_t num_pages, int64_t page_stride_elems,
+                            const int32_t *page_table, int64_t page_table_ld,
+                            const int32_t *seq_lens, const int32_t *out_table,
+                            int64_t out_table_ld, const int32_t *kept, int64_t kept_ld,
+                            const int32_t *kept_lens, int32_t num_reqs, int32_t kept_cols,
+                            const float *mass, int64_t mass_ld, int64_t mass_cols,
+                            float *mass_out, int64_t mass_out_ld, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,3 +21,11 @@ from .oracle import (  # noqa: F401
     quantize_query_rows,
     query_scale_exponent,
 )
+from .budget import (  # noqa: F401
+    attention_mass,
+    evict_select,
+    history_rows,
+    kv_compact,
+    rope_frequencies,
+    rope_rotate,
+)

@@ -16,6 +16,7 @@ HEADER_PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__fil
 
 _i32, _i64, _sz, _p, _f = (ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p,
                            ctypes.c_float)
+_d = ctypes.c_double
 
 # name -> (restype, argtypes); mirrors include/plmla.h
 SIGNATURES = {
@@ -47,6 +48,23 @@ SIGNATURES = {
     "mla_quantize_queries_fp8": (ctypes.c_int, [_p, _p, _i64, _p, _p, _p]),
     "mla_merge_partials": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _p, _p]),
     "mla_dcp_shard": (ctypes.c_int, [_p, _i64, _p, _i32, _i32, _i32, _p, _i64, _p, _p]),
+    "mla_rope_turns": (ctypes.c_int, [_i32, _d, _i32, _d, _d, _d, _d, _p]),
+    "mla_rope": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _f, _i64, _i32, _i32, _i32, _i32, _i32,
+                                _p, _i64, _i64, _p]),
+    "mla_kv_append_rope": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _p, _i64, _p, _i32, _i32, _p,
+                                          _p, _f, _i32, _p, _i64, _i64, _i32, _p, _p, _p]),
+    "mla_kv_append_rope_fp8": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _f, _p, _i64, _p, _i32,
+                                              _i32, _p, _p, _f, _i32, _p, _i64, _i64, _i32, _p,
+                                              _p, _p]),
+    "mla_attention_mass": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _p, _i64, _p, _i32, _i32,
+                                          _i32, _f, _f, _p, _i64, _i64, _p, _p]),
+    "mla_mass_workspace_size_fp8": (_sz, [_i32, _i32, _i32]),
+    "mla_attention_mass_fp8": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _f, _p, _i64, _p, _i32,
+                                              _i32, _i32, _f, _f, _p, _i64, _i64, _p, _sz, _p, _p]),
+    "mla_evict_select": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _i64, _p,
+                                        _p]),
+    "mla_kv_compact": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _p, _p, _i64, _p,
+                                      _i64, _p, _i32, _i32, _p, _i64, _i64, _p, _i64, _p, _p]),
     "mla_set_page_checks": (None, [_i32]),
     "mla_set_split_mode": (ctypes.c_int, [_i32]),
     "mla_get_split_mode": (_i32, []),

@@ -6,6 +6,7 @@ C ABI.  PyTorch only supplies device memory and the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -462,3 +463,376 @@ def _append(latent_new, rope_new, slab, page_table, seq_lens, n_new, status, str
     else:
         rc = lib.mla_kv_append(*head, *tail)
     _native.check(rc, "mla_kv_append_fp8" if fp8 else "mla_kv_append")
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, accumulated weights, eviction
+# ---------------------------------------------------------------------------
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
+_ROPE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on(device, **tensors):
+    """Checks that every tensor (or None) lies on `device`; returns the context
+    that makes it current for the launch."""
+    for name, t in tensors.items():
+        _require(t is None or t.device == device, f"{name} must be on {device}")
+    return _NO_GUARD if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _check_ints(t, name, shape):
+    _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
+             and t.is_contiguous() and tuple(t.shape) == tuple(shape),
+             f"{name} must be a contiguous CUDA int32 tensor of shape {tuple(shape)}")
+
+
+def _check_table(t, name, num_reqs):
+    _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
+             and t.dim() == 2 and t.shape[0] == num_reqs and t.shape[1] >= 1
+             and t.stride(1) == 1 and (num_reqs == 1 or t.stride(0) >= t.shape[1]),
+             f"{name} must be a CUDA int32 [{num_reqs}, columns] view with unit column stride")
+
+
+def _row_stride(t):
+    """Stride between the rows of a 2-D view (its width where there is one row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check_status(status):
+    _require(status is None or (status.is_cuda and status.dtype == torch.int32
+                                and status.numel() >= 1), "status must be a CUDA int32 tensor")
+
+
+def _check_pool(slab, fp8):
+    want = torch.uint8 if fp8 else torch.bfloat16
+    _require(isinstance(slab, torch.Tensor) and slab.is_cuda and slab.dtype == want
+             and slab.dim() == 2 and slab.stride(1) == 1,
+             f"slab must be a CUDA {want} [num_pages, page_stride] view")
+    _require(slab.shape[1] >= PAGE_TOKENS * ROW, "slab page too small")
+
+
+def _check_mass(t, name, num_reqs):
+    _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.float32
+             and t.dim() == 2 and t.shape[0] == num_reqs and t.shape[1] >= 1
+             and t.stride(1) == 1 and (num_reqs == 1 or t.stride(0) >= t.shape[1]),
+             f"{name} must be a CUDA fp32 [{num_reqs}, tokens] view with unit column stride")
+
+
+class RopeTable:
+    """Rotary frequencies on a device (see rope_table): `turns` int64 [dim / 2],
+    2^-64 turns per position; `magnitude` scales the rotated pairs."""
+
+    def __init__(self, turns, magnitude):
+        self.turns, self.magnitude, self.dim = turns, float(magnitude), 2 * turns.numel()
+
+
+def rope_table(dim=ROPE, *, base=10000.0, scaling="none", factor=1.0, original_len=0, low=1.0,
+               high=32.0, magnitude=None, device=None) -> RopeTable:
+    """The rotary frequencies f_i = base^(-2 i / dim) of mla_rope and
+    mla_kv_append_rope, for a context longer than the trained one divided by
+    ``factor``: every one ("linear"), or by parts ("by_parts") -- pairs that turn
+    fewer than ``low`` times over ``original_len`` positions are divided, those
+    that turn more than ``high`` times kept, and a ramp joins the two.
+    ``magnitude`` scales the rotated pairs; by default 1, and 0.1 ln(factor) + 1 by
+    parts.  Make the table once and keep it: it is copied to the device here."""
+    _require(scaling in ROPE_SCALINGS, f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    host = torch.empty(max(dim, 0) // 2, dtype=torch.int64)
+    status = _native.lib().mla_rope_turns(int(dim), float(base), ROPE_SCALINGS[scaling],
+                                          float(factor), float(original_len), float(low),
+                                          float(high), host.data_ptr())
+    if status != 0:
+        raise ValueError(f"invalid rotary table: {_native.strerror(status)}")
+    if magnitude is None:
+        magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "by_parts" else 1.0
+    _require(math.isfinite(magnitude), "magnitude must be finite")
+    return RopeTable(host.to(device or "cuda"), magnitude)
+
+
+def _head_strides(t):
+    """(token stride, head stride) of a [T, H, D] view, 0 along extents of one."""
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _span(t):
+    """First and last byte of a view with non-negative strides."""
+    first = t.data_ptr()
+    return first, first + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * \
+        t.element_size()
+
+
+def _check_apart(a, b, what):
+    """Refuses two views whose address ranges meet."""
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    _require(a1 <= b0 or b1 <= a0, what)
+
+
+def mla_rope(x, positions, table, *, layout="half", inverse=False, out=None, stream=None):
+    """Rotary positions: x [T, H, D] (bf16, fp16 or fp32; any token and head
+    strides, so ``q[..., 128:]`` rotates the last part of wider heads) turned by
+    positions [T] int32.  ``layout`` pairs element i with i + D/2 ("half") or 2i
+    with 2i + 1 ("interleaved"); ``inverse`` negates the angles, which is the
+    gradient of the forward call.  ``out`` may be x itself (in place); returns it
+    (a new contiguous tensor by default)."""
+    _require(isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _ROPE_TYPES and x.dim() == 3,
+             "x must be a CUDA bf16, fp16 or fp32 tensor [T, H, D]")
+    T, H, D = x.shape
+    _require(D == table.dim, f"x has {D} elements per head, the table {table.dim}")
+    _require(layout in ROPE_LAYOUTS, f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    _require(x.stride(2) == 1, "the elements of a head must be contiguous")
+    _check_ints(positions, "positions", (T,))
+    if out is None:
+        out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
+    else:
+        _require(out.is_cuda and out.dtype == x.dtype and out.shape == x.shape
+                 and out.stride(2) == 1, "out must be like x, each head contiguous")
+        if T and H:
+            ts, hs = _head_strides(out)
+            _require((H == 1 or hs >= D) and (T == 1 or ts >= D) and
+                     (T == 1 or H == 1 or ts >= (H - 1) * hs + D or hs >= (T - 1) * ts + D),
+                     "heads of out overlap")
+            if not (out.data_ptr() == x.data_ptr() and _head_strides(out) == _head_strides(x)):
+                _check_apart(x, out, "out must be x or not overlap it")
+    if T == 0 or H == 0:
+        return out
+    with _on(x.device, positions=positions, table=table.turns, out=out):
+        status = _native.lib().mla_rope(
+            x.data_ptr(), *_head_strides(x), positions.data_ptr(), table.turns.data_ptr(),
+            table.magnitude, T, H, D, _ROPE_TYPES[x.dtype], ROPE_LAYOUTS[layout], int(inverse),
+            out.data_ptr(), *_head_strides(out), _stream_ptr(stream, x.device))
+    _native.check(status, "mla_rope")
+    return out
+
+
+def mla_kv_append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, *,
+                       positions=None, layout="half", q_rope=None, q_out=None, status=None,
+                       stream=None):
+    """mla_kv_append of rope keys that are not rotated yet, and in the same launch
+    the rotation of the same tokens' queries.  ``positions`` [R*n_new] int32 (by
+    default each token's index in its history; give the true positions where a
+    history has lost tokens).  ``q_rope`` bf16 [R*n_new, H, 64], any token and head
+    strides, is rotated into ``q_out`` (contiguous, new by default), mla_decode's
+    q_rope; returns it (None without q_rope)."""
+    return _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, positions,
+                        layout, q_rope, q_out, status, stream, None)
+
+
+def mla_kv_append_rope_fp8(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, *,
+                           kv_scale, positions=None, layout="half", q_rope=None, q_out=None,
+                           status=None, stream=None):
+    """mla_kv_append_rope into E4M3 pages (slab and kv_scale as in
+    mla_kv_append_fp8)."""
+    _require(math.isfinite(kv_scale) and kv_scale > 0, "kv_scale must be finite and > 0")
+    return _append_rope(latent_new, rope_new, _byte_view(slab), page_table, seq_lens, n_new, table,
+                        positions, layout, q_rope, q_out, status, stream, float(kv_scale))
+
+
+def _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, positions, layout,
+                 q_rope, q_out, status, stream, kv_scale):
+    fp8 = kv_scale is not None
+    _require(isinstance(seq_lens, torch.Tensor) and seq_lens.dim() == 1,
+             "seq_lens must be a contiguous CUDA int32 vector")
+    R = seq_lens.shape[0]
+    rows = R * n_new
+    _check_ints(seq_lens, "seq_lens", (R,))
+    _check_bf16(latent_new, "latent_new", (rows, LATENT))
+    _check_bf16(rope_new, "rope_new", (rows, ROPE))
+    _check_pool(slab, fp8)
+    _check_table(page_table, "page_table", R)
+    _require(layout in ROPE_LAYOUTS, f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    _require(table.dim == ROPE, f"the table must have dim {ROPE}")
+    if positions is not None:
+        _check_ints(positions, "positions", (rows,))
+    _check_status(status)
+    q = (None, 0, 0, 0, None)
+    if q_rope is None:
+        _require(q_out is None, "q_out needs q_rope")
+    else:
+        _require(q_rope.is_cuda and q_rope.dtype == torch.bfloat16 and q_rope.dim() == 3
+                 and q_rope.shape[0] == rows and q_rope.shape[2] == ROPE
+                 and q_rope.stride(2) == 1,
+                 f"q_rope must be a CUDA bf16 [{rows}, H, {ROPE}] view with contiguous heads")
+        if q_out is None:
+            q_out = torch.empty(q_rope.shape, dtype=torch.bfloat16, device=q_rope.device)
+        else:
+            _check_bf16(q_out, "q_out", q_rope.shape)
+            if q_out.numel():
+                _check_apart(q_rope, q_out, "q_out must not overlap q_rope")
+        if q_out.numel():
+            q = (q_rope.data_ptr(), *_head_strides(q_rope), q_rope.shape[1], q_out.data_ptr())
+    lib = _native.lib()
+    with _on(slab.device, latent_new=latent_new, rope_new=rope_new, page_table=page_table,
+             seq_lens=seq_lens, table=table.turns, positions=positions, q_rope=q_rope, q_out=q_out,
+             status=status):
+        head = (latent_new.data_ptr(), rope_new.data_ptr(), slab.data_ptr(), slab.shape[0],
+                _page_stride(slab))
+        tail = (page_table.data_ptr(), _row_stride(page_table), seq_lens.data_ptr(), R,
+                int(n_new), None if positions is None else positions.data_ptr(),
+                table.turns.data_ptr(), table.magnitude, ROPE_LAYOUTS[layout], *q,
+                None if status is None else status.data_ptr(), _stream_ptr(stream, slab.device))
+        if fp8:
+            rc = lib.mla_kv_append_rope_fp8(*head, kv_scale, *tail)
+        else:
+            rc = lib.mla_kv_append_rope(*head, *tail)
+    _native.check(rc, "mla_kv_append_rope_fp8" if fp8 else "mla_kv_append_rope")
+    return q_out
+
+
+def _page_stride(slab):
+    return slab.stride(0) if slab.shape[0] > 1 else slab.shape[1]
+
+
+def allocate_mass_workspace(num_reqs, n_q, num_heads, device=None):
+    """A workspace tensor (uint8) of the size mla_attention_mass_fp8 needs."""
+    n = _native.lib().mla_mass_workspace_size_fp8(num_reqs, n_q, num_heads)
+    if n == 0:
+        raise ValueError("invalid shape for mla_mass_workspace_size_fp8")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_attention_mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, *, n_q=1,
+                       scale=DEFAULT_SCALE, decay=1.0, status=None, stream=None):
+    """Adds to mass [R, tokens] fp32 the attention weight that this step's query
+    rows gave every cached token (decay * mass + the sum over drafts and heads);
+    returns mass.  The queries, pool and histories are mla_decode's, ``lse`` is
+    what it returned.  Layers that share a page table accumulate into one mass, a
+    call each; ``decay`` 0 overwrites.  ``status``: optional CUDA int32 tensor of
+    one element that the kernel sets to 33 or 34 where a history leaves the page
+    table, the pool or its row of mass.  Asynchronous."""
+    return _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, scale, decay,
+                 None, None, status, stream)
+
+
+def mla_attention_mass_fp8(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, *,
+                           kv_scale, n_q=1, scale=DEFAULT_SCALE, decay=1.0, workspace=None,
+                           status=None, stream=None):
+    """mla_attention_mass over E4M3 pages (slab and kv_scale as in mla_decode_fp8).
+    The workspace comes from allocate_mass_workspace."""
+    _require(math.isfinite(kv_scale) and kv_scale > 0, "kv_scale must be finite and > 0")
+    return _mass(q_nope_absorbed, q_rope, lse, _byte_view(slab), page_table, seq_lens, mass, n_q,
+                 scale, decay, float(kv_scale), workspace, status, stream)
+
+
+def _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, scale, decay,
+          kv_scale, workspace, status, stream):
+    fp8 = kv_scale is not None
+    _require(q_nope_absorbed.dim() == 3, "q_nope_absorbed must be [R*n_q, H, 512]")
+    T, H, _ = q_nope_absorbed.shape
+    _require(n_q >= 1 and T % n_q == 0, "first dimension must be num_reqs * n_q")
+    R = T // n_q
+    device = slab.device
+    _check_bf16(q_nope_absorbed, "q_nope_absorbed", (T, H, LATENT))
+    _check_bf16(q_rope, "q_rope", (T, H, ROPE))
+    _require(lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()
+             and tuple(lse.shape) == (T, H), "lse must be a contiguous CUDA fp32 [T, H]")
+    _check_pool(slab, fp8)
+    _check_table(page_table, "page_table", R)
+    _check_ints(seq_lens, "seq_lens", (R,))
+    _check_mass(mass, "mass", R)
+    _check_status(status)
+    lib = _native.lib()
+    if fp8 and workspace is None:
+        workspace = allocate_mass_workspace(R, n_q, H, device)
+    with _on(device, q_nope_absorbed=q_nope_absorbed, q_rope=q_rope, lse=lse,
+             page_table=page_table, seq_lens=seq_lens, mass=mass, workspace=workspace,
+             status=status):
+        head = (q_nope_absorbed.data_ptr(), q_rope.data_ptr(), lse.data_ptr(), slab.data_ptr(),
+                slab.shape[0], _page_stride(slab))
+        tail = (page_table.data_ptr(), _row_stride(page_table), seq_lens.data_ptr(), R, n_q, H,
+                float(scale), float(decay), mass.data_ptr(), _row_stride(mass), mass.shape[1])
+        end = (None if status is None else status.data_ptr(), _stream_ptr(stream, device))
+        if fp8:
+            _require(workspace.is_cuda and workspace.is_contiguous(),
+                     "workspace must be CUDA memory")
+            rc = lib.mla_attention_mass_fp8(*head, kv_scale, *tail, workspace.data_ptr(),
+                                            workspace.numel() * workspace.element_size(), *end)
+        else:
+            rc = lib.mla_attention_mass(*head, *tail, *end)
+    _native.check(rc, "mla_attention_mass_fp8" if fp8 else "mla_attention_mass")
+    return mass
+
+
+def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_lens=None,
+                     stream=None):
+    """Which tokens of each history stay within ``keep``: the first ``sink``, the
+    last ``recent`` and the heaviest of the rest by mass [R, tokens] fp32 (ties to
+    the lower index).  Returns (kept [R, min(keep, tokens)] int32 ascending
+    indices, kept_lens [R] int32 = min(keep, seq_lens)); entries of kept past a
+    row's count are not written."""
+    _require(isinstance(mass, torch.Tensor) and mass.dim() == 2, "mass must be [R, tokens]")
+    R = mass.shape[0]
+    _check_mass(mass, "mass", R)
+    _check_ints(seq_lens, "seq_lens", (R,))
+    _require(keep >= 1 and sink >= 0 and recent >= 0 and sink + recent <= keep,
+             "keep >= 1, sink and recent >= 0, and sink + recent <= keep are needed")
+    cols = min(int(keep), mass.shape[1])
+    if kept is None:
+        kept = torch.empty(R, cols, dtype=torch.int32, device=mass.device)
+    _check_table(kept, "kept", R)
+    _require(kept.shape[1] >= cols, f"kept needs {cols} columns")
+    if kept_lens is None:
+        kept_lens = torch.empty(R, dtype=torch.int32, device=mass.device)
+    _check_ints(kept_lens, "kept_lens", (R,))
+    with _on(mass.device, seq_lens=seq_lens, kept=kept, kept_lens=kept_lens):
+        status = _native.lib().mla_evict_select(
+            mass.data_ptr(), _row_stride(mass), mass.shape[1], seq_lens.data_ptr(), R, int(keep),
+            int(sink), int(recent), kept.data_ptr(), _row_stride(kept), kept_lens.data_ptr(),
+            _stream_ptr(stream, mass.device))
+    _native.check(status, "mla_evict_select")
+    return kept, kept_lens
+
+
+def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, mass=None,
+                   mass_out=None, status=None, stream=None):
+    """Copies each history's kept rows (kept, kept_lens from mla_evict_select), for
+    every layer's pool in ``slabs`` (bf16, or uint8 / float8_e4m3fn), into the
+    fresh pages of out_table [R, columns]: row i of the new history is token
+    kept[r, i].  The fresh pages must be distinct and none of those read.  ``mass``
+    rows are carried into ``mass_out`` (a new [R, kept columns] tensor by default);
+    returns mass_out (None without mass).  ``status``: optional CUDA int32 tensor
+    of one element, set to 33 where an index or page is out of range (such rows are
+    skipped).  The old pages are not changed.  Asynchronous."""
+    _require(isinstance(slabs, (list, tuple)) and len(slabs) >= 1, "slabs must be a list of pools")
+    fp8 = slabs[0].dtype != torch.bfloat16
+    if fp8:
+        slabs = [_byte_view(s) for s in slabs]
+    first = slabs[0]
+    for s in slabs:
+        _check_pool(s, fp8)
+        _require(s.shape == first.shape and s.stride(0) == first.stride(0)
+                 and s.device == first.device, "the layers' slabs must share their shape")
+    _require(isinstance(kept, torch.Tensor) and kept.dim() == 2, "kept must be [R, columns]")
+    R, cols = kept.shape
+    _check_table(kept, "kept", R)
+    _check_ints(kept_lens, "kept_lens", (R,))
+    _check_ints(seq_lens, "seq_lens", (R,))
+    _check_table(page_table, "page_table", R)
+    _check_table(out_table, "out_table", R)
+    _check_status(status)
+    if mass is None:
+        _require(mass_out is None, "mass_out needs mass")
+    else:
+        _check_mass(mass, "mass", R)
+        if mass_out is None:
+            mass_out = torch.empty(R, cols, dtype=torch.float32, device=mass.device)
+        _check_mass(mass_out, "mass_out", R)
+        _require(mass_out.shape[1] >= cols, f"mass_out needs {cols} columns")
+        _check_apart(mass, mass_out, "mass_out must not overlap mass")
+    L = len(slabs)
+    bases = (ctypes.c_void_p * L)(*[s.data_ptr() for s in slabs])
+    with _on(first.device, page_table=page_table, seq_lens=seq_lens, out_table=out_table,
+             kept=kept, kept_lens=kept_lens, mass=mass, mass_out=mass_out, status=status):
+        rc = _native.lib().mla_kv_compact(
+            L, ctypes.cast(bases, ctypes.c_void_p), 1 if fp8 else 2, first.shape[0],
+            _page_stride(first), page_table.data_ptr(), _row_stride(page_table),
+            seq_lens.data_ptr(), out_table.data_ptr(), _row_stride(out_table), kept.data_ptr(),
+            _row_stride(kept), kept_lens.data_ptr(), R, cols,
+            None if mass is None else mass.data_ptr(), 0 if mass is None else _row_stride(mass),
+            0 if mass is None else mass.shape[1],
+            None if mass is None else mass_out.data_ptr(),
+            0 if mass is None else _row_stride(mass_out),
+            None if status is None else status.data_ptr(), _stream_ptr(stream, first.device))
+    _native.check(rc, "mla_kv_compact")
+    return mass_out

@@ -30,6 +30,9 @@ SOURCES = [
     "plmla_append.cu",
     "plmla_check.cu",
     "plmla_dcp.cu",
+    "plmla_rope.cu",
+    "plmla_mass.cu",
+    "plmla_evict.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

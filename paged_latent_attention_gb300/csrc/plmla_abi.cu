@@ -683,3 +683,292 @@ extern "C" plmla_status mla_quantize_queries_fp8(const void *q_nope_absorbed, co
                                             static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
 }
+
+// ---------------------------------------------------------------------------
+// rotary positions, accumulated weights, eviction
+// ---------------------------------------------------------------------------
+
+extern "C" plmla_status mla_rope_turns(int32_t dim, double base, int32_t scaling, double factor,
+                                       double original_len, double low, double high,
+                                       uint64_t *turns)
+{
+    if (turns == nullptr || dim < 2 || dim > kMaxRopeDim || dim % 2 != 0 || !isfinite(base) ||
+        !(base > 1.0) || scaling < PLMLA_ROPE_PLAIN || scaling > PLMLA_ROPE_BY_PARTS)
+        return PLMLA_INVALID_ARGUMENT;
+    if (scaling != PLMLA_ROPE_PLAIN && !(isfinite(factor) && factor >= 1.0))
+        return PLMLA_INVALID_ARGUMENT;
+    if (scaling == PLMLA_ROPE_BY_PARTS &&
+        !(isfinite(original_len) && original_len > 0.0 && low >= 0.0 && low < high &&
+          isfinite(high)))
+        return PLMLA_INVALID_ARGUMENT;
+    for (int32_t i = 0; i < dim / 2; ++i) {
+        // turns per position, at most 1 / (2 pi)
+        double f = pow(base, -2.0 * i / dim) / 6.283185307179586477;
+        if (scaling == PLMLA_ROPE_LINEAR) {
+            f /= factor;
+        } else if (scaling == PLMLA_ROPE_BY_PARTS) {
+            const double g = fmin(fmax((original_len * f - low) / (high - low), 0.0), 1.0);
+            f = (1.0 - g) * f / factor + g * f;
+        }
+        turns[i] = (uint64_t)ldexp(f, 64);
+    }
+    return PLMLA_OK;
+}
+
+extern "C" plmla_status mla_rope(const void *x, int64_t tok_stride, int64_t head_stride,
+                                 const int32_t *positions, const uint64_t *turns, float magnitude,
+                                 int64_t tokens, int32_t heads, int32_t dim, int32_t dtype,
+                                 int32_t layout, int32_t inverse, void *out,
+                                 int64_t out_tok_stride, int64_t out_head_stride, void *stream)
+{
+    if (tokens < 0 || heads < 1 || heads > kMaxRopeHeads || dim < 2 || dim > kMaxRopeDim ||
+        dim % 2 != 0 || dtype < PLMLA_BF16 || dtype > PLMLA_FP32 || layout < PLMLA_ROPE_HALF ||
+        layout > PLMLA_ROPE_INTERLEAVED || !isfinite(magnitude))
+        return PLMLA_INVALID_ARGUMENT;
+    if (tokens == 0)
+        return PLMLA_OK;
+    const size_t size = dtype == PLMLA_FP32 ? 4 : 2;
+    if (x == nullptr || out == nullptr || positions == nullptr || turns == nullptr ||
+        !aligned(x, size) || !aligned(out, size) || !aligned(positions, 4) || !aligned(turns, 8))
+        return PLMLA_INVALID_ARGUMENT;
+    if (x == out && (tok_stride != out_tok_stride || head_stride != out_head_stride))
+        return PLMLA_INVALID_ARGUMENT;
+    const int sms = current_sm_count();
+    if (sms <= 0)
+        return PLMLA_CUDA_ERROR;
+    const RopeView v = {x, out, tok_stride, head_stride, out_tok_stride, out_head_stride,
+                        tokens, heads, dim};
+    const cudaError_t err = launch_rope(v, positions, turns, magnitude, inverse, dtype, layout,
+                                        sms, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
+}
+
+namespace {
+
+plmla_status append_rope_impl(const void *latent_new, const void *rope_new, void *slab_base,
+                              bool fp8, int64_t num_pages, int64_t page_stride_elems,
+                              float kv_scale, const int32_t *page_table, int64_t page_table_ld,
+                              const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+                              const int32_t *positions, const uint64_t *turns, float magnitude,
+                              int32_t layout, const void *q, int64_t q_tok_stride,
+                              int64_t q_head_stride, int32_t num_heads, void *q_out,
+                              int32_t *status, void *stream)
+{
+    if (num_reqs < 1 || n_new < 0 || layout < PLMLA_ROPE_HALF || layout > PLMLA_ROPE_INTERLEAVED ||
+        !isfinite(magnitude))
+        return PLMLA_INVALID_ARGUMENT;
+    if (n_new == 0)
+        return PLMLA_OK;
+    if (latent_new == nullptr || rope_new == nullptr || slab_base == nullptr ||
+        page_table == nullptr || seq_lens == nullptr || turns == nullptr)
+        return PLMLA_INVALID_ARGUMENT;
+    if (!aligned(latent_new, 16) || !aligned(rope_new, 16) || !aligned(slab_base, 16) ||
+        !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(turns, 8) ||
+        (positions != nullptr && !aligned(positions, 4)) ||
+        (status != nullptr && !aligned(status, 4)))
+        return PLMLA_INVALID_ARGUMENT;
+    if (num_pages < 1 || page_table_ld < 1 || page_stride_elems < (int64_t)kPageTokens * kRow ||
+        page_stride_elems % (fp8 ? 16 : 8) != 0 || !(isfinite(kv_scale) && kv_scale > 0.f))
+        return PLMLA_INVALID_ARGUMENT;
+    if (q != nullptr && (q_out == nullptr || q_out == q || num_heads < 1 ||
+                         num_heads > kMaxRopeHeads || !aligned(q, 2) || !aligned(q_out, 16)))
+        return PLMLA_INVALID_ARGUMENT;
+    const int sms = current_sm_count();
+    if (sms <= 0)
+        return PLMLA_CUDA_ERROR;
+    const RopeView v = {q, q_out, q_tok_stride, q_head_stride, (int64_t)num_heads * kRope, kRope,
+                        (int64_t)num_reqs * n_new, q != nullptr ? num_heads : 0, kRope};
+    const cudaError_t err = launch_append_rope(latent_new, rope_new, slab_base, fp8, num_pages,
+                                               page_stride_elems, kv_scale, page_table,
+                                               page_table_ld, seq_lens, num_reqs, n_new, positions,
+                                               turns, magnitude, layout, v, status, sms,
+                                               static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
+}
+
+}  // namespace
+
+extern "C" plmla_status mla_kv_append_rope(
+    const void *latent_new, const void *rope_new, void *slab_base, int64_t num_pages,
+    int64_t page_stride_elems, const int32_t *page_table, int64_t page_table_ld,
+    const int32_t *seq_lens, int32_t num_reqs, int32_t n_new, const int32_t *positions,
+    const uint64_t *turns, float magnitude, int32_t layout, const void *q, int64_t q_tok_stride,
+    int64_t q_head_stride, int32_t num_heads, void *q_out, int32_t *status, void *stream)
+{
+    return append_rope_impl(latent_new, rope_new, slab_base, false, num_pages, page_stride_elems,
+                            1.f, page_table, page_table_ld, seq_lens, num_reqs, n_new, positions,
+                            turns, magnitude, layout, q, q_tok_stride, q_head_stride, num_heads,
+                            q_out, status, stream);
+}
+
+extern "C" plmla_status mla_kv_append_rope_fp8(
+    const void *latent_new, const void *rope_new, void *slab_base, int64_t num_pages,
+    int64_t page_stride_elems, float kv_scale, const int32_t *page_table, int64_t page_table_ld,
+    const int32_t *seq_lens, int32_t num_reqs, int32_t n_new, const int32_t *positions,
+    const uint64_t *turns, float magnitude, int32_t layout, const void *q, int64_t q_tok_stride,
+    int64_t q_head_stride, int32_t num_heads, void *q_out, int32_t *status, void *stream)
+{
+    return append_rope_impl(latent_new, rope_new, slab_base, true, num_pages, page_stride_elems,
+                            kv_scale, page_table, page_table_ld, seq_lens, num_reqs, n_new,
+                            positions, turns, magnitude, layout, q, q_tok_stride, q_head_stride,
+                            num_heads, q_out, status, stream);
+}
+
+namespace {
+
+plmla_status mass_impl(const void *q_nope_absorbed, const void *q_rope, const float *lse,
+                       const void *slab_base, bool fp8, int64_t num_pages,
+                       int64_t page_stride_elems, float kv_scale, const int32_t *page_table,
+                       int64_t page_table_ld, const int32_t *seq_lens, int32_t num_reqs,
+                       int32_t n_q_per_req, int32_t num_heads, float scale, float decay,
+                       float *mass, int64_t mass_ld, int64_t mass_cols, void *workspace,
+                       size_t workspace_bytes, int32_t *status, void *stream)
+{
+    if (q_nope_absorbed == nullptr || q_rope == nullptr || lse == nullptr ||
+        slab_base == nullptr || page_table == nullptr || seq_lens == nullptr || mass == nullptr)
+        return PLMLA_INVALID_ARGUMENT;
+    if (!shape_ok(num_reqs, n_q_per_req, num_heads) || num_pages < 1 || num_pages > INT32_MAX ||
+        page_table_ld < 1 || mass_cols < 1 || mass_ld < mass_cols ||
+        page_stride_elems < (int64_t)kPageTokens * kRow ||
+        page_stride_elems % (fp8 ? 16 : 8) != 0 || !isfinite(scale) || !isfinite(decay) ||
+        !(isfinite(kv_scale) && kv_scale > 0.f))
+        return PLMLA_INVALID_ARGUMENT;
+    if (!aligned(q_nope_absorbed, 16) || !aligned(q_rope, 16) || !aligned(lse, 4) ||
+        !aligned(slab_base, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(mass, 4) || (status != nullptr && !aligned(status, 4)))
+        return PLMLA_INVALID_ARGUMENT;
+    MassArgs a = {};
+    a.slab = slab_base;
+    a.num_pages = num_pages;
+    a.page_stride = page_stride_elems;
+    a.page_table = page_table;
+    a.table_ld = page_table_ld;
+    a.seq_lens = seq_lens;
+    a.num_reqs = num_reqs;
+    a.n_q = n_q_per_req;
+    a.heads = num_heads;
+    a.rows = n_q_per_req * num_heads;
+    a.q_nope = static_cast<const __nv_bfloat16 *>(q_nope_absorbed);
+    a.q_rope = static_cast<const __nv_bfloat16 *>(q_rope);
+    a.lse = lse;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    a.kv_scale = kv_scale;
+    a.decay = decay;
+    a.mass = mass;
+    a.mass_ld = mass_ld;
+    a.mass_cols = mass_cols;
+    a.status = status;
+    const int sms = current_sm_count();
+    if (sms <= 0)
+        return PLMLA_CUDA_ERROR;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (fp8) {
+        const size_t rows = (size_t)num_reqs * a.rows;
+        if (workspace == nullptr || !aligned(workspace, kAlign))
+            return PLMLA_INVALID_ARGUMENT;
+        if (workspace_bytes < mla_mass_workspace_size_fp8(num_reqs, n_q_per_req, num_heads))
+            return PLMLA_WORKSPACE_TOO_SMALL;
+        uint8_t *q8 = static_cast<uint8_t *>(workspace);
+        int32_t *qexp = reinterpret_cast<int32_t *>(q8 + align_up(2 * (size_t)kRow * rows));
+        if (launch_quantize(a.q_nope, a.q_rope, (int)rows, q8, qexp, s) != cudaSuccess)
+            return PLMLA_CUDA_ERROR;
+        a.q8 = q8;
+        a.qexp = qexp;
+    }
+    return launch_mass(a, sms, s) == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
+}
+
+}  // namespace
+
+extern "C" size_t mla_mass_workspace_size_fp8(int32_t num_reqs, int32_t n_q, int32_t num_heads)
+{
+    if (!shape_ok(num_reqs, n_q, num_heads))
+        return 0;
+    const size_t rows = (size_t)num_reqs * n_q * num_heads;
+    return align_up(2 * (size_t)kRow * rows) + align_up(sizeof(int32_t) * rows);
+}
+
+extern "C" plmla_status mla_attention_mass(
+    const void *q_nope_absorbed, const void *q_rope, const float *lse, const void *slab_base,
+    int64_t num_pages, int64_t page_stride_elems, const int32_t *page_table, int64_t page_table_ld,
+    const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads, float scale,
+    float decay, float *mass, int64_t mass_ld, int64_t mass_cols, int32_t *status, void *stream)
+{
+    return mass_impl(q_nope_absorbed, q_rope, lse, slab_base, false, num_pages, page_stride_elems,
+                     1.f, page_table, page_table_ld, seq_lens, num_reqs, n_q_per_req, num_heads,
+                     scale, decay, mass, mass_ld, mass_cols, nullptr, 0, status, stream);
+}
+
+extern "C" plmla_status mla_attention_mass_fp8(
+    const void *q_nope_absorbed, const void *q_rope, const float *lse, const void *slab_base,
+    int64_t num_pages, int64_t page_stride_elems, float kv_scale, const int32_t *page_table,
+    int64_t page_table_ld, const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req,
+    int32_t num_heads, float scale, float decay, float *mass, int64_t mass_ld, int64_t mass_cols,
+    void *workspace, size_t workspace_bytes, int32_t *status, void *stream)
+{
+    return mass_impl(q_nope_absorbed, q_rope, lse, slab_base, true, num_pages, page_stride_elems,
+                     kv_scale, page_table, page_table_ld, seq_lens, num_reqs, n_q_per_req,
+                     num_heads, scale, decay, mass, mass_ld, mass_cols, workspace, workspace_bytes,
+                     status, stream);
+}
+
+extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld,
+                                         int64_t mass_cols, const int32_t *seq_lens,
+                                         int32_t num_reqs, int32_t keep, int32_t sink,
+                                         int32_t recent, int32_t *kept, int64_t kept_ld,
+                                         int32_t *kept_lens, void *stream)
+{
+    if (mass == nullptr || seq_lens == nullptr || kept == nullptr || kept_lens == nullptr ||
+        num_reqs < 1 || num_reqs > kMaxReqs || mass_cols < 1 || mass_ld < mass_cols || keep < 1 || sink < 0 || recent < 0 ||
+        (int64_t)sink + recent > keep || kept_ld < (keep < mass_cols ? keep : mass_cols) ||
+        !aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4))
+        return PLMLA_INVALID_ARGUMENT;
+    const int sms = current_sm_count();
+    if (sms <= 0)
+        return PLMLA_CUDA_ERROR;
+    const cudaError_t err = launch_select(mass, mass_ld, mass_cols, seq_lens, num_reqs, keep, sink, recent,
+                                          kept, kept_ld, kept_lens, sms,
+                                          static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
+}
+
+extern "C" plmla_status mla_kv_compact(int32_t num_layers, void *const *slab_base,
+                                       int32_t elem_bytes, int64_t num_pages,
+                                       int64_t page_stride_elems, const int32_t *page_table,
+                                       int64_t page_table_ld, const int32_t *seq_lens,
+                                       const int32_t *out_table, int64_t out_table_ld,
+                                       const int32_t *kept, int64_t kept_ld,
+                                       const int32_t *kept_lens, int32_t num_reqs,
+                                       int32_t kept_cols, const float *mass, int64_t mass_ld,
+                                       int64_t mass_cols, float *mass_out, int64_t mass_out_ld,
+                                       int32_t *status, void *stream)
+{
+    if (num_layers < 1 || num_layers > kMaxLayers || slab_base == nullptr ||
+        (elem_bytes != 1 && elem_bytes != 2) || page_table == nullptr || seq_lens == nullptr ||
+        out_table == nullptr || out_table == page_table || kept == nullptr ||
+        kept_lens == nullptr || num_reqs < 1 || num_reqs > kMaxReqs || kept_cols < 0 ||
+        kept_ld < kept_cols || num_pages < 1 || page_table_ld < 1 || out_table_ld < 1 ||
+        page_stride_elems < (int64_t)kPageTokens * kRow ||
+        page_stride_elems * elem_bytes % 16 != 0)
+        return PLMLA_INVALID_ARGUMENT;
+    if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(out_table, 4) ||
+        !aligned(kept, 4) || !aligned(kept_lens, 4) || (status != nullptr && !aligned(status, 4)))
+        return PLMLA_INVALID_ARGUMENT;
+    if ((mass == nullptr) != (mass_out == nullptr) ||
+        (mass != nullptr && (mass == mass_out || mass_cols < 1 || mass_ld < mass_cols ||
+                             mass_out_ld < kept_cols ||
+                             !aligned(mass, 4) || !aligned(mass_out, 4))))
+        return PLMLA_INVALID_ARGUMENT;
+    for (int32_t l = 0; l < num_layers; ++l)
+        if (slab_base[l] == nullptr || !aligned(slab_base[l], 16))
+            return PLMLA_INVALID_ARGUMENT;
+    if (kept_cols == 0)
+        return PLMLA_OK;
+    const cudaError_t err =
+        launch_compact(num_layers, slab_base, elem_bytes == 1, num_pages,
+                       page_stride_elems * elem_bytes, page_table, page_table_ld, seq_lens,
+                       out_table, out_table_ld, kept, kept_ld, kept_lens, num_reqs, kept_cols, mass,
+                       mass_ld, mass_cols, mass_out, mass_out_ld, status,
+                       static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
+}

@@ -124,6 +124,63 @@ cudaError_t launch_append_fp8(const void *latent, const void *rope, void *slab,
                               const int32_t *table, int64_t table_ld, const int32_t *seq_lens,
                               int num_reqs, int n_new, int32_t *status, cudaStream_t stream);
 
+// Rotary positions (plmla_rope.cu): heads of `dim` elements, unit stride within a
+// head, other strides in elements.
+struct RopeView {
+    const void *x;
+    void *out;
+    int64_t tok_stride, head_stride, out_tok_stride, out_head_stride;
+    int64_t tokens;
+    int heads, dim;
+};
+constexpr int kMaxRopeDim = 1024, kMaxRopeHeads = 65535;
+constexpr int kRopeBf16 = 0, kRopeFp16 = 1, kRopeFp32 = 2;   // element types
+cudaError_t launch_rope(const RopeView &v, const int32_t *positions, const uint64_t *turns,
+                        float magnitude, int inverse, int dtype, int interleaved, int sms,
+                        cudaStream_t stream);
+// The append with the rope part rotated, and the same tokens' query heads (none
+// when v.heads is 0); positions may be null (the row's index in its history).
+cudaError_t launch_append_rope(const void *latent, const void *rope, void *slab, bool fp8,
+                               int64_t num_pages, int64_t page_stride, float kv_scale,
+                               const int32_t *table, int64_t table_ld, const int32_t *seq_lens,
+                               int num_reqs, int n_new, const int32_t *positions,
+                               const uint64_t *turns, float magnitude, int interleaved,
+                               const RopeView &v, int32_t *status, int sms, cudaStream_t stream);
+
+// Accumulated attention weight (plmla_mass.cu).
+constexpr int32_t kStatusMassLength = 34;       // a history longer than its row of weights
+struct MassArgs {
+    const void *slab;                   // bf16 elements, or E4M3 bytes (q8 set)
+    int64_t num_pages, page_stride;
+    const int32_t *page_table;
+    int64_t table_ld;
+    const int32_t *seq_lens;
+    int num_reqs, n_q, heads, rows;     // rows = n_q * heads
+    const __nv_bfloat16 *q_nope, *q_rope;
+    const uint8_t *q8;                  // E4M3: [2, num_reqs * rows, 576], hi plane then lo
+    const int32_t *qexp;
+    const float *lse;                   // [num_reqs * rows], natural log
+    float scale_log2, kv_scale;         // softmax scale * log2(e)
+    float decay;
+    float *mass;
+    int64_t mass_ld, mass_cols;         // row stride, and the columns a row has
+    int32_t *status;                    // may be null
+};
+cudaError_t launch_mass(const MassArgs &args, int sms, cudaStream_t stream);
+
+// Eviction (plmla_evict.cu).
+constexpr int kCompactLayers = 64;              // layers of one compaction launch
+cudaError_t launch_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
+                          const int32_t *seq_lens, int num_reqs, int keep, int sink, int recent, int32_t *kept,
+                          int64_t kept_ld, int32_t *kept_lens, int sms, cudaStream_t stream);
+cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t num_pages,
+                           int64_t page_bytes, const int32_t *table, int64_t table_ld,
+                           const int32_t *seq_lens, const int32_t *out_table, int64_t out_ld,
+                           const int32_t *kept, int64_t kept_ld, const int32_t *kept_lens,
+                           int num_reqs, int keep, const float *mass, int64_t mass_ld,
+                           int64_t mass_cols, float *mass_out, int64_t mass_out_ld, int32_t *status,
+                           cudaStream_t stream);
+
 // Shared by the query quantiser (plan grid) and the FP8 append: one E4M3 byte
 // pair from two floats, round to nearest even, saturating to +-448.
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
