@@ -6,7 +6,6 @@ C ABI.  PyTorch only supplies device memory and the current stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -468,57 +467,99 @@ def _append(latent_new, rope_new, slab, page_table, seq_lens, n_new, status, str
 # ---------------------------------------------------------------------------
 # rotary positions, accumulated weights, eviction
 # ---------------------------------------------------------------------------
+#
+# A decode step's calls of these take a few microseconds on the device, so their
+# checks are written to be quick: messages are only formatted on failure, a
+# tensor's device is read as an index (-1 for host memory), and the current device
+# and stream come from torch's raw accessors instead of the wrapping objects.
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
 _ROPE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_NO_GUARD = contextlib.nullcontext()
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
 
-def _on(device, **tensors):
-    """Checks that every tensor (or None) lies on `device`; returns the context
-    that makes it current for the launch."""
-    for name, t in tensors.items():
-        _require(t is None or t.device == device, f"{name} must be on {device}")
-    return _NO_GUARD if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _fail(message):
+    raise ValueError(message)
 
 
-def _check_ints(t, name, shape):
-    _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
-             and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-             f"{name} must be a contiguous CUDA int32 tensor of shape {tuple(shape)}")
+def _launch(dev, fn, where, stream, *args):
+    """Calls the library with the stream as last argument, device `dev` current."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status != 0:
+        raise _native.PlmlaError(status, where)
 
 
-def _check_table(t, name, num_reqs):
-    _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32
-             and t.dim() == 2 and t.shape[0] == num_reqs and t.shape[1] >= 1
-             and t.stride(1) == 1 and (num_reqs == 1 or t.stride(0) >= t.shape[1]),
-             f"{name} must be a CUDA int32 [{num_reqs}, columns] view with unit column stride")
+def _vector(t, name, dev, n):
+    """A contiguous int32 vector of n elements on device `dev`."""
+    if not (t.dtype is _I32 and t.get_device() == dev and t.dim() == 1 and t.shape[0] == n
+            and t.is_contiguous()):
+        _fail(f"{name} must be a contiguous int32 tensor [{n}] on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _row_stride(t):
-    """Stride between the rows of a 2-D view (its width where there is one row)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, name, dev, dtype, n):
+    """(address, row stride, columns) of an [n, columns] view with unit column
+    stride and rows that do not overlap."""
+    shape = t.shape
+    if not (t.dtype is dtype and t.get_device() == dev and len(shape) == 2 and shape[0] == n
+            and shape[1] >= 1):
+        _fail(f"{name} must be a {dtype} tensor [{n}, columns] on cuda:{dev}")
+    ld, unit = t.stride()
+    cols = shape[1]
+    if n == 1:
+        ld = cols
+    if (unit != 1 and cols > 1) or ld < cols:
+        _fail(f"{name} must have unit column stride and rows that do not overlap")
+    return t.data_ptr(), ld, cols
 
 
-def _check_status(status):
-    _require(status is None or (status.is_cuda and status.dtype == torch.int32
-                                and status.numel() >= 1), "status must be a CUDA int32 tensor")
+def _dense(t, name, dev, shape, dtype=_BF16):
+    if not (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        _fail(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _check_pool(slab, fp8):
-    want = torch.uint8 if fp8 else torch.bfloat16
-    _require(isinstance(slab, torch.Tensor) and slab.is_cuda and slab.dtype == want
-             and slab.dim() == 2 and slab.stride(1) == 1,
-             f"slab must be a CUDA {want} [num_pages, page_stride] view")
-    _require(slab.shape[1] >= PAGE_TOKENS * ROW, "slab page too small")
+def _pool(slab, fp8):
+    """(address, pages, page stride) of a pool [num_pages, page_stride]."""
+    shape = slab.shape
+    if not (slab.dtype is (_U8 if fp8 else _BF16) and slab.is_cuda and len(shape) == 2
+            and shape[1] >= PAGE_TOKENS * ROW and slab.stride(1) == 1):
+        _fail(f"slab must be a CUDA {_U8 if fp8 else _BF16} view [num_pages, page_stride >= "
+              f"{PAGE_TOKENS * ROW}] with contiguous pages")
+    return slab.data_ptr(), shape[0], slab.stride(0) if shape[0] > 1 else shape[1]
 
 
-def _check_mass(t, name, num_reqs):
-    _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.float32
-             and t.dim() == 2 and t.shape[0] == num_reqs and t.shape[1] >= 1
-             and t.stride(1) == 1 and (num_reqs == 1 or t.stride(0) >= t.shape[1]),
-             f"{name} must be a CUDA fp32 [{num_reqs}, tokens] view with unit column stride")
+def _flag(status, dev):
+    if status is None:
+        return None
+    if not (status.dtype is _I32 and status.get_device() == dev and status.numel() >= 1):
+        _fail(f"status must be an int32 tensor on cuda:{dev}")
+    return status.data_ptr()
+
+
+def _heads(t):
+    """(token stride, head stride) of a [T, H, D] view, 0 along extents of one."""
+    T, H, _ = t.shape
+    ts, hs, _ = t.stride()
+    return (ts if T > 1 else 0), (hs if H > 1 else 0)
+
+
+def _check_apart(a, b, message):
+    """Refuses two views whose address ranges meet."""
+    def span(t):
+        first = t.data_ptr()
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return first, first + (last + 1) * t.element_size()
+    (a0, a1), (b0, b1) = span(a), span(b)
+    if a0 < b1 and b0 < a1:
+        _fail(message)
 
 
 class RopeTable:
@@ -527,6 +568,11 @@ class RopeTable:
 
     def __init__(self, turns, magnitude):
         self.turns, self.magnitude, self.dim = turns, float(magnitude), 2 * turns.numel()
+
+    def address(self, dev, dim):
+        if self.dim != dim or self.turns.get_device() != dev:
+            _fail(f"the rotary table must have dim {dim} and lie on cuda:{dev}")
+        return self.turns.data_ptr()
 
 
 def rope_table(dim=ROPE, *, base=10000.0, scaling="none", factor=1.0, original_len=0, low=1.0,
@@ -538,35 +584,26 @@ def rope_table(dim=ROPE, *, base=10000.0, scaling="none", factor=1.0, original_l
     that turn more than ``high`` times kept, and a ramp joins the two.
     ``magnitude`` scales the rotated pairs; by default 1, and 0.1 ln(factor) + 1 by
     parts.  Make the table once and keep it: it is copied to the device here."""
-    _require(scaling in ROPE_SCALINGS, f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    if scaling not in ROPE_SCALINGS:
+        _fail(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
     host = torch.empty(max(dim, 0) // 2, dtype=torch.int64)
     status = _native.lib().mla_rope_turns(int(dim), float(base), ROPE_SCALINGS[scaling],
                                           float(factor), float(original_len), float(low),
                                           float(high), host.data_ptr())
     if status != 0:
-        raise ValueError(f"invalid rotary table: {_native.strerror(status)}")
+        _fail(f"invalid rotary table: {_native.strerror(status)}")
     if magnitude is None:
         magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "by_parts" else 1.0
-    _require(math.isfinite(magnitude), "magnitude must be finite")
+    if not math.isfinite(magnitude):
+        _fail("magnitude must be finite")
     return RopeTable(host.to(device or "cuda"), magnitude)
 
 
-def _head_strides(t):
-    """(token stride, head stride) of a [T, H, D] view, 0 along extents of one."""
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
-
-
-def _span(t):
-    """First and last byte of a view with non-negative strides."""
-    first = t.data_ptr()
-    return first, first + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * \
-        t.element_size()
-
-
-def _check_apart(a, b, what):
-    """Refuses two views whose address ranges meet."""
-    (a0, a1), (b0, b1) = _span(a), _span(b)
-    _require(a1 <= b0 or b1 <= a0, what)
+def _layout(layout):
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
+        _fail(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    return code
 
 
 def mla_rope(x, positions, table, *, layout="half", inverse=False, out=None, stream=None):
@@ -576,34 +613,37 @@ def mla_rope(x, positions, table, *, layout="half", inverse=False, out=None, str
     with 2i + 1 ("interleaved"); ``inverse`` negates the angles, which is the
     gradient of the forward call.  ``out`` may be x itself (in place); returns it
     (a new contiguous tensor by default)."""
-    _require(isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _ROPE_TYPES and x.dim() == 3,
-             "x must be a CUDA bf16, fp16 or fp32 tensor [T, H, D]")
+    kind = _ROPE_TYPES.get(x.dtype)
+    dev = x.get_device()
+    if kind is None or dev < 0 or x.dim() != 3 or x.stride(2) != 1:
+        _fail("x must be a CUDA bf16, fp16 or fp32 tensor [T, H, D] with contiguous heads")
     T, H, D = x.shape
-    _require(D == table.dim, f"x has {D} elements per head, the table {table.dim}")
-    _require(layout in ROPE_LAYOUTS, f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    _require(x.stride(2) == 1, "the elements of a head must be contiguous")
-    _check_ints(positions, "positions", (T,))
+    code = _layout(layout)
+    at, turns = _vector(positions, "positions", dev, T), table.address(dev, D)
     if out is None:
         out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
     else:
-        _require(out.is_cuda and out.dtype == x.dtype and out.shape == x.shape
-                 and out.stride(2) == 1, "out must be like x, each head contiguous")
-        if T and H:
-            ts, hs = _head_strides(out)
-            _require((H == 1 or hs >= D) and (T == 1 or ts >= D) and
-                     (T == 1 or H == 1 or ts >= (H - 1) * hs + D or hs >= (T - 1) * ts + D),
-                     "heads of out overlap")
-            if not (out.data_ptr() == x.data_ptr() and _head_strides(out) == _head_strides(x)):
-                _check_apart(x, out, "out must be x or not overlap it")
-    if T == 0 or H == 0:
-        return out
-    with _on(x.device, positions=positions, table=table.turns, out=out):
-        status = _native.lib().mla_rope(
-            x.data_ptr(), *_head_strides(x), positions.data_ptr(), table.turns.data_ptr(),
-            table.magnitude, T, H, D, _ROPE_TYPES[x.dtype], ROPE_LAYOUTS[layout], int(inverse),
-            out.data_ptr(), *_head_strides(out), _stream_ptr(stream, x.device))
-    _native.check(status, "mla_rope")
+        _check_rope_out(x, out, dev)
+    if T and H:
+        _launch(dev, _native.lib().mla_rope, "mla_rope", stream, x.data_ptr(), *_heads(x), at,
+                turns, table.magnitude, T, H, D, kind, code, bool(inverse), out.data_ptr(),
+                *_heads(out))
     return out
+
+
+def _check_rope_out(x, out, dev):
+    if not (out.dtype is x.dtype and out.get_device() == dev and out.shape == x.shape
+            and out.stride(2) == 1):
+        _fail("out must be like x, each head contiguous")
+    T, H, D = out.shape
+    if T == 0 or H == 0:
+        return
+    ts, hs = _heads(out)
+    if not ((H == 1 or hs >= D) and (T == 1 or ts >= D)
+            and (T == 1 or H == 1 or ts >= (H - 1) * hs + D or hs >= (T - 1) * ts + D)):
+        _fail("heads of out overlap")
+    if not (out.data_ptr() == x.data_ptr() and _heads(out) == _heads(x)):
+        _check_apart(x, out, "out must be x or not overlap it")
 
 
 def mla_kv_append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, *,
@@ -624,72 +664,63 @@ def mla_kv_append_rope_fp8(latent_new, rope_new, slab, page_table, seq_lens, n_n
                            status=None, stream=None):
     """mla_kv_append_rope into E4M3 pages (slab and kv_scale as in
     mla_kv_append_fp8)."""
-    _require(math.isfinite(kv_scale) and kv_scale > 0, "kv_scale must be finite and > 0")
     return _append_rope(latent_new, rope_new, _byte_view(slab), page_table, seq_lens, n_new, table,
-                        positions, layout, q_rope, q_out, status, stream, float(kv_scale))
+                        positions, layout, q_rope, q_out, status, stream, _kv_scale(kv_scale))
+
+
+def _kv_scale(kv_scale):
+    if not (math.isfinite(kv_scale) and kv_scale > 0):
+        _fail("kv_scale must be finite and > 0")
+    return float(kv_scale)
 
 
 def _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, positions, layout,
                  q_rope, q_out, status, stream, kv_scale):
-    fp8 = kv_scale is not None
-    _require(isinstance(seq_lens, torch.Tensor) and seq_lens.dim() == 1,
-             "seq_lens must be a contiguous CUDA int32 vector")
-    R = seq_lens.shape[0]
+    base, pages, page_stride = _pool(slab, kv_scale is not None)
+    dev = slab.get_device()
+    R = seq_lens.shape[0] if seq_lens.dim() == 1 else 0
     rows = R * n_new
-    _check_ints(seq_lens, "seq_lens", (R,))
-    _check_bf16(latent_new, "latent_new", (rows, LATENT))
-    _check_bf16(rope_new, "rope_new", (rows, ROPE))
-    _check_pool(slab, fp8)
-    _check_table(page_table, "page_table", R)
-    _require(layout in ROPE_LAYOUTS, f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    _require(table.dim == ROPE, f"the table must have dim {ROPE}")
-    if positions is not None:
-        _check_ints(positions, "positions", (rows,))
-    _check_status(status)
+    lens = _vector(seq_lens, "seq_lens", dev, R)
+    latent = _dense(latent_new, "latent_new", dev, (rows, LATENT))
+    rope = _dense(rope_new, "rope_new", dev, (rows, ROPE))
+    ids, ids_ld, _ = _rows(page_table, "page_table", dev, _I32, R)
+    at = None if positions is None else _vector(positions, "positions", dev, rows)
     q = (None, 0, 0, 0, None)
     if q_rope is None:
-        _require(q_out is None, "q_out needs q_rope")
+        if q_out is not None:
+            _fail("q_out needs q_rope")
     else:
-        _require(q_rope.is_cuda and q_rope.dtype == torch.bfloat16 and q_rope.dim() == 3
-                 and q_rope.shape[0] == rows and q_rope.shape[2] == ROPE
-                 and q_rope.stride(2) == 1,
-                 f"q_rope must be a CUDA bf16 [{rows}, H, {ROPE}] view with contiguous heads")
+        shape = q_rope.shape
+        if not (q_rope.dtype is _BF16 and q_rope.get_device() == dev and len(shape) == 3
+                and shape[0] == rows and shape[2] == ROPE and q_rope.stride(2) == 1):
+            _fail(f"q_rope must be a bf16 view [{rows}, H, {ROPE}] on cuda:{dev} with contiguous "
+                  "heads")
         if q_out is None:
-            q_out = torch.empty(q_rope.shape, dtype=torch.bfloat16, device=q_rope.device)
+            q_out = torch.empty(shape, dtype=_BF16, device=q_rope.device)
         else:
-            _check_bf16(q_out, "q_out", q_rope.shape)
+            _dense(q_out, "q_out", dev, shape)
             if q_out.numel():
                 _check_apart(q_rope, q_out, "q_out must not overlap q_rope")
-        if q_out.numel():
-            q = (q_rope.data_ptr(), *_head_strides(q_rope), q_rope.shape[1], q_out.data_ptr())
+        if rows and shape[1]:
+            q = (q_rope.data_ptr(), *_heads(q_rope), shape[1], q_out.data_ptr())
+    tail = (ids, ids_ld, lens, R, n_new, at, table.address(dev, ROPE), table.magnitude,
+            _layout(layout), *q, _flag(status, dev))
     lib = _native.lib()
-    with _on(slab.device, latent_new=latent_new, rope_new=rope_new, page_table=page_table,
-             seq_lens=seq_lens, table=table.turns, positions=positions, q_rope=q_rope, q_out=q_out,
-             status=status):
-        head = (latent_new.data_ptr(), rope_new.data_ptr(), slab.data_ptr(), slab.shape[0],
-                _page_stride(slab))
-        tail = (page_table.data_ptr(), _row_stride(page_table), seq_lens.data_ptr(), R,
-                int(n_new), None if positions is None else positions.data_ptr(),
-                table.turns.data_ptr(), table.magnitude, ROPE_LAYOUTS[layout], *q,
-                None if status is None else status.data_ptr(), _stream_ptr(stream, slab.device))
-        if fp8:
-            rc = lib.mla_kv_append_rope_fp8(*head, kv_scale, *tail)
-        else:
-            rc = lib.mla_kv_append_rope(*head, *tail)
-    _native.check(rc, "mla_kv_append_rope_fp8" if fp8 else "mla_kv_append_rope")
+    if kv_scale is not None:
+        _launch(dev, lib.mla_kv_append_rope_fp8, "mla_kv_append_rope_fp8", stream, latent, rope,
+                base, pages, page_stride, kv_scale, *tail)
+    else:
+        _launch(dev, lib.mla_kv_append_rope, "mla_kv_append_rope", stream, latent, rope, base,
+                pages, page_stride, *tail)
     return q_out
-
-
-def _page_stride(slab):
-    return slab.stride(0) if slab.shape[0] > 1 else slab.shape[1]
 
 
 def allocate_mass_workspace(num_reqs, n_q, num_heads, device=None):
     """A workspace tensor (uint8) of the size mla_attention_mass_fp8 needs."""
     n = _native.lib().mla_mass_workspace_size_fp8(num_reqs, n_q, num_heads)
     if n == 0:
-        raise ValueError("invalid shape for mla_mass_workspace_size_fp8")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        _fail("invalid shape for mla_mass_workspace_size_fp8")
+    return torch.empty(n, dtype=_U8, device=device or "cuda")
 
 
 def mla_attention_mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, *, n_q=1,
@@ -710,47 +741,39 @@ def mla_attention_mass_fp8(q_nope_absorbed, q_rope, lse, slab, page_table, seq_l
                            status=None, stream=None):
     """mla_attention_mass over E4M3 pages (slab and kv_scale as in mla_decode_fp8).
     The workspace comes from allocate_mass_workspace."""
-    _require(math.isfinite(kv_scale) and kv_scale > 0, "kv_scale must be finite and > 0")
     return _mass(q_nope_absorbed, q_rope, lse, _byte_view(slab), page_table, seq_lens, mass, n_q,
-                 scale, decay, float(kv_scale), workspace, status, stream)
+                 scale, decay, _kv_scale(kv_scale), workspace, status, stream)
 
 
 def _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, scale, decay,
           kv_scale, workspace, status, stream):
-    fp8 = kv_scale is not None
-    _require(q_nope_absorbed.dim() == 3, "q_nope_absorbed must be [R*n_q, H, 512]")
-    T, H, _ = q_nope_absorbed.shape
-    _require(n_q >= 1 and T % n_q == 0, "first dimension must be num_reqs * n_q")
+    base, pages, page_stride = _pool(slab, kv_scale is not None)
+    dev = slab.get_device()
+    shape = q_nope_absorbed.shape
+    if len(shape) != 3 or n_q < 1 or shape[0] % n_q != 0:
+        _fail("q_nope_absorbed must be [R*n_q, H, 512]")
+    T, H, _ = shape
     R = T // n_q
-    device = slab.device
-    _check_bf16(q_nope_absorbed, "q_nope_absorbed", (T, H, LATENT))
-    _check_bf16(q_rope, "q_rope", (T, H, ROPE))
-    _require(lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()
-             and tuple(lse.shape) == (T, H), "lse must be a contiguous CUDA fp32 [T, H]")
-    _check_pool(slab, fp8)
-    _check_table(page_table, "page_table", R)
-    _check_ints(seq_lens, "seq_lens", (R,))
-    _check_mass(mass, "mass", R)
-    _check_status(status)
+    qn = _dense(q_nope_absorbed, "q_nope_absorbed", dev, (T, H, LATENT))
+    qr = _dense(q_rope, "q_rope", dev, (T, H, ROPE))
+    l = _dense(lse, "lse", dev, (T, H), _F32)
+    ids, ids_ld, _ = _rows(page_table, "page_table", dev, _I32, R)
+    lens = _vector(seq_lens, "seq_lens", dev, R)
+    out = _rows(mass, "mass", dev, _F32, R)
+    flag = _flag(status, dev)
     lib = _native.lib()
-    if fp8 and workspace is None:
-        workspace = allocate_mass_workspace(R, n_q, H, device)
-    with _on(device, q_nope_absorbed=q_nope_absorbed, q_rope=q_rope, lse=lse,
-             page_table=page_table, seq_lens=seq_lens, mass=mass, workspace=workspace,
-             status=status):
-        head = (q_nope_absorbed.data_ptr(), q_rope.data_ptr(), lse.data_ptr(), slab.data_ptr(),
-                slab.shape[0], _page_stride(slab))
-        tail = (page_table.data_ptr(), _row_stride(page_table), seq_lens.data_ptr(), R, n_q, H,
-                float(scale), float(decay), mass.data_ptr(), _row_stride(mass), mass.shape[1])
-        end = (None if status is None else status.data_ptr(), _stream_ptr(stream, device))
-        if fp8:
-            _require(workspace.is_cuda and workspace.is_contiguous(),
-                     "workspace must be CUDA memory")
-            rc = lib.mla_attention_mass_fp8(*head, kv_scale, *tail, workspace.data_ptr(),
-                                            workspace.numel() * workspace.element_size(), *end)
-        else:
-            rc = lib.mla_attention_mass(*head, *tail, *end)
-    _native.check(rc, "mla_attention_mass_fp8" if fp8 else "mla_attention_mass")
+    tail = (ids, ids_ld, lens, R, n_q, H, scale, decay, *out)
+    if kv_scale is None:
+        _launch(dev, lib.mla_attention_mass, "mla_attention_mass", stream, qn, qr, l, base, pages,
+                page_stride, *tail, flag)
+    else:
+        if workspace is None:
+            workspace = allocate_mass_workspace(R, n_q, H, slab.device)
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _fail(f"workspace must be contiguous memory on cuda:{dev}")
+        _launch(dev, lib.mla_attention_mass_fp8, "mla_attention_mass_fp8", stream, qn, qr, l, base,
+                pages, page_stride, kv_scale, *tail, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), flag)
     return mass
 
 
@@ -761,26 +784,24 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
     the lower index).  Returns (kept [R, min(keep, tokens)] int32 ascending
     indices, kept_lens [R] int32 = min(keep, seq_lens)); entries of kept past a
     row's count are not written."""
-    _require(isinstance(mass, torch.Tensor) and mass.dim() == 2, "mass must be [R, tokens]")
-    R = mass.shape[0]
-    _check_mass(mass, "mass", R)
-    _check_ints(seq_lens, "seq_lens", (R,))
-    _require(keep >= 1 and sink >= 0 and recent >= 0 and sink + recent <= keep,
-             "keep >= 1, sink and recent >= 0, and sink + recent <= keep are needed")
-    cols = min(int(keep), mass.shape[1])
+    dev = mass.get_device()
+    if mass.dim() != 2 or dev < 0:
+        _fail("mass must be a CUDA tensor [R, tokens]")
+    R, tokens = mass.shape
+    weights = _rows(mass, "mass", dev, _F32, R)
+    lens = _vector(seq_lens, "seq_lens", dev, R)
+    if not (keep >= 1 and sink >= 0 and recent >= 0 and sink + recent <= keep):
+        _fail("keep >= 1, sink and recent >= 0, and sink + recent <= keep are needed")
+    cols = min(keep, tokens)
     if kept is None:
-        kept = torch.empty(R, cols, dtype=torch.int32, device=mass.device)
-    _check_table(kept, "kept", R)
-    _require(kept.shape[1] >= cols, f"kept needs {cols} columns")
+        kept = torch.empty(R, cols, dtype=_I32, device=mass.device)
     if kept_lens is None:
-        kept_lens = torch.empty(R, dtype=torch.int32, device=mass.device)
-    _check_ints(kept_lens, "kept_lens", (R,))
-    with _on(mass.device, seq_lens=seq_lens, kept=kept, kept_lens=kept_lens):
-        status = _native.lib().mla_evict_select(
-            mass.data_ptr(), _row_stride(mass), mass.shape[1], seq_lens.data_ptr(), R, int(keep),
-            int(sink), int(recent), kept.data_ptr(), _row_stride(kept), kept_lens.data_ptr(),
-            _stream_ptr(stream, mass.device))
-    _native.check(status, "mla_evict_select")
+        kept_lens = torch.empty(R, dtype=_I32, device=mass.device)
+    ids, ids_ld, have = _rows(kept, "kept", dev, _I32, R)
+    if have < cols:
+        _fail(f"kept needs {cols} columns")
+    _launch(dev, _native.lib().mla_evict_select, "mla_evict_select", stream, *weights, lens, R,
+            keep, sink, recent, ids, ids_ld, _vector(kept_lens, "kept_lens", dev, R))
     return kept, kept_lens
 
 
@@ -794,45 +815,41 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
     returns mass_out (None without mass).  ``status``: optional CUDA int32 tensor
     of one element, set to 33 where an index or page is out of range (such rows are
     skipped).  The old pages are not changed.  Asynchronous."""
-    _require(isinstance(slabs, (list, tuple)) and len(slabs) >= 1, "slabs must be a list of pools")
-    fp8 = slabs[0].dtype != torch.bfloat16
-    if fp8:
-        slabs = [_byte_view(s) for s in slabs]
+    if not isinstance(slabs, (list, tuple)) or not slabs:
+        _fail("slabs must be a list of pools")
     first = slabs[0]
-    for s in slabs:
-        _check_pool(s, fp8)
-        _require(s.shape == first.shape and s.stride(0) == first.stride(0)
-                 and s.device == first.device, "the layers' slabs must share their shape")
-    _require(isinstance(kept, torch.Tensor) and kept.dim() == 2, "kept must be [R, columns]")
-    R, cols = kept.shape
-    _check_table(kept, "kept", R)
-    _check_ints(kept_lens, "kept_lens", (R,))
-    _check_ints(seq_lens, "seq_lens", (R,))
-    _check_table(page_table, "page_table", R)
-    _check_table(out_table, "out_table", R)
-    _check_status(status)
+    dtype, fp8 = first.dtype, first.dtype is not _BF16
+    base, pages, page_stride = _pool(_byte_view(first) if fp8 else first, fp8)
+    dev, layers = first.get_device(), len(slabs)
+    bases = (ctypes.c_void_p * layers)(base)
+    shape, strides = first.shape, first.stride()
+    for i in range(1, layers):
+        s = slabs[i]
+        if not (s.dtype is dtype and s.get_device() == dev and s.shape == shape
+                and s.stride() == strides):
+            _fail("the layers' slabs must share their type, shape and strides")
+        bases[i] = s.data_ptr()
+    if kept.dim() != 2:
+        _fail("kept must be [R, columns]")
+    R = kept.shape[0]
+    idx, idx_ld, cols = _rows(kept, "kept", dev, _I32, R)
+    ids, ids_ld, _ = _rows(page_table, "page_table", dev, _I32, R)
+    outs, outs_ld, _ = _rows(out_table, "out_table", dev, _I32, R)
+    carried = (None, 0, 0, None, 0)
     if mass is None:
-        _require(mass_out is None, "mass_out needs mass")
+        if mass_out is not None:
+            _fail("mass_out needs mass")
     else:
-        _check_mass(mass, "mass", R)
+        weights = _rows(mass, "mass", dev, _F32, R)
         if mass_out is None:
-            mass_out = torch.empty(R, cols, dtype=torch.float32, device=mass.device)
-        _check_mass(mass_out, "mass_out", R)
-        _require(mass_out.shape[1] >= cols, f"mass_out needs {cols} columns")
+            mass_out = torch.empty(R, cols, dtype=_F32, device=mass.device)
+        dst, dst_ld, have = _rows(mass_out, "mass_out", dev, _F32, R)
+        if have < cols:
+            _fail(f"mass_out needs {cols} columns")
         _check_apart(mass, mass_out, "mass_out must not overlap mass")
-    L = len(slabs)
-    bases = (ctypes.c_void_p * L)(*[s.data_ptr() for s in slabs])
-    with _on(first.device, page_table=page_table, seq_lens=seq_lens, out_table=out_table,
-             kept=kept, kept_lens=kept_lens, mass=mass, mass_out=mass_out, status=status):
-        rc = _native.lib().mla_kv_compact(
-            L, ctypes.cast(bases, ctypes.c_void_p), 1 if fp8 else 2, first.shape[0],
-            _page_stride(first), page_table.data_ptr(), _row_stride(page_table),
-            seq_lens.data_ptr(), out_table.data_ptr(), _row_stride(out_table), kept.data_ptr(),
-            _row_stride(kept), kept_lens.data_ptr(), R, cols,
-            None if mass is None else mass.data_ptr(), 0 if mass is None else _row_stride(mass),
-            0 if mass is None else mass.shape[1],
-            None if mass is None else mass_out.data_ptr(),
-            0 if mass is None else _row_stride(mass_out),
-            None if status is None else status.data_ptr(), _stream_ptr(stream, first.device))
-    _native.check(rc, "mla_kv_compact")
+        carried = (*weights, dst, dst_ld)
+    _launch(dev, _native.lib().mla_kv_compact, "mla_kv_compact", stream, layers, bases,
+            1 if fp8 else 2, pages, page_stride, ids, ids_ld,
+            _vector(seq_lens, "seq_lens", dev, R), outs, outs_ld, idx, idx_ld,
+            _vector(kept_lens, "kept_lens", dev, R), R, cols, *carried, _flag(status, dev))
     return mass_out
