@@ -923,11 +923,8 @@ extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld,
         (int64_t)sink + recent > keep || kept_ld < (keep < mass_cols ? keep : mass_cols) ||
         !aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4))
         return PLMLA_INVALID_ARGUMENT;
-    const int sms = current_sm_count();
-    if (sms <= 0)
-        return PLMLA_CUDA_ERROR;
-    const cudaError_t err = launch_select(mass, mass_ld, mass_cols, seq_lens, num_reqs, keep, sink, recent,
-                                          kept, kept_ld, kept_lens, sms,
+    const cudaError_t err = launch_select(mass, mass_ld, mass_cols, seq_lens, num_reqs, keep,
+                                          sink, recent, kept, kept_ld, kept_lens,
                                           static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
 }
