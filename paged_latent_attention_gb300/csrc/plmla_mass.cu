@@ -13,23 +13,32 @@
 // NaN) stay in their own lanes, which are not stored.
 //
 // Work.  Tiles of 128 tokens (always inside one page), numbered through the
-// requests, are dealt to one persistent CTA per SM in equal contiguous runs; the
-// CTA that has a tile writes its tokens, so there are no atomics and the result
-// does not depend on timing.  Which operand stays in shared memory goes by the
-// query rows per request (n_q * heads):
-//   up to 128 rows  Q of the request is resident (rows x 1152 B) and the tiles
-//                   stream through a ring of 16 KB column blocks: each KV byte is
-//                   read once and bounds the kernel;
-//   more            the tile is resident and the query rows stream past it from L2
-//                   in chunks of 128: the tensor cores bound the kernel.
-// Both cases issue the same MMAs (M = 128, N <= 128 rows, fp32 accumulators in
-// four TMEM buffers of 128 columns).  E4M3 pages take the two-part query of the
-// FP8 decode: the hi and the lo part multiply the same tile into one accumulator.
+// requests, are dealt to persistent workers (a CTA, or a pair of CTAs with a tile
+// each) in equal contiguous runs; the CTA that has a tile writes its tokens, so
+// there are no atomics and the result does not depend on timing.  The form goes by
+// the query rows per request (n_q * heads):
+//   up to 128 rows  one CTA; Q of the request is resident (rows x 1152 B) and the
+//                   tiles stream through a ring of 16 KB column blocks: each KV
+//                   byte is read once and bounds the kernel;
+//   up to 256       a CTA pair (cta_group::2, M = 256 tokens): Q is resident in
+//                   halves, one in each CTA, the tiles stream;
+//   more            a CTA pair; its two tiles are resident and the query rows
+//                   stream past them from L2 in chunks of 256, half into each CTA:
+//                   the tensor cores bound the kernel.  The next tiles are
+//                   prefetched into L2 meanwhile.
+// In a pair every SM fetches only half of the query rows that its tensor cores
+// multiply, and each operand byte in shared memory serves twice the products: with
+// one CTA and N = 128 shared memory and L2 bounded the kernel at 40% of the bf16
+// peak.  E4M3 pages take the two-part query of the FP8 decode: the hi and the lo
+// part multiply the same tile into one accumulator.
 //
-// Warp roles (320 threads): warp 0 = producer, warp 1 = MMA issuer and TMEM
-// owner, warps 2..9 = two groups of four that take the (tile, row chunk) units in
-// turn.  Every mbarrier wait is bounded as in the decode; a wait that gives up
-// stops the CTA's stores and sets the status word.
+// Warp roles (320 threads): warp 0 = producer, warp 1 = MMA issuer (of the pair's
+// even CTA) and TMEM owner, warps 2..9 = two groups of four that take the (tile,
+// row chunk) units in turn.  In a pair both producers' copies complete on the even
+// CTA's barriers, and MMA commits release slots and publish accumulators in both.
+// Every mbarrier wait is bounded as in the decode; a wait that gives up stops the
+// CTA's stores and sets the status word, and cluster barriers keep both CTAs of a
+// pair until neither can touch the other.
 #include <math.h>
 
 #include "plmla_ptx.cuh"
@@ -40,8 +49,8 @@ namespace {
 constexpr int kMassThreads = 320;
 constexpr int kMassSlot = kTile * 128;          // ring slot: 128 rows of 128 bytes
 constexpr int kMassMaxSlots = 12;
-constexpr int kMassChunk = 128;                 // query rows of one MMA and one TMEM buffer
-constexpr int kMassBufs = 4;
+constexpr int kMassChunk = 128;                 // query rows of one MMA per CTA
+constexpr int kMassCols = 512;                  // TMEM columns: buffers of kMassChunk * CG
 constexpr int kMassSmem = 232448;
 constexpr double kLog2e = 1.4426950408889634074;
 
@@ -49,7 +58,7 @@ struct MassBars {
     uint64_t full[kMassMaxSlots], empty[kMassMaxSlots];   // ring
     uint64_t k_full[9], k_empty[9];                       // resident tile, per column block
     uint64_t q_full, q_empty;                             // resident queries
-    uint64_t s_full[kMassBufs], s_free[kMassBufs];        // accumulators
+    uint64_t s_full[4], s_free[4];                        // accumulators
     uint64_t drain;
 };
 
@@ -57,12 +66,12 @@ struct MassMisc {
     MassBars bars;
     uint32_t tmem;
     int abort, status;
-    alignas(16) float neg_lse[2][2][kMassChunk];    // [group][buffer] -lse log2 e of the unit's rows
-    float factor[2][2][kMassChunk];     // E4M3: scale log2 e kv_scale 2^e of the row
-    int limit[2][2][kMassChunk];        // tokens the row sees
+    alignas(16) float neg_lse[2][2][2 * kMassChunk];    // [group][buffer] -lse log2 e of the unit's rows
+    float factor[2][2][2 * kMassChunk];     // E4M3: scale log2 e kv_scale 2^e of the row
+    int limit[2][2][2 * kMassChunk];        // tokens the row sees
     float part[2][kTile];               // second group's sums of a tile
-    int64_t warp_sum[kMassThreads / 32];
-    int64_t start[kMaxReqs + 1];        // first tile of each request
+    // first step of each request (32 bits hold them: every token has a float of mass)
+    int start[kMaxReqs + 1], warp_sum[kMassThreads / 32];
 };
 
 // Column blocks of one 576-wide row: 9 of 64 bf16, or 5 of 128 E4M3 bytes (the
@@ -78,11 +87,11 @@ struct MassFmt {
 
 __device__ __forceinline__ uint32_t bar_of(const uint64_t &b) { return smem_u32(&b); }
 
-// Position in the request-major tile order.
+// Position in the request-major order of steps.
 struct TileWalk {
-    const int64_t *start;
+    const int *start;
     int r;
-    __device__ int64_t local(int64_t g)          // tile g's index within its request r
+    __device__ int local(int g)                  // step g's index within its request r
     {
         while (g >= start[r + 1])
             ++r;
@@ -90,15 +99,22 @@ struct TileWalk {
     }
 };
 
-template <bool F8, bool QRES>
+// CG = CTAs of a worker (1, or a pair); QRES = queries resident, tiles streaming.
+// half = query rows per CTA of one MMA (N / CG) when QRES.
+template <bool F8, int CG, bool QRES>
 __global__ void __launch_bounds__(kMassThreads, 1)
 mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_qn,
-            const __grid_constant__ CUtensorMap tm_qr, const MassArgs a, const int slots)
+            const __grid_constant__ CUtensorMap tm_qr, const MassArgs a, const int half,
+            const int slots)
 {
     using F = MassFmt<F8>;
+    constexpr int kSpan = kTile * CG;                         // tokens of a worker's step
+    constexpr int kWidth = kMassChunk * CG;                   // query rows of a chunk, at most
+    constexpr int kBufs = kMassCols / kWidth;
+
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t s_res = smem_u32(smem);                    // resident operand
-    const uint32_t res_bytes = QRES ? (uint32_t)a.rows * 2 * kRow : (uint32_t)F::tile_bytes;
+    const uint32_t res_bytes = QRES ? (uint32_t)half * 2 * kRow : (uint32_t)F::tile_bytes;
     const uint32_t s_ring = s_res + res_bytes;
     MassMisc &m = *reinterpret_cast<MassMisc *>(smem + res_bytes + slots * kMassSlot);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -119,9 +135,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         }
         mbar_init(bar_of(m.bars.q_full), 1);
         mbar_init(bar_of(m.bars.q_empty), 1);
-        for (int i = 0; i < kMassBufs; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(bar_of(m.bars.s_full[i]), 1);
-            mbar_init(bar_of(m.bars.s_free[i]), 4);           // one arrival per warp of a group
+            mbar_init(bar_of(m.bars.s_free[i]), 4 * CG);      // one arrival per warp of a group
         }
         mbar_init(bar_of(m.bars.drain), 1);
         m.abort = 0;
@@ -130,15 +146,22 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         fence_proxy_async();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&m.tmem)),
-                     "r"(kMassBufs * kMassChunk));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&m.tmem)),
+                         "r"(kMassCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&m.tmem)),
+                         "r"(kMassCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        }
     }
     // tiles per request, prefix-summed; four requests a thread
     {
         const int64_t cap = min(a.mass_cols, a.table_ld * kPageTokens);
-        int64_t own[4], sum = 0;
+        int own[4], sum = 0;
         int bad = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -146,13 +169,13 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const int64_t L = r < a.num_reqs ? (int64_t)a.seq_lens[r] : 0;
             if (L > cap && blockIdx.x == 0)
                 bad = L > a.table_ld * kPageTokens ? kStatusAppendPage : kStatusMassLength;
-            own[e] = L <= 0 ? 0 : (min(L, cap) + kTile - 1) / kTile;
+            own[e] = L <= 0 ? 0 : (int)((min(L, cap) + kSpan - 1) / kSpan);
             sum += own[e];
         }
-        int64_t x = sum;
+        int x = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o)
                 x += y;
         }
@@ -175,12 +198,31 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         }
         __syncthreads();
     }
+    if constexpr (CG == 2)
+        cluster_sync();                 // the pair's barriers are initialised
     const uint32_t tmem = m.tmem;
-    const int64_t total = m.start[a.num_reqs];
-    const int64_t g0 = total / gridDim.x * blockIdx.x + min((int64_t)blockIdx.x, total % gridDim.x);
-    const int64_t g1 = g0 + total / gridDim.x + (blockIdx.x < total % gridDim.x ? 1 : 0);
+    const int rank = CG == 2 ? (int)cluster_rank() : 0;
+    const int total = m.start[a.num_reqs];
+    const int workers = (int)gridDim.x / CG, worker = (int)blockIdx.x / CG;
+    const int g0 = total / workers * worker + min(worker, total % workers);
+    const int g1 = g0 + total / workers + (worker < total % workers ? 1 : 0);
     TileWalk walk = {m.start, 0};
-    const int chunks = QRES ? 1 : (a.rows + kMassChunk - 1) / kMassChunk;
+    const int chunks = QRES ? 1 : (a.rows + kWidth - 1) / kWidth;
+    // query rows of chunk c per CTA: a pair's N is a multiple of 32 (the rows past the
+    // request's are multiplied and not used)
+    auto chunk_half = [&](int c) {
+        if constexpr (QRES)
+            return half;
+        return min(kMassChunk, (a.rows - c * kWidth + 31) / 32 * 16);
+    };
+    // the even CTA's copy of a barrier, where the pair's copies complete
+    auto lead = [&](const uint64_t &b) { return CG == 2 ? map_rank(bar_of(b), 0) : bar_of(b); };
+    auto commit = [&](const uint64_t &b) {
+        if constexpr (CG == 2)
+            mma_commit_pair(bar_of(b));
+        else
+            mma_commit(bar_of(b));
+    };
     volatile int *abort_flag = &m.abort;
     int32_t *status = &m.status;
 
@@ -190,11 +232,37 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         int slot = 0, issued = 0, q_loads = 0, cur = -1;
         uint32_t phase = 0;
         bool ok = true;
+        auto expect = [&](const uint64_t &b, uint32_t bytes) {
+            if (rank == 0)
+                mbar_arrive_expect_tx(bar_of(b), CG * bytes);
+        };
+        auto load_q = [&](uint32_t dst, const CUtensorMap *map, int col, int row, uint32_t bar) {
+            if constexpr (CG == 2)
+                tma_load_2d_pair(dst, map, col, row, bar);
+            else
+                tma_load_2d(dst, map, col, row, bar);
+        };
+        auto load_k = [&](uint32_t dst, int col, int tok, int page, uint32_t bar) {
+            if constexpr (CG == 2)
+                tma_load_3d_pair(dst, &tm_k, col, tok, page, bar, once);
+            else
+                tma_load_3d_hint(dst, &tm_k, col, tok, page, bar, once);
+        };
         auto ring_slot = [&](uint32_t bytes) -> bool {
             if (!wait_bounded(bar_of(m.bars.empty[slot]), phase ^ 1, abort_flag, status, 2))
                 return false;
-            mbar_arrive_expect_tx(bar_of(m.bars.full[slot]), bytes);
+            expect(m.bars.full[slot], bytes);
             return true;
+        };
+        // page and first row of this CTA's tile of step i of request r
+        auto tile_at = [&](int r, int i, int *tok) -> int {
+            const int64_t t = (int64_t)i * kSpan + rank * kTile;
+            *tok = (int)(t % kPageTokens);
+            int page = t / kPageTokens < a.table_ld
+                           ? a.page_table[(int64_t)r * a.table_ld + t / kPageTokens] : 0;
+            if (page < 0 || (int64_t)page >= a.num_pages)
+                page = 0;                                     // reported and not stored below
+            return page;
         };
         auto ring_next = [&]() {
             ++issued;
@@ -204,13 +272,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
         };
         int64_t n = 0, k_loads = 0;         // tiles so far, blocks of resident tiles issued
-        for (int64_t g = g0; g < g1 && ok; ++g, ++n) {
-            const int64_t i = walk.local(g);
+        for (int g = g0; g < g1 && ok; ++g, ++n) {
+            const int i = walk.local(g);
             const int r = walk.r;
-            int page = a.page_table[(int64_t)r * a.table_ld + i * kTile / kPageTokens];
-            if (page < 0 || (int64_t)page >= a.num_pages)
-                page = 0;                                     // reported and not stored below
-            const int tok = (int)(i * kTile % kPageTokens);
+            int tok;
+            const int page = tile_at(r, i, &tok);
             if constexpr (QRES) {
                 if (r != cur) {
                     if (q_loads > 0 && !wait_bounded(bar_of(m.bars.q_empty), (q_loads - 1) & 1,
@@ -218,16 +284,15 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = bar_of(m.bars.q_full);
-                    const int row = r * a.rows;
-                    mbar_arrive_expect_tx(bar, (uint32_t)a.rows * 2 * kRow);
+                    const uint32_t bar = lead(m.bars.q_full);
+                    expect(m.bars.q_full, (uint32_t)half * 2 * kRow);
                     for (int p = 0; p < F::parts; ++p) {
-                        const uint32_t dst = s_res + p * a.rows * kRow;
-                        const int at = row + p * a.num_reqs * a.rows;
+                        const uint32_t dst = s_res + p * half * kRow;
+                        const int at = (p * a.num_reqs + r) * a.rows + rank * half;
                         for (int k = 0; k < F::blocks - 1; ++k)
-                            tma_load_2d(dst + k * a.rows * 128, &tm_qn, F::step * k, at, bar);
-                        tma_load_2d(dst + (F::blocks - 1) * a.rows * 128, &tm_qr,
-                                    F8 ? kLatent : 0, at, bar);
+                            load_q(dst + k * half * 128, &tm_qn, F::step * k, at, bar);
+                        load_q(dst + (F::blocks - 1) * half * 128, &tm_qr, F8 ? kLatent : 0, at,
+                               bar);
                     }
                     ++q_loads;
                     cur = r;
@@ -238,25 +303,35 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         ok = false;
                         break;
                     }
-                    tma_load_3d_hint(s_ring + slot * kMassSlot, &tm_k, F::step * k, tok, page,
-                                     bar_of(m.bars.full[slot]), once);
+                    load_k(s_ring + slot * kMassSlot, F::step * k, tok, page,
+                           lead(m.bars.full[slot]));
                     ring_next();
                 }
             } else {
+                // the next step's tile comes to L2 while this one is multiplied
+                if (g + 1 < g1) {
+                    TileWalk ahead = walk;
+                    const int next = ahead.local(g + 1);
+                    int tok1;
+                    const int page1 = tile_at(ahead.r, next, &tok1);
+#pragma unroll 1
+                    for (int k = 0; k < F::blocks; ++k)
+                        tma_prefetch_3d(&tm_k, F::step * k, tok1, page1);
+                }
 #pragma unroll 1
                 for (int c = 0; c < chunks && ok; ++c) {
+                    const int row = c * kWidth + rank * chunk_half(c);
 #pragma unroll 1
                     for (int k = 0; k < F::blocks && ok; ++k) {
                         if (c == 0) {
-                            const uint32_t bar = bar_of(m.bars.k_full[k]);
                             if (n > 0 && !wait_bounded(bar_of(m.bars.k_empty[k]), (n - 1) & 1,
                                                        abort_flag, status, 3)) {
                                 ok = false;
                                 break;
                             }
-                            mbar_arrive_expect_tx(bar, kMassSlot);
-                            tma_load_3d_hint(s_res + k * kMassSlot, &tm_k, F::step * k, tok, page,
-                                             bar, once);
+                            expect(m.bars.k_full[k], kMassSlot);
+                            load_k(s_res + k * kMassSlot, F::step * k, tok, page,
+                                   lead(m.bars.k_full[k]));
                             ++k_loads;
                         }
                         for (int p = 0; p < F::parts; ++p) {
@@ -265,33 +340,33 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 ok = false;
                                 break;
                             }
-                            const int at = r * a.rows + c * kMassChunk + p * a.num_reqs * a.rows;
-                            tma_load_2d(s_ring + slot * kMassSlot, rope ? &tm_qr : &tm_qn,
-                                        rope ? (F8 ? kLatent : 0) : F::step * k, at,
-                                        bar_of(m.bars.full[slot]));
+                            load_q(s_ring + slot * kMassSlot, rope ? &tm_qr : &tm_qn,
+                                   rope ? (F8 ? kLatent : 0) : F::step * k,
+                                   (p * a.num_reqs + r) * a.rows + row, lead(m.bars.full[slot]));
                             ring_next();
                         }
                     }
                 }
             }
         }
-        // every issued copy lands before the CTA can exit
-        if (q_loads > 0)
+        // every issued copy lands before the CTA can exit (in a pair the even CTA waits
+        // for both, and the odd one for it, at the cluster barrier below)
+        if (q_loads > 0 && rank == 0)
             wait_drain(bar_of(m.bars.q_full), (q_loads - 1) & 1);
-        for (int it = issued > slots ? issued - slots : 0; it < issued; ++it)
+        for (int it = issued > slots ? issued - slots : 0; it < issued && rank == 0; ++it)
             wait_drain(bar_of(m.bars.full[it % slots]), (uint32_t)(it / slots) & 1u);
-        for (int64_t it = k_loads > F::blocks ? k_loads - F::blocks : 0; it < k_loads; ++it)
+        for (int64_t it = k_loads > F::blocks ? k_loads - F::blocks : 0;
+             it < k_loads && rank == 0; ++it)
             wait_drain(bar_of(m.bars.k_full[it % F::blocks]), (uint32_t)(it / F::blocks) & 1u);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---------------------------------------------------------- MMA issuer
         int slot = 0, q_loads = 0, cur = -1;
         uint32_t phase = 0;
         int64_t u = 0, n = 0;                                 // units and tiles so far
         bool ok = true, issued = false;
-        for (int64_t g = g0; g < g1 && ok; ++g, ++n) {
-            const int64_t i = walk.local(g);
+        for (int g = g0; g < g1 && ok; ++g, ++n) {
+            walk.local(g);
             const int r = walk.r;
-            (void)i;
             if constexpr (QRES) {
                 if (r != cur) {
                     if (!wait_bounded(bar_of(m.bars.q_full), q_loads & 1, abort_flag, status, 4)) {
@@ -304,17 +379,16 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
 #pragma unroll 1
             for (int c = 0; c < chunks && ok; ++c, ++u) {
-                const int buf = (int)(u % kMassBufs);
-                if (u >= kMassBufs && !wait_bounded(bar_of(m.bars.s_free[buf]),
-                                                    (uint32_t)(u / kMassBufs - 1) & 1u, abort_flag,
-                                                    status, 5)) {
+                const int buf = (int)(u % kBufs);
+                if (u >= kBufs && !wait_bounded(bar_of(m.bars.s_free[buf]),
+                                                (uint32_t)(u / kBufs - 1) & 1u, abort_flag, status,
+                                                5)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int cols = QRES ? a.rows : min(kMassChunk, a.rows - c * kMassChunk);
-                const uint32_t idesc = idesc_for<F8>(128, cols, false, false);
-                const uint32_t d = tmem + kMassChunk * buf;
+                const uint32_t idesc = idesc_for<F8>(128 * CG, CG * chunk_half(c), false, false);
+                const uint32_t d = tmem + kWidth * buf;
 #pragma unroll 1
                 for (int k = 0; k < F::blocks && ok; ++k) {
                     const bool rope = k == F::blocks - 1;
@@ -330,7 +404,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         uint32_t s_k, s_q;
                         if constexpr (QRES) {
                             s_k = s_ring + slot * kMassSlot;
-                            s_q = s_res + p * a.rows * kRow + k * a.rows * 128;
+                            s_q = s_res + p * half * kRow + k * half * 128;
                         } else {
                             if (!wait_bounded(bar_of(m.bars.full[slot]), phase, abort_flag, status,
                                               7)) {
@@ -347,11 +421,16 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         const int mmas = F::mmas(k);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            if (kk < mmas)
-                                mma<F8>(d, da + 2 * kk, db + 2 * kk, idesc, (k | p | kk) != 0);
+                            if (kk < mmas) {
+                                if constexpr (CG == 2)
+                                    mma_pair<F8>(d, da + 2 * kk, db + 2 * kk, idesc,
+                                                 (k | p | kk) != 0);
+                                else
+                                    mma<F8>(d, da + 2 * kk, db + 2 * kk, idesc, (k | p | kk) != 0);
+                            }
                         issued = true;
                         if (!QRES || p == F::parts - 1) {
-                            mma_commit(bar_of(m.bars.empty[slot]));
+                            commit(m.bars.empty[slot]);
                             if (++slot == slots) {
                                 slot = 0;
                                 phase ^= 1;
@@ -359,19 +438,19 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         }
                     }
                     if (!QRES && ok && c == chunks - 1)
-                        mma_commit(bar_of(m.bars.k_empty[k]));
+                        commit(m.bars.k_empty[k]);
                 }
                 if (!ok)
                     break;
-                mma_commit(bar_of(m.bars.s_full[buf]));
+                commit(m.bars.s_full[buf]);
             }
             if constexpr (QRES) {
                 if (ok && g + 1 >= m.start[r + 1])            // the request's last tile
-                    mma_commit(bar_of(m.bars.q_empty));
+                    commit(m.bars.q_empty);
             }
         }
         if (issued) {
-            mma_commit(bar_of(m.bars.drain));
+            commit(m.bars.drain);
             wait_drain(bar_of(m.bars.drain), 0);
         }
     } else if (warp >= 2) {
@@ -385,48 +464,50 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         int staged = 0, cur = -1, L = 0;
         bool ok = true;
         const float scale_log2 = a.scale_log2;
-        for (int64_t g = g0; g < g1; ++g, ++n) {
-            const int64_t i = walk.local(g);
+        for (int g = g0; g < g1; ++g, ++n) {
+            const int i = walk.local(g);
             const int r = walk.r;
             if (r != cur)
                 L = a.seq_lens[r];
-            const int64_t t = i * kTile + tok;
+            const int64_t t0 = (int64_t)i * kSpan + rank * kTile, t = t0 + tok;
             // the owner of the tile's sums: the unit's group, or the first group
             const bool mine = QRES ? (u & 1) == group : group == 0;
-            const int page = a.page_table[(int64_t)r * a.table_ld + i * kTile / kPageTokens];
+            // (the pair's second tile may lie past the history)
+            const bool inside = t0 < L && t0 / kPageTokens < a.table_ld;
+            const int page =
+                inside ? a.page_table[(int64_t)r * a.table_ld + t0 / kPageTokens] : 0;
             const bool page_ok = page >= 0 && (int64_t)page < a.num_pages;
             if (!page_ok && mine && me == 0)
                 atomicExch(status, kStatusAppendPage);
-            const bool store = mine && page_ok && t < L && t < a.mass_cols;
+            const bool store = mine && inside && page_ok && t < L && t < a.mass_cols;
             float *out = a.mass + (int64_t)r * a.mass_ld + t;
             const float old = store && a.decay != 0.f ? a.decay * *out : 0.f;
             // every row of the request sees the whole tile
-            const bool visible = (i + 1) * kTile <= (int64_t)L - (a.n_q - 1);
+            const bool visible = t0 + kTile <= (int64_t)L - (a.n_q - 1);
             float acc = 0.f;
             for (int c = 0; c < chunks; ++c, ++u) {
                 if ((u & 1) != group)
                     continue;
-                const int cols = QRES ? a.rows : min(kMassChunk, a.rows - c * kMassChunk);
+                const int cols = QRES ? a.rows : min(kWidth, a.rows - c * kWidth);
                 if (!QRES || r != cur) {
                     // stage the unit's rows; the other buffer may still be read
                     ++staged;
                     const int b = staged & 1;
-                    if (me < cols) {
-                        const int row = c * kMassChunk + me;
+                    for (int e = me; e < cols; e += kTile) {
+                        const int row = c * kWidth + e;
                         const int64_t at = (int64_t)r * a.rows + row;
                         const float lse = a.lse[at];
                         // a row without weights (lse -inf) adds nothing: 2^-inf
-                        m.neg_lse[group][b][me] =
-                            isinf(lse) ? -INFINITY : -lse * (float)kLog2e;
-                        m.limit[group][b][me] = L - (a.n_q - 1 - row / a.heads);
+                        m.neg_lse[group][b][e] = isinf(lse) ? -INFINITY : -lse * (float)kLog2e;
+                        m.limit[group][b][e] = L - (a.n_q - 1 - row / a.heads);
                         if constexpr (F8)
-                            m.factor[group][b][me] = ldexpf(scale_log2 * a.kv_scale, a.qexp[at]);
+                            m.factor[group][b][e] = ldexpf(scale_log2 * a.kv_scale, a.qexp[at]);
                     }
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                     cur = r;
                 }
-                const int buf = (int)(u % kMassBufs);
-                if (ok && !wait_bounded(bar_of(m.bars.s_full[buf]), (uint32_t)(u / kMassBufs) & 1u,
+                const int buf = (int)(u % kBufs);
+                if (ok && !wait_bounded(bar_of(m.bars.s_full[buf]), (uint32_t)(u / kBufs) & 1u,
                                         abort_flag, status, 8))
                     ok = false;
                 tc_fence_after();
@@ -437,7 +518,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += 16) {
                     uint32_t x[16];
-                    tmem_ld16(taddr + kMassChunk * buf + c0, x);
+                    tmem_ld16(taddr + kWidth * buf + c0, x);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -466,8 +547,12 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_of(m.bars.s_free[buf]));
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_cluster(lead(m.bars.s_free[buf]));
+                    else
+                        mbar_arrive(bar_of(m.bars.s_free[buf]));
+                }
                 acc += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
             if constexpr (!QRES) {
@@ -484,23 +569,33 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 
     tc_fence_before();
     __syncthreads();
+    // a pair leaves together: no copy, commit or arrival is on its way to either CTA
+    // (every wait above is bounded, so all threads get here)
+    if constexpr (CG == 2)
+        cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kMassBufs * kMassChunk));
+        if constexpr (CG == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(kMassCols));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(kMassCols));
     }
     if (threadIdx.x == 0 && m.status != 0 && a.status != nullptr)
         atomicExch(a.status, m.status);
 }
 
-template <bool F8, bool QRES>
-cudaError_t launch_mass_mode(const MassArgs &a, int sms, cudaStream_t stream)
+template <bool F8, int CG, bool QRES>
+cudaError_t launch_mass_form(const MassArgs &a, int sms, cudaStream_t stream)
 {
     const CUtensorMapDataType dt = F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const cuuint64_t es = F8 ? 1 : 2;
     const cuuint64_t rows = (cuuint64_t)a.num_reqs * a.rows;
-    const cuuint32_t q_rows = QRES ? (cuuint32_t)a.rows : (cuuint32_t)kMassChunk;
+    // rows of one query box: a pair splits N, a multiple of 32, in halves
+    const int half = !QRES ? kMassChunk : CG == 1 ? a.rows : (a.rows + 31) / 32 * 16;
+    const cuuint32_t q_rows = (cuuint32_t)half;
     CUtensorMap k, qn, qr;
     const cuuint64_t k_dims[3] = {(cuuint64_t)kRow, (cuuint64_t)kPageTokens, (cuuint64_t)a.num_pages};
     const cuuint64_t k_strides[2] = {(cuuint64_t)kRow * es, (cuuint64_t)a.page_stride * es};
@@ -522,28 +617,44 @@ cudaError_t launch_mass_mode(const MassArgs &a, int sms, cudaStream_t stream)
     }
     if (!ok)
         return cudaErrorInvalidValue;
-    const int res = QRES ? a.rows * 2 * kRow : MassFmt<F8>::tile_bytes;
+    const int res = QRES ? half * 2 * kRow : MassFmt<F8>::tile_bytes;
     int slots = (kMassSmem - res - (int)sizeof(MassMisc)) / kMassSlot;
     slots = slots < kMassMaxSlots ? slots : kMassMaxSlots;
     const int smem = res + slots * kMassSlot + (int)sizeof(MassMisc);
-    cudaError_t err = cudaFuncSetAttribute(mass_kernel<F8, QRES>,
+    cudaError_t err = cudaFuncSetAttribute(mass_kernel<F8, CG, QRES>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kMassSmem);
     if (err != cudaSuccess)
         return err;
-    mass_kernel<F8, QRES><<<sms, kMassThreads, smem, stream>>>(k, qn, qr, a, slots);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / CG * CG));
+    cfg.blockDim = dim3(kMassThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mass_kernel<F8, CG, QRES>, k, qn, qr, a, half, slots);
+}
+
+template <bool F8>
+cudaError_t launch_mass_typed(const MassArgs &a, int sms, cudaStream_t stream)
+{
+    if (a.rows <= kMassChunk)
+        return launch_mass_form<F8, 1, true>(a, sms, stream);
+    return a.rows <= 2 * kMassChunk ? launch_mass_form<F8, 2, true>(a, sms, stream)
+                                    : launch_mass_form<F8, 2, false>(a, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_mass(const MassArgs &a, int sms, cudaStream_t stream)
 {
-    const bool resident = a.rows <= kMassChunk;
-    if (a.q8 != nullptr)
-        return resident ? launch_mass_mode<true, true>(a, sms, stream)
-                        : launch_mass_mode<true, false>(a, sms, stream);
-    return resident ? launch_mass_mode<false, true>(a, sms, stream)
-                    : launch_mass_mode<false, false>(a, sms, stream);
+    return a.q8 != nullptr ? launch_mass_typed<true>(a, sms, stream)
+                           : launch_mass_typed<false>(a, sms, stream);
 }
 
 }  // namespace plmla
