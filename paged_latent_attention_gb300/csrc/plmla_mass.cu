@@ -50,7 +50,7 @@ constexpr int kMassThreads = 320;
 constexpr int kMassSlot = kTile * 128;          // ring slot: 128 rows of 128 bytes
 constexpr int kMassMaxSlots = 12;
 constexpr int kMassChunk = 128;                 // query rows of one MMA per CTA
-constexpr int kMassCols = 512;                  // TMEM columns: buffers of kMassChunk * CG
+constexpr int kMassCols = 512;                  // TMEM columns: two buffers of 256
 constexpr int kMassSmem = 232448;
 constexpr double kLog2e = 1.4426950408889634074;
 
@@ -110,7 +110,13 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     using F = MassFmt<F8>;
     constexpr int kSpan = kTile * CG;                         // tokens of a worker's step
     constexpr int kWidth = kMassChunk * CG;                   // query rows of a chunk, at most
-    constexpr int kBufs = kMassCols / kWidth;
+    // One CTA keeps two column sets that the epilogue adds: the scores of the query's
+    // hi and lo part (E4M3; one MMA of N = 2 rows), or of the even and the odd column
+    // blocks (bf16; shorter accumulation chains lose less).
+    constexpr int kSets = CG == 1 ? 2 : 1;
+    constexpr int kParts = F8 && CG == 2 ? 2 : 1;             // MMAs per K step, one a query part
+    constexpr int kBufCols = kWidth * kSets;
+    constexpr int kBufs = kMassCols / kBufCols;
 
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t s_res = smem_u32(smem);                    // resident operand
@@ -286,13 +292,18 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     }
                     const uint32_t bar = lead(m.bars.q_full);
                     expect(m.bars.q_full, (uint32_t)half * 2 * kRow);
+                    // E4M3: a pair keeps each part whole, one CTA the parts' rows of a
+                    // column block together (the rope block's rows are 64 bytes)
+                    constexpr bool stacked = F8 && CG == 1;
                     for (int p = 0; p < F::parts; ++p) {
-                        const uint32_t dst = s_res + p * half * kRow;
+                        const uint32_t dst = s_res + (stacked ? 0 : p * half * kRow);
+                        const uint32_t pitch = half * 128 * (stacked ? 2 : 1);
                         const int at = (p * a.num_reqs + r) * a.rows + rank * half;
                         for (int k = 0; k < F::blocks - 1; ++k)
-                            load_q(dst + k * half * 128, &tm_qn, F::step * k, at, bar);
-                        load_q(dst + (F::blocks - 1) * half * 128, &tm_qr, F8 ? kLatent : 0, at,
-                               bar);
+                            load_q(dst + k * pitch + (stacked ? p * half * 128 : 0), &tm_qn,
+                                   F::step * k, at, bar);
+                        load_q(dst + (F::blocks - 1) * pitch + (stacked ? p * half * 64 : 0), &tm_qr,
+                               F8 ? kLatent : 0, at, bar);
                     }
                     ++q_loads;
                     cur = r;
@@ -387,8 +398,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     break;
                 }
                 tc_fence_after();
-                const uint32_t idesc = idesc_for<F8>(128 * CG, CG * chunk_half(c), false, false);
-                const uint32_t d = tmem + kWidth * buf;
+                const uint32_t idesc = idesc_for<F8>(
+                    128 * CG, (F8 && CG == 1 ? 2 : CG) * chunk_half(c), false, false);
+                const uint32_t d = tmem + kBufCols * buf;
 #pragma unroll 1
                 for (int k = 0; k < F::blocks && ok; ++k) {
                     const bool rope = k == F::blocks - 1;
@@ -400,11 +412,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         }
                     }
 #pragma unroll 1
-                    for (int p = 0; p < F::parts; ++p) {
+                    for (int p = 0; p < kParts; ++p) {
                         uint32_t s_k, s_q;
                         if constexpr (QRES) {
                             s_k = s_ring + slot * kMassSlot;
-                            s_q = s_res + p * half * kRow + k * half * 128;
+                            s_q = s_res + p * half * kRow + k * half * 128 * (F8 && CG == 1 ? 2 : 1);
                         } else {
                             if (!wait_bounded(bar_of(m.bars.full[slot]), phase, abort_flag, status,
                                               7)) {
@@ -425,11 +437,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 if constexpr (CG == 2)
                                     mma_pair<F8>(d, da + 2 * kk, db + 2 * kk, idesc,
                                                  (k | p | kk) != 0);
+                                else if constexpr (F8)
+                                    mma_e4m3(d, da + 2 * kk, db + 2 * kk, idesc, (k | kk) != 0);
                                 else
-                                    mma<F8>(d, da + 2 * kk, db + 2 * kk, idesc, (k | p | kk) != 0);
+                                    mma_bf16(d + (k & 1) * half, da + 2 * kk, db + 2 * kk, idesc,
+                                             (k >> 1 | kk) != 0);
                             }
                         issued = true;
-                        if (!QRES || p == F::parts - 1) {
+                        if (!QRES || p == kParts - 1) {
                             commit(m.bars.empty[slot]);
                             if (++slot == slots) {
                                 slot = 0;
@@ -518,8 +533,17 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += 16) {
                     uint32_t x[16];
-                    tmem_ld16(taddr + kWidth * buf + c0, x);
-                    tmem_wait_ld();
+                    tmem_ld16(taddr + kBufCols * buf + c0, x);
+                    if constexpr (kSets == 2) {
+                        uint32_t y[16];
+                        tmem_ld16(taddr + kBufCols * buf + half + c0, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
+                    } else {
+                        tmem_wait_ld();
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float4 l4 = neg[c0 / 4 + e];
