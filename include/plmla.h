@@ -584,7 +584,7 @@ enum { PLMLA_BF16 = 0, PLMLA_FP16 = 1, PLMLA_FP32 = 2 };
  *                        t_i = original_len f_i / (2 pi), the turns of pair i over
  *                        the original context (Peng et al., YaRN, 2023, section 3.2)
  *
- * dim    even, 2 .. 1024;  base finite and > 1;  factor finite and >= 1;
+ * dim    even, 2 .. 512;  base finite and > 1;  factor finite and >= 1;
  *        by parts: original_len > 0, 0 <= low < high
  * turns  HOST array of dim / 2, written; copy it to the device for the calls below
  */
@@ -600,7 +600,7 @@ plmla_status mla_rope_turns(int32_t dim, double base, int32_t scaling, double fa
  * positions    int32 [tokens], device
  * turns        uint64 [dim / 2], device (mla_rope_turns)
  * magnitude    finite factor of the rotated pairs (1, or a scaled rotation's)
- * tokens       >= 0;  heads 1 .. 65535;  dim even, 2 .. 1024
+ * tokens       >= 0;  heads 1 .. 65535;  dim even, 2 .. 512
  * dtype        PLMLA_BF16, PLMLA_FP16 or PLMLA_FP32 elements; computed in fp32 and
  *              rounded once
  * layout       PLMLA_ROPE_HALF or PLMLA_ROPE_INTERLEAVED

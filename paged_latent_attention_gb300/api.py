@@ -477,6 +477,7 @@ ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
 _ROPE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_E4M3 = torch.float8_e4m3fn
 
 
 def _fail(message):
@@ -529,10 +530,11 @@ def _dense(t, name, dev, shape, dtype=_BF16):
 def _pool(slab, fp8):
     """(address, pages, page stride) of a pool [num_pages, page_stride]."""
     shape = slab.shape
-    if not (slab.dtype is (_U8 if fp8 else _BF16) and slab.is_cuda and len(shape) == 2
-            and shape[1] >= PAGE_TOKENS * ROW and slab.stride(1) == 1):
-        _fail(f"slab must be a CUDA {_U8 if fp8 else _BF16} view [num_pages, page_stride >= "
-              f"{PAGE_TOKENS * ROW}] with contiguous pages")
+    dtype = slab.dtype
+    if not ((dtype is _E4M3 or dtype is _U8 if fp8 else dtype is _BF16) and slab.is_cuda
+            and len(shape) == 2 and shape[1] >= PAGE_TOKENS * ROW and slab.stride(1) == 1):
+        _fail(f"slab must be a CUDA {'E4M3 (uint8 or float8_e4m3fn)' if fp8 else 'bf16'} view "
+              f"[num_pages, page_stride >= {PAGE_TOKENS * ROW}] with contiguous pages")
     return slab.data_ptr(), shape[0], slab.stride(0) if shape[0] > 1 else shape[1]
 
 
@@ -621,7 +623,7 @@ def mla_rope(x, positions, table, *, layout="half", inverse=False, out=None, str
     code = _layout(layout)
     at, turns = _vector(positions, "positions", dev, T), table.address(dev, D)
     if out is None:
-        out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
     else:
         _check_rope_out(x, out, dev)
     if T and H:
@@ -664,7 +666,7 @@ def mla_kv_append_rope_fp8(latent_new, rope_new, slab, page_table, seq_lens, n_n
                            status=None, stream=None):
     """mla_kv_append_rope into E4M3 pages (slab and kv_scale as in
     mla_kv_append_fp8)."""
-    return _append_rope(latent_new, rope_new, _byte_view(slab), page_table, seq_lens, n_new, table,
+    return _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table,
                         positions, layout, q_rope, q_out, status, stream, _kv_scale(kv_scale))
 
 
@@ -741,7 +743,7 @@ def mla_attention_mass_fp8(q_nope_absorbed, q_rope, lse, slab, page_table, seq_l
                            status=None, stream=None):
     """mla_attention_mass over E4M3 pages (slab and kv_scale as in mla_decode_fp8).
     The workspace comes from allocate_mass_workspace."""
-    return _mass(q_nope_absorbed, q_rope, lse, _byte_view(slab), page_table, seq_lens, mass, n_q,
+    return _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q,
                  scale, decay, _kv_scale(kv_scale), workspace, status, stream)
 
 
@@ -819,7 +821,7 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
         _fail("slabs must be a list of pools")
     first = slabs[0]
     dtype, fp8 = first.dtype, first.dtype is not _BF16
-    base, pages, page_stride = _pool(_byte_view(first) if fp8 else first, fp8)
+    base, pages, page_stride = _pool(first, fp8)
     dev, layers = first.get_device(), len(slabs)
     bases = (ctypes.c_void_p * layers)(base)
     shape, strides = first.shape, first.stride()

@@ -133,7 +133,7 @@ struct RopeView {
     int64_t tokens;
     int heads, dim;
 };
-constexpr int kMaxRopeDim = 1024, kMaxRopeHeads = 65535;
+constexpr int kMaxRopeDim = 512, kMaxRopeHeads = 65535;
 constexpr int kRopeBf16 = 0, kRopeFp16 = 1, kRopeFp32 = 2;   // element types
 cudaError_t launch_rope(const RopeView &v, const int32_t *positions, const uint64_t *turns,
                         float magnitude, int inverse, int dtype, int interleaved, int sms,

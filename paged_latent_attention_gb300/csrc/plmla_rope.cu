@@ -17,7 +17,11 @@
 // Bound by memory: every element is read and written once.  A block computes
 // the (cos, sin) pairs of its tokens once in shared memory and applies them to
 // all its heads; its loads are issued before that, so that the trigonometry
-// hides behind them.
+// hides behind them.  Instructions count as well as bytes: with 16-bit elements
+// converted one by one, units placed by integer divisions and 16 KB in flight per
+// block at two blocks an SM, 8,192 tokens of 64 bf16 heads took 47 us; converted in
+// pairs, placed by multiplications and at four blocks an SM they take 24 us (5.5
+// TB/s), fp32 heads 44 us (6.1 TB/s).
 #include <cuda_fp16.h>
 
 #include "plmla_internal.cuh"
@@ -26,7 +30,8 @@ namespace plmla {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;              // units of one thread in flight
+constexpr int kRopeUnroll = 2;              // units of one thread in flight
+constexpr int kRopeBlocks = 4;              // blocks of an SM
 constexpr int kRopeTable = 2048;            // (cos, sin) pairs of one block
 
 // m cos(a), m sin(a) of a = pos * turns (2^-64 turns), negated angle for sign < 0.
@@ -48,28 +53,92 @@ __device__ __forceinline__ float2 rope_cos_sin(int32_t pos, uint64_t turns, floa
     return make_float2(magnitude * cs, magnitude * (inverse ? -sn : sn));
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
-
-// VEC elements loaded and stored as one access.
+// VEC elements of T as one access, widened to and rounded from fp32 a 32-bit word
+// (two 16-bit elements) at a time.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Vec {
-    T v[VEC];
+struct Vec;
+
+template <int VEC>
+struct alignas(4 * VEC) Vec<float, VEC> {
+    float v[VEC];
+    __device__ __forceinline__ void widen(float (&f)[VEC]) const
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            f[e] = v[e];
+    }
+    __device__ __forceinline__ void round(const float (&f)[VEC])
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            v[e] = f[e];
+    }
+};
+
+template <int VEC>
+struct alignas(2 * VEC) Vec<__nv_bfloat16, VEC> {
+    uint32_t w[VEC / 2];
+    __device__ __forceinline__ void widen(float (&f)[VEC]) const
+    {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void round(const float (&f)[VEC])
+    {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+};
+
+template <int VEC>
+struct alignas(2 * VEC) Vec<__half, VEC> {
+    __half2 w[VEC / 2];
+    __device__ __forceinline__ void widen(float (&f)[VEC]) const
+    {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            const float2 x = __half22float2(w[e]);
+            f[2 * e] = x.x;
+            f[2 * e + 1] = x.y;
+        }
+    }
+    __device__ __forceinline__ void round(const float (&f)[VEC])
+    {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e)
+            w[e] = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+    }
+};
+
+template <>
+struct Vec<__nv_bfloat16, 1> {
+    __nv_bfloat16 v;
+    __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = __bfloat162float(v); }
+    __device__ __forceinline__ void round(const float (&f)[1]) { v = __float2bfloat16_rn(f[0]); }
+};
+
+template <>
+struct Vec<__half, 1> {
+    __half v;
+    __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = __half2float(v); }
+    __device__ __forceinline__ void round(const float (&f)[1]) { v = __float2half_rn(f[0]); }
+};
+
+// u / d by one multiplication, exact for u d < 2^32 (a block's units and rows).
+struct Divisor {
+    uint32_t d, m;
+    Divisor() = default;
+    explicit Divisor(uint32_t n) : d(n), m(n > 1 ? (uint32_t)((1ull << 32) / n + 1) : 0u) {}
+    __device__ __forceinline__ int div(int u) const
+    {
+        return m != 0u ? (int)__umulhi((uint32_t)u, m) : u;
+    }
 };
 
 struct RopeArgs {
@@ -84,6 +153,7 @@ struct RopeArgs {
     int heads, half;              // pairs per head
     int tok_block, head_block;    // tokens and heads of one block
     int head_blocks;
+    Divisor per_head, by_heads, by_half;   // units of a head, heads, pairs of a head
 };
 
 // Block `block` of the rotation: tokens [t0, t0 + tok_block), heads
@@ -97,9 +167,9 @@ __device__ __forceinline__ void rope_block(const RopeArgs &a, int64_t block, flo
     const int h0 = (int)(block % a.head_blocks) * a.head_block;
     const int nt = (int)min((int64_t)a.tok_block, a.tokens - t0);
     const int nh = min(a.head_block, a.heads - h0);
-    const int per_head = a.half / VEC;
+    const int per_head = (int)a.per_head.d;
     const int units = nt * nh * per_head;
-    const T *x = static_cast<const T *>(a.x);
+    const T *in = static_cast<const T *>(a.x);
     T *out = static_cast<T *>(a.out);
     bool have_table = false;
     for (int u0 = threadIdx.x; u0 < units || !have_table; u0 += kRopeThreads * kRopeUnroll) {
@@ -111,18 +181,20 @@ __device__ __forceinline__ void rope_block(const RopeArgs &a, int64_t block, flo
             const int u = u0 + j * kRopeThreads;
             if (u >= units)
                 break;
-            const int row = u / per_head, h = h0 + row % nh;
-            tok[j] = row / nh;
-            pair[j] = u % per_head * VEC;
+            // a block of several tokens has all the heads
+            const int row = a.per_head.div(u);
+            tok[j] = nt > 1 ? a.by_heads.div(row) : 0;
+            const int h = h0 + row - tok[j] * nh;
+            pair[j] = (u - row * per_head) * VEC;
             const int first = INTER ? 2 * pair[j] : pair[j];
-            const T *src = x + (t0 + tok[j]) * a.tok_stride + h * a.head_stride + first;
+            const T *src = in + (t0 + tok[j]) * a.tok_stride + h * a.head_stride + first;
             dst[j] = (t0 + tok[j]) * a.out_tok_stride + h * a.out_head_stride + first;
             lo[j] = *reinterpret_cast<const Vec<T, VEC> *>(src);
             hi[j] = *reinterpret_cast<const Vec<T, VEC> *>(src + (INTER ? VEC : a.half));
         }
         if (!have_table) {
             for (int i = threadIdx.x; i < nt * a.half; i += kRopeThreads) {
-                const int t = i / a.half, p = i % a.half;
+                const int t = a.by_half.div(i), p = i - t * a.half;
                 table[i] = rope_cos_sin(position(t0 + t), a.turns[p], a.magnitude, a.inverse != 0);
             }
             __syncthreads();
@@ -133,27 +205,29 @@ __device__ __forceinline__ void rope_block(const RopeArgs &a, int64_t block, flo
             if (u0 + j * kRopeThreads >= units)
                 break;
             const float2 *cs = table + tok[j] * a.half + pair[j];
-            Vec<T, VEC> olo, ohi;
+            float x[VEC], y[VEC], u[VEC], v[VEC];
+            lo[j].widen(x);
+            hi[j].widen(y);
             if constexpr (INTER && VEC > 1) {
 #pragma unroll
-                for (int e = 0; e < VEC / 2; ++e) {
-                    const float2 p = cs[e], q = cs[VEC / 2 + e];
-                    const float x0 = to_f32(lo[j].v[2 * e]), y0 = to_f32(lo[j].v[2 * e + 1]);
-                    const float x1 = to_f32(hi[j].v[2 * e]), y1 = to_f32(hi[j].v[2 * e + 1]);
-                    olo.v[2 * e] = from_f32<T>(x0 * p.x - y0 * p.y);
-                    olo.v[2 * e + 1] = from_f32<T>(x0 * p.y + y0 * p.x);
-                    ohi.v[2 * e] = from_f32<T>(x1 * q.x - y1 * q.y);
-                    ohi.v[2 * e + 1] = from_f32<T>(x1 * q.y + y1 * q.x);
+                for (int e = 0; e < VEC; e += 2) {
+                    const float2 p = cs[e / 2], q = cs[(VEC + e) / 2];
+                    u[e] = x[e] * p.x - x[e + 1] * p.y;
+                    u[e + 1] = x[e] * p.y + x[e + 1] * p.x;
+                    v[e] = y[e] * q.x - y[e + 1] * q.y;
+                    v[e + 1] = y[e] * q.y + y[e + 1] * q.x;
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float2 p = cs[e];
-                    const float xv = to_f32(lo[j].v[e]), yv = to_f32(hi[j].v[e]);
-                    olo.v[e] = from_f32<T>(xv * p.x - yv * p.y);
-                    ohi.v[e] = from_f32<T>(xv * p.y + yv * p.x);
+                    u[e] = x[e] * p.x - y[e] * p.y;
+                    v[e] = x[e] * p.y + y[e] * p.x;
                 }
             }
+            Vec<T, VEC> olo, ohi;
+            olo.round(u);
+            ohi.round(v);
             *reinterpret_cast<Vec<T, VEC> *>(out + dst[j]) = olo;
             *reinterpret_cast<Vec<T, VEC> *>(out + dst[j] + (INTER ? VEC : a.half)) = ohi;
         }
@@ -161,7 +235,7 @@ __device__ __forceinline__ void rope_block(const RopeArgs &a, int64_t block, flo
 }
 
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const RopeArgs a)
 {
     __shared__ float2 table[kRopeTable];
     rope_block<T, VEC, INTER>(a, blockIdx.x, table, [&](int64_t t) { return a.positions[t]; });
@@ -172,6 +246,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
 int64_t rope_tiling(RopeArgs *a, int vec, int sms)
 {
     const int per_head = a->half / vec;
+    a->per_head = Divisor((uint32_t)per_head);
+    a->by_heads = Divisor((uint32_t)a->heads);
+    a->by_half = Divisor((uint32_t)a->half);
     const int64_t total = a->tokens * a->heads * per_head;
     const int unroll = total >= (int64_t)4 * sms * kRopeThreads * kRopeUnroll ? kRopeUnroll : 1;
     const int want = kRopeThreads * unroll;
@@ -339,7 +416,7 @@ __device__ __forceinline__ void append_rope_row(const AppendRopeArgs &a, const R
 // The first blocks write the new rows (eight warps, a row each), the rest rotate
 // the same tokens' query heads: one launch for the step.
 template <bool F8, bool INTER, int VEC>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 append_rope_kernel(const AppendRopeArgs a, const RopeArgs q)
 {
     __shared__ float2 table[kRopeTable];
@@ -377,7 +454,7 @@ cudaError_t launch_rope(const RopeView &v, const int32_t *positions, const uint6
     if (v.tokens == 0 || v.heads == 0)
         return cudaSuccess;
     RopeArgs a = {v.x, v.out, v.tok_stride, v.head_stride, v.out_tok_stride, v.out_head_stride,
-                  positions, turns, magnitude, inverse, v.tokens, v.heads, v.dim / 2, 0, 0, 0};
+                  positions, turns, magnitude, inverse, v.tokens, v.heads, v.dim / 2};
     switch (dtype) {
     case kRopeBf16: return launch_typed<__nv_bfloat16>(a, interleaved != 0, sms, stream);
     case kRopeFp16: return launch_typed<__half>(a, interleaved != 0, sms, stream);
@@ -397,7 +474,7 @@ cudaError_t launch_append_rope(const void *latent, const void *rope, void *slab,
     if (rows == 0)
         return cudaSuccess;
     RopeArgs q = {v.x, v.out, v.tok_stride, v.head_stride, v.out_tok_stride, v.out_head_stride,
-                  positions, turns, magnitude, 0, rows, v.heads, kRope / 2, 0, 0, 0};
+                  positions, turns, magnitude, 0, rows, v.heads, kRope / 2};
     const bool vec = rope_vectors(q, 8, 2);
     const int64_t q_blocks = v.heads > 0 ? rope_tiling(&q, vec ? 8 : 1, sms) : 0;
     const int64_t append_blocks = (rows + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
