@@ -58,20 +58,21 @@ struct MassBars {
     uint64_t full[kMassMaxSlots], empty[kMassMaxSlots];   // ring
     uint64_t k_full[9], k_empty[9];                       // resident tile, per column block
     uint64_t q_full, q_empty;                             // resident queries
-    uint64_t s_full[4], s_free[4];                        // accumulators
+    uint64_t s_full[2], s_free[2];                        // accumulators
     uint64_t drain;
 };
 
+// Small on purpose: with bf16 pages it leaves room for a fifth ring slot beside 147
+// KB of resident operand.
+template <bool F8>
 struct MassMisc {
     MassBars bars;
     uint32_t tmem;
     int abort, status;
-    alignas(16) float neg_lse[2][2][2 * kMassChunk];    // [group][buffer] -lse log2 e of the unit's rows
-    float factor[2][2][2 * kMassChunk];     // E4M3: scale log2 e kv_scale 2^e of the row
-    int limit[2][2][2 * kMassChunk];        // tokens the row sees
-    float part[2][kTile];               // second group's sums of a tile
-    // first step of each request (32 bits hold them: every token has a float of mass)
-    int start[kMaxReqs + 1], warp_sum[kMassThreads / 32];
+    int first_req, first_step;          // this worker's first request, and its first step
+    alignas(16) float neg_lse[2][2 * kMassChunk];             // [group] -lse log2 e of the rows
+    alignas(16) float factor[F8 ? 2 : 1][F8 ? 2 * kMassChunk : 4];  // scale log2 e kv_scale 2^e
+    float part[kTile];                  // second group's sums of a tile
 };
 
 // Column blocks of one 576-wide row: 9 of 64 bf16, or 5 of 128 E4M3 bytes (the
@@ -87,17 +88,93 @@ struct MassFmt {
 
 __device__ __forceinline__ uint32_t bar_of(const uint64_t &b) { return smem_u32(&b); }
 
-// Position in the request-major order of steps.
-struct TileWalk {
-    const int *start;
-    int r;
-    __device__ int local(int g)                  // step g's index within its request r
+// Position in the request-major order of steps: step g of the whole is step g -
+// first of request r.
+struct StepWalk {
+    const int32_t *lens;
+    int64_t cap;                        // tokens that a row of mass and of pages hold
+    int span, r, first, end;
+    __device__ int steps(int r) const
     {
-        while (g >= start[r + 1])
-            ++r;
-        return g - start[r];
+        const int64_t L = lens[r];
+        return L <= 0 ? 0 : (int)((min(L, cap) + span - 1) / span);
+    }
+    __device__ void begin(int r0, int f)
+    {
+        r = r0;
+        first = f;
+        end = f + steps(r0);
+    }
+    __device__ int local(int g)
+    {
+        while (g >= end) {
+            first = end;
+            end += steps(++r);
+        }
+        return g - first;
     }
 };
+
+// Adds the weights of 16 columns (scores in SETS column sets) of this thread's token
+// to sum; MASKED: of the columns from `first` on.
+template <bool F8, int SETS, bool MASKED>
+__device__ __forceinline__ void add_weights(const uint32_t (&v)[SETS][16], const float4 *neg,
+                                            const float4 *fac, float scale_log2, int first,
+                                            float (&sum)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float4 l4 = neg[e];
+        const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+        float f[4] = {scale_log2, scale_log2, scale_log2, scale_log2};
+        if constexpr (F8) {
+            const float4 f4 = fac[e];
+            f[0] = f4.x, f[1] = f4.y, f[2] = f4.z, f[3] = f4.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float score = __uint_as_float(v[0][4 * e + j]);
+            if constexpr (SETS == 2)
+                score += __uint_as_float(v[1][4 * e + j]);
+            const float w = fast_exp2(fmaf(score, f[j], l[j]));
+            sum[j] += !MASKED || 4 * e + j >= first ? w : 0.f;
+        }
+    }
+}
+
+// The weights of `cols` columns (a multiple of 16) from TMEM address `at`, the second
+// set `half` columns on: 16 at a time, the next on their way while the last are summed.
+template <bool F8, int SETS, bool MASKED>
+__device__ __forceinline__ void sum_columns(uint32_t at, int half, int cols, const float4 *neg,
+                                            const float4 *fac, float scale_log2, int first,
+                                            float (&sum)[4])
+{
+    uint32_t x[SETS][16], y[SETS][16];
+    tmem_ld16(at, x[0]);
+    if constexpr (SETS == 2)
+        tmem_ld16(at + half, x[1]);
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        tmem_wait_ld();
+        if (c + 16 < cols) {
+            tmem_ld16(at + c + 16, y[0]);
+            if constexpr (SETS == 2)
+                tmem_ld16(at + half + c + 16, y[1]);
+        }
+        add_weights<F8, SETS, MASKED>(x, neg + c / 4, fac + (F8 ? c / 4 : 0), scale_log2, first - c,
+                                      sum);
+        if (c + 16 < cols) {
+            tmem_wait_ld();
+            if (c + 32 < cols) {
+                tmem_ld16(at + c + 32, x[0]);
+                if constexpr (SETS == 2)
+                    tmem_ld16(at + half + c + 32, x[1]);
+            }
+            add_weights<F8, SETS, MASKED>(y, neg + c / 4 + 4, fac + (F8 ? c / 4 + 4 : 0),
+                                          scale_log2, first - c - 16, sum);
+        }
+    }
+}
 
 // CG = CTAs of a worker (1, or a pair); QRES = queries resident, tiles streaming.
 // half = query rows per CTA of one MMA (N / CG) when QRES.
@@ -116,13 +193,15 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     constexpr int kSets = CG == 1 ? 2 : 1;
     constexpr int kParts = F8 && CG == 2 ? 2 : 1;             // MMAs per K step, one a query part
     constexpr int kBufCols = kWidth * kSets;
-    constexpr int kBufs = kMassCols / kBufCols;
+    constexpr int kBufs = 2;
+    static_assert(kBufs * kBufCols == kMassCols, "TMEM columns");
 
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t s_res = smem_u32(smem);                    // resident operand
     const uint32_t res_bytes = QRES ? (uint32_t)half * 2 * kRow : (uint32_t)F::tile_bytes;
     const uint32_t s_ring = s_res + res_bytes;
-    MassMisc &m = *reinterpret_cast<MassMisc *>(smem + res_bytes + slots * kMassSlot);
+    MassMisc<F8> &m =
+        *reinterpret_cast<MassMisc<F8> *>(smem + res_bytes + slots * kMassSlot);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((s_res & 1023u) != 0u) {       // cannot be with no static shared memory
         if (threadIdx.x == 0 && a.status != nullptr)
@@ -164,18 +243,23 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         }
     }
-    // tiles per request, prefix-summed; four requests a thread
+    const int rank = CG == 2 ? (int)cluster_rank() : 0;
+    const int workers = (int)gridDim.x / CG, worker = (int)blockIdx.x / CG;
+    StepWalk walk = {a.seq_lens, min(a.mass_cols, a.table_ld * kPageTokens), kSpan, 0, 0, 0};
+    int g0, g1;                         // this worker's steps
     {
-        const int64_t cap = min(a.mass_cols, a.table_ld * kPageTokens);
-        int own[4], sum = 0;
-        int bad = 0;
+        // steps per request (four a thread), prefix-summed; the thread in whose
+        // requests the worker's first step falls notes where.  32 bits hold the sums:
+        // every token has a float of mass.
+        int *warp_sum = reinterpret_cast<int *>(m.part);
+        int own[4], sum = 0, bad = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = 4 * (int)threadIdx.x + e;
-            const int64_t L = r < a.num_reqs ? (int64_t)a.seq_lens[r] : 0;
-            if (L > cap && blockIdx.x == 0)
-                bad = L > a.table_ld * kPageTokens ? kStatusAppendPage : kStatusMassLength;
-            own[e] = L <= 0 ? 0 : (int)((min(L, cap) + kSpan - 1) / kSpan);
+            own[e] = r < a.num_reqs ? walk.steps(r) : 0;
+            if (r < a.num_reqs && a.seq_lens[r] > walk.cap && blockIdx.x == 0)
+                bad = a.seq_lens[r] > a.table_ld * kPageTokens ? kStatusAppendPage
+                                                               : kStatusMassLength;
             sum += own[e];
         }
         int x = sum;
@@ -186,33 +270,35 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 x += y;
         }
         if (lane == 31)
-            m.warp_sum[warp] = x;
+            warp_sum[warp] = x;
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
         if (bad != 0)
             m.status = bad;
         x -= sum;
-        for (int w = 0; w < warp; ++w)
-            x += m.warp_sum[w];
+        int total = 0;
+        for (int w = 0; w < kMassThreads / 32; ++w) {
+            x += w < warp ? warp_sum[w] : 0;
+            total += warp_sum[w];
+        }
+        g0 = total / workers * worker + min(worker, total % workers);
+        g1 = g0 + total / workers + (worker < total % workers ? 1 : 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 4 * (int)threadIdx.x + e;
-            if (r <= a.num_reqs)
-                m.start[r] = x;
+            if (x <= g0 && g0 < x + own[e]) {
+                m.first_req = 4 * (int)threadIdx.x + e;
+                m.first_step = x;
+            }
             x += own[e];
         }
         __syncthreads();
+        if (g0 < g1)
+            walk.begin(m.first_req, m.first_step);
     }
     if constexpr (CG == 2)
         cluster_sync();                 // the pair's barriers are initialised
     const uint32_t tmem = m.tmem;
-    const int rank = CG == 2 ? (int)cluster_rank() : 0;
-    const int total = m.start[a.num_reqs];
-    const int workers = (int)gridDim.x / CG, worker = (int)blockIdx.x / CG;
-    const int g0 = total / workers * worker + min(worker, total % workers);
-    const int g1 = g0 + total / workers + (worker < total % workers ? 1 : 0);
-    TileWalk walk = {m.start, 0};
     const int chunks = QRES ? 1 : (a.rows + kWidth - 1) / kWidth;
     // query rows of chunk c per CTA: a pair's N is a multiple of 32 (the rows past the
     // request's are multiplied and not used)
@@ -283,6 +369,16 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const int r = walk.r;
             int tok;
             const int page = tile_at(r, i, &tok);
+            // the next step's tile comes to L2 while this one is resident
+            if (!QRES && g + 1 < g1) {
+                StepWalk ahead = walk;
+                const int next = ahead.local(g + 1);
+                int tok1;
+                const int page1 = tile_at(ahead.r, next, &tok1);
+#pragma unroll 1
+                for (int k = 0; k < F::blocks; ++k)
+                    tma_prefetch_3d(&tm_k, F::step * k, tok1, page1);
+            }
             if constexpr (QRES) {
                 if (r != cur) {
                     if (q_loads > 0 && !wait_bounded(bar_of(m.bars.q_empty), (q_loads - 1) & 1,
@@ -319,16 +415,6 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     ring_next();
                 }
             } else {
-                // the next step's tile comes to L2 while this one is multiplied
-                if (g + 1 < g1) {
-                    TileWalk ahead = walk;
-                    const int next = ahead.local(g + 1);
-                    int tok1;
-                    const int page1 = tile_at(ahead.r, next, &tok1);
-#pragma unroll 1
-                    for (int k = 0; k < F::blocks; ++k)
-                        tma_prefetch_3d(&tm_k, F::step * k, tok1, page1);
-                }
 #pragma unroll 1
                 for (int c = 0; c < chunks && ok; ++c) {
                     const int row = c * kWidth + rank * chunk_half(c);
@@ -460,7 +546,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 commit(m.bars.s_full[buf]);
             }
             if constexpr (QRES) {
-                if (ok && g + 1 >= m.start[r + 1])            // the request's last tile
+                if (ok && g + 1 >= walk.end)                  // the request's last step
                     commit(m.bars.q_empty);
             }
         }
@@ -475,11 +561,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const int group = (warp - 2) >> 2, quad = warp & 3;
         const int tok = 32 * quad + lane, me = ((warp - 2) & 3) * 32 + lane;
         const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16);
-        int64_t u = 0, n = 0;
-        int staged = 0, cur = -1, L = 0;
+        int64_t u = 0;
+        int cur = -1, L = 0;
         bool ok = true;
         const float scale_log2 = a.scale_log2;
-        for (int g = g0; g < g1; ++g, ++n) {
+        for (int g = g0; g < g1; ++g) {
             const int i = walk.local(g);
             const int r = walk.r;
             if (r != cur)
@@ -499,24 +585,25 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const float old = store && a.decay != 0.f ? a.decay * *out : 0.f;
             // every row of the request sees the whole tile
             const bool visible = t0 + kTile <= (int64_t)L - (a.n_q - 1);
+            // the token's first query row: draft j sees it from L - (n_q - 1 - j) > t on
+            const int first_row =
+                t < L ? max(0, (int)(t - L) + a.n_q) * a.heads : 0x7FFFFFFF;
             float acc = 0.f;
             for (int c = 0; c < chunks; ++c, ++u) {
                 if ((u & 1) != group)
                     continue;
                 const int cols = QRES ? a.rows : min(kWidth, a.rows - c * kWidth);
+                const int row0 = c * kWidth;
                 if (!QRES || r != cur) {
-                    // stage the unit's rows; the other buffer may still be read
-                    ++staged;
-                    const int b = staged & 1;
+                    // stage the unit's rows, once the group has done with the last ones
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                     for (int e = me; e < cols; e += kTile) {
-                        const int row = c * kWidth + e;
-                        const int64_t at = (int64_t)r * a.rows + row;
+                        const int64_t at = (int64_t)r * a.rows + row0 + e;
                         const float lse = a.lse[at];
                         // a row without weights (lse -inf) adds nothing: 2^-inf
-                        m.neg_lse[group][b][e] = isinf(lse) ? -INFINITY : -lse * (float)kLog2e;
-                        m.limit[group][b][e] = L - (a.n_q - 1 - row / a.heads);
+                        m.neg_lse[group][e] = isinf(lse) ? -INFINITY : -lse * (float)kLog2e;
                         if constexpr (F8)
-                            m.factor[group][b][e] = ldexpf(scale_log2 * a.kv_scale, a.qexp[at]);
+                            m.factor[group][e] = ldexpf(scale_log2 * a.kv_scale, a.qexp[at]);
                     }
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                     cur = r;
@@ -526,49 +613,15 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                         abort_flag, status, 8))
                     ok = false;
                 tc_fence_after();
-                const float4 *neg = reinterpret_cast<const float4 *>(m.neg_lse[group][staged & 1]);
-                const float4 *fac = reinterpret_cast<const float4 *>(m.factor[group][staged & 1]);
-                const int4 *lim = reinterpret_cast<const int4 *>(m.limit[group][staged & 1]);
+                const float4 *neg = reinterpret_cast<const float4 *>(m.neg_lse[group]);
+                const float4 *fac = reinterpret_cast<const float4 *>(m.factor[F8 ? group : 0]);
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                for (int c0 = 0; c0 < cols; c0 += 16) {
-                    uint32_t x[16];
-                    tmem_ld16(taddr + kBufCols * buf + c0, x);
-                    if constexpr (kSets == 2) {
-                        uint32_t y[16];
-                        tmem_ld16(taddr + kBufCols * buf + half + c0, y);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
-                    } else {
-                        tmem_wait_ld();
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 l4 = neg[c0 / 4 + e];
-                        float f[4] = {scale_log2, scale_log2, scale_log2, scale_log2};
-                        if constexpr (F8) {
-                            const float4 f4 = fac[c0 / 4 + e];
-                            f[0] = f4.x, f[1] = f4.y, f[2] = f4.z, f[3] = f4.w;
-                        }
-                        float w[4];
-                        w[0] = fast_exp2(fmaf(__uint_as_float(x[4 * e]), f[0], l4.x));
-                        w[1] = fast_exp2(fmaf(__uint_as_float(x[4 * e + 1]), f[1], l4.y));
-                        w[2] = fast_exp2(fmaf(__uint_as_float(x[4 * e + 2]), f[2], l4.z));
-                        w[3] = fast_exp2(fmaf(__uint_as_float(x[4 * e + 3]), f[3], l4.w));
-                        if (!visible) {
-                            const int4 v = lim[c0 / 4 + e];
-                            w[0] = t < v.x ? w[0] : 0.f;
-                            w[1] = t < v.y ? w[1] : 0.f;
-                            w[2] = t < v.z ? w[2] : 0.f;
-                            w[3] = t < v.w ? w[3] : 0.f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            sum[j] += w[j];
-                    }
-                }
+                const uint32_t at = taddr + kBufCols * buf;
+                if (visible)
+                    sum_columns<F8, kSets, false>(at, half, cols, neg, fac, scale_log2, 0, sum);
+                else
+                    sum_columns<F8, kSets, true>(at, half, cols, neg, fac, scale_log2,
+                                                 first_row - row0, sum);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -581,10 +634,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
             if constexpr (!QRES) {
                 if (group == 1)
-                    m.part[n & 1][tok] = acc;
+                    m.part[tok] = acc;
                 asm volatile("bar.sync 3, 256;" ::: "memory");
                 if (group == 0)
-                    acc += m.part[n & 1][tok];
+                    acc += m.part[tok];
+                asm volatile("bar.sync 3, 256;" ::: "memory");
             }
             if (store && ok && !*abort_flag)
                 *out = old + acc;
@@ -642,9 +696,9 @@ cudaError_t launch_mass_form(const MassArgs &a, int sms, cudaStream_t stream)
     if (!ok)
         return cudaErrorInvalidValue;
     const int res = QRES ? half * 2 * kRow : MassFmt<F8>::tile_bytes;
-    int slots = (kMassSmem - res - (int)sizeof(MassMisc)) / kMassSlot;
+    int slots = (kMassSmem - res - (int)sizeof(MassMisc<F8>)) / kMassSlot;
     slots = slots < kMassMaxSlots ? slots : kMassMaxSlots;
-    const int smem = res + slots * kMassSlot + (int)sizeof(MassMisc);
+    const int smem = res + slots * kMassSlot + (int)sizeof(MassMisc<F8>);
     cudaError_t err = cudaFuncSetAttribute(mass_kernel<F8, CG, QRES>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kMassSmem);
     if (err != cudaSuccess)
