@@ -718,12 +718,19 @@ plmla_status mla_attention_mass_fp8(const void *q_nope_absorbed, const void *q_r
  *              min(keep, L_r) indices in ascending order; later entries are not
  *              written
  * kept_lens    int32 [num_reqs], written: min(keep, L_r)
- * One kernel, deterministic.
+ * workspace    NULL, or device scratch of at least mla_evict_workspace_size(...) bytes,
+ *              256-byte aligned, whose contents on entry are irrelevant: with it long
+ *              rows of few requests are searched by every SM instead of one cluster
+ *              per request (the result is the same).  The size is 0 for shapes that
+ *              make no use of it.
+ * Deterministic.
  */
+size_t mla_evict_workspace_size(int32_t num_reqs, int64_t mass_cols);
 plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
                               const int32_t *seq_lens, int32_t num_reqs, int32_t keep,
                               int32_t sink, int32_t recent, int32_t *kept, int64_t kept_ld,
-                              int32_t *kept_lens, void *stream);
+                              int32_t *kept_lens, void *workspace, size_t workspace_bytes,
+                              void *stream);
 
 /*
  * mla_kv_compact -- copy the kept token rows of each history into fresh pages, for

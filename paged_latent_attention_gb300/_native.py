@@ -61,8 +61,9 @@ SIGNATURES = {
     "mla_mass_workspace_size_fp8": (_sz, [_i32, _i32, _i32]),
     "mla_attention_mass_fp8": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _f, _p, _i64, _p, _i32,
                                               _i32, _i32, _f, _f, _p, _i64, _i64, _p, _sz, _p, _p]),
+    "mla_evict_workspace_size": (_sz, [_i32, _i64]),
     "mla_evict_select": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _i64, _p,
-                                        _p]),
+                                        _p, _sz, _p]),
     "mla_kv_compact": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _p, _p, _i64, _p,
                                       _i64, _p, _i32, _i32, _p, _i64, _i64, _p, _i64, _p, _p]),
     "mla_set_page_checks": (None, [_i32]),

@@ -779,13 +779,21 @@ def _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, s
     return mass
 
 
+def allocate_evict_workspace(num_reqs, tokens, device=None):
+    """A workspace tensor (uint8) for mla_evict_select on mass [num_reqs, tokens] (of
+    no bytes where that shape makes no use of one)."""
+    return torch.empty(_native.lib().mla_evict_workspace_size(num_reqs, tokens), dtype=_U8,
+                       device=device or "cuda")
+
+
 def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_lens=None,
-                     stream=None):
+                     workspace=None, stream=None):
     """Which tokens of each history stay within ``keep``: the first ``sink``, the
     last ``recent`` and the heaviest of the rest by mass [R, tokens] fp32 (ties to
     the lower index).  Returns (kept [R, min(keep, tokens)] int32 ascending
     indices, kept_lens [R] int32 = min(keep, seq_lens)); entries of kept past a
-    row's count are not written."""
+    row's count are not written.  The workspace comes from allocate_evict_workspace
+    (a new one by default)."""
     dev = mass.get_device()
     if mass.dim() != 2 or dev < 0:
         _fail("mass must be a CUDA tensor [R, tokens]")
@@ -802,8 +810,17 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
     ids, ids_ld, have = _rows(kept, "kept", dev, _I32, R)
     if have < cols:
         _fail(f"kept needs {cols} columns")
-    _launch(dev, _native.lib().mla_evict_select, "mla_evict_select", stream, *weights, lens, R,
-            keep, sink, recent, ids, ids_ld, _vector(kept_lens, "kept_lens", dev, R))
+    lib, scratch, size = _native.lib(), None, 0
+    if workspace is None:
+        size = lib.mla_evict_workspace_size(R, tokens)
+        if size:
+            workspace = torch.empty(size, dtype=_U8, device=mass.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _fail(f"workspace must be contiguous memory on cuda:{dev}")
+    if workspace is not None and workspace.numel():
+        scratch, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(dev, lib.mla_evict_select, "mla_evict_select", stream, *weights, lens, R, keep, sink,
+            recent, ids, ids_ld, _vector(kept_lens, "kept_lens", dev, R), scratch, size)
     return kept, kept_lens
 
 

@@ -912,19 +912,35 @@ extern "C" plmla_status mla_attention_mass_fp8(
                      status, stream);
 }
 
-extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld,
-                                         int64_t mass_cols, const int32_t *seq_lens,
-                                         int32_t num_reqs, int32_t keep, int32_t sink,
-                                         int32_t recent, int32_t *kept, int64_t kept_ld,
-                                         int32_t *kept_lens, void *stream)
+extern "C" size_t mla_evict_workspace_size(int32_t num_reqs, int64_t mass_cols)
+{
+    if (num_reqs < 1 || num_reqs > kMaxReqs || mass_cols < 1)
+        return 0;
+    const int parts = select_parts(num_reqs, mass_cols, current_sm_count());
+    return parts > 0 ? align_up(select_workspace(num_reqs, parts)) : 0;
+}
+
+extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
+                                         const int32_t *seq_lens, int32_t num_reqs, int32_t keep,
+                                         int32_t sink, int32_t recent, int32_t *kept,
+                                         int64_t kept_ld, int32_t *kept_lens, void *workspace,
+                                         size_t workspace_bytes, void *stream)
 {
     if (mass == nullptr || seq_lens == nullptr || kept == nullptr || kept_lens == nullptr ||
-        num_reqs < 1 || num_reqs > kMaxReqs || mass_cols < 1 || mass_ld < mass_cols || keep < 1 || sink < 0 || recent < 0 ||
-        (int64_t)sink + recent > keep || kept_ld < (keep < mass_cols ? keep : mass_cols) ||
-        !aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4))
+        num_reqs < 1 || num_reqs > kMaxReqs || mass_cols < 1 || mass_ld < mass_cols || keep < 1 ||
+        sink < 0 || recent < 0 || (int64_t)sink + recent > keep ||
+        kept_ld < (keep < mass_cols ? keep : mass_cols) || !aligned(mass, 4) ||
+        !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4) ||
+        !aligned(workspace, kAlign))
         return PLMLA_INVALID_ARGUMENT;
+    int parts = 0;
+    if (workspace != nullptr) {
+        parts = select_parts(num_reqs, mass_cols, current_sm_count());
+        if (parts > 0 && workspace_bytes < select_workspace(num_reqs, parts))
+            return PLMLA_WORKSPACE_TOO_SMALL;
+    }
     const cudaError_t err = launch_select(mass, mass_ld, mass_cols, seq_lens, num_reqs, keep,
-                                          sink, recent, kept, kept_ld, kept_lens,
+                                          sink, recent, kept, kept_ld, kept_lens, parts, workspace,
                                           static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
 }

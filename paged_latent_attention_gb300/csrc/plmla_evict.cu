@@ -26,7 +26,7 @@ namespace cg = cooperative_groups;
 // candidates, the histograms meet through distributed shared memory, and a CTA's
 // output offset is the sum of the counts before it (which its histograms give),
 // so the indices come out in ascending order without a sort.  The first
-// kSelCache keys of a slice stay in shared memory after their first read.
+// kSelCache weights of a slice stay in shared memory after their first read.
 //
 // Weights are read four at a time (aligned groups; the ends of a slice element by
 // element).  The first histogram of a large CTA has four copies, interleaved so that
@@ -38,9 +38,11 @@ constexpr int kSelSmall = 4096, kSelSmallThreads = 256;   // take smaller ones, 
 constexpr int kSelBins = 2048;
 constexpr int kSelCoarse = kSelBins / 64;     // sums of 64 bins
 constexpr int kSelBatch = 4;                  // groups of four that a thread has in flight
-constexpr int kSelCache = 38912;              // keys of a slice kept in shared memory
+constexpr int kSelCache = 38912;              // weights of a slice kept in shared memory
 constexpr int kSelChunk = 8192;               // groups of four written out at a time
 constexpr int kSelMaxCluster = 16;
+constexpr int kSelLong = 28672;               // weights of a slice from which parts pay,
+constexpr int kSelPartThreads = 512;          // in CTAs of which two passes' fit an SM
 
 struct SelectArgs {
     const float *mass;
@@ -55,7 +57,7 @@ struct SelectArgs {
 
 template <int NT>
 struct SelectSmem {
-    static constexpr int copies = NT >= kSelThreads ? 4 : 1;   // of hist[0]
+    static constexpr int copies = NT > kSelSmallThreads ? 4 : 1;   // of hist[0]
     // (arrays read in vectors are aligned for them)
     alignas(16) uint32_t hist[3][kSelBins];    // this CTA's, one per digit, read by the whole cluster
     alignas(16) uint32_t copied[copies > 1 ? kSelBins * copies : 4];
@@ -74,6 +76,11 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     const uint32_t u = __float_as_uint(w + 0.f);
     const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     return w == w ? key : 0u;
+}
+
+__device__ __forceinline__ uint4 weight_keys(const float4 &w)
+{
+    return make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
 }
 
 __device__ __forceinline__ uint32_t warp_inclusive(uint32_t x, int lane)
@@ -103,134 +110,323 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sum, u
     return (warp > 0 ? before : 0u) + x - v;
 }
 
+// One request's candidates and the slice of them that part `me` of `parts` takes.
+// Candidates [sink, hi) lie in groups of four aligned weights: group g holds tokens
+// 4 g - skew .. 4 g - skew + 3.
+struct Slice {
+    const float *mass;
+    uint32_t skew, first, last, first_bits, last_bits;
+    uint32_t g0, g1;                   // this part's groups
+
+    __device__ Slice(const float *row, int sink, int hi, uint32_t me, uint32_t parts) : mass(row)
+    {
+        skew = (uint32_t)(reinterpret_cast<uintptr_t>(mass) / 4) & 3u;
+        const uint32_t v0 = (uint32_t)sink + skew, v1 = (uint32_t)hi + skew;
+        first = v0 / 4;
+        const uint32_t groups = (v1 + 3) / 4 - first, per = (groups + parts - 1) / parts;
+        last = first + groups - 1;
+        first_bits = 0xFu & (0xFu << (v0 - 4 * first));
+        last_bits = 0xFu >> (4 * last + 4 - v1);
+        g0 = first + min(groups, me * per);
+        g1 = first + min(groups, (me + 1) * per);
+    }
+    // which of group g's elements are candidates: all but in the outermost groups
+    __device__ uint32_t valid(uint32_t g) const
+    {
+        return (g == first ? first_bits : 0xFu) & (g == last ? last_bits : 0xFu);
+    }
+    // Group g's weights where all four are candidates, else zeros, which whoever uses
+    // them replaces by edge(g): one predicated load, so that several go out together
+    // (with both cases here each load waited for the one before).
+    __device__ float4 fetch(uint32_t g) const
+    {
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (valid(g) == 0xFu)
+            w = *reinterpret_cast<const float4 *>(mass + ((int64_t)4 * g - skew));
+        return w;
+    }
+    __device__ float4 edge(uint32_t g) const
+    {
+        const float *p = mass + ((int64_t)4 * g - skew);
+        const uint32_t bits = valid(g);
+        return make_float4(bits & 1u ? p[0] : 0.f, bits & 2u ? p[1] : 0.f, bits & 4u ? p[2] : 0.f,
+                           bits & 8u ? p[3] : 0.f);
+    }
+    __device__ int32_t token(uint32_t g) const { return (int32_t)(4 * g - skew); }
+};
+
+// Where the keys of a slice are: groups before `split` in shared memory.
+struct Source {
+    const uint4 *cache;
+    uint32_t split;
+};
+
+// The weights of groups at + i + j NT, i = this thread's first, for j < kSelBatch.
+template <int NT>
+__device__ __forceinline__ void load_batch(const Slice &s, uint32_t g, float4 (&w)[kSelBatch])
+{
+#pragma unroll
+    for (int j = 0; j < kSelBatch; ++j)
+        w[j] = s.fetch(min(g + j * NT, s.last));
+}
+
+// f(i, keys of group at + i) for this thread's i of [0, n).  The groups lie on one side
+// of src.split.  Loads go out kSelBatch together; where the threads are few enough for
+// the registers (kSelPartThreads) the next batch goes out before the last is used, and
+// the first may have been loaded by the caller (`ready`).  WARPS: whole warps run, with
+// other groups' keys for i >= n.
+template <int NT, bool WARPS, typename F>
+__device__ __forceinline__ void batched(const Slice &s, const Source &src, uint32_t at, uint32_t n,
+                                        F f, const float4 (*ready)[kSelBatch] = nullptr)
+{
+    constexpr bool ahead = NT == kSelPartThreads;
+    const uint32_t end = WARPS ? (n + 31) / 32 * 32 : n;
+    if (at + n <= src.split) {
+        const uint4 *p = src.cache + (at - s.g0);
+#pragma unroll 2
+        for (uint32_t i = threadIdx.x; i < end; i += NT)
+            f(i, p[WARPS ? min(i, n - 1) : i]);
+        return;
+    }
+    float4 w[kSelBatch];
+    if (ready != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j)
+            w[j] = (*ready)[j];
+    } else if (ahead) {
+        load_batch<NT>(s, at + threadIdx.x, w);
+    }
+    for (uint32_t i = threadIdx.x; i < end; i += kSelBatch * NT) {
+        float4 next[kSelBatch];
+        if constexpr (ahead)
+            load_batch<NT>(s, at + i + kSelBatch * NT, next);
+        else
+            load_batch<NT>(s, at + i, w);
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j)
+            if (i + j * NT < end) {
+                const uint32_t g = min(at + i + j * NT, s.last);
+                if (s.valid(g) != 0xFu)
+                    w[j] = s.edge(g);
+                f(i + j * NT, weight_keys(w[j]));
+            }
+        if constexpr (ahead) {
+#pragma unroll
+            for (int j = 0; j < kSelBatch; ++j)
+                w[j] = next[j];
+        }
+    }
+}
+
+// What a request keeps without a choice, written by its parts together: everything
+// if it fits, else the first `sink` and the last `recent` tokens.  Whether there is
+// a choice left to make, and among which tokens.
+template <int NT>
+__device__ __forceinline__ bool select_forced(const SelectArgs &a, int r, int me, int parts, int L,
+                                              bool write)
+{
+    int32_t *kept = a.kept + (int64_t)r * a.kept_ld;
+    const int tid = threadIdx.x;
+    if (write && me == 0 && tid == 0)
+        a.kept_lens[r] = min(L, a.keep);
+    if (L <= a.keep) {
+        for (int i = me * NT + tid; i < L && write; i += parts * NT)
+            kept[i] = i;
+        return false;
+    }
+    for (int i = me * NT + tid; i < a.sink + a.recent && write; i += parts * NT) {
+        if (i < a.sink)
+            kept[i] = i;
+        else
+            kept[a.keep - a.recent + (i - a.sink)] = L - a.recent + (i - a.sink);
+    }
+    return a.keep > a.sink + a.recent;
+}
+
+__device__ __forceinline__ int select_length(const SelectArgs &a, int r)
+{
+    const int64_t L = a.seq_lens[r];
+    return (int)(L < 0 ? 0 : (L > a.mass_cols ? a.mass_cols : L));
+}
+
+// The first digit's histogram of a slice (zeroed before); keep(i, keys) sees each group.
+template <int NT, typename Keep>
+__device__ __forceinline__ void count_first(SelectSmem<NT> &sm, const Slice &s, Keep keep,
+                                            const float4 (*ready)[kSelBatch] = nullptr)
+{
+    constexpr int copies = SelectSmem<NT>::copies;
+    uint32_t *hist = copies > 1 ? sm.copied + threadIdx.x % copies : sm.hist[0];
+    batched<NT, false>(s, Source{nullptr, s.g0}, s.g0, s.g1 - s.g0, [&](uint32_t i, const uint4 &q) {
+        const uint32_t bits = s.valid(s.g0 + i);
+        keep(i, q);
+        if (bits & 1u) atomicAdd(&hist[(q.x >> 21) * copies], 1u);
+        if (bits & 2u) atomicAdd(&hist[(q.y >> 21) * copies], 1u);
+        if (bits & 4u) atomicAdd(&hist[(q.z >> 21) * copies], 1u);
+        if (bits & 8u) atomicAdd(&hist[(q.w >> 21) * copies], 1u);
+    }, ready);
+    if constexpr (copies > 1) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < kSelBins; b += NT) {
+            const uint4 c = *reinterpret_cast<const uint4 *>(&sm.copied[b * copies]);
+            sm.hist[0][b] = (c.x + c.y) + (c.z + c.w);
+        }
+    }
+}
+
+// Digit 1 or 2 (`pass`): its bits, and the histogram of the keys that match `prefix`,
+// the digits found before: those from `least` on, `width` of them.
+__device__ __forceinline__ int digit_shift(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
+__device__ __forceinline__ int digit_bits(int pass) { return pass == 2 ? 10 : 11; }
+
+template <int NT>
+__device__ __forceinline__ void count_matching(uint32_t *hist, const Slice &s, const Source &src,
+                                               int pass, uint32_t prefix,
+                                               const float4 (*ready)[kSelBatch] = nullptr)
+{
+    const int shift = digit_shift(pass), top = shift + digit_bits(pass);
+    const uint32_t least = prefix << top, width = 1u << top;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const uint32_t at = side == 0 ? s.g0 : src.split;
+        const uint32_t n = (side == 0 ? src.split : s.g1) - at;
+        batched<NT, false>(s, src, at, n, [&](uint32_t i, const uint4 &q) {
+            const uint32_t x[4] = {q.x - least, q.y - least, q.z - least, q.w - least};
+            if (min(min(x[0], x[1]), min(x[2], x[3])) >= width)
+                return;
+            const uint32_t v = s.valid(at + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (x[e] < width && (v >> e & 1u))
+                    atomicAdd(&hist[x[e] >> shift], 1u);
+        }, ready);
+    }
+}
+
+// A warp's search, from the top, for the lane in whose count n the rank'th falls;
+// rank becomes the rank within it.
+__device__ __forceinline__ int find_lane(uint32_t n, int lane, uint32_t *rank)
+{
+    const uint32_t upto = warp_inclusive(n, lane);
+    const int at = __ffs(__ballot_sync(0xffffffffu, *rank <= upto)) - 1;
+    *rank -= __shfl_sync(0xffffffffu, upto - n, at);
+    return at;
+}
+
+// Writes the slice's tokens that stay, in order: keys above T, and those equal to it
+// from the eq_before'th on until `rank` of them have been taken.  gt_before: keys
+// above T before the slice; eq_own: the slice's keys equal to T.
+template <int NT>
+__device__ __forceinline__ void write_kept(SelectSmem<NT> &sm, const Slice &s, const Source &src,
+                                           int32_t *kept, uint32_t T, uint32_t rank,
+                                           uint32_t gt_before, uint32_t eq_before, uint32_t eq_own,
+                                           const float4 (*ready)[kSelBatch] = nullptr)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    // All, some or none of the slice's equal keys stay.  Unless it is some, one
+    // comparison tells who stays.
+    const bool some = rank > eq_before && rank < eq_before + eq_own;
+    const uint32_t least = rank > eq_before ? T : T + 1;
+    if (!some) {
+        // output offset of the first to stay: those before it, above and equal
+        gt_before += min(eq_before, rank);
+        eq_before = 0;
+    }
+    for (uint32_t c0 = s.g0, c1; c0 < s.g1; c0 = c1) {
+        c1 = min(s.g1, c0 + kSelChunk);
+        if (c0 < src.split)
+            c1 = min(c1, src.split);               // on one side of it
+        const uint32_t segs = (c1 - c0 + 31) / 32;
+        batched<NT, true>(s, src, c0, c1 - c0, [&](uint32_t i, const uint4 &q) {
+            uint32_t f;
+            if (!some)
+                f = (q.x >= least ? 1u : 0u) | (q.y >= least ? 2u : 0u) |
+                    (q.z >= least ? 4u : 0u) | (q.w >= least ? 8u : 0u);
+            else
+                f = (q.x > T ? 1u : 0u) | (q.y > T ? 2u : 0u) | (q.z > T ? 4u : 0u) |
+                    (q.w > T ? 8u : 0u) | (q.x == T ? 16u : 0u) | (q.y == T ? 32u : 0u) |
+                    (q.z == T ? 64u : 0u) | (q.w == T ? 128u : 0u);
+            const uint32_t v = i < c1 - c0 ? s.valid(c0 + i) : 0u;
+            f &= v | (v << 4);
+            sm.flags[i] = (unsigned char)f;
+            // a warp's lanes hold the groups of one segment
+            const uint32_t n = __popc(f & 0xFu) | ((uint32_t)__popc(f >> 4) << 16);
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0)
+                sm.seg[i / 32] = sum;
+        }, c0 == s.g0 ? ready : nullptr);
+        __syncthreads();
+        uint32_t total;
+        const uint32_t off =
+            block_scan<NT>(tid < (int)segs ? sm.seg[tid] : 0u, sm.warp_sum[0], &total);
+        if (tid < (int)segs)
+            sm.seg[tid] = off;
+        __syncthreads();
+        for (uint32_t i = tid; i < segs * 32; i += NT) {
+            const uint32_t f = sm.flags[i];
+            const uint32_t n = __popc(f & 0xFu) | ((uint32_t)__popc(f >> 4) << 16);
+            const uint32_t at = sm.seg[i / 32] + warp_inclusive(n, lane) - n;
+            uint32_t gb = gt_before + (at & 0xFFFFu), eb = eq_before + (at >> 16);
+            if (f == 0)
+                continue;
+            const int32_t t = s.token(c0 + i);
+            if (!some) {
+                int32_t *to = kept + gb;
+                if (f & 1u) *to++ = t;
+                if (f & 2u) *to++ = t + 1;
+                if (f & 4u) *to++ = t + 2;
+                if (f & 8u) *to++ = t + 3;
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool gt = (f >> e) & 1u, eq = (f >> (4 + e)) & 1u;
+                if (gt || (eq && eb < rank))
+                    kept[gb + min(eb, rank)] = t + e;
+                gb += gt;
+                eb += eq;
+            }
+        }
+        gt_before += total & 0xFFFFu;
+        eq_before += total >> 16;
+        __syncthreads();
+    }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
 {
     extern __shared__ uint4 cache[];
-    using Smem = SelectSmem<NT>;
-    __shared__ Smem sm;
+    __shared__ SelectSmem<NT> sm;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
     const int r = blockIdx.x / C;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t L64 = a.seq_lens[r];
+    const int L = select_length(a, r);
     {
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         for (int b = tid; b < 3 * kSelBins / 4; b += NT)
             reinterpret_cast<uint4 *>(sm.hist)[b] = zero;
-        for (int b = tid; b < kSelBins * Smem::copies / 4 && Smem::copies > 1; b += NT)
+        for (int b = tid; b < (int)(sizeof(sm.copied) / 16); b += NT)
             reinterpret_cast<uint4 *>(sm.copied)[b] = zero;
     }
-    const int L = (int)(L64 < 0 ? 0 : (L64 > a.mass_cols ? a.mass_cols : L64));
-    const float *mass = a.mass + (int64_t)r * a.mass_ld;
-    int32_t *kept = a.kept + (int64_t)r * a.kept_ld;
-    if (L <= a.keep) {             // everything stays
-        for (int i = me * NT + tid; i < L; i += C * NT)
-            kept[i] = i;
-        if (me == 0 && tid == 0)
-            a.kept_lens[r] = L;
+    if (!select_forced<NT>(a, r, me, C, L, true))
         return;                    // the whole cluster takes this branch
-    }
-    const int hi = L - a.recent;
-    const uint32_t k = (uint32_t)(a.keep - a.sink - a.recent);
-    for (int i = me * NT + tid; i < a.sink + a.recent; i += C * NT) {
-        if (i < a.sink)
-            kept[i] = i;
-        else
-            kept[a.keep - a.recent + (i - a.sink)] = hi + (i - a.sink);
-    }
-    if (me == 0 && tid == 0)
-        a.kept_lens[r] = a.keep;
-    if (k == 0)
-        return;
-
-    // candidates [sink, hi) in groups of four aligned weights: group g holds
-    // tokens 4 g - skew .. 4 g - skew + 3
-    const uint32_t skew = (uint32_t)(reinterpret_cast<uintptr_t>(mass) / 4) & 3u;
-    const uint32_t v0 = (uint32_t)a.sink + skew, v1 = (uint32_t)hi + skew;
-    const uint32_t first = v0 / 4, groups = (v1 + 3) / 4 - first;
-    const uint32_t per = (groups + C - 1) / C;
-    const uint32_t g0 = first + min(groups, me * per), g1 = first + min(groups, (me + 1) * per);
-    // which of group g's elements are candidates: all but in the outermost groups
-    const uint32_t last = first + groups - 1;
-    const uint32_t first_bits = 0xFu & (0xFu << (v0 - 4 * first));
-    const uint32_t last_bits = 0xFu >> (4 * last + 4 - v1);
-    auto valid = [&](uint32_t g) -> uint32_t {
-        return (g == first ? first_bits : 0xFu) & (g == last ? last_bits : 0xFu);
-    };
-    auto fetch = [&](uint32_t g) -> uint4 {
-        const float *p = mass + ((int64_t)4 * g - skew);
-        const uint32_t bits = valid(g);
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (bits == 0xFu) {
-            w = *reinterpret_cast<const float4 *>(p);
-        } else {
-            if (bits & 1u) w.x = p[0];
-            if (bits & 2u) w.y = p[1];
-            if (bits & 4u) w.z = p[2];
-            if (bits & 8u) w.w = p[3];
-        }
-        return make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
-    };
+    const Slice s(a.mass + (int64_t)r * a.mass_ld, a.sink, L - a.recent, me, C);
     const uint32_t cached = (uint32_t)a.cache_groups;
-    auto keys = [&](uint32_t g) -> uint4 { return g - g0 < cached ? cache[g - g0] : fetch(g); };
-    // f(g, keys of group g) over this thread's groups of [lo, hi), the loads of
-    // kSelBatch groups in flight together
-    auto batched = [&](uint32_t lo, uint32_t hi, auto load, auto f) {
-        for (uint32_t g = lo + tid; g < hi; g += kSelBatch * NT) {
-            uint4 q[kSelBatch];
-#pragma unroll
-            for (int j = 0; j < kSelBatch; ++j)
-                if (g + j * NT < hi)
-                    q[j] = load(g + j * NT);
-#pragma unroll
-            for (int j = 0; j < kSelBatch; ++j)
-                if (g + j * NT < hi)
-                    f(g + j * NT, q[j]);
-        }
-    };
-
-    // first digit, filling the cache
+    const Source src = {cache, min(s.g1, s.g0 + cached)};
     __syncthreads();
-    {
-        uint32_t *hist = Smem::copies > 1 ? sm.copied + lane % Smem::copies : sm.hist[0];
-        batched(g0, g1, fetch, [&](uint32_t g, const uint4 &q) {
-            const uint32_t bits = valid(g);
-            if (g - g0 < cached)
-                cache[g - g0] = q;
-            if (bits & 1u) atomicAdd(&hist[(q.x >> 21) * Smem::copies], 1u);
-            if (bits & 2u) atomicAdd(&hist[(q.y >> 21) * Smem::copies], 1u);
-            if (bits & 4u) atomicAdd(&hist[(q.z >> 21) * Smem::copies], 1u);
-            if (bits & 8u) atomicAdd(&hist[(q.w >> 21) * Smem::copies], 1u);
-        });
-        if constexpr (Smem::copies > 1) {
-            __syncthreads();
-            for (int b = tid; b < kSelBins; b += NT) {
-                const uint4 c = *reinterpret_cast<const uint4 *>(&sm.copied[b * Smem::copies]);
-                sm.hist[0][b] = (c.x + c.y) + (c.z + c.w);
-            }
-        }
-    }
-    uint32_t prefix = 0, rank = k;             // the rank'th largest among the matching keys
+    count_first<NT>(sm, s, [&](uint32_t i, const uint4 &q) {
+        if (i < cached)
+            cache[i] = q;
+    });
+    // the rank'th largest among the keys that match `prefix`
+    uint32_t prefix = 0, rank = (uint32_t)(a.keep - a.sink - a.recent);
     uint32_t above_T = 0;                      // this thread's share of the CTA's keys above T
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         uint32_t *hist = sm.hist[pass];
-        if (pass > 0) {
-            // keys that match the digits found: those from `least` on, `width` of them
-            const uint32_t least = prefix << (shift + bits), width = 1u << (shift + bits);
-            batched(g0, g1, keys, [&](uint32_t g, const uint4 &q) {
-                const uint32_t x[4] = {q.x - least, q.y - least, q.z - least, q.w - least};
-                if (min(min(x[0], x[1]), min(x[2], x[3])) >= width)
-                    return;
-                const uint32_t v = valid(g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (x[e] < width && (v >> e & 1u))
-                        atomicAdd(&hist[x[e] >> shift], 1u);
-            });
-        }
+        if (pass > 0)
+            count_matching<NT>(hist, s, src, pass, prefix);
         // Which bin holds the rank'th largest: first among the 32 sums of 64 bins,
         // then among that sum's 64 bins.  In a cluster thread t brings a peer's value
         // to shared memory; every warp then finds the same answer for itself.
@@ -255,10 +451,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
         uint32_t n = 0;
         for (int c = 0; c < C; ++c)
             n += sums[32 * c + 31 - lane];              // from the top
-        uint32_t below = warp_inclusive(n, lane);
-        const int at = __ffs(__ballot_sync(0xffffffffu, rank <= below)) - 1;
-        rank -= __shfl_sync(0xffffffffu, below - n, at);
-        const int base = 64 * (31 - at);
+        const int base = 64 * (31 - find_lane(n, lane, &rank));
         fine += base;
         if (C > 1) {
             if (tid < 64 * C)
@@ -272,16 +465,14 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
             n0 += v.x;
             n1 += v.y;
         }
-        below = warp_inclusive(n0 + n1, lane);
-        const int pair = __ffs(__ballot_sync(0xffffffffu, rank <= below)) - 1;
-        rank -= __shfl_sync(0xffffffffu, below - n0 - n1, pair);
+        const int pair = find_lane(n0 + n1, lane, &rank);
         n1 = __shfl_sync(0xffffffffu, n1, pair);
         uint32_t bin = (uint32_t)(base + 63 - 2 * pair);
         if (rank > n1) {
             rank -= n1;
             --bin;
         }
-        prefix = (prefix << bits) | bin;
+        prefix = (prefix << digit_bits(pass)) | bin;
 #pragma unroll
         for (int j = 0; j < kSelCoarse / (NT / 32); ++j) {
             const uint32_t b = 64u * (warp + j * (NT / 32)) + 2u * lane;
@@ -301,82 +492,148 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
         cluster.sync();
     else
         __syncthreads();
-    // keys above T all stay, and the first `rank` of those equal to T: all, some or
-    // none of this CTA's.  Unless it is some, one comparison tells who stays.
     uint32_t gt_before = 0, eq_before = 0;
     for (int c = 0; c < me; ++c) {
         gt_before += *cluster.map_shared_rank(&sm.counts[0], c);
         eq_before += *cluster.map_shared_rank(&sm.counts[1], c);
     }
-    const uint32_t eq_own = sm.counts[1];
-    const bool some = rank > eq_before && rank < eq_before + eq_own;
-    const uint32_t least = rank > eq_before ? T : T + 1;
-    if (!some) {
-        // output offset of the first to stay: those before it, above and equal
-        gt_before += min(eq_before, rank);
-        eq_before = 0;
-    }
-    for (uint32_t c0 = g0; c0 < g1; c0 += kSelChunk) {
-        const uint32_t c1 = min(g1, c0 + kSelChunk), segs = (c1 - c0 + 31) / 32;
-        // whole warps run, so that every segment's counts are summed by 32 lanes
-        auto load = [&](uint32_t i) { return c0 + i < c1 ? keys(c0 + i) : make_uint4(0, 0, 0, 0); };
-        batched(0, segs * 32, load, [&](uint32_t i, const uint4 &q) {
-            uint32_t f = 0;
-            if (c0 + i < c1) {
-                if (!some)
-                    f = (q.x >= least ? 1u : 0u) | (q.y >= least ? 2u : 0u) |
-                        (q.z >= least ? 4u : 0u) | (q.w >= least ? 8u : 0u);
-                else
-                    f = (q.x > T ? 1u : 0u) | (q.y > T ? 2u : 0u) | (q.z > T ? 4u : 0u) |
-                        (q.w > T ? 8u : 0u) | (q.x == T ? 16u : 0u) | (q.y == T ? 32u : 0u) |
-                        (q.z == T ? 64u : 0u) | (q.w == T ? 128u : 0u);
-                const uint32_t v = valid(c0 + i);
-                f &= v | (v << 4);
-            }
-            sm.flags[i] = (unsigned char)f;
-            const uint32_t n = __popc(f & 0xFu) | ((uint32_t)__popc(f >> 4) << 16);
-            const uint32_t s = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0)
-                sm.seg[i / 32] = s;
-        });
-        __syncthreads();
-        uint32_t total;
-        const uint32_t off =
-            block_scan<NT>(tid < (int)segs ? sm.seg[tid] : 0u, sm.warp_sum[0], &total);
-        if (tid < (int)segs)
-            sm.seg[tid] = off;
-        __syncthreads();
-        for (uint32_t i = tid; i < segs * 32; i += NT) {
-            const uint32_t f = sm.flags[i];
-            const uint32_t n = __popc(f & 0xFu) | ((uint32_t)__popc(f >> 4) << 16);
-            const uint32_t at = sm.seg[i / 32] + warp_inclusive(n, lane) - n;
-            uint32_t gb = gt_before + (at & 0xFFFFu), eb = eq_before + (at >> 16);
-            if (f == 0)
-                continue;
-            if (!some) {
-                int32_t *to = kept + a.sink + gb;
-                const int32_t t = (int32_t)(4 * (c0 + i) - skew);
-                if (f & 1u) *to++ = t;
-                if (f & 2u) *to++ = t + 1;
-                if (f & 4u) *to++ = t + 2;
-                if (f & 8u) *to++ = t + 3;
-                continue;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool gt = (f >> e) & 1u, eq = (f >> (4 + e)) & 1u;
-                if (gt || (eq && eb < rank))
-                    kept[a.sink + gb + min(eb, rank)] = (int32_t)(4 * (c0 + i) + e - skew);
-                gb += gt;
-                eb += eq;
-            }
-        }
-        gt_before += total & 0xFFFFu;
-        eq_before += total >> 16;
-        __syncthreads();
-    }
+    write_kept<NT>(sm, s, src, a.kept + (int64_t)r * a.kept_ld + a.sink, T, rank, gt_before,
+                   eq_before, sm.counts[1]);
     if (C > 1)
         cluster.sync();            // no CTA leaves while its counts may still be read
+}
+
+// Long rows, few of them: a cluster has 16 SMs at most, so the same search runs as
+// four kernels in which every request has `parts` CTAs (one per SM together), whose
+// histograms meet in a workspace.  Pass p finds digit p - 1 among the parts'
+// histograms (each CTA for itself: 32 sums and 64 bins per part, a few KB from L2),
+// counts digit p of its slice, and notes how many keys above the final threshold the
+// parts before it have shown so far; the last pass writes.  Each pass reads the slice
+// again, from L2, its first loads before the pass ahead of it has finished.
+// Measured against the cluster form: one row of a million weights 26 us (45), of four
+// millions 41 us (141), four rows of a million 39 us (44), two of 500,000 23 us (26);
+// below kSelLong weights a slice the cluster wins (one row of 300,000 22 us, 23 in
+// parts).
+struct SelectParts {
+    int parts;
+    uint32_t *hist;                // [request][3][part][kSelBins]
+    uint32_t *coarse;              // [request][3][part][kSelCoarse]
+    uint32_t *before;              // [request][part] keys above T in the parts before
+    uint2 *state;                  // [request][3] prefix and rank once digit p is found
+};
+
+template <int PASS>
+__global__ void __launch_bounds__(kSelPartThreads, 2) select_part_kernel(const SelectArgs a,
+                                                                         const SelectParts p)
+{
+    constexpr int NT = kSelPartThreads, kWarps = NT / 32;
+    __shared__ SelectSmem<NT> sm;
+    __shared__ uint4 red[kWarps][32];
+    const int r = blockIdx.x / p.parts, me = blockIdx.x % p.parts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    // The next pass's CTAs take their places beside these and wait for this grid to
+    // finish; until then they read only what was there before the first pass.
+    if constexpr (PASS < 3)
+        asm volatile("griddepcontrol.launch_dependents;");
+    const int L = select_length(a, r);
+    if (!select_forced<NT>(a, r, me, p.parts, L, PASS == 0))
+        return;
+    const Slice s(a.mass + (int64_t)r * a.mass_ld, a.sink, L - a.recent, me, p.parts);
+    float4 ready[kSelBatch];
+    load_batch<NT>(s, s.g0 + tid, ready);
+    if constexpr (PASS == 0) {
+        for (int b = tid; b < (int)(sizeof(sm.copied) / 16); b += NT)
+            reinterpret_cast<uint4 *>(sm.copied)[b] = zero;
+    } else if constexpr (PASS < 3) {
+        for (int b = tid; b < kSelBins / 4; b += NT)
+            reinterpret_cast<uint4 *>(sm.hist[PASS])[b] = zero;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Source src = {nullptr, s.g0};
+    uint32_t prefix = 0, rank = (uint32_t)(a.keep - a.sink - a.recent);
+    uint32_t gt_before = 0, eq_before = 0, eq_own = 0;
+    if constexpr (PASS > 0) {
+        constexpr int found = PASS - 1;        // the digit to find
+        if constexpr (PASS > 1) {
+            const uint2 st = p.state[3 * r + found - 1];
+            prefix = st.x;
+            rank = st.y;
+            gt_before = p.before[(int64_t)r * p.parts + me];
+        }
+        const uint32_t *coarse = p.coarse + ((int64_t)3 * r + found) * p.parts * kSelCoarse;
+        const uint32_t *hist = p.hist + ((int64_t)3 * r + found) * p.parts * kSelBins;
+        // warp w sums parts w, w + kWarps, ...: of all parts, and of those before this one
+        uint32_t n = 0, b = 0;
+        for (int c = warp; c < p.parts; c += kWarps) {
+            const uint32_t v = coarse[c * kSelCoarse + lane];
+            n += v;
+            b += c < me ? v : 0u;
+        }
+        red[warp][31 - lane] = make_uint4(n, b, 0u, 0u);       // from the top
+        __syncthreads();
+        n = b = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            const uint4 v = red[w][lane];
+            n += v.x;
+            b += v.y;
+        }
+        const int at = find_lane(n, lane, &rank);
+        gt_before += __reduce_add_sync(0xffffffffu, lane < at ? b : 0u);
+        const int base = 64 * (31 - at);
+        __syncthreads();
+        uint4 v = zero;                        // lower and upper bin of all parts; of those before
+        for (int c = warp; c < p.parts; c += kWarps) {
+            const uint2 x =
+                *reinterpret_cast<const uint2 *>(hist + c * kSelBins + base + 62 - 2 * lane);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += c < me ? x.x : 0u;
+            v.w += c < me ? x.y : 0u;
+        }
+        red[warp][lane] = v;
+        __syncthreads();
+        v = zero;
+        for (int w = 0; w < kWarps; ++w) {
+            const uint4 x = red[w][lane];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        const int pair = find_lane(v.x + v.y, lane, &rank);
+        const uint32_t n1 = __shfl_sync(0xffffffffu, v.y, pair);
+        const bool lower = rank > n1;
+        gt_before += __reduce_add_sync(0xffffffffu, lane < pair ? v.z + v.w
+                                                    : lane == pair && lower ? v.w : 0u);
+        eq_before = __shfl_sync(0xffffffffu, lower ? v.z : v.w, pair);
+        if (lower)
+            rank -= n1;
+        const uint32_t bin = (uint32_t)(base + 63 - 2 * pair) - (lower ? 1u : 0u);
+        prefix = (prefix << digit_bits(found)) | bin;
+        eq_own = hist[me * kSelBins + bin];
+        if (PASS < 3 && tid == 0) {
+            p.before[(int64_t)r * p.parts + me] = gt_before;
+            if (me == 0)
+                p.state[3 * r + found] = make_uint2(prefix, rank);
+        }
+    }
+    if constexpr (PASS == 3) {
+        write_kept<NT>(sm, s, src, a.kept + (int64_t)r * a.kept_ld + a.sink, prefix, rank,
+                       gt_before, eq_before, eq_own, &ready);
+    } else {
+        __syncthreads();
+        if constexpr (PASS == 0)
+            count_first<NT>(sm, s, [](uint32_t, const uint4 &) {}, &ready);
+        else
+            count_matching<NT>(sm.hist[PASS], s, src, PASS, prefix, &ready);
+        __syncthreads();
+        const int64_t at = ((int64_t)3 * r + PASS) * p.parts + me;
+        for (int w = warp; w < kSelCoarse; w += kWarps) {
+            const uint2 own = *reinterpret_cast<const uint2 *>(sm.hist[PASS] + 64 * w + 2 * lane);
+            reinterpret_cast<uint2 *>(p.hist + at * kSelBins + 64 * w)[lane] = own;
+            const uint32_t part = __reduce_add_sync(0xffffffffu, own.x + own.y);
+            if (lane == 0)
+                p.coarse[at * kSelCoarse + w] = part;
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -461,6 +718,15 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
     }
 }
 
+cudaError_t select_attributes(const void *kernel)
+{
+    const cudaError_t err = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(4 * kSelCache));
+    return err != cudaSuccess
+               ? err
+               : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 // Clusters of 2^log CTAs that the device holds at once (0: none, or it cannot say).
 int select_max_clusters(int log)
 {
@@ -469,6 +735,9 @@ int select_max_clusters(int log)
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return 0;
     if (cached[dev][log] == 0) {
+        if (select_attributes(reinterpret_cast<const void *>(select_kernel<kSelThreads>)) !=
+            cudaSuccess)
+            return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(1u << log);
         cfg.blockDim = dim3(kSelThreads);
@@ -490,46 +759,84 @@ int select_max_clusters(int log)
     return cached[dev][log] - 1;
 }
 
+// log2 of the CTAs per request.  Rows of at most kSelSmall weights: one small CTA
+// each.  Longer ones: the widest cluster that leaves a CTA 4096 weights and has room
+// for every request at once.  (More clusters than the device holds take turns: 16
+// histories of 100,000 tokens took 32 us in clusters of 8, 21 us in clusters of 4.)
+int select_cluster_log(int num_reqs, int64_t mass_cols)
+{
+    int log = mass_cols <= kSelSmall ? 0 : 4;
+    while (log > 0 && (mass_cols < ((int64_t)4096 << log) || num_reqs > select_max_clusters(log)))
+        --log;
+    return log;
+}
+
 }  // namespace
+
+// Parts per request of the form for long rows (0: the cluster form serves as well):
+// where a cluster's slices pass kSelLong weights and every request can have at least
+// twice the cluster's SMs.
+int select_parts(int num_reqs, int64_t mass_cols, int sms)
+{
+    const int log = select_cluster_log(num_reqs, mass_cols);
+    const int parts = sms / num_reqs;
+    return mass_cols >> log > kSelLong && parts >= 2 << log ? parts : 0;
+}
+
+size_t select_workspace(int num_reqs, int parts)
+{
+    // per request: state, and per part three histograms, their sums and a count
+    return (size_t)num_reqs *
+           (3 * sizeof(uint2) + (size_t)parts * sizeof(uint32_t) * (3 * (kSelBins + kSelCoarse) + 1));
+}
 
 cudaError_t launch_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
                           const int32_t *seq_lens, int num_reqs, int keep, int sink, int recent,
-                          int32_t *kept, int64_t kept_ld, int32_t *kept_lens,
-                          cudaStream_t stream)
+                          int32_t *kept, int64_t kept_ld, int32_t *kept_lens, int parts,
+                          void *workspace, cudaStream_t stream)
 {
-    // Rows of at most kSelSmall weights: one small CTA each.  Longer ones: the widest
-    // cluster that leaves a CTA 4096 weights and has room for every request at once.
+    SelectArgs a = {mass, mass_ld, mass_cols, seq_lens, keep, sink, recent, kept, kept_ld,
+                    kept_lens, 0};
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (parts > 0) {
+        SelectParts p = {parts};
+        p.state = static_cast<uint2 *>(workspace);
+        p.hist = reinterpret_cast<uint32_t *>(p.state + 3 * num_reqs);
+        p.coarse = p.hist + (size_t)num_reqs * 3 * parts * kSelBins;
+        p.before = p.coarse + (size_t)num_reqs * 3 * parts * kSelCoarse;
+        // later passes are launched ahead of the end of the one before
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)(num_reqs * parts));
+        cfg.blockDim = dim3(kSelPartThreads);
+        cudaError_t err = cudaLaunchKernelEx(&cfg, select_part_kernel<0>, a, p);
+        cfg.numAttrs = 1;
+        if (err == cudaSuccess)
+            err = cudaLaunchKernelEx(&cfg, select_part_kernel<1>, a, p);
+        if (err == cudaSuccess)
+            err = cudaLaunchKernelEx(&cfg, select_part_kernel<2>, a, p);
+        return err == cudaSuccess ? cudaLaunchKernelEx(&cfg, select_part_kernel<3>, a, p) : err;
+    }
     const bool small = mass_cols <= kSelSmall;
     const void *kernel = small ? reinterpret_cast<const void *>(select_kernel<kSelSmallThreads>)
                                : reinterpret_cast<const void *>(select_kernel<kSelThreads>);
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)(4 * kSelCache));
-    if (err == cudaSuccess && !small)
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t err = select_attributes(kernel);
     if (err != cudaSuccess)
         return err;
-    // (More clusters than the device holds at once take turns: 16 histories of 100,000
-    // tokens took 32 us in clusters of 8, against 20 us in clusters of 4.)
-    int log = small ? 0 : 4;
-    while (log > 0 && (mass_cols < ((int64_t)4096 << log) || num_reqs > select_max_clusters(log)))
-        --log;
-    const int cluster = 1 << log;
+    const int cluster = 1 << select_cluster_log(num_reqs, mass_cols);
     // a slice of the longest history, up to kSelCache weights
     const int64_t groups = (mass_cols + 3) / 4 + 1, slice = (groups + cluster - 1) / cluster;
-    const int cache_groups = (int)(slice < kSelCache / 4 ? slice : kSelCache / 4);
-    SelectArgs a = {mass, mass_ld, mass_cols, seq_lens, keep, sink, recent, kept, kept_ld,
-                    kept_lens, cache_groups};
-    cudaLaunchConfig_t cfg = {};
+    a.cache_groups = (int)(slice < kSelCache / 4 ? slice : kSelCache / 4);
     cfg.gridDim = dim3((unsigned)(num_reqs * cluster));
     cfg.blockDim = dim3(small ? kSelSmallThreads : kSelThreads);
-    cfg.dynamicSmemBytes = sizeof(uint4) * (size_t)cache_groups;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cfg.dynamicSmemBytes = sizeof(uint4) * (size_t)a.cache_groups;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
     void *args[1] = {&a};
     return cudaLaunchKernelExC(&cfg, kernel, args);

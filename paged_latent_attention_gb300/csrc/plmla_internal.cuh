@@ -172,7 +172,11 @@ cudaError_t launch_mass(const MassArgs &args, int sms, cudaStream_t stream);
 constexpr int kCompactLayers = 64;              // layers of one compaction launch
 cudaError_t launch_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
                           const int32_t *seq_lens, int num_reqs, int keep, int sink, int recent, int32_t *kept,
-                          int64_t kept_ld, int32_t *kept_lens, cudaStream_t stream);
+                          int64_t kept_ld, int32_t *kept_lens, int parts, void *workspace,
+                          cudaStream_t stream);
+// CTAs per request of the form for long rows (0: none), and its workspace in bytes.
+int select_parts(int num_reqs, int64_t mass_cols, int sms);
+size_t select_workspace(int num_reqs, int parts);
 cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t num_pages,
                            int64_t page_bytes, const int32_t *table, int64_t table_ld,
                            const int32_t *seq_lens, const int32_t *out_table, int64_t out_ld,

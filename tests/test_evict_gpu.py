@@ -8,7 +8,7 @@ import torch
 
 import oracle
 from helpers import SCALE, assert_parity
-from paged_latent_attention_gb300 import api, inputs
+from paged_latent_attention_gb300 import _native, api, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -38,7 +38,8 @@ def _check_select(mass, lens, keep, sink, recent):
     ([1], 1, 0, 0), ([0, 1, 2, 3], 2, 1, 1), ([1000, 2000], 512, 4, 64), ([33, 32, 31], 32, 0, 0),
     ([5000, 12, 4097], 700, 0, 0), ([5000, 12, 4097], 700, 350, 350), ([5000, 4097], 1, 0, 0),
     ([9000, 20_000, 0], 8999, 17, 101), ([40_000, 33_000, 90_001], 20_000, 4, 1000),
-    ([7] * 300, 3, 1, 1), ([6000] * 90, 100, 2, 30), ([400_000], 60_000, 4, 512)])
+    ([7] * 300, 3, 1, 1), ([6000] * 90, 100, 2, 30), ([400_000], 60_000, 4, 512),
+    ([300_000, 7, 299_999], 500, 3, 5), ([1_000_003], 1, 0, 0), ([270_000, 270_001], 270_000, 1, 9)])
 def test_selection_matches_the_oracle(lengths, keep, sink, recent):
     g = torch.Generator().manual_seed(len(lengths) + keep)
     mass = torch.empty(len(lengths), max(max(lengths), 1)).exponential_(generator=g).pow_(3).cuda()
@@ -46,7 +47,7 @@ def test_selection_matches_the_oracle(lengths, keep, sink, recent):
 
 
 @pytest.mark.parametrize("kind", ["equal", "few", "signs", "special", "nan", "tiny"])
-@pytest.mark.parametrize("L,keep", [(3000, 1000), (70_000, 30_001)])
+@pytest.mark.parametrize("L,keep", [(3000, 1000), (70_000, 30_001), (280_000, 100_003)])
 def test_ties_signs_and_special_values(kind, L, keep):
     g = torch.Generator().manual_seed(L)
     m = torch.randn(2, L, generator=g)
@@ -67,6 +68,29 @@ def test_ties_signs_and_special_values(kind, L, keep):
     else:
         m = m * 1e-42                      # subnormal weights
     _check_select(m.cuda(), [L, L - 1], keep, 2, 3)
+
+
+def test_long_rows_with_and_without_a_workspace():
+    """The form for long rows takes a workspace; without one (through the C entry) the
+    cluster form gives the same indices, and too small a one is refused."""
+    g = torch.Generator().manual_seed(1)
+    R, L, keep = 2, 500_001, 40_000
+    mass = torch.randint(0, 50_000, (R, L), generator=g).float().cuda()
+    lens = torch.tensor([L, 300_000], dtype=torch.int32, device="cuda")
+    size = _native.lib().mla_evict_workspace_size(R, L)
+    assert size > 0 and api.allocate_evict_workspace(R, 2000).numel() == 0
+    want, n = api.mla_evict_select(mass, lens, keep, sink=4, recent=100)
+    dirty = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        got, m = api.mla_evict_select(mass, lens, keep, sink=4, recent=100, workspace=dirty)
+        assert torch.equal(got, want) and torch.equal(m, n)
+    got.fill_(-1)
+    call = (mass.data_ptr(), L, L, lens.data_ptr(), R, keep, 4, 100, got.data_ptr(), keep,
+            m.data_ptr())
+    assert _native.lib().mla_evict_select(*call, None, 0, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert _native.lib().mla_evict_select(*call, dirty.data_ptr(), size // 2, None) == 3
 
 
 def test_selection_views_bits_and_graphs():
