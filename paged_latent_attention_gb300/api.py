@@ -496,6 +496,15 @@ def _launch(dev, fn, where, stream, *args):
         raise _native.PlmlaError(status, where)
 
 
+def _empty(shape, dtype, device, stream):
+    """New memory for a call on `stream`: the allocator keeps it from other streams'
+    tensors until that stream has passed the call."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _vector(t, name, dev, n):
     """A contiguous int32 vector of n elements on device `dev`."""
     if not (t.dtype is _I32 and t.get_device() == dev and t.dim() == 1 and t.shape[0] == n
@@ -623,7 +632,7 @@ def mla_rope(x, positions, table, *, layout="half", inverse=False, out=None, str
     code = _layout(layout)
     at, turns = _vector(positions, "positions", dev, T), table.address(dev, D)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        out = _empty((T, H, D), x.dtype, x.device, stream)
     else:
         _check_rope_out(x, out, dev)
     if T and H:
@@ -679,7 +688,7 @@ def _kv_scale(kv_scale):
 def _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, positions, layout,
                  q_rope, q_out, status, stream, kv_scale):
     base, pages, page_stride = _pool(slab, kv_scale is not None)
-    dev = slab.get_device()
+    dev, n_new = slab.get_device(), int(n_new)
     R = seq_lens.shape[0] if seq_lens.dim() == 1 else 0
     rows = R * n_new
     lens = _vector(seq_lens, "seq_lens", dev, R)
@@ -698,7 +707,7 @@ def _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table,
             _fail(f"q_rope must be a bf16 view [{rows}, H, {ROPE}] on cuda:{dev} with contiguous "
                   "heads")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=_BF16, device=q_rope.device)
+            q_out = _empty(shape, _BF16, q_rope.device, stream)
         else:
             _dense(q_out, "q_out", dev, shape)
             if q_out.numel():
@@ -750,7 +759,7 @@ def mla_attention_mass_fp8(q_nope_absorbed, q_rope, lse, slab, page_table, seq_l
 def _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, scale, decay,
           kv_scale, workspace, status, stream):
     base, pages, page_stride = _pool(slab, kv_scale is not None)
-    dev = slab.get_device()
+    dev, n_q = slab.get_device(), int(n_q)
     shape = q_nope_absorbed.shape
     if len(shape) != 3 or n_q < 1 or shape[0] % n_q != 0:
         _fail("q_nope_absorbed must be [R*n_q, H, 512]")
@@ -764,13 +773,14 @@ def _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, s
     out = _rows(mass, "mass", dev, _F32, R)
     flag = _flag(status, dev)
     lib = _native.lib()
-    tail = (ids, ids_ld, lens, R, n_q, H, scale, decay, *out)
+    tail = (ids, ids_ld, lens, R, n_q, H, float(scale), float(decay), *out)
     if kv_scale is None:
         _launch(dev, lib.mla_attention_mass, "mla_attention_mass", stream, qn, qr, l, base, pages,
                 page_stride, *tail, flag)
     else:
         if workspace is None:
-            workspace = allocate_mass_workspace(R, n_q, H, slab.device)
+            size = lib.mla_mass_workspace_size_fp8(R, n_q, H)
+            workspace = _empty(size, _U8, slab.device, stream)
         if workspace.get_device() != dev or not workspace.is_contiguous():
             _fail(f"workspace must be contiguous memory on cuda:{dev}")
         _launch(dev, lib.mla_attention_mass_fp8, "mla_attention_mass_fp8", stream, qn, qr, l, base,
@@ -798,15 +808,16 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
     if mass.dim() != 2 or dev < 0:
         _fail("mass must be a CUDA tensor [R, tokens]")
     R, tokens = mass.shape
+    keep, sink, recent = int(keep), int(sink), int(recent)
     weights = _rows(mass, "mass", dev, _F32, R)
     lens = _vector(seq_lens, "seq_lens", dev, R)
-    if not (keep >= 1 and sink >= 0 and recent >= 0 and sink + recent <= keep):
+    if not (1 <= keep < 1 << 31 and sink >= 0 and recent >= 0 and sink + recent <= keep):
         _fail("keep >= 1, sink and recent >= 0, and sink + recent <= keep are needed")
     cols = min(keep, tokens)
     if kept is None:
-        kept = torch.empty(R, cols, dtype=_I32, device=mass.device)
+        kept = _empty((R, cols), _I32, mass.device, stream)
     if kept_lens is None:
-        kept_lens = torch.empty(R, dtype=_I32, device=mass.device)
+        kept_lens = _empty(R, _I32, mass.device, stream)
     ids, ids_ld, have = _rows(kept, "kept", dev, _I32, R)
     if have < cols:
         _fail(f"kept needs {cols} columns")
@@ -814,7 +825,7 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
     if workspace is None:
         size = lib.mla_evict_workspace_size(R, tokens)
         if size:
-            workspace = torch.empty(size, dtype=_U8, device=mass.device)
+            workspace = _empty(size, _U8, mass.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _fail(f"workspace must be contiguous memory on cuda:{dev}")
     if workspace is not None and workspace.numel():
@@ -861,7 +872,7 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
     else:
         weights = _rows(mass, "mass", dev, _F32, R)
         if mass_out is None:
-            mass_out = torch.empty(R, cols, dtype=_F32, device=mass.device)
+            mass_out = _empty((R, cols), _F32, mass.device, stream)
         dst, dst_ld, have = _rows(mass_out, "mass_out", dev, _F32, R)
         if have < cols:
             _fail(f"mass_out needs {cols} columns")

@@ -537,8 +537,11 @@ __global__ void __launch_bounds__(kSelPartThreads, 2) select_part_kernel(const S
     if constexpr (PASS < 3)
         asm volatile("griddepcontrol.launch_dependents;");
     const int L = select_length(a, r);
-    if (!select_forced<NT>(a, r, me, p.parts, L, PASS == 0))
+    if (!select_forced<NT>(a, r, me, p.parts, L, PASS == 0)) {
+        // (no grid ends before the one ahead of it)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
+    }
     const Slice s(a.mass + (int64_t)r * a.mass_ld, a.sink, L - a.recent, me, p.parts);
     float4 ready[kSelBatch];
     load_batch<NT>(s, s.g0 + tid, ready);

@@ -84,6 +84,16 @@ def test_long_rows_with_and_without_a_workspace():
     for _ in range(2):
         got, m = api.mla_evict_select(mass, lens, keep, sink=4, recent=100, workspace=dirty)
         assert torch.equal(got, want) and torch.equal(m, n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.mla_evict_select(mass, lens, keep, sink=4, recent=100, kept=got, kept_lens=m,
+                             workspace=dirty)
+    lens.copy_(torch.tensor([keep, 400_001], dtype=torch.int32))   # a row without a choice
+    mass.copy_(mass.flip(1))
+    graph.replay()
+    want = oracle.evict_select(mass.cpu().numpy(), lens.tolist(), keep, 4, 100)
+    assert [got[r].tolist() for r in range(R)] == want and m.tolist() == [keep, keep]
+    want = torch.tensor(want, dtype=torch.int32, device="cuda")
     got.fill_(-1)
     call = (mass.data_ptr(), L, L, lens.data_ptr(), R, keep, 4, 100, got.data_ptr(), keep,
             m.data_ptr())
@@ -270,6 +280,9 @@ def test_front_end_refusals():
         lambda: api.mla_evict_select(mass, lens, 0),
         lambda: api.mla_evict_select(mass, lens, 10, sink=6, recent=5),
         lambda: api.mla_evict_select(mass, lens, 10, sink=-1),
+        lambda: api.mla_evict_select(mass, lens, 1 << 31),
+        lambda: api.mla_evict_select(mass[:, ::2], lens, 10),
+        lambda: api.mla_evict_select(mass, lens, 10, workspace=torch.zeros(9)),
         lambda: api.mla_evict_select(mass.half(), lens, 10),
         lambda: api.mla_evict_select(mass, lens[:1], 10),
         lambda: api.mla_evict_select(mass, lens, 10,
