@@ -117,15 +117,29 @@ struct StepWalk {
     }
 };
 
-// Adds the weights of 16 columns (scores in SETS column sets) of this thread's token
-// to sum; MASKED: of the columns from `first` on.
-template <bool F8, int SETS, bool MASKED>
-__device__ __forceinline__ void add_weights(const uint32_t (&v)[SETS][16], const float4 *neg,
+// Columns that a thread reads from TMEM at a time: two batches of SETS sets fit its
+// registers.
+template <int SETS>
+constexpr int kMassBatch = SETS == 4 ? 8 : 16;
+
+template <int W>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[W])
+{
+    if constexpr (W == 16)
+        tmem_ld16(taddr, r);
+    else
+        tmem_ld8(taddr, r);
+}
+
+// Adds the weights of W columns (scores in SETS column sets) of this thread's token to
+// sum; MASKED: of the columns from `first` on.
+template <bool F8, int SETS, bool MASKED, int W>
+__device__ __forceinline__ void add_weights(const uint32_t (&v)[SETS][W], const float4 *neg,
                                             const float4 *fac, float scale_log2, int first,
                                             float (&sum)[4])
 {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < W / 4; ++e) {
         const float4 l4 = neg[e];
         const float l[4] = {l4.x, l4.y, l4.z, l4.w};
         float f[4] = {scale_log2, scale_log2, scale_log2, scale_log2};
@@ -138,49 +152,52 @@ __device__ __forceinline__ void add_weights(const uint32_t (&v)[SETS][16], const
             float score = __uint_as_float(v[0][4 * e + j]);
             if constexpr (SETS == 2)
                 score += __uint_as_float(v[1][4 * e + j]);
+            if constexpr (SETS == 4)
+                score = (score + __uint_as_float(v[1][4 * e + j])) +
+                        (__uint_as_float(v[2][4 * e + j]) + __uint_as_float(v[3][4 * e + j]));
             const float w = fast_exp2(fmaf(score, f[j], l[j]));
             sum[j] += !MASKED || 4 * e + j >= first ? w : 0.f;
         }
     }
 }
 
-// The weights of `cols` columns (a multiple of 16) from TMEM address `at`, the second
-// set `half` columns on: 16 at a time, the next on their way while the last are summed.
+// The weights of `cols` columns (a multiple of 16) from TMEM address `at`, each further
+// set `half` columns on: a batch at a time, the next on its way while the last is summed.
 template <bool F8, int SETS, bool MASKED>
 __device__ __forceinline__ void sum_columns(uint32_t at, int half, int cols, const float4 *neg,
                                             const float4 *fac, float scale_log2, int first,
                                             float (&sum)[4])
 {
-    uint32_t x[SETS][16], y[SETS][16];
-    tmem_ld16(at, x[0]);
-    if constexpr (SETS == 2)
-        tmem_ld16(at + half, x[1]);
+    constexpr int W = kMassBatch<SETS>;
+    uint32_t x[SETS][W], y[SETS][W];
+    auto fetch = [&](int c, uint32_t(&v)[SETS][W]) {
+#pragma unroll
+        for (int i = 0; i < SETS; ++i)
+            tmem_ld_cols<W>(at + i * half + c, v[i]);
+    };
+    auto add = [&](int c, const uint32_t(&v)[SETS][W]) {
+        add_weights<F8, SETS, MASKED, W>(v, neg + c / 4, fac + (F8 ? c / 4 : 0), scale_log2,
+                                         first - c, sum);
+    };
+    fetch(0, x);
 #pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
+    for (int c = 0; c < cols; c += 2 * W) {
         tmem_wait_ld();
-        if (c + 16 < cols) {
-            tmem_ld16(at + c + 16, y[0]);
-            if constexpr (SETS == 2)
-                tmem_ld16(at + half + c + 16, y[1]);
-        }
-        add_weights<F8, SETS, MASKED>(x, neg + c / 4, fac + (F8 ? c / 4 : 0), scale_log2, first - c,
-                                      sum);
-        if (c + 16 < cols) {
+        if (c + W < cols)
+            fetch(c + W, y);
+        add(c, x);
+        if (c + W < cols) {
             tmem_wait_ld();
-            if (c + 32 < cols) {
-                tmem_ld16(at + c + 32, x[0]);
-                if constexpr (SETS == 2)
-                    tmem_ld16(at + half + c + 32, x[1]);
-            }
-            add_weights<F8, SETS, MASKED>(y, neg + c / 4 + 4, fac + (F8 ? c / 4 + 4 : 0),
-                                          scale_log2, first - c - 16, sum);
+            if (c + 2 * W < cols)
+                fetch(c + 2 * W, x);
+            add(c + W, y);
         }
     }
 }
 
 // CG = CTAs of a worker (1, or a pair); QRES = queries resident, tiles streaming.
 // half = query rows per CTA of one MMA (N / CG) when QRES.
-template <bool F8, int CG, bool QRES>
+template <bool F8, int CG, bool QRES, int SETS>
 __global__ void __launch_bounds__(kMassThreads, 1)
 mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_qn,
             const __grid_constant__ CUtensorMap tm_qr, const MassArgs a, const int half,
@@ -189,14 +206,15 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     using F = MassFmt<F8>;
     constexpr int kSpan = kTile * CG;                         // tokens of a worker's step
     constexpr int kWidth = kMassChunk * CG;                   // query rows of a chunk, at most
-    // One CTA keeps two column sets that the epilogue adds: the scores of the query's
-    // hi and lo part (E4M3; one MMA of N = 2 rows), or of the even and the odd column
-    // blocks (bf16; shorter accumulation chains lose less).
-    constexpr int kSets = CG == 1 ? 2 : 1;
+    // One CTA keeps SETS column sets that the epilogue adds: the scores of the query's
+    // hi and lo part (E4M3; one MMA of N = 2 rows), or of every SETS'th column block
+    // (bf16).  The tensor core's fp32 accumulator truncates, so a score of 36 MMAs in one
+    // chain loses more than fp32 arithmetic would: weights off by 1.7e-6 (2-norm) with
+    // one chain, 8.7e-7 with two and less with four, at no cost in time.
     constexpr int kParts = F8 && CG == 2 ? 2 : 1;             // MMAs per K step, one a query part
-    constexpr int kBufCols = kWidth * kSets;
+    constexpr int kBufCols = kMassCols / 2;
     constexpr int kBufs = 2;
-    static_assert(kBufs * kBufCols == kMassCols, "TMEM columns");
+    static_assert(CG == 1 || SETS == 1, "column sets");
 
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t s_res = smem_u32(smem);                    // resident operand
@@ -530,8 +548,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 else if constexpr (F8)
                                     mma_e4m3(d, da + 2 * kk, db + 2 * kk, idesc, (k | kk) != 0);
                                 else
-                                    mma_bf16(d + (k & 1) * half, da + 2 * kk, db + 2 * kk, idesc,
-                                             (k >> 1 | kk) != 0);
+                                    mma_bf16(d + k % SETS * half, da + 2 * kk, db + 2 * kk, idesc,
+                                             (k / SETS | kk) != 0);
                             }
                         issued = true;
                         if (!QRES || p == kParts - 1) {
@@ -622,9 +640,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
                 const uint32_t at = taddr + kBufCols * buf;
                 if (visible)
-                    sum_columns<F8, kSets, false>(at, half, cols, neg, fac, scale_log2, 0, sum);
+                    sum_columns<F8, SETS, false>(at, half, cols, neg, fac, scale_log2, 0, sum);
                 else
-                    sum_columns<F8, kSets, true>(at, half, cols, neg, fac, scale_log2,
+                    sum_columns<F8, SETS, true>(at, half, cols, neg, fac, scale_log2,
                                                  first_row - row0, sum);
                 tc_fence_before();
                 __syncwarp();
@@ -668,7 +686,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         atomicExch(a.status, m.status);
 }
 
-template <bool F8, int CG, bool QRES>
+template <bool F8, int CG, bool QRES, int SETS>
 cudaError_t launch_mass_form(const MassArgs &a, int sms, cudaStream_t stream)
 {
     const CUtensorMapDataType dt = F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -703,7 +721,7 @@ cudaError_t launch_mass_form(const MassArgs &a, int sms, cudaStream_t stream)
     int slots = (kMassSmem - res - (int)sizeof(MassMisc<F8>)) / kMassSlot;
     slots = slots < kMassMaxSlots ? slots : kMassMaxSlots;
     const int smem = res + slots * kMassSlot + (int)sizeof(MassMisc<F8>);
-    cudaError_t err = cudaFuncSetAttribute(mass_kernel<F8, CG, QRES>,
+    cudaError_t err = cudaFuncSetAttribute(mass_kernel<F8, CG, QRES, SETS>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kMassSmem);
     if (err != cudaSuccess)
         return err;
@@ -722,16 +740,18 @@ cudaError_t launch_mass_form(const MassArgs &a, int sms, cudaStream_t stream)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = F8 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mass_kernel<F8, CG, QRES>, k, qn, qr, a, half, slots);
+    return cudaLaunchKernelEx(&cfg, mass_kernel<F8, CG, QRES, SETS>, k, qn, qr, a, half, slots);
 }
 
 template <bool F8>
 cudaError_t launch_mass_typed(const MassArgs &a, int sms, cudaStream_t stream)
 {
+    if (!F8 && a.rows <= kMassChunk / 2)
+        return launch_mass_form<F8, 1, true, F8 ? 2 : 4>(a, sms, stream);
     if (a.rows <= kMassChunk)
-        return launch_mass_form<F8, 1, true>(a, sms, stream);
-    return a.rows <= 2 * kMassChunk ? launch_mass_form<F8, 2, true>(a, sms, stream)
-                                    : launch_mass_form<F8, 2, false>(a, sms, stream);
+        return launch_mass_form<F8, 1, true, 2>(a, sms, stream);
+    return a.rows <= 2 * kMassChunk ? launch_mass_form<F8, 2, true, 1>(a, sms, stream)
+                                    : launch_mass_form<F8, 2, false, 1>(a, sms, stream);
 }
 
 }  // namespace
