@@ -230,16 +230,13 @@ __device__ __forceinline__ bool select_forced(const SelectArgs &a, int r, int me
     if (write && me == 0 && tid == 0)
         a.kept_lens[r] = min(L, a.keep);
     if (L <= a.keep) {
-        for (int i = me * NT + tid; i < L && write; i += parts * NT)
-            kept[i] = i;
+        for (uint32_t i = me * NT + tid; i < (uint32_t)L && write; i += parts * NT)
+            kept[i] = (int32_t)i;
         return false;
     }
-    for (int i = me * NT + tid; i < a.sink + a.recent && write; i += parts * NT) {
-        if (i < a.sink)
-            kept[i] = i;
-        else
-            kept[a.keep - a.recent + (i - a.sink)] = L - a.recent + (i - a.sink);
-    }
+    const uint32_t sink = a.sink, ends = sink + a.recent;
+    for (uint32_t i = me * NT + tid; i < ends && write; i += parts * NT)
+        kept[i < sink ? i : a.keep - ends + i] = (int32_t)(i < sink ? i : L - ends + i);
     return a.keep > a.sink + a.recent;
 }
 
@@ -678,10 +675,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
     constexpr int rows = 32 * kCompactVecs / row_vecs;           // rows per warp: 4 or 8
     const int lane = threadIdx.x & 31;
     const int r = blockIdx.y;
-    const int i0 = (blockIdx.x * (kCompactThreads / 32) + (threadIdx.x >> 5)) * rows;
+    const int64_t start = ((int64_t)blockIdx.x * (kCompactThreads / 32) + (threadIdx.x >> 5)) * rows;
     const int n = min(a.keep, a.kept_lens[r]);
-    if (i0 >= n)
+    if (start >= n)
         return;
+    const int i0 = (int)start;
     unsigned char *slab = static_cast<unsigned char *>(a.slab[blockIdx.z]);
     int64_t src = -1, dst = -1;                                  // lane i: row i0 + i
     if (lane < rows && i0 + lane < n) {
@@ -876,7 +874,7 @@ cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t
         a.mass_out = mass_out;
         a.mass_out_ld = mass_out_ld;
         a.status = status;
-        const dim3 grid((unsigned)((keep + per_block - 1) / per_block), (unsigned)num_reqs,
+        const dim3 grid((unsigned)(((int64_t)keep + per_block - 1) / per_block), (unsigned)num_reqs,
                         (unsigned)n);
         if (fp8)
             compact_kernel<true><<<grid, kCompactThreads, 0, stream>>>(a);

@@ -210,7 +210,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     // hi and lo part (E4M3; one MMA of N = 2 rows), or of every SETS'th column block
     // (bf16).  The tensor core's fp32 accumulator truncates, so a score of 36 MMAs in one
     // chain loses more than fp32 arithmetic would: weights off by 1.7e-6 (2-norm) with
-    // one chain, 8.7e-7 with two and less with four, at no cost in time.
+    // one chain, 8.7e-7 with two and 4.7e-7, as in fp32 arithmetic, with four, at no cost in
+    // time.
     constexpr int kParts = F8 && CG == 2 ? 2 : 1;             // MMAs per K step, one a query part
     constexpr int kBufCols = kMassCols / 2;
     constexpr int kBufs = 2;
