@@ -578,6 +578,10 @@ class RopeTable:
     2^-64 turns per position; `magnitude` scales the rotated pairs."""
 
     def __init__(self, turns, magnitude):
+        if not (turns.dtype is torch.int64 and turns.dim() == 1 and turns.is_contiguous()):
+            _fail("turns must be a contiguous int64 tensor [dim / 2]")
+        if not math.isfinite(magnitude):
+            _fail("magnitude must be finite")
         self.turns, self.magnitude, self.dim = turns, float(magnitude), 2 * turns.numel()
 
     def address(self, dev, dim):
@@ -605,8 +609,6 @@ def rope_table(dim=ROPE, *, base=10000.0, scaling="none", factor=1.0, original_l
         _fail(f"invalid rotary table: {_native.strerror(status)}")
     if magnitude is None:
         magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "by_parts" else 1.0
-    if not math.isfinite(magnitude):
-        _fail("magnitude must be finite")
     return RopeTable(host.to(device or "cuda"), magnitude)
 
 

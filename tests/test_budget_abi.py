@@ -72,6 +72,17 @@ def test_rope_table_refusals():
     assert table.dim == 32 and abs(table.magnitude - 1.1) < 1e-12
 
 
+@pytest.mark.parametrize("turns,magnitude", [
+    (torch.zeros(32), 1.0), (torch.zeros(32, dtype=torch.int32), 1.0),
+    (torch.zeros(64, dtype=torch.int64)[::2], 1.0),
+    (torch.zeros(4, 8, dtype=torch.int64), 1.0),
+    (torch.zeros(32, dtype=torch.int64), math.nan)])
+def test_rope_tables_of_other_forms_are_refused(turns, magnitude):
+    """The kernels read dim / 2 consecutive 64-bit values."""
+    with pytest.raises(ValueError):
+        api.RopeTable(turns, magnitude)
+
+
 def test_rope_arguments(lib):
     base = dict(x=FAKE, ts=64, hs=64, pos=FAKE, turns=FAKE, mag=1.0, T=2, H=1, dim=64, dt=0,
                 layout=0, inv=0, out=2 * FAKE, ots=64, ohs=64)
