@@ -669,7 +669,8 @@ plmla_status mla_kv_append_rope_fp8(const void *latent_new, const void *rope_new
  *
  * lse          fp32 [num_reqs * n_q, num_heads], natural log
  * mass         fp32, row r at mass + r * mass_ld, of mass_cols columns (mass_cols
- *              <= mass_ld, so that a view of a wider buffer works)
+ *              <= mass_ld, so that a view of a wider buffer works); the column of a
+ *              token that is new in its history must hold 0 (unless decay is 0)
  * decay        finite; 0 overwrites (the old values are not read)
  * status       optional device int32, as in mla_kv_append: set to 33 if a history
  *              needs a page column past page_table_ld or a page ID outside the
@@ -751,7 +752,9 @@ plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_c
  * mass         NULL, or fp32 rows of mass_cols columns (row stride mass_ld) whose
  *              kept entries are copied to mass_out[r, i] (row stride mass_out_ld >=
  *              kept_cols); the two must not overlap.  An index past mass_cols
- *              leaves its mass_out entry as it is.
+ *              leaves its mass_out entry as it is, and so do the entries from
+ *              kept_lens[r] on: they have to be 0 before mla_attention_mass adds the
+ *              weights of the tokens appended there.
  * status       optional device int32, as in mla_kv_append: set to 33 if an index or
  *              a page is out of range; such rows are skipped
  */

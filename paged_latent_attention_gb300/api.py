@@ -740,7 +740,8 @@ def mla_attention_mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens,
                        scale=DEFAULT_SCALE, decay=1.0, status=None, stream=None):
     """Adds to mass [R, tokens] fp32 the attention weight that this step's query
     rows gave every cached token (decay * mass + the sum over drafts and heads);
-    returns mass.  The queries, pool and histories are mla_decode's, ``lse`` is
+    returns mass.  The entry of a token that is new in its history must hold 0: make
+    mass with zeros, as wide as the histories may become.  The queries, pool and histories are mla_decode's, ``lse`` is
     what it returned.  Layers that share a page table accumulate into one mass, a
     call each; ``decay`` 0 overwrites.  ``status``: optional CUDA int32 tensor of
     one element that the kernel sets to 33 or 34 where a history leaves the page
@@ -843,8 +844,10 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
     every layer's pool in ``slabs`` (bf16, or uint8 / float8_e4m3fn), into the
     fresh pages of out_table [R, columns]: row i of the new history is token
     kept[r, i].  The fresh pages must be distinct and none of those read.  ``mass``
-    rows are carried into ``mass_out`` (a new [R, kept columns] tensor by default);
-    returns mass_out (None without mass).  ``status``: optional CUDA int32 tensor
+    rows are carried into ``mass_out`` (by default a new tensor as wide as mass, so
+    that the histories can grow again, with zeros where the next tokens' weights
+    come; in a given one those entries stay as they are and have to be 0); returns
+    mass_out (None without mass).  ``status``: optional CUDA int32 tensor
     of one element, set to 33 where an index or page is out of range (such rows are
     skipped).  The old pages are not changed.  Asynchronous."""
     if not isinstance(slabs, (list, tuple)) or not slabs:
@@ -874,7 +877,9 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
     else:
         weights = _rows(mass, "mass", dev, _F32, R)
         if mass_out is None:
-            mass_out = _empty((R, cols), _F32, mass.device, stream)
+            mass_out = _empty((R, max(cols, weights[2])), _F32, mass.device, stream)
+            with torch.cuda.stream(stream):
+                mass_out.zero_()
         dst, dst_ld, have = _rows(mass_out, "mass_out", dev, _F32, R)
         if have < cols:
             _fail(f"mass_out needs {cols} columns")
