@@ -497,11 +497,14 @@ def _launch(dev, fn, where, stream, *args):
 
 
 def _empty(shape, dtype, device, stream):
-    """New memory for a call on `stream`: the allocator keeps it from other streams'
-    tensors until that stream has passed the call."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """New memory for a call on `stream`.  It comes from that stream's own blocks: one of
+    the current stream's may still be in use there by work queued before it was freed.
+    Once freed, the allocator keeps it until the caller's stream has passed too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
