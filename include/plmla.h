@@ -634,6 +634,10 @@ plmla_status mla_rope(const void *x, int64_t tok_stride, int64_t head_stride,
  *              overlap q.
  * Other arguments, the skipped rows, the status word and errors as mla_kv_append.
  * The rotated key is computed in fp32 and rounded once.
+ *
+ * mla_kv_append_rope_ex is the same for a page table whose rows have page_table_cols
+ * (1 .. page_table_ld) entries, fewer than its row stride: a view of a wider buffer.
+ * Positions past those columns are skipped and reported as past page_table_ld above.
  */
 plmla_status mla_kv_append_rope(const void *latent_new, const void *rope_new, void *slab_base,
                                 int64_t num_pages, int64_t page_stride_elems,
@@ -644,8 +648,18 @@ plmla_status mla_kv_append_rope(const void *latent_new, const void *rope_new, vo
                                 int64_t q_head_stride, int32_t num_heads, void *q_out,
                                 int32_t *status, void *stream);
 
-/* mla_kv_append_rope into E4M3 pages (see mla_kv_append_fp8): the rotated fp32
- * value is divided by kv_scale and rounded once, to E4M3. */
+plmla_status mla_kv_append_rope_ex(const void *latent_new, const void *rope_new, void *slab_base,
+                                   int64_t num_pages, int64_t page_stride_elems,
+                                   const int32_t *page_table, int64_t page_table_ld,
+                                   int64_t page_table_cols, const int32_t *seq_lens,
+                                   int32_t num_reqs, int32_t n_new, const int32_t *positions,
+                                   const uint64_t *turns, float magnitude, int32_t layout,
+                                   const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+                                   int32_t num_heads, void *q_out, int32_t *status, void *stream);
+
+/* mla_kv_append_rope and mla_kv_append_rope_ex into E4M3 pages (see
+ * mla_kv_append_fp8): the rotated fp32 value is divided by kv_scale and rounded
+ * once, to E4M3. */
 plmla_status mla_kv_append_rope_fp8(const void *latent_new, const void *rope_new, void *slab_base,
                                     int64_t num_pages, int64_t page_stride_elems, float kv_scale,
                                     const int32_t *page_table, int64_t page_table_ld,
@@ -654,6 +668,16 @@ plmla_status mla_kv_append_rope_fp8(const void *latent_new, const void *rope_new
                                     float magnitude, int32_t layout, const void *q,
                                     int64_t q_tok_stride, int64_t q_head_stride, int32_t num_heads,
                                     void *q_out, int32_t *status, void *stream);
+plmla_status mla_kv_append_rope_fp8_ex(const void *latent_new, const void *rope_new,
+                                       void *slab_base, int64_t num_pages,
+                                       int64_t page_stride_elems, float kv_scale,
+                                       const int32_t *page_table, int64_t page_table_ld,
+                                       int64_t page_table_cols, const int32_t *seq_lens,
+                                       int32_t num_reqs, int32_t n_new, const int32_t *positions,
+                                       const uint64_t *turns, float magnitude, int32_t layout,
+                                       const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+                                       int32_t num_heads, void *q_out, int32_t *status,
+                                       void *stream);
 
 /*
  * mla_attention_mass -- add to every cached token the attention weight that this
@@ -680,6 +704,10 @@ plmla_status mla_kv_append_rope_fp8(const void *latent_new, const void *rope_new
  * Other arguments as in mla_decode (num_reqs 1 .. 1024, n_q 1 .. 256, num_heads a
  * multiple of 16 up to 128).  One kernel; no atomics: the same inputs give the
  * same bits.
+ *
+ * mla_attention_mass_ex is the same for a page table whose rows have page_table_cols
+ * (1 .. page_table_ld) entries, fewer than its row stride: tokens past those columns
+ * are reported with 33 and left as they are.
  */
 plmla_status mla_attention_mass(const void *q_nope_absorbed, const void *q_rope, const float *lse,
                                 const void *slab_base, int64_t num_pages,
@@ -688,6 +716,14 @@ plmla_status mla_attention_mass(const void *q_nope_absorbed, const void *q_rope,
                                 int32_t n_q_per_req, int32_t num_heads, float scale, float decay,
                                 float *mass, int64_t mass_ld, int64_t mass_cols, int32_t *status,
                                 void *stream);
+plmla_status mla_attention_mass_ex(const void *q_nope_absorbed, const void *q_rope,
+                                   const float *lse, const void *slab_base, int64_t num_pages,
+                                   int64_t page_stride_elems, const int32_t *page_table,
+                                   int64_t page_table_ld, int64_t page_table_cols,
+                                   const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req,
+                                   int32_t num_heads, float scale, float decay, float *mass,
+                                   int64_t mass_ld, int64_t mass_cols, int32_t *status,
+                                   void *stream);
 
 /*
  * mla_attention_mass_fp8 -- mla_attention_mass over E4M3 pages (see
@@ -704,6 +740,15 @@ plmla_status mla_attention_mass_fp8(const void *q_nope_absorbed, const void *q_r
                                     int32_t num_heads, float scale, float decay, float *mass,
                                     int64_t mass_ld, int64_t mass_cols, void *workspace,
                                     size_t workspace_bytes, int32_t *status, void *stream);
+plmla_status mla_attention_mass_fp8_ex(const void *q_nope_absorbed, const void *q_rope,
+                                       const float *lse, const void *slab_base, int64_t num_pages,
+                                       int64_t page_stride_elems, float kv_scale,
+                                       const int32_t *page_table, int64_t page_table_ld,
+                                       int64_t page_table_cols, const int32_t *seq_lens,
+                                       int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads,
+                                       float scale, float decay, float *mass, int64_t mass_ld,
+                                       int64_t mass_cols, void *workspace, size_t workspace_bytes,
+                                       int32_t *status, void *stream);
 
 /*
  * mla_evict_select -- the tokens of each history that stay within a budget: the
@@ -757,6 +802,10 @@ plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_c
  *              weights of the tokens appended there.
  * status       optional device int32, as in mla_kv_append: set to 33 if an index or
  *              a page is out of range; such rows are skipped
+ *
+ * mla_kv_compact_ex is the same for tables whose rows have page_table_cols (1 ..
+ * page_table_ld) and out_table_cols (1 .. out_table_ld) entries, fewer than their
+ * row strides: rows that need a page past those columns are skipped and reported.
  */
 plmla_status mla_kv_compact(int32_t num_layers, void *const *slab_base, int32_t elem_bytes,
                             int64_t num_pages, int64_t page_stride_elems,
@@ -766,6 +815,16 @@ plmla_status mla_kv_compact(int32_t num_layers, void *const *slab_base, int32_t 
                             const int32_t *kept_lens, int32_t num_reqs, int32_t kept_cols,
                             const float *mass, int64_t mass_ld, int64_t mass_cols,
                             float *mass_out, int64_t mass_out_ld, int32_t *status, void *stream);
+plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32_t elem_bytes,
+                               int64_t num_pages, int64_t page_stride_elems,
+                               const int32_t *page_table, int64_t page_table_ld,
+                               int64_t page_table_cols, const int32_t *seq_lens,
+                               const int32_t *out_table, int64_t out_table_ld,
+                               int64_t out_table_cols, const int32_t *kept, int64_t kept_ld,
+                               const int32_t *kept_lens, int32_t num_reqs, int32_t kept_cols,
+                               const float *mass, int64_t mass_ld, int64_t mass_cols,
+                               float *mass_out, int64_t mass_out_ld, int32_t *status,
+                               void *stream);
 
 #ifdef __cplusplus
 }

@@ -56,16 +56,30 @@ SIGNATURES = {
     "mla_kv_append_rope_fp8": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _f, _p, _i64, _p, _i32,
                                               _i32, _p, _p, _f, _i32, _p, _i64, _i64, _i32, _p,
                                               _p, _p]),
+    "mla_kv_append_rope_ex": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i32,
+                                             _i32, _p, _p, _f, _i32, _p, _i64, _i64, _i32, _p, _p,
+                                             _p]),
+    "mla_kv_append_rope_fp8_ex": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _f, _p, _i64, _i64, _p,
+                                                 _i32, _i32, _p, _p, _f, _i32, _p, _i64, _i64,
+                                                 _i32, _p, _p, _p]),
     "mla_attention_mass": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _p, _i64, _p, _i32, _i32,
                                           _i32, _f, _f, _p, _i64, _i64, _p, _p]),
+    "mla_attention_mass_ex": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i32,
+                                             _i32, _i32, _f, _f, _p, _i64, _i64, _p, _p]),
     "mla_mass_workspace_size_fp8": (_sz, [_i32, _i32, _i32]),
     "mla_attention_mass_fp8": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _f, _p, _i64, _p, _i32,
                                               _i32, _i32, _f, _f, _p, _i64, _i64, _p, _sz, _p, _p]),
+    "mla_attention_mass_fp8_ex": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _f, _p, _i64, _i64,
+                                                 _p, _i32, _i32, _i32, _f, _f, _p, _i64, _i64, _p,
+                                                 _sz, _p, _p]),
     "mla_evict_workspace_size": (_sz, [_i32, _i64]),
     "mla_evict_select": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _i64, _p,
                                         _p, _sz, _p]),
     "mla_kv_compact": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _p, _p, _i64, _p,
                                       _i64, _p, _i32, _i32, _p, _i64, _i64, _p, _i64, _p, _p]),
+    "mla_kv_compact_ex": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i64,
+                                         _i64, _p, _i64, _p, _i32, _i32, _p, _i64, _i64, _p, _i64,
+                                         _p, _p]),
     "mla_set_page_checks": (None, [_i32]),
     "mla_set_split_mode": (ctypes.c_int, [_i32]),
     "mla_get_split_mode": (_i32, []),

@@ -699,7 +699,7 @@ def _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table,
     lens = _vector(seq_lens, "seq_lens", dev, R)
     latent = _dense(latent_new, "latent_new", dev, (rows, LATENT))
     rope = _dense(rope_new, "rope_new", dev, (rows, ROPE))
-    ids, ids_ld, _ = _rows(page_table, "page_table", dev, _I32, R)
+    ids = _rows(page_table, "page_table", dev, _I32, R)
     at = None if positions is None else _vector(positions, "positions", dev, rows)
     q = (None, 0, 0, 0, None)
     if q_rope is None:
@@ -719,14 +719,14 @@ def _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table,
                 _check_apart(q_rope, q_out, "q_out must not overlap q_rope")
         if rows and shape[1]:
             q = (q_rope.data_ptr(), *_heads(q_rope), shape[1], q_out.data_ptr())
-    tail = (ids, ids_ld, lens, R, n_new, at, table.address(dev, ROPE), table.magnitude,
+    tail = (*ids, lens, R, n_new, at, table.address(dev, ROPE), table.magnitude,
             _layout(layout), *q, _flag(status, dev))
     lib = _native.lib()
     if kv_scale is not None:
-        _launch(dev, lib.mla_kv_append_rope_fp8, "mla_kv_append_rope_fp8", stream, latent, rope,
+        _launch(dev, lib.mla_kv_append_rope_fp8_ex, "mla_kv_append_rope_fp8", stream, latent, rope,
                 base, pages, page_stride, kv_scale, *tail)
     else:
-        _launch(dev, lib.mla_kv_append_rope, "mla_kv_append_rope", stream, latent, rope, base,
+        _launch(dev, lib.mla_kv_append_rope_ex, "mla_kv_append_rope", stream, latent, rope, base,
                 pages, page_stride, *tail)
     return q_out
 
@@ -774,23 +774,23 @@ def _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, s
     qn = _dense(q_nope_absorbed, "q_nope_absorbed", dev, (T, H, LATENT))
     qr = _dense(q_rope, "q_rope", dev, (T, H, ROPE))
     l = _dense(lse, "lse", dev, (T, H), _F32)
-    ids, ids_ld, _ = _rows(page_table, "page_table", dev, _I32, R)
+    ids = _rows(page_table, "page_table", dev, _I32, R)
     lens = _vector(seq_lens, "seq_lens", dev, R)
     out = _rows(mass, "mass", dev, _F32, R)
     flag = _flag(status, dev)
     lib = _native.lib()
-    tail = (ids, ids_ld, lens, R, n_q, H, float(scale), float(decay), *out)
+    tail = (*ids, lens, R, n_q, H, float(scale), float(decay), *out)
     if kv_scale is None:
-        _launch(dev, lib.mla_attention_mass, "mla_attention_mass", stream, qn, qr, l, base, pages,
-                page_stride, *tail, flag)
+        _launch(dev, lib.mla_attention_mass_ex, "mla_attention_mass", stream, qn, qr, l, base,
+                pages, page_stride, *tail, flag)
     else:
         if workspace is None:
             size = lib.mla_mass_workspace_size_fp8(R, n_q, H)
             workspace = _empty(size, _U8, slab.device, stream)
         if workspace.get_device() != dev or not workspace.is_contiguous():
             _fail(f"workspace must be contiguous memory on cuda:{dev}")
-        _launch(dev, lib.mla_attention_mass_fp8, "mla_attention_mass_fp8", stream, qn, qr, l, base,
-                pages, page_stride, kv_scale, *tail, workspace.data_ptr(),
+        _launch(dev, lib.mla_attention_mass_fp8_ex, "mla_attention_mass_fp8", stream, qn, qr, l,
+                base, pages, page_stride, kv_scale, *tail, workspace.data_ptr(),
                 workspace.numel() * workspace.element_size(), flag)
     return mass
 
@@ -871,8 +871,8 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
         _fail("kept must be [R, columns]")
     R = kept.shape[0]
     idx, idx_ld, cols = _rows(kept, "kept", dev, _I32, R)
-    ids, ids_ld, _ = _rows(page_table, "page_table", dev, _I32, R)
-    outs, outs_ld, _ = _rows(out_table, "out_table", dev, _I32, R)
+    ids = _rows(page_table, "page_table", dev, _I32, R)
+    outs = _rows(out_table, "out_table", dev, _I32, R)
     carried = (None, 0, 0, None, 0)
     if mass is None:
         if mass_out is not None:
@@ -888,8 +888,8 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
             _fail(f"mass_out needs {cols} columns")
         _check_apart(mass, mass_out, "mass_out must not overlap mass")
         carried = (*weights, dst, dst_ld)
-    _launch(dev, _native.lib().mla_kv_compact, "mla_kv_compact", stream, layers, bases,
-            1 if fp8 else 2, pages, page_stride, ids, ids_ld,
-            _vector(seq_lens, "seq_lens", dev, R), outs, outs_ld, idx, idx_ld,
+    _launch(dev, _native.lib().mla_kv_compact_ex, "mla_kv_compact", stream, layers, bases,
+            1 if fp8 else 2, pages, page_stride, *ids,
+            _vector(seq_lens, "seq_lens", dev, R), *outs, idx, idx_ld,
             _vector(kept_lens, "kept_lens", dev, R), R, cols, *carried, _flag(status, dev))
     return mass_out

@@ -748,8 +748,8 @@ namespace {
 plmla_status append_rope_impl(const void *latent_new, const void *rope_new, void *slab_base,
                               bool fp8, int64_t num_pages, int64_t page_stride_elems,
                               float kv_scale, const int32_t *page_table, int64_t page_table_ld,
-                              const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
-                              const int32_t *positions, const uint64_t *turns, float magnitude,
+                              int64_t page_table_cols, const int32_t *seq_lens, int32_t num_reqs,
+                              int32_t n_new, const int32_t *positions, const uint64_t *turns, float magnitude,
                               int32_t layout, const void *q, int64_t q_tok_stride,
                               int64_t q_head_stride, int32_t num_heads, void *q_out,
                               int32_t *status, void *stream)
@@ -767,7 +767,8 @@ plmla_status append_rope_impl(const void *latent_new, const void *rope_new, void
         (positions != nullptr && !aligned(positions, 4)) ||
         (status != nullptr && !aligned(status, 4)))
         return PLMLA_INVALID_ARGUMENT;
-    if (num_pages < 1 || page_table_ld < 1 || page_stride_elems < (int64_t)kPageTokens * kRow ||
+    if (num_pages < 1 || page_table_cols < 1 || page_table_ld < page_table_cols ||
+        page_stride_elems < (int64_t)kPageTokens * kRow ||
         page_stride_elems % (fp8 ? 16 : 8) != 0 || !(isfinite(kv_scale) && kv_scale > 0.f))
         return PLMLA_INVALID_ARGUMENT;
     if (q != nullptr && (q_out == nullptr || q_out == q || num_heads < 1 ||
@@ -780,13 +781,27 @@ plmla_status append_rope_impl(const void *latent_new, const void *rope_new, void
                         (int64_t)num_reqs * n_new, q != nullptr ? num_heads : 0, kRope};
     const cudaError_t err = launch_append_rope(latent_new, rope_new, slab_base, fp8, num_pages,
                                                page_stride_elems, kv_scale, page_table,
-                                               page_table_ld, seq_lens, num_reqs, n_new, positions,
-                                               turns, magnitude, layout, v, status, sms,
-                                               static_cast<cudaStream_t>(stream));
+                                               page_table_ld, page_table_cols, seq_lens, num_reqs,
+                                               n_new, positions, turns, magnitude, layout, v,
+                                               status, sms, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
 }
 
 }  // namespace
+
+extern "C" plmla_status mla_kv_append_rope_ex(
+    const void *latent_new, const void *rope_new, void *slab_base, int64_t num_pages,
+    int64_t page_stride_elems, const int32_t *page_table, int64_t page_table_ld,
+    int64_t page_table_cols, const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+    const int32_t *positions, const uint64_t *turns, float magnitude, int32_t layout, const void *q,
+    int64_t q_tok_stride, int64_t q_head_stride, int32_t num_heads, void *q_out, int32_t *status,
+    void *stream)
+{
+    return append_rope_impl(latent_new, rope_new, slab_base, false, num_pages, page_stride_elems,
+                            1.f, page_table, page_table_ld, page_table_cols, seq_lens, num_reqs,
+                            n_new, positions, turns, magnitude, layout, q, q_tok_stride,
+                            q_head_stride, num_heads, q_out, status, stream);
+}
 
 extern "C" plmla_status mla_kv_append_rope(
     const void *latent_new, const void *rope_new, void *slab_base, int64_t num_pages,
@@ -795,10 +810,24 @@ extern "C" plmla_status mla_kv_append_rope(
     const uint64_t *turns, float magnitude, int32_t layout, const void *q, int64_t q_tok_stride,
     int64_t q_head_stride, int32_t num_heads, void *q_out, int32_t *status, void *stream)
 {
-    return append_rope_impl(latent_new, rope_new, slab_base, false, num_pages, page_stride_elems,
-                            1.f, page_table, page_table_ld, seq_lens, num_reqs, n_new, positions,
-                            turns, magnitude, layout, q, q_tok_stride, q_head_stride, num_heads,
-                            q_out, status, stream);
+    return mla_kv_append_rope_ex(latent_new, rope_new, slab_base, num_pages, page_stride_elems,
+                                 page_table, page_table_ld, page_table_ld, seq_lens, num_reqs,
+                                 n_new, positions, turns, magnitude, layout, q, q_tok_stride,
+                                 q_head_stride, num_heads, q_out, status, stream);
+}
+
+extern "C" plmla_status mla_kv_append_rope_fp8_ex(
+    const void *latent_new, const void *rope_new, void *slab_base, int64_t num_pages,
+    int64_t page_stride_elems, float kv_scale, const int32_t *page_table, int64_t page_table_ld,
+    int64_t page_table_cols, const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+    const int32_t *positions, const uint64_t *turns, float magnitude, int32_t layout, const void *q,
+    int64_t q_tok_stride, int64_t q_head_stride, int32_t num_heads, void *q_out, int32_t *status,
+    void *stream)
+{
+    return append_rope_impl(latent_new, rope_new, slab_base, true, num_pages, page_stride_elems,
+                            kv_scale, page_table, page_table_ld, page_table_cols, seq_lens,
+                            num_reqs, n_new, positions, turns, magnitude, layout, q, q_tok_stride,
+                            q_head_stride, num_heads, q_out, status, stream);
 }
 
 extern "C" plmla_status mla_kv_append_rope_fp8(
@@ -808,10 +837,10 @@ extern "C" plmla_status mla_kv_append_rope_fp8(
     const uint64_t *turns, float magnitude, int32_t layout, const void *q, int64_t q_tok_stride,
     int64_t q_head_stride, int32_t num_heads, void *q_out, int32_t *status, void *stream)
 {
-    return append_rope_impl(latent_new, rope_new, slab_base, true, num_pages, page_stride_elems,
-                            kv_scale, page_table, page_table_ld, seq_lens, num_reqs, n_new,
-                            positions, turns, magnitude, layout, q, q_tok_stride, q_head_stride,
-                            num_heads, q_out, status, stream);
+    return mla_kv_append_rope_fp8_ex(latent_new, rope_new, slab_base, num_pages, page_stride_elems,
+                                     kv_scale, page_table, page_table_ld, page_table_ld, seq_lens,
+                                     num_reqs, n_new, positions, turns, magnitude, layout, q,
+                                     q_tok_stride, q_head_stride, num_heads, q_out, status, stream);
 }
 
 namespace {
@@ -819,16 +848,17 @@ namespace {
 plmla_status mass_impl(const void *q_nope_absorbed, const void *q_rope, const float *lse,
                        const void *slab_base, bool fp8, int64_t num_pages,
                        int64_t page_stride_elems, float kv_scale, const int32_t *page_table,
-                       int64_t page_table_ld, const int32_t *seq_lens, int32_t num_reqs,
-                       int32_t n_q_per_req, int32_t num_heads, float scale, float decay,
-                       float *mass, int64_t mass_ld, int64_t mass_cols, void *workspace,
-                       size_t workspace_bytes, int32_t *status, void *stream)
+                       int64_t page_table_ld, int64_t page_table_cols, const int32_t *seq_lens,
+                       int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads, float scale,
+                       float decay, float *mass, int64_t mass_ld, int64_t mass_cols,
+                       void *workspace, size_t workspace_bytes, int32_t *status, void *stream)
 {
     if (q_nope_absorbed == nullptr || q_rope == nullptr || lse == nullptr ||
         slab_base == nullptr || page_table == nullptr || seq_lens == nullptr || mass == nullptr)
         return PLMLA_INVALID_ARGUMENT;
     if (!shape_ok(num_reqs, n_q_per_req, num_heads) || num_pages < 1 || num_pages > INT32_MAX ||
-        page_table_ld < 1 || mass_cols < 1 || mass_ld < mass_cols ||
+        page_table_cols < 1 || page_table_ld < page_table_cols || mass_cols < 1 ||
+        mass_ld < mass_cols ||
         page_stride_elems < (int64_t)kPageTokens * kRow ||
         page_stride_elems % (fp8 ? 16 : 8) != 0 || !isfinite(scale) || !isfinite(decay) ||
         !(isfinite(kv_scale) && kv_scale > 0.f))
@@ -843,6 +873,7 @@ plmla_status mass_impl(const void *q_nope_absorbed, const void *q_rope, const fl
     a.page_stride = page_stride_elems;
     a.page_table = page_table;
     a.table_ld = page_table_ld;
+    a.table_cols = page_table_cols;
     a.seq_lens = seq_lens;
     a.num_reqs = num_reqs;
     a.n_q = n_q_per_req;
@@ -888,15 +919,42 @@ extern "C" size_t mla_mass_workspace_size_fp8(int32_t num_reqs, int32_t n_q, int
     return align_up(2 * (size_t)kRow * rows) + align_up(sizeof(int32_t) * rows);
 }
 
+extern "C" plmla_status mla_attention_mass_ex(
+    const void *q_nope_absorbed, const void *q_rope, const float *lse, const void *slab_base,
+    int64_t num_pages, int64_t page_stride_elems, const int32_t *page_table, int64_t page_table_ld,
+    int64_t page_table_cols, const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req,
+    int32_t num_heads, float scale, float decay, float *mass, int64_t mass_ld, int64_t mass_cols,
+    int32_t *status, void *stream)
+{
+    return mass_impl(q_nope_absorbed, q_rope, lse, slab_base, false, num_pages, page_stride_elems,
+                     1.f, page_table, page_table_ld, page_table_cols, seq_lens, num_reqs,
+                     n_q_per_req, num_heads, scale, decay, mass, mass_ld, mass_cols, nullptr, 0,
+                     status, stream);
+}
+
 extern "C" plmla_status mla_attention_mass(
     const void *q_nope_absorbed, const void *q_rope, const float *lse, const void *slab_base,
     int64_t num_pages, int64_t page_stride_elems, const int32_t *page_table, int64_t page_table_ld,
     const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads, float scale,
     float decay, float *mass, int64_t mass_ld, int64_t mass_cols, int32_t *status, void *stream)
 {
-    return mass_impl(q_nope_absorbed, q_rope, lse, slab_base, false, num_pages, page_stride_elems,
-                     1.f, page_table, page_table_ld, seq_lens, num_reqs, n_q_per_req, num_heads,
-                     scale, decay, mass, mass_ld, mass_cols, nullptr, 0, status, stream);
+    return mla_attention_mass_ex(q_nope_absorbed, q_rope, lse, slab_base, num_pages,
+                                 page_stride_elems, page_table, page_table_ld, page_table_ld,
+                                 seq_lens, num_reqs, n_q_per_req, num_heads, scale, decay, mass,
+                                 mass_ld, mass_cols, status, stream);
+}
+
+extern "C" plmla_status mla_attention_mass_fp8_ex(
+    const void *q_nope_absorbed, const void *q_rope, const float *lse, const void *slab_base,
+    int64_t num_pages, int64_t page_stride_elems, float kv_scale, const int32_t *page_table,
+    int64_t page_table_ld, int64_t page_table_cols, const int32_t *seq_lens, int32_t num_reqs,
+    int32_t n_q_per_req, int32_t num_heads, float scale, float decay, float *mass, int64_t mass_ld,
+    int64_t mass_cols, void *workspace, size_t workspace_bytes, int32_t *status, void *stream)
+{
+    return mass_impl(q_nope_absorbed, q_rope, lse, slab_base, true, num_pages, page_stride_elems,
+                     kv_scale, page_table, page_table_ld, page_table_cols, seq_lens, num_reqs,
+                     n_q_per_req, num_heads, scale, decay, mass, mass_ld, mass_cols, workspace,
+                     workspace_bytes, status, stream);
 }
 
 extern "C" plmla_status mla_attention_mass_fp8(
@@ -906,10 +964,11 @@ extern "C" plmla_status mla_attention_mass_fp8(
     int32_t num_heads, float scale, float decay, float *mass, int64_t mass_ld, int64_t mass_cols,
     void *workspace, size_t workspace_bytes, int32_t *status, void *stream)
 {
-    return mass_impl(q_nope_absorbed, q_rope, lse, slab_base, true, num_pages, page_stride_elems,
-                     kv_scale, page_table, page_table_ld, seq_lens, num_reqs, n_q_per_req,
-                     num_heads, scale, decay, mass, mass_ld, mass_cols, workspace, workspace_bytes,
-                     status, stream);
+    return mla_attention_mass_fp8_ex(q_nope_absorbed, q_rope, lse, slab_base, num_pages,
+                                     page_stride_elems, kv_scale, page_table, page_table_ld,
+                                     page_table_ld, seq_lens, num_reqs, n_q_per_req, num_heads,
+                                     scale, decay, mass, mass_ld, mass_cols, workspace,
+                                     workspace_bytes, status, stream);
 }
 
 extern "C" size_t mla_evict_workspace_size(int32_t num_reqs, int64_t mass_cols)
@@ -945,22 +1004,21 @@ extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int
     return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
 }
 
-extern "C" plmla_status mla_kv_compact(int32_t num_layers, void *const *slab_base,
-                                       int32_t elem_bytes, int64_t num_pages,
-                                       int64_t page_stride_elems, const int32_t *page_table,
-                                       int64_t page_table_ld, const int32_t *seq_lens,
-                                       const int32_t *out_table, int64_t out_table_ld,
-                                       const int32_t *kept, int64_t kept_ld,
-                                       const int32_t *kept_lens, int32_t num_reqs,
-                                       int32_t kept_cols, const float *mass, int64_t mass_ld,
-                                       int64_t mass_cols, float *mass_out, int64_t mass_out_ld,
-                                       int32_t *status, void *stream)
+extern "C" plmla_status mla_kv_compact_ex(
+    int32_t num_layers, void *const *slab_base, int32_t elem_bytes, int64_t num_pages,
+    int64_t page_stride_elems, const int32_t *page_table, int64_t page_table_ld,
+    int64_t page_table_cols, const int32_t *seq_lens, const int32_t *out_table,
+    int64_t out_table_ld, int64_t out_table_cols, const int32_t *kept, int64_t kept_ld,
+    const int32_t *kept_lens, int32_t num_reqs, int32_t kept_cols, const float *mass,
+    int64_t mass_ld, int64_t mass_cols, float *mass_out, int64_t mass_out_ld, int32_t *status,
+    void *stream)
 {
     if (num_layers < 1 || num_layers > kMaxLayers || slab_base == nullptr ||
         (elem_bytes != 1 && elem_bytes != 2) || page_table == nullptr || seq_lens == nullptr ||
         out_table == nullptr || out_table == page_table || kept == nullptr ||
         kept_lens == nullptr || num_reqs < 1 || num_reqs > kMaxReqs || kept_cols < 0 ||
-        kept_ld < kept_cols || num_pages < 1 || page_table_ld < 1 || out_table_ld < 1 ||
+        kept_ld < kept_cols || num_pages < 1 || page_table_cols < 1 ||
+        page_table_ld < page_table_cols || out_table_cols < 1 || out_table_ld < out_table_cols ||
         page_stride_elems < (int64_t)kPageTokens * kRow ||
         page_stride_elems * elem_bytes % 16 != 0)
         return PLMLA_INVALID_ARGUMENT;
@@ -979,9 +1037,27 @@ extern "C" plmla_status mla_kv_compact(int32_t num_layers, void *const *slab_bas
         return PLMLA_OK;
     const cudaError_t err =
         launch_compact(num_layers, slab_base, elem_bytes == 1, num_pages,
-                       page_stride_elems * elem_bytes, page_table, page_table_ld, seq_lens,
-                       out_table, out_table_ld, kept, kept_ld, kept_lens, num_reqs, kept_cols, mass,
-                       mass_ld, mass_cols, mass_out, mass_out_ld, status,
+                       page_stride_elems * elem_bytes, page_table, page_table_ld, page_table_cols,
+                       seq_lens, out_table, out_table_ld, out_table_cols, kept, kept_ld, kept_lens,
+                       num_reqs, kept_cols, mass, mass_ld, mass_cols, mass_out, mass_out_ld, status,
                        static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
+}
+
+extern "C" plmla_status mla_kv_compact(int32_t num_layers, void *const *slab_base,
+                                       int32_t elem_bytes, int64_t num_pages,
+                                       int64_t page_stride_elems, const int32_t *page_table,
+                                       int64_t page_table_ld, const int32_t *seq_lens,
+                                       const int32_t *out_table, int64_t out_table_ld,
+                                       const int32_t *kept, int64_t kept_ld,
+                                       const int32_t *kept_lens, int32_t num_reqs,
+                                       int32_t kept_cols, const float *mass, int64_t mass_ld,
+                                       int64_t mass_cols, float *mass_out, int64_t mass_out_ld,
+                                       int32_t *status, void *stream)
+{
+    return mla_kv_compact_ex(num_layers, slab_base, elem_bytes, num_pages, page_stride_elems,
+                             page_table, page_table_ld, page_table_ld, seq_lens, out_table,
+                             out_table_ld, out_table_ld, kept, kept_ld, kept_lens, num_reqs,
+                             kept_cols, mass, mass_ld, mass_cols, mass_out, mass_out_ld, status,
+                             stream);
 }

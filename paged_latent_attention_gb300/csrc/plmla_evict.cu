@@ -653,10 +653,10 @@ struct CompactArgs {
     void *slab[kCompactLayers];
     int64_t num_pages, page_bytes;
     const int32_t *table;
-    int64_t table_ld;
+    int64_t table_ld, table_cols;
     const int32_t *seq_lens;
     const int32_t *out_table;
-    int64_t out_ld;
+    int64_t out_ld, out_cols;
     const int32_t *kept;
     int64_t kept_ld;
     const int32_t *kept_lens;
@@ -686,8 +686,8 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
         const int i = i0 + lane;
         const int t = a.kept[(int64_t)r * a.kept_ld + i];
         int from = -1, to = -1;
-        if (t >= 0 && t < a.seq_lens[r] && t / kPageTokens < a.table_ld &&
-            i / kPageTokens < a.out_ld) {
+        if (t >= 0 && t < a.seq_lens[r] && t / kPageTokens < a.table_cols &&
+            i / kPageTokens < a.out_cols) {
             from = a.table[(int64_t)r * a.table_ld + t / kPageTokens];
             to = a.out_table[(int64_t)r * a.out_ld + i / kPageTokens];
         }
@@ -845,11 +845,11 @@ cudaError_t launch_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
 
 cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t num_pages,
                            int64_t page_bytes, const int32_t *table, int64_t table_ld,
-                           const int32_t *seq_lens, const int32_t *out_table, int64_t out_ld,
-                           const int32_t *kept, int64_t kept_ld, const int32_t *kept_lens,
-                           int num_reqs, int keep, const float *mass, int64_t mass_ld,
-                           int64_t mass_cols, float *mass_out, int64_t mass_out_ld, int32_t *status,
-                           cudaStream_t stream)
+                           int64_t table_cols, const int32_t *seq_lens, const int32_t *out_table,
+                           int64_t out_ld, int64_t out_cols, const int32_t *kept, int64_t kept_ld,
+                           const int32_t *kept_lens, int num_reqs, int keep, const float *mass,
+                           int64_t mass_ld, int64_t mass_cols, float *mass_out,
+                           int64_t mass_out_ld, int32_t *status, cudaStream_t stream)
 {
     const int per_block = kCompactThreads / 32 * (32 * kCompactVecs / (fp8 ? 36 : 72));
     for (int l0 = 0; l0 < num_layers; l0 += kCompactLayers) {
@@ -861,9 +861,11 @@ cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t
         a.page_bytes = page_bytes;
         a.table = table;
         a.table_ld = table_ld;
+        a.table_cols = table_cols;
         a.seq_lens = seq_lens;
         a.out_table = out_table;
         a.out_ld = out_ld;
+        a.out_cols = out_cols;
         a.kept = kept;
         a.kept_ld = kept_ld;
         a.kept_lens = kept_lens;

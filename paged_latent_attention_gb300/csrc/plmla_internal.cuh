@@ -142,10 +142,11 @@ cudaError_t launch_rope(const RopeView &v, const int32_t *positions, const uint6
 // when v.heads is 0); positions may be null (the row's index in its history).
 cudaError_t launch_append_rope(const void *latent, const void *rope, void *slab, bool fp8,
                                int64_t num_pages, int64_t page_stride, float kv_scale,
-                               const int32_t *table, int64_t table_ld, const int32_t *seq_lens,
-                               int num_reqs, int n_new, const int32_t *positions,
-                               const uint64_t *turns, float magnitude, int interleaved,
-                               const RopeView &v, int32_t *status, int sms, cudaStream_t stream);
+                               const int32_t *table, int64_t table_ld, int64_t table_cols,
+                               const int32_t *seq_lens, int num_reqs, int n_new,
+                               const int32_t *positions, const uint64_t *turns, float magnitude,
+                               int interleaved, const RopeView &v, int32_t *status, int sms,
+                               cudaStream_t stream);
 
 // Accumulated attention weight (plmla_mass.cu).
 constexpr int32_t kStatusMassLength = 34;       // a history longer than its row of weights
@@ -153,7 +154,7 @@ struct MassArgs {
     const void *slab;                   // bf16 elements, or E4M3 bytes (q8 set)
     int64_t num_pages, page_stride;
     const int32_t *page_table;
-    int64_t table_ld;
+    int64_t table_ld, table_cols;       // row stride, and the columns a row has
     const int32_t *seq_lens;
     int num_reqs, n_q, heads, rows;     // rows = n_q * heads
     const __nv_bfloat16 *q_nope, *q_rope;
@@ -179,11 +180,11 @@ int select_parts(int num_reqs, int64_t mass_cols, int sms);
 size_t select_workspace(int num_reqs, int parts);
 cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t num_pages,
                            int64_t page_bytes, const int32_t *table, int64_t table_ld,
-                           const int32_t *seq_lens, const int32_t *out_table, int64_t out_ld,
-                           const int32_t *kept, int64_t kept_ld, const int32_t *kept_lens,
-                           int num_reqs, int keep, const float *mass, int64_t mass_ld,
-                           int64_t mass_cols, float *mass_out, int64_t mass_out_ld, int32_t *status,
-                           cudaStream_t stream);
+                           int64_t table_cols, const int32_t *seq_lens, const int32_t *out_table,
+                           int64_t out_ld, int64_t out_cols, const int32_t *kept, int64_t kept_ld,
+                           const int32_t *kept_lens, int num_reqs, int keep, const float *mass,
+                           int64_t mass_ld, int64_t mass_cols, float *mass_out,
+                           int64_t mass_out_ld, int32_t *status, cudaStream_t stream);
 
 // Shared by the query quantiser (plan grid) and the FP8 append: one E4M3 byte
 // pair from two floats, round to nearest even, saturating to +-448.

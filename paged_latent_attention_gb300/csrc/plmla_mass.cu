@@ -266,7 +266,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     }
     const int rank = CG == 2 ? (int)cluster_rank() : 0;
     const int workers = (int)gridDim.x / CG, worker = (int)blockIdx.x / CG;
-    StepWalk walk = {a.seq_lens, min(a.mass_cols, a.table_ld * kPageTokens), kSpan, 0, 0, 0};
+    StepWalk walk = {a.seq_lens, min(a.mass_cols, a.table_cols * kPageTokens), kSpan, 0, 0, 0};
     int g0, g1;                         // this worker's steps
     {
         // steps per request (four a thread), prefix-summed; the thread in whose
@@ -279,8 +279,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const int r = 4 * (int)threadIdx.x + e;
             own[e] = r < a.num_reqs ? walk.steps(r) : 0;
             if (r < a.num_reqs && a.seq_lens[r] > walk.cap && blockIdx.x == 0)
-                bad = a.seq_lens[r] > a.table_ld * kPageTokens ? kStatusAppendPage
-                                                               : kStatusMassLength;
+                bad = a.seq_lens[r] > a.table_cols * kPageTokens ? kStatusAppendPage
+                                                                 : kStatusMassLength;
             sum += own[e];
         }
         int x = sum;
@@ -373,7 +373,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         auto tile_at = [&](int r, int i, int *tok) -> int {
             const int64_t t = (int64_t)i * kSpan + rank * kTile;
             *tok = (int)(t % kPageTokens);
-            int page = t / kPageTokens < a.table_ld
+            int page = t / kPageTokens < a.table_cols
                            ? a.page_table[(int64_t)r * a.table_ld + t / kPageTokens] : 0;
             if (page < 0 || (int64_t)page >= a.num_pages)
                 page = 0;                                     // reported and not stored below
@@ -597,7 +597,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             // the owner of the tile's sums: the unit's group, or the first group
             const bool mine = QRES ? (u & 1) == group : group == 0;
             // (the pair's second tile may lie past the history)
-            const bool inside = t0 < L && t0 / kPageTokens < a.table_ld;
+            const bool inside = t0 < L && t0 / kPageTokens < a.table_cols;
             const int page =
                 inside ? a.page_table[(int64_t)r * a.table_ld + t0 / kPageTokens] : 0;
             const bool page_ok = page >= 0 && (int64_t)page < a.num_pages;

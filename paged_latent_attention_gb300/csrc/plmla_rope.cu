@@ -304,7 +304,7 @@ struct AppendRopeArgs {
     int64_t num_pages, page_stride;
     float kv_scale;
     const int32_t *table;
-    int64_t table_ld;
+    int64_t table_ld, table_cols;
     const int32_t *seq_lens;
     int num_reqs, n_new;
     int32_t *status;
@@ -329,7 +329,7 @@ __device__ __forceinline__ void append_rope_row(const AppendRopeArgs &a, const R
         return;
     }
     int page = -1;
-    if (p / kPageTokens < a.table_ld)
+    if (p / kPageTokens < a.table_cols)
         page = a.table[(int64_t)r * a.table_ld + p / kPageTokens];
     if (page < 0 || (int64_t)page >= a.num_pages) {
         if (lane == 0 && a.status != nullptr)
@@ -465,10 +465,11 @@ cudaError_t launch_rope(const RopeView &v, const int32_t *positions, const uint6
 
 cudaError_t launch_append_rope(const void *latent, const void *rope, void *slab, bool fp8,
                                int64_t num_pages, int64_t page_stride, float kv_scale,
-                               const int32_t *table, int64_t table_ld, const int32_t *seq_lens,
-                               int num_reqs, int n_new, const int32_t *positions,
-                               const uint64_t *turns, float magnitude, int interleaved,
-                               const RopeView &v, int32_t *status, int sms, cudaStream_t stream)
+                               const int32_t *table, int64_t table_ld, int64_t table_cols,
+                               const int32_t *seq_lens, int num_reqs, int n_new,
+                               const int32_t *positions, const uint64_t *turns, float magnitude,
+                               int interleaved, const RopeView &v, int32_t *status, int sms,
+                               cudaStream_t stream)
 {
     const int64_t rows = (int64_t)num_reqs * n_new;
     if (rows == 0)
@@ -481,8 +482,9 @@ cudaError_t launch_append_rope(const void *latent, const void *rope, void *slab,
     if (append_blocks + q_blocks > INT32_MAX)
         return cudaErrorInvalidValue;
     const AppendRopeArgs a = {static_cast<const uint4 *>(latent), static_cast<const uint4 *>(rope),
-                              slab, num_pages, page_stride, kv_scale, table, table_ld, seq_lens,
-                              num_reqs, n_new, status, positions, rows, (int)append_blocks};
+                              slab, num_pages, page_stride, kv_scale, table, table_ld,
+                              table_cols, seq_lens, num_reqs, n_new, status, positions, rows,
+                              (int)append_blocks};
     const unsigned grid = (unsigned)(append_blocks + q_blocks);
     if (fp8)
         return interleaved ? launch_append_typed<true, true>(a, q, vec, grid, stream)
