@@ -729,7 +729,8 @@ plmla_status mla_attention_mass_ex(const void *q_nope_absorbed, const void *q_ro
  * mla_attention_mass_fp8 -- mla_attention_mass over E4M3 pages (see
  * mla_decode_fp8: kv_scale, page strides in bytes).  The workspace, of at least
  * mla_mass_workspace_size_fp8(...) bytes and 256-byte aligned, holds the query
- * rows in two E4M3 parts; its contents on entry are irrelevant.
+ * rows in two E4M3 parts; its contents on entry are irrelevant, and calls that may
+ * run at once need one each.
  */
 size_t mla_mass_workspace_size_fp8(int32_t num_reqs, int32_t n_q, int32_t num_heads);
 plmla_status mla_attention_mass_fp8(const void *q_nope_absorbed, const void *q_rope,
@@ -757,7 +758,8 @@ plmla_status mla_attention_mass_fp8_ex(const void *q_nope_absorbed, const void *
  * number and -0 as 0.  A history of at most `keep` tokens stays whole.
  *
  * mass         fp32, row r at mass + r * mass_ld, of mass_cols columns; a longer
- *              history is taken as mass_cols long
+ *              history is taken as mass_cols long, so that its newest tokens, the
+ *              last `recent` among them, do not stay (reported by mla_evict_select_ex)
  * seq_lens     int32 [num_reqs], device; num_reqs 1 .. 1024
  * keep         1 .. 2^31 - 1, sink >= 0, recent >= 0, sink + recent <= keep
  * kept         int32, row r at kept + r * kept_ld (kept_ld >= min(keep, mass_cols)):
@@ -768,8 +770,11 @@ plmla_status mla_attention_mass_fp8_ex(const void *q_nope_absorbed, const void *
  *              256-byte aligned, whose contents on entry are irrelevant: with it long
  *              rows of few requests are searched by every SM instead of one cluster
  *              per request (the result is the same).  The size is 0 for shapes that
- *              make no use of it.
+ *              make no use of it.  Calls that may run at once need one each.
  * Deterministic.
+ *
+ * mla_evict_select_ex also takes `status`, an optional device int32 as in
+ * mla_kv_append: set to 34 if a history is longer than mass_cols.
  */
 size_t mla_evict_workspace_size(int32_t num_reqs, int64_t mass_cols);
 plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
@@ -777,6 +782,11 @@ plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_c
                               int32_t sink, int32_t recent, int32_t *kept, int64_t kept_ld,
                               int32_t *kept_lens, void *workspace, size_t workspace_bytes,
                               void *stream);
+plmla_status mla_evict_select_ex(const float *mass, int64_t mass_ld, int64_t mass_cols,
+                                 const int32_t *seq_lens, int32_t num_reqs, int32_t keep,
+                                 int32_t sink, int32_t recent, int32_t *kept, int64_t kept_ld,
+                                 int32_t *kept_lens, void *workspace, size_t workspace_bytes,
+                                 int32_t *status, void *stream);
 
 /*
  * mla_kv_compact -- copy the kept token rows of each history into fresh pages, for

@@ -75,6 +75,8 @@ SIGNATURES = {
     "mla_evict_workspace_size": (_sz, [_i32, _i64]),
     "mla_evict_select": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _i64, _p,
                                         _p, _sz, _p]),
+    "mla_evict_select_ex": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _i64,
+                                           _p, _p, _sz, _p, _p]),
     "mla_kv_compact": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _p, _p, _i64, _p,
                                       _i64, _p, _i32, _i32, _p, _i64, _i64, _p, _i64, _p, _p]),
     "mla_kv_compact_ex": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i64,

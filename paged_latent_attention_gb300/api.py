@@ -757,7 +757,8 @@ def mla_attention_mass_fp8(q_nope_absorbed, q_rope, lse, slab, page_table, seq_l
                            kv_scale, n_q=1, scale=DEFAULT_SCALE, decay=1.0, workspace=None,
                            status=None, stream=None):
     """mla_attention_mass over E4M3 pages (slab and kv_scale as in mla_decode_fp8).
-    The workspace comes from allocate_mass_workspace."""
+    The workspace comes from allocate_mass_workspace (a new one by default); calls
+    that may run at once need one each."""
     return _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q,
                  scale, decay, _kv_scale(kv_scale), workspace, status, stream)
 
@@ -803,13 +804,16 @@ def allocate_evict_workspace(num_reqs, tokens, device=None):
 
 
 def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_lens=None,
-                     workspace=None, stream=None):
+                     workspace=None, status=None, stream=None):
     """Which tokens of each history stay within ``keep``: the first ``sink``, the
     last ``recent`` and the heaviest of the rest by mass [R, tokens] fp32 (ties to
     the lower index).  Returns (kept [R, min(keep, tokens)] int32 ascending
     indices, kept_lens [R] int32 = min(keep, seq_lens)); entries of kept past a
-    row's count are not written.  The workspace comes from allocate_evict_workspace
-    (a new one by default)."""
+    row's count are not written.  A history longer than its row of mass is taken as
+    ``tokens`` long and loses its newest tokens, ``recent`` or not: ``status``, an
+    optional CUDA int32 tensor of one element, is then set to 34.  The workspace
+    comes from allocate_evict_workspace (a new one by default); calls that may run
+    at once need one each.  Asynchronous."""
     dev = mass.get_device()
     if mass.dim() != 2 or dev < 0:
         _fail("mass must be a CUDA tensor [R, tokens]")
@@ -836,8 +840,9 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
         _fail(f"workspace must be contiguous memory on cuda:{dev}")
     if workspace is not None and workspace.numel():
         scratch, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch(dev, lib.mla_evict_select, "mla_evict_select", stream, *weights, lens, R, keep, sink,
-            recent, ids, ids_ld, _vector(kept_lens, "kept_lens", dev, R), scratch, size)
+    _launch(dev, lib.mla_evict_select_ex, "mla_evict_select", stream, *weights, lens, R, keep,
+            sink, recent, ids, ids_ld, _vector(kept_lens, "kept_lens", dev, R), scratch, size,
+            _flag(status, dev))
     return kept, kept_lens
 
 

@@ -979,18 +979,18 @@ extern "C" size_t mla_evict_workspace_size(int32_t num_reqs, int64_t mass_cols)
     return parts > 0 ? align_up(select_workspace(num_reqs, parts)) : 0;
 }
 
-extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
-                                         const int32_t *seq_lens, int32_t num_reqs, int32_t keep,
-                                         int32_t sink, int32_t recent, int32_t *kept,
-                                         int64_t kept_ld, int32_t *kept_lens, void *workspace,
-                                         size_t workspace_bytes, void *stream)
+extern "C" plmla_status mla_evict_select_ex(const float *mass, int64_t mass_ld, int64_t mass_cols,
+                                            const int32_t *seq_lens, int32_t num_reqs, int32_t keep,
+                                            int32_t sink, int32_t recent, int32_t *kept,
+                                            int64_t kept_ld, int32_t *kept_lens, void *workspace,
+                                            size_t workspace_bytes, int32_t *status, void *stream)
 {
     if (mass == nullptr || seq_lens == nullptr || kept == nullptr || kept_lens == nullptr ||
         num_reqs < 1 || num_reqs > kMaxReqs || mass_cols < 1 || mass_ld < mass_cols || keep < 1 ||
         sink < 0 || recent < 0 || (int64_t)sink + recent > keep ||
         kept_ld < (keep < mass_cols ? keep : mass_cols) || !aligned(mass, 4) ||
         !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4) ||
-        !aligned(workspace, kAlign))
+        !aligned(workspace, kAlign) || (status != nullptr && !aligned(status, 4)))
         return PLMLA_INVALID_ARGUMENT;
     int parts = 0;
     if (workspace != nullptr) {
@@ -1000,8 +1000,19 @@ extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int
     }
     const cudaError_t err = launch_select(mass, mass_ld, mass_cols, seq_lens, num_reqs, keep,
                                           sink, recent, kept, kept_ld, kept_lens, parts, workspace,
-                                          static_cast<cudaStream_t>(stream));
+                                          status, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR;
+}
+
+extern "C" plmla_status mla_evict_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
+                                         const int32_t *seq_lens, int32_t num_reqs, int32_t keep,
+                                         int32_t sink, int32_t recent, int32_t *kept,
+                                         int64_t kept_ld, int32_t *kept_lens, void *workspace,
+                                         size_t workspace_bytes, void *stream)
+{
+    return mla_evict_select_ex(mass, mass_ld, mass_cols, seq_lens, num_reqs, keep, sink, recent,
+                               kept, kept_ld, kept_lens, workspace, workspace_bytes, nullptr,
+                               stream);
 }
 
 extern "C" plmla_status mla_kv_compact_ex(

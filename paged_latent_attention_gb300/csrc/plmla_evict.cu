@@ -52,6 +52,7 @@ struct SelectArgs {
     int32_t *kept;
     int64_t kept_ld;
     int32_t *kept_lens;
+    int32_t *status;               // may be null
     int cache_groups;              // groups that the dynamic shared memory holds
 };
 
@@ -227,8 +228,11 @@ __device__ __forceinline__ bool select_forced(const SelectArgs &a, int r, int me
 {
     int32_t *kept = a.kept + (int64_t)r * a.kept_ld;
     const int tid = threadIdx.x;
-    if (write && me == 0 && tid == 0)
+    if (write && me == 0 && tid == 0) {
         a.kept_lens[r] = min(L, a.keep);
+        if (a.seq_lens[r] > L && a.status != nullptr)
+            atomicExch(a.status, kStatusMassLength);
+    }
     if (L <= a.keep) {
         for (uint32_t i = me * NT + tid; i < (uint32_t)L && write; i += parts * NT)
             kept[i] = (int32_t)i;
@@ -794,10 +798,10 @@ size_t select_workspace(int num_reqs, int parts)
 cudaError_t launch_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
                           const int32_t *seq_lens, int num_reqs, int keep, int sink, int recent,
                           int32_t *kept, int64_t kept_ld, int32_t *kept_lens, int parts,
-                          void *workspace, cudaStream_t stream)
+                          void *workspace, int32_t *status, cudaStream_t stream)
 {
     SelectArgs a = {mass, mass_ld, mass_cols, seq_lens, keep, sink, recent, kept, kept_ld,
-                    kept_lens, 0};
+                    kept_lens, status, 0};
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;

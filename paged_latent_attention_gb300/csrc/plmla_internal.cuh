@@ -172,9 +172,9 @@ cudaError_t launch_mass(const MassArgs &args, int sms, cudaStream_t stream);
 // Eviction (plmla_evict.cu).
 constexpr int kCompactLayers = 64;              // layers of one compaction launch
 cudaError_t launch_select(const float *mass, int64_t mass_ld, int64_t mass_cols,
-                          const int32_t *seq_lens, int num_reqs, int keep, int sink, int recent, int32_t *kept,
-                          int64_t kept_ld, int32_t *kept_lens, int parts, void *workspace,
-                          cudaStream_t stream);
+                          const int32_t *seq_lens, int num_reqs, int keep, int sink, int recent,
+                          int32_t *kept, int64_t kept_ld, int32_t *kept_lens, int parts,
+                          void *workspace, int32_t *status, cudaStream_t stream);
 // CTAs per request of the form for long rows (0: none), and its workspace in bytes.
 int select_parts(int num_reqs, int64_t mass_cols, int sms);
 size_t select_workspace(int num_reqs, int parts);

@@ -36,3 +36,8 @@ def test_columns_of_the_page_table(lib, kw):
     good = (4, 4)
     for ids, outs in ((tuple(kw.values()), good), (good, tuple(kw.values()))):
         assert lib.mla_kv_compact_ex(*head, FAKE, *ids, FAKE, 2 * FAKE, *outs, *tail) == 1
+
+
+def test_status_of_the_selection(lib):
+    assert lib.mla_evict_select_ex(FAKE, 100, 100, FAKE, 2, 10, 1, 2, FAKE, 10, FAKE, None, 0,
+                                   FAKE + 2, None) == 1

@@ -68,7 +68,8 @@ def test_evictions_one_after_another():
             SCALE, num_pages=w.num_pages)
         assert_parity(out, lse, ref_out, ref_lse, what=f"decode after {cycle} evictions")
 
-        kept, n = api.mla_evict_select(mass, _ints(lens), keep, sink=4, recent=recent)
+        kept, n = api.mla_evict_select(mass, _ints(lens), keep, sink=4, recent=recent,
+                                       status=status)
         want = oracle.evict_select(mass.cpu().numpy(), lens, keep, 4, recent)
         assert [kept[r, : len(k)].tolist() for r, k in enumerate(want)] == want
         for r, k in enumerate(want):

@@ -1,0 +1,29 @@
+"""Histories that have outgrown their rows of weights are reported by the selection."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from paged_latent_attention_gb300 import api
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("tokens,keep,recent", [(100, 30, 4), (100, 100, 7), (5000, 900, 60),
+                                                (500_000, 1000, 64)])
+@pytest.mark.parametrize("over", [0, 1, 2000])
+def test_a_history_past_its_row_is_reported(tokens, keep, recent, over):
+    """`over` tokens have no weight: they cannot stay, and the caller is told so."""
+    mass = torch.rand(2, tokens, device="cuda")
+    lens = [tokens // 3, tokens + over]
+    dev = torch.as_tensor(np.asarray(lens, dtype=np.int32), device="cuda")
+    for before in (0, 7):
+        status = torch.full((1,), before, dtype=torch.int32, device="cuda")
+        kept, n = api.mla_evict_select(mass, dev, keep, sink=2, recent=recent, status=status)
+        assert int(status.item()) == (34 if over else before)
+        want = oracle.evict_select(mass.cpu().numpy(), lens, keep, 2, recent)
+        assert [kept[r, : len(k)].tolist() for r, k in enumerate(want)] == want
+        assert n.tolist() == [len(k) for k in want]
+    for status in (torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            api.mla_evict_select(mass, dev, keep, status=status)
