@@ -577,6 +577,10 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             commit(m.bars.drain);
             wait_drain(bar_of(m.bars.drain), 0);
         }
+    } else if (CG == 2 && warp == 1 && lane == 0) {
+        // the even CTA's commits arrive here too: the last of them comes after the others
+        if (g0 < g1)
+            wait_drain(bar_of(m.bars.drain), 0);
     } else if (warp >= 2) {
         // ------------------------------------------------------------ weights
         // A wait that gives up clears `ok`: the loops run on without waiting or
@@ -670,8 +674,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 
     tc_fence_before();
     __syncthreads();
-    // a pair leaves together: no copy, commit or arrival is on its way to either CTA
-    // (every wait above is bounded, so all threads get here)
+    // A pair leaves together: no copy or arrival of one CTA is on its way to the other,
+    // and each has waited for its own copy of the last commit.  (Every wait above is
+    // bounded, so all threads get here.)
     if constexpr (CG == 2)
         cluster_sync();
     if (warp == 1) {
