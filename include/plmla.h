@@ -765,7 +765,8 @@ plmla_status mla_attention_mass_fp8_ex(const void *q_nope_absorbed, const void *
  * kept         int32, row r at kept + r * kept_ld (kept_ld >= min(keep, mass_cols)):
  *              min(keep, L_r) indices in ascending order; later entries are not
  *              written
- * kept_lens    int32 [num_reqs], written: min(keep, L_r)
+ * kept_lens    int32 [num_reqs], written: min(keep, L_r); must not overlap seq_lens
+ *              (which mla_kv_compact needs as it is)
  * workspace    NULL, or device scratch of at least mla_evict_workspace_size(...) bytes,
  *              256-byte aligned, whose contents on entry are irrelevant: with it long
  *              rows of few requests are searched by every SM instead of one cluster

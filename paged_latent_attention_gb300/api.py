@@ -809,7 +809,7 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
     last ``recent`` and the heaviest of the rest by mass [R, tokens] fp32 (ties to
     the lower index).  Returns (kept [R, min(keep, tokens)] int32 ascending
     indices, kept_lens [R] int32 = min(keep, seq_lens)); entries of kept past a
-    row's count are not written.  A history longer than its row of mass is taken as
+    row's count are not written, and neither may overlap an input.  A history longer than its row of mass is taken as
     ``tokens`` long and loses its newest tokens, ``recent`` or not: ``status``, an
     optional CUDA int32 tensor of one element, is then set to 34.  The workspace
     comes from allocate_evict_workspace (a new one by default); calls that may run
@@ -828,6 +828,8 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
         kept = _empty((R, cols), _I32, mass.device, stream)
     if kept_lens is None:
         kept_lens = _empty(R, _I32, mass.device, stream)
+    else:
+        _check_apart(kept_lens, seq_lens, "kept_lens must not overlap seq_lens")
     ids, ids_ld, have = _rows(kept, "kept", dev, _I32, R)
     if have < cols:
         _fail(f"kept needs {cols} columns")

@@ -27,3 +27,16 @@ def test_a_history_past_its_row_is_reported(tokens, keep, recent, over):
     for status in (torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32)):
         with pytest.raises(ValueError):
             api.mla_evict_select(mass, dev, keep, status=status)
+
+
+def test_lengths_are_not_overwritten():
+    """Every CTA of a request reads its length while one of them writes kept_lens: the
+    two in one place would race, and the compaction needs the lengths as they were."""
+    mass = torch.rand(3, 5000, device="cuda")
+    both = torch.tensor([5000, 4000, 10, 7], dtype=torch.int32, device="cuda")
+    for kept_lens in (both[:3], both[1:]):
+        with pytest.raises(ValueError):
+            api.mla_evict_select(mass, both[:3], 900, kept_lens=kept_lens)
+    apart = torch.tensor([5000, 4000, 10, 0, 0, 0], dtype=torch.int32, device="cuda")
+    _, n = api.mla_evict_select(mass, apart[:3], 900, kept_lens=apart[3:])
+    assert apart.tolist() == [5000, 4000, 10, 900, 900, 10] and n.data_ptr() == apart[3:].data_ptr()
