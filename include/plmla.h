@@ -807,12 +807,14 @@ plmla_status mla_evict_select_ex(const float *mass, int64_t mass_ld, int64_t mas
  *              min(kept_lens[r], kept_cols) on are not used; kept_cols 0 .. kept_ld
  * mass         NULL, or fp32 rows of mass_cols columns (row stride mass_ld) whose
  *              kept entries are copied to mass_out[r, i] (row stride mass_out_ld >=
- *              kept_cols); the two must not overlap.  An index past mass_cols
- *              leaves its mass_out entry as it is, and so do the entries from
- *              kept_lens[r] on: they have to be 0 before mla_attention_mass adds the
- *              weights of the tokens appended there.
+ *              kept_cols); the two must not overlap.  The
+ *              mass_out entry of an index past mass_cols stays as it is (and is
+ *              reported), and so do the entries from kept_lens[r] on: they have to be
+ *              0 before mla_attention_mass adds the weights of the tokens appended
+ *              there.
  * status       optional device int32, as in mla_kv_append: set to 33 if an index or
- *              a page is out of range; such rows are skipped
+ *              a page is out of range (such rows are skipped), to 34 if a kept token
+ *              has no column in mass (its row is copied, its weight is not)
  *
  * mla_kv_compact_ex is the same for tables whose rows have page_table_cols (1 ..
  * page_table_ld) and out_table_cols (1 .. out_table_ld) entries, fewer than their

@@ -857,9 +857,10 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
     rows are carried into ``mass_out`` (by default a new tensor as wide as mass, so
     that the histories can grow again, with zeros where the next tokens' weights
     come; in a given one those entries stay as they are and have to be 0); returns
-    mass_out (None without mass).  ``status``: optional CUDA int32 tensor
-    of one element, set to 33 where an index or page is out of range (such rows are
-    skipped).  The old pages are not changed.  Asynchronous."""
+    mass_out (None without mass).  ``status``: optional CUDA int32 tensor of one
+    element, set to 33 where an index or page is out of range (such rows are
+    skipped), to 34 where a kept token has no weight in mass (its row is copied).
+    The old pages are not changed.  Asynchronous."""
     if not isinstance(slabs, (list, tuple)) or not slabs:
         _fail("slabs must be a list of pools")
     first = slabs[0]

@@ -702,8 +702,12 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
             constexpr int row_bytes = F8 ? kRow : 2 * kRow;
             src = (int64_t)from * a.page_bytes + (int64_t)(t % kPageTokens) * row_bytes;
             dst = (int64_t)to * a.page_bytes + (int64_t)(i % kPageTokens) * row_bytes;
-            if (a.mass != nullptr && blockIdx.z == 0 && t < a.mass_cols)
-                a.mass_out[(int64_t)r * a.mass_out_ld + i] = a.mass[(int64_t)r * a.mass_ld + t];
+            if (a.mass != nullptr && blockIdx.z == 0) {
+                if (t < a.mass_cols)
+                    a.mass_out[(int64_t)r * a.mass_out_ld + i] = a.mass[(int64_t)r * a.mass_ld + t];
+                else if (a.status != nullptr)
+                    atomicExch(a.status, kStatusMassLength);
+            }
         }
     }
     uint4 v[kCompactVecs];
