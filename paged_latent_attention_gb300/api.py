@@ -615,6 +615,15 @@ def rope_table(dim=ROPE, *, base=10000.0, scaling="none", factor=1.0, original_l
     return RopeTable(host.to(device or "cuda"), magnitude)
 
 
+def _no_grad(name, *tensors):
+    """Refuses tensors whose gradients the call would lose without a word."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                _fail(f"{name} is not recorded by autograd: call it under torch.no_grad() or on "
+                      "detached tensors (the gradient of a rotation is mla_rope with inverse)")
+
+
 def _layout(layout):
     code = ROPE_LAYOUTS.get(layout)
     if code is None:
@@ -627,8 +636,10 @@ def mla_rope(x, positions, table, *, layout="half", inverse=False, out=None, str
     strides, so ``q[..., 128:]`` rotates the last part of wider heads) turned by
     positions [T] int32.  ``layout`` pairs element i with i + D/2 ("half") or 2i
     with 2i + 1 ("interleaved"); ``inverse`` negates the angles, which is the
-    gradient of the forward call.  ``out`` may be x itself (in place); returns it
-    (a new contiguous tensor by default)."""
+    gradient of the forward call: autograd does not record the call, so a tensor
+    that requires grad is refused while gradients are recorded.  ``out`` may be x
+    itself (in place); returns it (a new contiguous tensor by default)."""
+    _no_grad("mla_rope", x, out)
     kind = _ROPE_TYPES.get(x.dtype)
     dev = x.get_device()
     if kind is None or dev < 0 or x.dim() != 3 or x.stride(2) != 1:
@@ -670,7 +681,8 @@ def mla_kv_append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, 
     default each token's index in its history; give the true positions where a
     history has lost tokens).  ``q_rope`` bf16 [R*n_new, H, 64], any token and head
     strides, is rotated into ``q_out`` (contiguous, new by default), mla_decode's
-    q_rope; returns it (None without q_rope)."""
+    q_rope; returns it (None without q_rope).  As in mla_rope, a q_rope that
+    requires grad is refused while gradients are recorded."""
     return _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, positions,
                         layout, q_rope, q_out, status, stream, None)
 
@@ -692,6 +704,7 @@ def _kv_scale(kv_scale):
 
 def _append_rope(latent_new, rope_new, slab, page_table, seq_lens, n_new, table, positions, layout,
                  q_rope, q_out, status, stream, kv_scale):
+    _no_grad("the rotating append", q_rope, q_out)
     base, pages, page_stride = _pool(slab, kv_scale is not None)
     dev, n_new = slab.get_device(), int(n_new)
     R = seq_lens.shape[0] if seq_lens.dim() == 1 else 0
