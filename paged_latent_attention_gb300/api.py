@@ -809,11 +809,21 @@ def _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, s
     return mass
 
 
+def _evict_workspace_size(dev, num_reqs, tokens):
+    """The size depends on the device that the call will run on."""
+    size = _native.lib().mla_evict_workspace_size
+    if dev == torch._C._cuda_getDevice():
+        return size(num_reqs, tokens)
+    with torch.cuda.device(dev):
+        return size(num_reqs, tokens)
+
+
 def allocate_evict_workspace(num_reqs, tokens, device=None):
     """A workspace tensor (uint8) for mla_evict_select on mass [num_reqs, tokens] (of
     no bytes where that shape makes no use of one)."""
-    return torch.empty(_native.lib().mla_evict_workspace_size(num_reqs, tokens), dtype=_U8,
-                       device=device or "cuda")
+    device = torch.device(device or "cuda")
+    dev = torch.cuda.current_device() if device.index is None else device.index
+    return torch.empty(_evict_workspace_size(dev, num_reqs, tokens), dtype=_U8, device=device)
 
 
 def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_lens=None,
@@ -848,7 +858,7 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
         _fail(f"kept needs {cols} columns")
     lib, scratch, size = _native.lib(), None, 0
     if workspace is None:
-        size = lib.mla_evict_workspace_size(R, tokens)
+        size = _evict_workspace_size(dev, R, tokens)
         if size:
             workspace = _empty(size, _U8, mass.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
