@@ -4,6 +4,8 @@
 // fresh pages.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "plmla_internal.cuh"
 
 namespace plmla {
@@ -737,13 +739,15 @@ cudaError_t select_attributes(const void *kernel)
 }
 
 // Clusters of 2^log CTAs that the device holds at once (0: none, or it cannot say).
+// An answer is kept; a query that failed is made again by the next call.
 int select_max_clusters(int log)
 {
-    static int cached[64][5] = {};
+    static std::atomic<int> cached[64][5];         // the answer + 1
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return 0;
-    if (cached[dev][log] == 0) {
+    int n = cached[dev][log].load(std::memory_order_relaxed) - 1;
+    if (n < 0) {
         if (select_attributes(reinterpret_cast<const void *>(select_kernel<kSelThreads>)) !=
             cudaSuccess)
             return 0;
@@ -758,14 +762,13 @@ int select_max_clusters(int log)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, select_kernel<kSelThreads>, &cfg) != cudaSuccess) {
             cudaGetLastError();    // such clusters are not offered: take smaller ones
-            n = 0;
+            return 0;
         }
-        cached[dev][log] = n + 1;
+        cached[dev][log].store(n + 1, std::memory_order_relaxed);
     }
-    return cached[dev][log] - 1;
+    return n;
 }
 
 // log2 of the CTAs per request.  Rows of at most kSelSmall weights: one small CTA

@@ -40,3 +40,30 @@ def test_lengths_are_not_overwritten():
     apart = torch.tensor([5000, 4000, 10, 0, 0, 0], dtype=torch.int32, device="cuda")
     _, n = api.mla_evict_select(mass, apart[:3], 900, kept_lens=apart[3:])
     assert apart.tolist() == [5000, 4000, 10, 900, 900, 10] and n.data_ptr() == apart[3:].data_ptr()
+
+
+def test_threads_agree_on_the_form():
+    """The form of a selection goes by what the device holds at once, asked by whichever
+    thread comes first: all get the same size and the same tokens."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    shapes = [(1, 300), (3, 60_000), (2, 500_000), (1, 1_000_000), (40, 20_000)]
+
+    def sizes(_):
+        return [api.allocate_evict_workspace(*shape).numel() for shape in shapes]
+
+    mass = torch.rand(2, 500_000, device="cuda")
+    lens = torch.tensor([500_000, 400_000], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+
+    def select(_):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            kept, _ = api.mla_evict_select(mass, lens, 40_000, recent=10)
+            torch.cuda.current_stream().synchronize()
+            return kept
+
+    with ThreadPoolExecutor(8) as pool:
+        got = list(pool.map(sizes, range(64)))
+        kept = list(pool.map(select, range(16)))
+    assert all(s == got[0] for s in got) and got[0][2] > 0 and got[0][0] == 0
+    assert all(torch.equal(k, kept[0]) for k in kept)
