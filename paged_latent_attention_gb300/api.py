@@ -566,14 +566,24 @@ def _heads(t):
 
 
 def _check_apart(a, b, message):
-    """Refuses two views whose address ranges meet."""
+    """Refuses two views (of one type, with contiguous rows) that share elements, or whose
+    address ranges meet and whose strides do not show that they share none."""
     def span(t):
         first = t.data_ptr()
         last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
         return first, first + (last + 1) * t.element_size()
     (a0, a1), (b0, b1) = span(a), span(b)
-    if a0 < b1 and b0 < a1:
-        _fail(message)
+    if a0 >= b1 or b0 >= a1:
+        return
+    # rows in columns of one grid: [0, width of a) and [off, off + width of b) modulo the
+    # shortest stride, of which the others are multiples
+    strides = [s for t in (a, b) for n, s in zip(t.shape[:-1], t.stride()) if n > 1 and s > 0]
+    step = min(strides, default=0)
+    if step and all(s % step == 0 for s in strides) and (b0 - a0) % a.element_size() == 0:
+        off = (b0 - a0) // a.element_size() % step
+        if a.shape[-1] <= off <= step - b.shape[-1]:
+            return
+    _fail(message)
 
 
 class RopeTable:
