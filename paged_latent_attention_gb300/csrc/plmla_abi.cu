@@ -882,7 +882,7 @@ plmla_status mass_impl(const void *q_nope_absorbed, const void *q_rope, const fl
     a.q_nope = static_cast<const __nv_bfloat16 *>(q_nope_absorbed);
     a.q_rope = static_cast<const __nv_bfloat16 *>(q_rope);
     a.lse = lse;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    a.scale = scale;
     a.kv_scale = kv_scale;
     a.decay = decay;
     a.mass = mass;

@@ -161,7 +161,8 @@ struct MassArgs {
     const uint8_t *q8;                  // E4M3: [2, num_reqs * rows, 576], hi plane then lo
     const int32_t *qexp;
     const float *lse;                   // [num_reqs * rows], natural log
-    float scale_log2, kv_scale;         // softmax scale * log2(e)
+    float scale, kv_scale;              // softmax scale
+    float scale_log2;                   // times log2(e), set by the launch
     float decay;
     float *mass;
     int64_t mass_ld, mass_cols;         // row stride, and the columns a row has

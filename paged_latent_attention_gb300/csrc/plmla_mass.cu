@@ -85,6 +85,11 @@ struct MassFmt {
     static constexpr int step = F8 ? 128 : 64;
     static constexpr int parts = F8 ? 2 : 1;                  // query parts (hi, lo)
     static constexpr int tile_bytes = blocks * kMassSlot;
+    // the order of the products: bf16 takes the rope block in the middle (see kMassShort)
+    __device__ static int block(int i)
+    {
+        return F8 || i < blocks / 2 ? i : i == blocks / 2 ? blocks - 1 : i - 1;
+    }
     __device__ static int mmas(int block) { return F8 && block == 4 ? 2 : 4; }
 };
 
@@ -195,6 +200,21 @@ __device__ __forceinline__ void sum_columns(uint32_t at, int half, int cols, con
     }
 }
 
+// The tensor core's fp32 accumulator truncates: every MMA of a chain takes part of a unit
+// in the last place off the partial sum, always towards zero.  Where the partial sums grow
+// evenly to the score, the score ends up smaller by a share of itself, kMassShort of 2^-23
+// (found where the error against 64 bits is least; N(0, 1) rows, rows of unlike sizes and
+// rows with a common direction agree), and the epilogue's scale gives it back.  bf16: 4
+// for a chain of 36 MMAs, 2 of 18, 1 of 9; weights off by 1.5e-6 -> 1.4e-7 (2-norm; 32
+// queries of 64 heads), 8.5e-7 -> 2.8e-7 (128 rows), 5.6e-7 -> 2.2e-7 (64 rows), as in
+// fp32 arithmetic.  The rope block in the middle lets scores that come from the rope part
+// alone grow to half of the chain too: 2.8e-7 with it, 1.4e-6 with it at the end.  E4M3
+// products have few bits and mostly add up exactly: 1 for the 36 MMAs of a pair (5.3e-7 ->
+// 1.2e-7), 0 for a part's 18.  A score that comes whole from the first MMAs or the last is
+// off by about kMassShort of 2^-23, on either side, instead of by up to twice that.
+template <bool F8, int CG, int SETS>
+constexpr double kMassShort = F8 ? (CG == 2 ? 1.0 : 0.0) : 4.0 / SETS;
+
 // CG = CTAs of a worker (1, or a pair); QRES = queries resident, tiles streaming.
 // half = query rows per CTA of one MMA (N / CG) when QRES.
 template <bool F8, int CG, bool QRES, int SETS>
@@ -208,10 +228,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     constexpr int kWidth = kMassChunk * CG;                   // query rows of a chunk, at most
     // One CTA keeps SETS column sets that the epilogue adds: the scores of the query's
     // hi and lo part (E4M3; one MMA of N = 2 rows), or of every SETS'th column block
-    // (bf16).  The tensor core's fp32 accumulator truncates, so a score of 36 MMAs in one
-    // chain loses more than fp32 arithmetic would: weights off by 1.7e-6 (2-norm) with
-    // one chain, 8.7e-7 with two and 4.7e-7, as in fp32 arithmetic, with four, at no cost in
-    // time.
+    // (bf16), whose shorter chains of MMAs lose less to the accumulator's truncation
+    // (see kMassShort), at no cost in time.
     constexpr int kParts = F8 && CG == 2 ? 2 : 1;             // MMAs per K step, one a query part
     constexpr int kBufCols = kMassCols / 2;
     constexpr int kBufs = 2;
@@ -428,7 +446,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     cur = r;
                 }
 #pragma unroll 1
-                for (int k = 0; k < F::blocks; ++k) {
+                for (int i = 0; i < F::blocks; ++i) {
+                    const int k = F::block(i);
                     if (!ring_slot(kMassSlot)) {
                         ok = false;
                         break;
@@ -442,7 +461,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 for (int c = 0; c < chunks && ok; ++c) {
                     const int row = c * kWidth + rank * chunk_half(c);
 #pragma unroll 1
-                    for (int k = 0; k < F::blocks && ok; ++k) {
+                    for (int i = 0; i < F::blocks && ok; ++i) {
+                        const int k = F::block(i);
                         if (c == 0) {
                             if (n > 0 && !wait_bounded(bar_of(m.bars.k_empty[k]), (n - 1) & 1,
                                                        abort_flag, status, 3)) {
@@ -477,7 +497,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             wait_drain(bar_of(m.bars.full[it % slots]), (uint32_t)(it / slots) & 1u);
         for (int64_t it = k_loads > F::blocks ? k_loads - F::blocks : 0;
              it < k_loads && rank == 0; ++it)
-            wait_drain(bar_of(m.bars.k_full[it % F::blocks]), (uint32_t)(it / F::blocks) & 1u);
+            wait_drain(bar_of(m.bars.k_full[F::block((int)(it % F::blocks))]),
+                       (uint32_t)(it / F::blocks) & 1u);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---------------------------------------------------------- MMA issuer
         int slot = 0, q_loads = 0, cur = -1;
@@ -510,8 +531,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 const uint32_t idesc = idesc_for<F8>(
                     128 * CG, (F8 && CG == 1 ? 2 : CG) * chunk_half(c), false, false);
                 const uint32_t d = tmem + kBufCols * buf;
-#pragma unroll 1
-                for (int k = 0; k < F::blocks && ok; ++k) {
+                // unrolled: with the blocks' order and offsets worked out between the MMAs
+                // the window of 32 queries took 361 us instead of 329
+#pragma unroll
+                for (int i = 0; i < F::blocks && ok; ++i) {
+                    const int k = F::block(i);
                     const bool rope = k == F::blocks - 1;
                     if (QRES || c == 0) {
                         if (!wait_bounded(QRES ? bar_of(m.bars.full[slot]) : bar_of(m.bars.k_full[k]),
@@ -545,12 +569,12 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                             if (kk < mmas) {
                                 if constexpr (CG == 2)
                                     mma_pair<F8>(d, da + 2 * kk, db + 2 * kk, idesc,
-                                                 (k | p | kk) != 0);
+                                                 (i | p | kk) != 0);
                                 else if constexpr (F8)
-                                    mma_e4m3(d, da + 2 * kk, db + 2 * kk, idesc, (k | kk) != 0);
+                                    mma_e4m3(d, da + 2 * kk, db + 2 * kk, idesc, (i | kk) != 0);
                                 else
-                                    mma_bf16(d + k % SETS * half, da + 2 * kk, db + 2 * kk, idesc,
-                                             (k / SETS | kk) != 0);
+                                    mma_bf16(d + i % SETS * half, da + 2 * kk, db + 2 * kk, idesc,
+                                             (i / SETS | kk) != 0);
                             }
                         issued = true;
                         if (!QRES || p == kParts - 1) {
@@ -746,7 +770,9 @@ cudaError_t launch_mass_form(const MassArgs &a, int sms, cudaStream_t stream)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = F8 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mass_kernel<F8, CG, QRES, SETS>, k, qn, qr, a, half, slots);
+    MassArgs b = a;
+    b.scale_log2 = (float)((double)a.scale * kLog2e * (1.0 + kMassShort<F8, CG, SETS> * 0x1p-23));
+    return cudaLaunchKernelEx(&cfg, mass_kernel<F8, CG, QRES, SETS>, k, qn, qr, b, half, slots);
 }
 
 template <bool F8>
