@@ -861,8 +861,9 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
         kept = _empty((R, cols), _I32, mass.device, stream)
     if kept_lens is None:
         kept_lens = _empty(R, _I32, mass.device, stream)
-    else:
-        _check_apart(kept_lens, seq_lens, "kept_lens must not overlap seq_lens")
+    counts = _vector(kept_lens, "kept_lens", dev, R)
+    if abs(counts - lens) < 4 * R:
+        _fail("kept_lens must not overlap seq_lens")
     ids, ids_ld, have = _rows(kept, "kept", dev, _I32, R)
     if have < cols:
         _fail(f"kept needs {cols} columns")
@@ -876,8 +877,7 @@ def mla_evict_select(mass, seq_lens, keep, *, sink=0, recent=0, kept=None, kept_
     if workspace is not None and workspace.numel():
         scratch, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch(dev, lib.mla_evict_select_ex, "mla_evict_select", stream, *weights, lens, R, keep,
-            sink, recent, ids, ids_ld, _vector(kept_lens, "kept_lens", dev, R), scratch, size,
-            _flag(status, dev))
+            sink, recent, ids, ids_ld, counts, scratch, size, _flag(status, dev))
     return kept, kept_lens
 
 
