@@ -610,8 +610,13 @@ def rope_table(dim=ROPE, *, base=10000.0, scaling="none", factor=1.0, original_l
     ``factor``: every one ("linear"), or by parts ("by_parts") -- pairs that turn
     fewer than ``low`` times over ``original_len`` positions are divided, those
     that turn more than ``high`` times kept, and a ramp joins the two.
-    ``magnitude`` scales the rotated pairs; by default 1, and 0.1 ln(factor) + 1 by
-    parts.  Make the table once and keep it: it is copied to the device here."""
+    The ramp is linear in turns; some models' code has one in the pair index between
+    rounded bounds.  ``magnitude`` scales the rotated pairs; by default 1, and 0.1
+    ln(factor) + 1 by parts, which is meant for heads that are rotated whole: a head of
+    this library has 512 elements without a position, which that factor leaves alone,
+    so models with a latent part usually want ``magnitude=1`` and put the factor, squared,
+    into the softmax ``scale`` of mla_decode.  Make the table once and keep it: it is
+    copied to the device here."""
     if scaling not in ROPE_SCALINGS:
         _fail(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
     host = torch.empty(max(dim, 0) // 2, dtype=torch.int64)
@@ -769,7 +774,9 @@ def mla_attention_mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens,
     returns mass.  The entry of a token that is new in its history must hold 0: make
     mass with zeros, as wide as the histories may become.  The queries, pool and histories are mla_decode's, ``lse`` is
     what it returned.  Layers that share a page table accumulate into one mass, a
-    call each; ``decay`` 0 overwrites.  ``status``: optional CUDA int32 tensor of
+    call each (with the step's decay in the first of
+    these calls and 1 in the others); ``decay`` 0 overwrites.  Scores are fp32 sums: the
+    weights are within 3e-7 (2-norm, N(0, 1) rows) of 64-bit arithmetic.  ``status``: optional CUDA int32 tensor of
     one element that the kernel sets to 33 or 34 where a history leaves the page
     table, the pool or its row of mass.  Asynchronous."""
     return _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q, scale, decay,
@@ -780,6 +787,8 @@ def mla_attention_mass_fp8(q_nope_absorbed, q_rope, lse, slab, page_table, seq_l
                            kv_scale, n_q=1, scale=DEFAULT_SCALE, decay=1.0, workspace=None,
                            status=None, stream=None):
     """mla_attention_mass over E4M3 pages (slab and kv_scale as in mla_decode_fp8).
+    The queries are taken in two E4M3 parts, as in mla_decode_fp8: exact for elements
+    above 2^-2 of their row's scale, within 2^-10 of it below.
     The workspace comes from allocate_mass_workspace (a new one by default); calls
     that may run at once need one each."""
     return _mass(q_nope_absorbed, q_rope, lse, slab, page_table, seq_lens, mass, n_q,

@@ -765,7 +765,7 @@ cudaError_t launch_mass_form(const MassArgs &a, int sms, cudaStream_t stream)
     attr[0].val.clusterDim.x = CG;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    // E4M3 pages: launched while the queries are still being split (the kernel waits)
+    // E4M3 pages: CTAs start as those of the query split end, and wait for the whole split
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;

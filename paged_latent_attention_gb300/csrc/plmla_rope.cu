@@ -10,7 +10,8 @@
 // Angles.  f_i comes as turns[i] = f_i / (2 pi) in units of 2^-64 turns, so
 // p * turns[i] in 64-bit integers wraps modulo whole turns: the reduction of
 // the angle is exact for every position, where an fp32 product p f_i would be
-// off by 0.06 rad at a million.  The top 32 bits (2^-32 turns) are split into a
+// off by 0.06 rad at a million.  (turns itself is as good as a double: below
+// 1e-9 rad at a million, a few 1e-7 rad at 2^31.)  The top 32 bits (2^-32 turns) are split into a
 // quadrant and a remainder in [-1/8, 1/8) turns before the conversion to fp32,
 // which then rounds by at most 2^-26 half turns.
 //
@@ -19,9 +20,9 @@
 // all its heads; its loads are issued before that, so that the trigonometry
 // hides behind them.  Instructions count as well as bytes: with 16-bit elements
 // converted one by one, units placed by integer divisions and 16 KB in flight per
-// block at two blocks an SM, 8,192 tokens of 64 bf16 heads took 47 us; converted in
-// pairs, placed by multiplications and at four blocks an SM they take 24 us (5.5
-// TB/s), fp32 heads 44 us (6.1 TB/s).
+// block at two blocks an SM, 8,192 tokens of 64 bf16 heads took 38-41 us; converted in
+// pairs, placed by multiplications and at four blocks an SM they take 24-25 us (5.5
+// TB/s), fp32 heads 40-44 us (6.1-6.7 TB/s).
 #include <cuda_fp16.h>
 
 #include "plmla_internal.cuh"
@@ -272,8 +273,8 @@ bool rope_vectors(const RopeArgs &a, int vec, int size)
            a.head_stride % vec == 0 && a.out_tok_stride % vec == 0 && a.out_head_stride % vec == 0;
 }
 
-// The widest of the three accesses that the addresses, strides and the head's
-// half allow: 16 bytes, or single elements.
+// 16-byte accesses where the addresses, the strides and the head's half allow them,
+// else single elements.
 template <typename T>
 cudaError_t launch_typed(RopeArgs a, bool inter, int sms, cudaStream_t stream)
 {
