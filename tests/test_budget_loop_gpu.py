@@ -27,7 +27,7 @@ def _ints(a):
 
 
 def test_evictions_one_after_another():
-    """Three rounds of appends, decodes and accumulations, an eviction after each.
+    """Appends, decodes and accumulations, three times over with an eviction after each.
     Every step adds its H rows' weights (the decode's lse is within 1e-3: a row's
     weights sum to 1 within e^(2e-3) - 1), the tokens appended since an eviction
     among them; each eviction keeps the newest tokens; one history stays below the
