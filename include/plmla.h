@@ -848,6 +848,104 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
                                float *mass_out, int64_t mass_out_ld, int32_t *status,
                                void *stream);
 
+/*
+ * ---- several continuations of one prompt ------------------------------------
+ *
+ * Histories that go on from one another (the beams of a search, several answers to
+ * a prompt) share pages.  A pool's pages are owned by counts: ref_counts[p], int32
+ * [num_pages] on the device, is the number of rows (of any table) that hold page p;
+ * a page of count 0 is free.  A row of history length L holds the pages of its first
+ * ceil(L / 1536) columns.  The caller sets the counts of pages that it hands out
+ * itself; all other state is in the tables and lengths.  Calls on one pool must not run
+ * at once: they belong on one stream, or ordered by events.  Results depend on
+ * the arguments alone.
+ *
+ * status, in these calls, is an optional device int32 as in mla_kv_append:
+ *   32  a negative length or number of new tokens (the row is left as it is)
+ *   33  a page outside the pool (it is not counted), or a history longer than a row of
+ *       its table (a source row counts as empty, a row that gives up pages gives up those it has)
+ *   35  no free page (the row, and those after it that need pages, are left as they are)
+ *   36  a parent >= num_rows (the out row becomes empty)
+ *   37  a page that a row holds but whose count is 0 (the count stays 0)
+ *
+ * mla_pages_fork -- row i of out_table becomes the history of row parents[i] of
+ * page_table (parents[i] < 0: an empty one), with the same pages: what the out row held
+ * before is given up, as when one counted pointer is assigned to another.  No cache
+ * row is copied; mla_pages_reserve does that for the partly filled page before the
+ * histories grow apart.
+ *
+ * page_table, seq_lens    num_rows (1 .. 1024) rows of page_table_cols (1 ..
+ *                         page_table_ld) columns, not changed
+ * parents                 int32 [out_rows]; out_rows 1 .. 1024
+ * out_table, out_lens     rows and lengths, updated; out_lens must hold valid lengths on
+ *                         entry (0 for rows without pages).  Columns past a
+ *                         history's pages are not written.  They must not overlap
+ *                         page_table and seq_lens.
+ */
+plmla_status mla_pages_fork(const int32_t *page_table, int64_t page_table_ld,
+                            int64_t page_table_cols, const int32_t *seq_lens, int32_t num_rows,
+                            const int32_t *parents, int32_t out_rows, int32_t *ref_counts,
+                            int64_t num_pages, int32_t *out_table, int64_t out_table_ld,
+                            int64_t out_table_cols, int32_t *out_lens, int32_t *status,
+                            void *stream);
+
+/* mla_pages_free -- every row gives up its pages; seq_lens becomes 0. */
+plmla_status mla_pages_free(const int32_t *page_table, int64_t page_table_ld,
+                            int64_t page_table_cols, int32_t *seq_lens, int32_t num_rows,
+                            int32_t *ref_counts, int64_t num_pages, int32_t *status, void *stream);
+
+/*
+ * mla_pages_reserve -- room for new tokens behind every history, so that an append
+ * may write them: rows in order take free pages (the lowest first) for columns
+ * ceil(L / 1536) .. ceil((L + n) / 1536) - 1, and a row whose last page is partly filled
+ * and held by others too takes one more, into which the page's rows (of every layer) are copied
+ * first.  Of several rows that share such a page the last keeps it.
+ *
+ * slab_base, elem_bytes, page_stride_elems   the layers' pools as in mla_kv_compact
+ * seq_lens     int32 [num_reqs]: the histories BEFORE the new tokens (num_reqs 1 .. 1024)
+ * n_new        >= 0 for every row, or per row in n_new_of (int32 [num_reqs], device, may be
+ *              NULL); a row with 0 is left as it is
+ * workspace    device scratch of at least mla_pages_workspace_size(num_reqs) bytes, 256-byte
+ *              aligned, contents irrelevant; calls that may run at once need one each
+ * A row whose pages cannot be had (35) must not be appended to: its last page may be shared.
+ */
+size_t mla_pages_workspace_size(int32_t num_reqs);
+plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base, int32_t elem_bytes,
+                               int64_t num_pages, int64_t page_stride_elems, int32_t *page_table,
+                               int64_t page_table_ld, int64_t page_table_cols,
+                               const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+                               const int32_t *n_new_of, int32_t *ref_counts, void *workspace,
+                               size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * mla_beam_select -- beam search's step: of the candidates
+ *   cand[b, k, v] = scores[b, k] + logits[b, k, v] - ln sum_u exp(logits[b, k, u])
+ * of batch entry b the `beams` largest in descending order, ties to the lowest
+ * k * vocab + v.  A beam with ended[b, k] != 0 offers end_token alone, at scores[b, k]; a beam
+ * whose score or log-sum-exp is not finite (an unused beam: -inf; a row with NaN)
+ * offers nothing.  What is not offered counts as -inf, in the order of ties.
+ *
+ * logits       dtype (PLMLA_BF16, PLMLA_FP16, PLMLA_FP32), row b * beams + k at logits +
+ *              row * logits_ld elements, logits_ld >= vocab
+ * batch, beams beams 1 .. 64, batch * beams <= 65535, beams * vocab < 2^31
+ * ended        uint8 [batch * beams], or NULL;  end_token 0 .. vocab - 1 where it is given
+ * tokens       int32 [batch * beams]: v
+ * parents      int32 [batch * beams]: the row b * beams + k it goes on from (as
+ *              mla_pages_fork takes it)
+ * out_scores   fp32 [batch * beams]: the candidates; must not be scores
+ * workspace    device scratch of at least mla_beam_workspace_size(...) bytes (of the current
+ *              device), 256-byte aligned, contents irrelevant; calls that may run at once
+ *              need one each
+ * Log-sum-exps and candidates are held in 64 bits, so the order is that of the formula
+ * wherever candidates differ by 1e-6 or more.  Deterministic.
+ */
+size_t mla_beam_workspace_size(int32_t batch, int32_t beams, int32_t vocab);
+plmla_status mla_beam_select(const void *logits, int64_t logits_ld, int32_t dtype,
+                             const float *scores, const uint8_t *ended, int32_t end_token,
+                             int32_t batch, int32_t beams, int32_t vocab, int32_t *tokens,
+                             int32_t *parents, float *out_scores, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

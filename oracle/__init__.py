@@ -29,3 +29,8 @@ from .budget import (  # noqa: F401
     rope_frequencies,
     rope_rotate,
 )
+from .branch import (  # noqa: F401
+    beam_select,
+    pages_fork,
+    pages_reserve,
+)

@@ -943,3 +943,187 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
             _vector(seq_lens, "seq_lens", dev, R), *outs, idx, idx_ld,
             _vector(kept_lens, "kept_lens", dev, R), R, cols, *carried, _flag(status, dev))
     return mass_out
+
+
+# ---------------------------------------------------------------------------
+# several continuations of one prompt
+# ---------------------------------------------------------------------------
+
+
+def _counts(ref_counts, dev):
+    """(address, pages) of a pool's counts."""
+    if not (ref_counts.dtype is _I32 and ref_counts.get_device() == dev
+            and ref_counts.dim() == 1 and ref_counts.is_contiguous()):
+        _fail(f"ref_counts must be a contiguous int32 tensor [num_pages] on cuda:{dev}")
+    return ref_counts.data_ptr(), ref_counts.shape[0]
+
+
+def _disjoint(a, b, message):
+    """Refuses two contiguous vectors that share bytes."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    if (a0 < b0 + b.numel() * b.element_size() and b0 < a0 + a.numel() * a.element_size()):
+        _fail(message)
+
+
+def mla_pages_fork(page_table, seq_lens, parents, ref_counts, out_table, out_lens, *, status=None,
+                   stream=None):
+    """Row i of out_table [N, columns] becomes the history of row parents[i] (int32
+    [N]; negative: an empty history) of page_table [R, columns], with the same pages;
+    what the out row held before is given up.  ref_counts int32 [num_pages] follows:
+    the rows that hold each page (0: free).  out_lens int32 [N] must hold the out
+    rows' lengths on entry, 0 where they hold nothing (zeros, at first).  No cache
+    row moves: mla_pages_reserve copies the partly filled page before the histories
+    grow apart.  ``status``: optional CUDA int32 tensor of one element, set to 33
+    (a page outside the pool, or a table too short), 36 (a parent that is no row) or 37 (a
+    held page whose count is 0).  Returns (out_table, out_lens).  Asynchronous; calls
+    on one pool belong on one stream."""
+    dev = page_table.get_device()
+    if dev < 0 or seq_lens.dim() != 1 or parents.dim() != 1:
+        _fail("page_table [R, columns], seq_lens [R] and parents [N] must be CUDA tensors")
+    R, N = seq_lens.shape[0], parents.shape[0]
+    src = _rows(page_table, "page_table", dev, _I32, R)
+    lens = _vector(seq_lens, "seq_lens", dev, R)
+    at = _vector(parents, "parents", dev, N)
+    counts = _counts(ref_counts, dev)
+    dst = _rows(out_table, "out_table", dev, _I32, N)
+    got = _vector(out_lens, "out_lens", dev, N)
+    if R and N:
+        _check_apart(page_table, out_table, "out_table must not overlap page_table")
+        _disjoint(seq_lens, out_lens, "out_lens must not overlap seq_lens")
+    _launch(dev, _native.lib().mla_pages_fork, "mla_pages_fork", stream, *src, lens, R, at, N,
+            *counts, *dst, got, _flag(status, dev))
+    return out_table, out_lens
+
+
+def mla_pages_free(page_table, seq_lens, ref_counts, *, status=None, stream=None):
+    """Every row of page_table [R, columns] gives up its pages: their ref_counts go
+    down by one and seq_lens becomes 0.  ``status`` as in mla_pages_fork (33, 37).
+    Asynchronous."""
+    dev = page_table.get_device()
+    if dev < 0 or seq_lens.dim() != 1:
+        _fail("page_table [R, columns] and seq_lens [R] must be CUDA tensors")
+    R = seq_lens.shape[0]
+    _launch(dev, _native.lib().mla_pages_free, "mla_pages_free", stream,
+            *_rows(page_table, "page_table", dev, _I32, R),
+            _vector(seq_lens, "seq_lens", dev, R), R, *_counts(ref_counts, dev),
+            _flag(status, dev))
+
+
+def mla_pages_reserve(slabs, page_table, seq_lens, n_new, ref_counts, *, workspace=None,
+                      status=None, stream=None):
+    """Room for ``n_new`` tokens (an int, or int32 [R]) behind every history, so that
+    an append may write them: free pages, the lowest first, go into page_table's next
+    columns, and a partly filled last page that other rows hold too is copied (in
+    every layer's pool of ``slabs``: bf16, or uint8 / float8_e4m3fn) into a page of
+    the row's own; of several rows that share one the last keeps it.  seq_lens holds
+    the histories before the new tokens, and stays.  ``status``: optional CUDA int32
+    tensor of one element, set to 32 (a negative length or count), 33 (a table too
+    short, or a page outside the pool), 35 (no free page: this row and the later ones
+    that need pages are left as they are and must not be appended to) or 37.  The
+    workspace (uint8, mla_pages_workspace_size; a new one by default) must not be shared by
+    calls that may run at once.  Returns page_table.  Asynchronous."""
+    if not isinstance(slabs, (list, tuple)) or not slabs:
+        _fail("slabs must be a list of pools")
+    first = slabs[0]
+    dtype, fp8 = first.dtype, first.dtype is not _BF16
+    base, pages, page_stride = _pool(first, fp8)
+    dev, layers = first.get_device(), len(slabs)
+    bases = (ctypes.c_void_p * layers)(base)
+    shape, strides = first.shape, first.stride()
+    for i in range(1, layers):
+        s = slabs[i]
+        if not (s.dtype is dtype and s.get_device() == dev and s.shape == shape
+                and s.stride() == strides):
+            _fail("the layers' slabs must share their type, shape and strides")
+        bases[i] = s.data_ptr()
+    R = seq_lens.shape[0] if seq_lens.dim() == 1 else 0
+    ids = _rows(page_table, "page_table", dev, _I32, R)
+    lens = _vector(seq_lens, "seq_lens", dev, R)
+    each, new = 0, None
+    if isinstance(n_new, torch.Tensor):
+        new = _vector(n_new, "n_new", dev, R)
+    else:
+        each = int(n_new)
+        if not 0 <= each < 1 << 31:
+            _fail("n_new must be >= 0")
+    counts, have = _counts(ref_counts, dev)
+    if have != pages:
+        _fail(f"ref_counts must have an entry for each of the pool's {pages} pages")
+    lib = _native.lib()
+    if workspace is None:
+        workspace = _empty(lib.mla_pages_workspace_size(R), _U8, first.device, stream)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _fail(f"workspace must be contiguous memory on cuda:{dev}")
+    _launch(dev, lib.mla_pages_reserve, "mla_pages_reserve", stream, layers, bases,
+            1 if fp8 else 2, pages, page_stride, *ids, lens, R, each, new, counts,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _flag(status, dev))
+    return page_table
+
+
+def _beam_workspace_size(dev, batch, beams, vocab):
+    """The size depends on the device that the call will run on."""
+    size = _native.lib().mla_beam_workspace_size
+    if dev == torch._C._cuda_getDevice():
+        return size(batch, beams, vocab)
+    with torch.cuda.device(dev):
+        return size(batch, beams, vocab)
+
+
+def allocate_beam_workspace(batch, beams, vocab, device=None):
+    """A workspace tensor (uint8) of the size mla_beam_select needs."""
+    device = torch.device(device or "cuda")
+    dev = torch.cuda.current_device() if device.index is None else device.index
+    n = _beam_workspace_size(dev, batch, beams, vocab)
+    if n == 0:
+        _fail("invalid shape for mla_beam_workspace_size")
+    return torch.empty(n, dtype=_U8, device=device)
+
+
+def mla_beam_select(logits, scores, *, ended=None, end_token=-1, tokens=None, parents=None,
+                    out_scores=None, workspace=None, stream=None):
+    """Beam search's step: logits [B*K, vocab] (bf16, fp16 or fp32; rows at any
+    stride) of the beams with scores [B, K] fp32.  Of each batch entry's candidates
+    scores + log_softmax(logits) the K largest, in descending order (ties to the
+    lowest beam, then token): returns (tokens [B, K] int32, parents [B, K] int32,
+    scores [B, K] fp32), where parents are rows of logits, as mla_pages_fork takes
+    them (parents.view(-1)).  ``ended`` bool [B, K] marks beams that offer
+    ``end_token`` alone, at their score; a beam whose score is -inf, or whose logits
+    hold NaN, offers nothing.  K is at most 64.  Tensors that require grad are
+    refused while gradients are recorded.  The workspace comes from
+    allocate_beam_workspace (a new one by default); calls that may run at once need
+    one each.  Asynchronous."""
+    kind = _ROPE_TYPES.get(logits.dtype)
+    dev = logits.get_device()
+    if kind is None or dev < 0 or logits.dim() != 2 or scores.dim() != 2:
+        _fail("logits must be a CUDA bf16, fp16 or fp32 tensor [B*K, vocab], scores [B, K]")
+    if torch.is_grad_enabled() and (logits.requires_grad or scores.requires_grad):
+        _fail("mla_beam_select is not recorded by autograd: call it under torch.no_grad() or on "
+              "detached tensors")
+    B, K = scores.shape
+    shape = (B, K)
+    rows = _rows(logits, "logits", dev, logits.dtype, B * K)
+    have = _dense(scores, "scores", dev, shape, _F32)
+    flags = None
+    if ended is not None:
+        if ended.dtype is not torch.bool and ended.dtype is not _U8:
+            _fail("ended must be a bool (or uint8) tensor")
+        flags = _dense(ended, "ended", dev, shape, ended.dtype)
+    if tokens is None:
+        tokens = _empty(shape, _I32, logits.device, stream)
+    if parents is None:
+        parents = _empty(shape, _I32, logits.device, stream)
+    if out_scores is None:
+        out_scores = _empty(shape, _F32, logits.device, stream)
+    else:
+        _disjoint(scores, out_scores, "out_scores must not overlap scores")
+    out = (_dense(tokens, "tokens", dev, shape, _I32), _dense(parents, "parents", dev, shape, _I32),
+           _dense(out_scores, "out_scores", dev, shape, _F32))
+    if workspace is None:
+        workspace = _empty(_beam_workspace_size(dev, B, K, rows[2]), _U8, logits.device, stream)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _fail(f"workspace must be contiguous memory on cuda:{dev}")
+    _launch(dev, _native.lib().mla_beam_select, "mla_beam_select", stream, rows[0], rows[1], kind,
+            have, flags, int(end_token), B, K, rows[2], *out, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return tokens, parents, out_scores

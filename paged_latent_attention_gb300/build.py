@@ -33,6 +33,9 @@ SOURCES = [
     "plmla_rope.cu",
     "plmla_mass.cu",
     "plmla_evict.cu",
+    "plmla_pages.cu",
+    "plmla_beam.cu",
+    "plmla_branch_abi.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

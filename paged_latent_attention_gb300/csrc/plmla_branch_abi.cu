@@ -1,0 +1,178 @@
+// plmla_branch_abi.cu -- host side of the entries for several continuations of one prompt
+// (page ownership, beam selection), declared in include/plmla.h.
+//
+// Arguments are checked and the kernels enqueued on the caller's stream; nothing here
+// allocates device memory, synchronises, or reads device data back.
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "plmla.h"
+#include "plmla_internal.cuh"
+
+using namespace plmla;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// SMs of the current device (kept per device), or 0.
+int device_sms()
+{
+    static std::atomic<int> cached[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0)
+        return 0;
+    if (dev < 64 && (sms = cached[dev].load(std::memory_order_relaxed)) > 0)
+        return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    if (dev < 64)
+        cached[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
+
+bool table_ok(const int32_t *table, int64_t ld, int64_t cols, int32_t rows)
+{
+    return table != nullptr && aligned(table, 4) && cols >= 1 && ld >= cols && rows >= 1 &&
+           rows <= kMaxReqs;
+}
+
+bool words_ok(const int32_t *p) { return p != nullptr && aligned(p, 4); }
+
+bool counts_ok(const int32_t *counts, int64_t num_pages, const int32_t *status)
+{
+    return words_ok(counts) && num_pages >= 1 && num_pages <= INT32_MAX &&
+           (status == nullptr || aligned(status, 4));
+}
+
+plmla_status result(cudaError_t err) { return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR; }
+
+}  // namespace
+
+extern "C" plmla_status mla_pages_fork(const int32_t *page_table, int64_t page_table_ld,
+                                       int64_t page_table_cols, const int32_t *seq_lens,
+                                       int32_t num_rows, const int32_t *parents, int32_t out_rows,
+                                       int32_t *ref_counts, int64_t num_pages, int32_t *out_table,
+                                       int64_t out_table_ld, int64_t out_table_cols,
+                                       int32_t *out_lens, int32_t *status, void *stream)
+{
+    if (!table_ok(page_table, page_table_ld, page_table_cols, num_rows) ||
+        !table_ok(out_table, out_table_ld, out_table_cols, out_rows) || !words_ok(seq_lens) ||
+        !words_ok(parents) || !words_ok(out_lens) || !counts_ok(ref_counts, num_pages, status) ||
+        out_table == page_table || out_lens == seq_lens)
+        return PLMLA_INVALID_ARGUMENT;
+    const ForkArgs a = {page_table, page_table_ld, page_table_cols, seq_lens, num_rows,
+                        parents,    out_rows,      out_table,       out_table_ld, out_table_cols,
+                        out_lens,   ref_counts,    num_pages,       status};
+    return result(launch_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" plmla_status mla_pages_free(const int32_t *page_table, int64_t page_table_ld,
+                                       int64_t page_table_cols, int32_t *seq_lens,
+                                       int32_t num_rows, int32_t *ref_counts, int64_t num_pages,
+                                       int32_t *status, void *stream)
+{
+    if (!table_ok(page_table, page_table_ld, page_table_cols, num_rows) || !words_ok(seq_lens) ||
+        !counts_ok(ref_counts, num_pages, status))
+        return PLMLA_INVALID_ARGUMENT;
+    return result(launch_free(page_table, page_table_ld, page_table_cols, seq_lens, num_rows,
+                              ref_counts, num_pages, status, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t mla_pages_workspace_size(int32_t num_reqs)
+{
+    if (num_reqs < 1 || num_reqs > kMaxReqs)
+        return 0;
+    return kAlign + align_up(sizeof(int4) * (size_t)num_reqs);
+}
+
+extern "C" plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base,
+                                          int32_t elem_bytes, int64_t num_pages,
+                                          int64_t page_stride_elems, int32_t *page_table,
+                                          int64_t page_table_ld, int64_t page_table_cols,
+                                          const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+                                          const int32_t *n_new_of, int32_t *ref_counts,
+                                          void *workspace, size_t workspace_bytes, int32_t *status,
+                                          void *stream)
+{
+    if (num_layers < 1 || num_layers > kMaxLayers || slab_base == nullptr ||
+        (elem_bytes != 1 && elem_bytes != 2) ||
+        page_stride_elems < (int64_t)kPageTokens * kRow ||
+        page_stride_elems % (elem_bytes == 1 ? 16 : 8) != 0 ||
+        !table_ok(page_table, page_table_ld, page_table_cols, num_reqs) || !words_ok(seq_lens) ||
+        (n_new_of == nullptr ? n_new < 0 : !aligned(n_new_of, 4)) ||
+        !counts_ok(ref_counts, num_pages, status) || workspace == nullptr ||
+        !aligned(workspace, kAlign))
+        return PLMLA_INVALID_ARGUMENT;
+    for (int32_t l = 0; l < num_layers; ++l)
+        if (slab_base[l] == nullptr || !aligned(slab_base[l], 16))
+            return PLMLA_INVALID_ARGUMENT;
+    if (workspace_bytes < mla_pages_workspace_size(num_reqs))
+        return PLMLA_WORKSPACE_TOO_SMALL;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return PLMLA_CUDA_ERROR;
+    ReserveArgs a = {};
+    a.table = page_table;
+    a.ld = page_table_ld;
+    a.cols = page_table_cols;
+    a.lens = seq_lens;
+    a.num_reqs = num_reqs;
+    a.n_new = n_new;
+    a.n_new_of = n_new_of;
+    a.counts = ref_counts;
+    a.num_pages = num_pages;
+    a.num_jobs = static_cast<int32_t *>(workspace);
+    a.jobs = reinterpret_cast<int4 *>(static_cast<unsigned char *>(workspace) + kAlign);
+    a.status = status;
+    return result(launch_reserve(a, num_layers, slab_base, elem_bytes == 1,
+                                 page_stride_elems * elem_bytes, sms,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool beams_ok(int32_t batch, int32_t beams, int32_t vocab)
+{
+    return batch >= 1 && beams >= 1 && beams <= kMaxBeams && vocab >= 1 &&
+           (int64_t)batch * beams <= kMaxBeamRows && (int64_t)beams * vocab <= INT32_MAX;
+}
+
+}  // namespace
+
+extern "C" size_t mla_beam_workspace_size(int32_t batch, int32_t beams, int32_t vocab)
+{
+    const int sms = device_sms();
+    return beams_ok(batch, beams, vocab) && sms > 0 ? beam_workspace(batch, beams, vocab, sms) : 0;
+}
+
+extern "C" plmla_status mla_beam_select(const void *logits, int64_t logits_ld, int32_t dtype,
+                                        const float *scores, const uint8_t *ended,
+                                        int32_t end_token, int32_t batch, int32_t beams,
+                                        int32_t vocab, int32_t *tokens, int32_t *parents,
+                                        float *out_scores, void *workspace, size_t workspace_bytes,
+                                        void *stream)
+{
+    if (!beams_ok(batch, beams, vocab) || logits_ld < vocab ||
+        (dtype != PLMLA_BF16 && dtype != PLMLA_FP16 && dtype != PLMLA_FP32) ||
+        logits == nullptr || !aligned(logits, dtype == PLMLA_FP32 ? 4 : 2) || scores == nullptr ||
+        !aligned(scores, 4) || (ended != nullptr && (end_token < 0 || end_token >= vocab)) ||
+        !words_ok(tokens) || !words_ok(parents) || out_scores == nullptr ||
+        !aligned(out_scores, 4) || out_scores == scores || workspace == nullptr ||
+        !aligned(workspace, kAlign))
+        return PLMLA_INVALID_ARGUMENT;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return PLMLA_CUDA_ERROR;
+    if (workspace_bytes < beam_workspace(batch, beams, vocab, sms))
+        return PLMLA_WORKSPACE_TOO_SMALL;
+    const BeamArgs a = {logits, logits_ld, dtype, scores, ended, end_token, batch,
+                        beams,  vocab,     tokens, parents, out_scores};
+    return result(launch_beams(a, workspace, sms, static_cast<cudaStream_t>(stream)));
+}

@@ -187,6 +187,57 @@ cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t
                            int64_t mass_ld, int64_t mass_cols, float *mass_out,
                            int64_t mass_out_ld, int32_t *status, cudaStream_t stream);
 
+// Page ownership (plmla_pages.cu).
+constexpr int32_t kStatusNoPage = 35;           // no free page left
+constexpr int32_t kStatusParent = 36;           // a parent that is no row
+constexpr int32_t kStatusPageCount = 37;        // a held page that is not counted
+struct ForkArgs {
+    const int32_t *table;
+    int64_t ld, cols;
+    const int32_t *lens;
+    int rows;
+    const int32_t *parents;
+    int out_rows;
+    int32_t *out_table;
+    int64_t out_ld, out_cols;
+    int32_t *out_lens, *counts;
+    int64_t num_pages;
+    int32_t *status;                    // may be null
+};
+cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream);
+cudaError_t launch_free(const int32_t *table, int64_t ld, int64_t cols, int32_t *lens, int rows,
+                        int32_t *counts, int64_t num_pages, int32_t *status, cudaStream_t stream);
+struct ReserveArgs {
+    int32_t *table;
+    int64_t ld, cols;
+    const int32_t *lens;
+    int num_reqs, n_new;
+    const int32_t *n_new_of;            // per row, or null: n_new for all
+    int32_t *counts;
+    int64_t num_pages;
+    int4 *jobs;                         // workspace: [num_reqs] copies (from, to, rows)
+    int32_t *num_jobs;                  // workspace: how many
+    int32_t *status;                    // may be null
+};
+cudaError_t launch_reserve(const ReserveArgs &a, int num_layers, void *const *slabs, bool fp8,
+                           int64_t page_bytes, int sms, cudaStream_t stream);
+
+// Beam selection (plmla_beam.cu).
+constexpr int kMaxBeams = 64;
+constexpr int kMaxBeamRows = 65535;             // batch * beams
+struct BeamArgs {
+    const void *logits;                 // [batch * beams] rows of `vocab`, stride ld
+    int64_t ld;
+    int type;                           // kRopeBf16, kRopeFp16 or kRopeFp32
+    const float *scores;                // [batch * beams]
+    const uint8_t *ended;               // [batch * beams], may be null
+    int end_token, batch, beams, vocab;
+    int32_t *tokens, *parents;          // [batch * beams]
+    float *out_scores;
+};
+size_t beam_workspace(int batch, int beams, int vocab, int sms);
+cudaError_t launch_beams(const BeamArgs &a, void *workspace, int sms, cudaStream_t stream);
+
 // Shared by the query quantiser (plan grid) and the FP8 append: one E4M3 byte
 // pair from two floats, round to nearest even, saturating to +-448.
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)

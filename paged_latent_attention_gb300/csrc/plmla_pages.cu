@@ -1,0 +1,365 @@
+// plmla_pages.cu -- ownership of cache pages by counts: histories that share pages are
+// forked, released, and given room to grow, on the device.
+//
+//   counts[p] = the table rows (and other holders) that hold page p; 0 = free
+//   fork      out[i] <- table[parents[i]]: counts follow, no row of the cache moves
+//   free      counts[p] -= 1 for every page of a row; its history becomes empty
+//   reserve   room for n new tokens behind every history: free pages in ascending order,
+//             and a partly filled last page that others hold too is copied first
+//             (in row order; the last of its holders keeps it)
+//
+// A pool has no other state than its counts: the free pages are found by a scan, which for
+// the pools that fit a GPU (160,000 pages of 1.77 MB at most) costs microseconds and keeps
+// the result a function of the arguments, whatever was freed in which order.
+//
+// Fork and free: one block per row, a page per thread; atomics on counts add up to the
+// same whole numbers in any order.  A page that an out row already holds in the same place
+// stays without touching its count (continuations share all but their last pages).  Both
+// are latency-bound: three dependent loads and an atomic.
+//
+// Reserve: one block plans (rows in threads, prefix sums, 16,384 counts a sweep), then a grid
+// of blocks copies the planned pages, one contiguous piece per (row, layer), at the copy
+// rate of HBM.  The copy is launched programmatically behind the plan.
+#include "plmla_internal.cuh"
+
+namespace plmla {
+namespace {
+
+constexpr int kForkThreads = 128;
+constexpr int kReserveThreads = 1024;
+constexpr int kSweep = 16 * kReserveThreads;    // counts that the block looks at together
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 4;                    // 16-byte vectors of a thread in flight
+constexpr int kCopyPiece = kCopyThreads * kCopyVecs;
+
+__device__ __forceinline__ void report(int32_t *status, int32_t code)
+{
+    if (status != nullptr)
+        atomicExch(status, code);
+}
+
+__device__ __forceinline__ void hold(int32_t *counts, int64_t num_pages, int page, int32_t *status)
+{
+    if (page < 0 || page >= num_pages)
+        report(status, kStatusAppendPage);
+    else
+        atomicAdd(counts + page, 1);
+}
+
+// A holder of the page finds it counted: what other rows of this launch give up never takes
+// the count below the holders that remain.
+__device__ __forceinline__ void give_up(int32_t *counts, int64_t num_pages, int page,
+                                        int32_t *status)
+{
+    if (page < 0 || page >= num_pages) {
+        report(status, kStatusAppendPage);
+    } else if (atomicSub(counts + page, 1) <= 0) {
+        atomicAdd(counts + page, 1);
+        report(status, kStatusPageCount);
+    }
+}
+
+__device__ __forceinline__ int pages_of(int len) { return len <= 0 ? 0 : (len - 1) / kPageTokens + 1; }
+
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a)
+{
+    const int i = blockIdx.x;
+    int32_t *out = a.out_table + (int64_t)i * a.out_ld;
+    const int parent = a.parents[i];
+    int old = pages_of(a.out_lens[i]), len = 0;
+    if (old > a.out_cols) {
+        old = (int)a.out_cols;
+        if (threadIdx.x == 0)
+            report(a.status, kStatusAppendPage);
+    }
+    if (parent >= 0 && parent < a.rows)
+        len = max(0, a.lens[parent]);
+    else if (parent >= a.rows && threadIdx.x == 0)
+        report(a.status, kStatusParent);
+    int pages = pages_of(len);
+    if (pages > a.cols || pages > a.out_cols) {
+        pages = len = 0;
+        if (threadIdx.x == 0)
+            report(a.status, kStatusAppendPage);
+    }
+    const int32_t *from = a.table + (int64_t)parent * a.ld;
+    for (int c = threadIdx.x; c < max(old, pages); c += kForkThreads) {
+        const int was = c < old ? out[c] : 0, now = c < pages ? from[c] : 0;
+        if (c < old && c < pages && was == now)
+            continue;
+        if (c < old)
+            give_up(a.counts, a.num_pages, was, a.status);
+        if (c < pages) {
+            hold(a.counts, a.num_pages, now, a.status);
+            out[c] = now;
+        }
+    }
+    __syncthreads();                            // every thread has read out_lens
+    if (threadIdx.x == 0)
+        a.out_lens[i] = len;
+}
+
+__global__ void __launch_bounds__(kForkThreads)
+free_kernel(const int32_t *table, int64_t ld, int64_t cols, int32_t *lens, int32_t *counts,
+            int64_t num_pages, int32_t *status)
+{
+    const int r = blockIdx.x;
+    int pages = pages_of(lens[r]);
+    if (pages > cols) {
+        pages = (int)cols;
+        if (threadIdx.x == 0)
+            report(status, kStatusAppendPage);
+    }
+    for (int c = threadIdx.x; c < pages; c += kForkThreads)
+        give_up(counts, num_pages, table[(int64_t)r * ld + c], status);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        lens[r] = 0;
+}
+
+// Exclusive prefix sum over the block's threads, and the total.
+__device__ __forceinline__ int block_scan(int v, int *warp_sum, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();                            // warp_sum of an earlier scan has been read
+    if (lane == 31)
+        warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = warp_sum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o)
+                s += y;
+        }
+        warp_sum[lane] = s;
+    }
+    __syncthreads();
+    *total = warp_sum[31];
+    return x - v + (warp == 0 ? 0 : warp_sum[warp - 1]);
+}
+
+// Which of the 16 pages from `first` on are free, a bit each.
+__device__ __forceinline__ uint32_t free_bits(const int32_t *counts, int64_t first, int64_t num_pages)
+{
+    uint32_t bits = 0;
+    if (first + 16 <= num_pages && (reinterpret_cast<uintptr_t>(counts) & 15u) == 0) {
+        const int4 *p = reinterpret_cast<const int4 *>(counts + first);
+        int4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = p[j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bits |= ((v[j].x == 0) | (v[j].y == 0) << 1 | (v[j].z == 0) << 2 | (v[j].w == 0) << 3)
+                    << (4 * j);
+    } else {
+        for (int j = 0; j < 16; ++j)
+            if (first + j < num_pages && counts[first + j] == 0)
+                bits |= 1u << j;
+    }
+    return bits;
+}
+
+__global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveArgs a)
+{
+    __shared__ int warp_sum[32];
+    __shared__ int last_sm[kMaxReqs];           // shared last page of a row, or -1
+    __shared__ int end_sm[kMaxReqs];            // pages that rows 0 .. r need together
+    __shared__ int col_sm[kMaxReqs];            // column of the row's first page needed
+    __shared__ int job_sm[kMaxReqs];            // the row's copy, or -1
+    __shared__ int granted;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int r = threadIdx.x;
+    int need = 0, part = 0, last = -1, holders = 0, col = 0;
+    bool parts = false;                         // the last page has other holders
+    if (r < a.num_reqs) {
+        const int len = a.lens[r];
+        const int add = a.n_new_of != nullptr ? a.n_new_of[r] : a.n_new;
+        const int64_t want = ((int64_t)len + add + kPageTokens - 1) / kPageTokens;
+        if (len < 0 || add < 0) {
+            report(a.status, kStatusAppendPosition);
+        } else if (want > a.cols) {
+            report(a.status, kStatusAppendPage);
+        } else if (add > 0) {
+            part = len % kPageTokens;
+            col = pages_of(len);
+            need = (int)want - col;
+            if (part != 0) {
+                last = a.table[(int64_t)r * a.ld + col - 1];
+                if (last < 0 || last >= a.num_pages) {
+                    report(a.status, kStatusAppendPage);
+                    need = 0;
+                } else {
+                    holders = a.counts[last];
+                    parts = holders > 1;
+                    if (holders < 1)
+                        report(a.status, kStatusPageCount);
+                }
+            }
+        }
+    }
+    last_sm[r] = parts ? last : -1;
+    if (__syncthreads_or(parts) && parts) {
+        int earlier = 0;
+        for (int j = 0; j < r; ++j)
+            earlier += last_sm[j] == last ? 1 : 0;
+        parts = holders - earlier > 1;          // the last holder keeps the page
+    }
+    need += parts ? 1 : 0;
+    int total, jobs;
+    const int first = block_scan(need, warp_sum, &total);
+    int job = block_scan(parts ? 1 : 0, warp_sum, &jobs);
+    end_sm[r] = first + need;
+    col_sm[r] = col - (parts ? 1 : 0);
+    job_sm[r] = parts ? job : -1;
+    if (r == 0)
+        granted = 0;
+    __syncthreads();
+
+    // the free pages that there are, as far as they are needed
+    uint32_t bits = 0;
+    int found = 0, rank = 0;
+    int64_t base = 0;
+    for (; base < a.num_pages && found < total; base += kSweep) {
+        bits = free_bits(a.counts, base + 16 * r, a.num_pages);
+        int here;
+        rank = found + block_scan(__popc(bits), warp_sum, &here);
+        found += here;
+    }
+    const bool served = need > 0 && first + need <= found;
+    if (need > 0 && !served)
+        report(a.status, kStatusNoPage);
+    if (served)
+        atomicMax(&granted, first + need);
+    if (parts && served) {
+        a.jobs[job].x = last;
+        a.jobs[job].z = part;
+        atomicSub(a.counts + last, 1);
+    }
+    const int copies = __syncthreads_count(parts && served);
+    if (r == 0)
+        *a.num_jobs = copies;                   // served rows come first
+    const int most = granted;
+
+    // page number q of them belongs to the row whose pages end past q
+    const bool once = base <= kSweep;           // one sweep: its bits are at hand
+    int before = 0;
+    for (int64_t at = 0; at < base && before < most; at += kSweep) {
+        if (!once) {
+            bits = free_bits(a.counts, at + 16 * r, a.num_pages);
+            int here;
+            rank = before + block_scan(__popc(bits), warp_sum, &here);
+            before += here;
+        } else {
+            before = most;
+        }
+        for (int q = rank; bits != 0 && q < most; ++q, bits &= bits - 1) {
+            const int page = (int)(at + 16 * r) + __ffs(bits) - 1;
+            int lo = 0, hi = a.num_reqs - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (end_sm[mid] > q)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            const int nth = q - (lo == 0 ? 0 : end_sm[lo - 1]);
+            a.table[(int64_t)lo * a.ld + col_sm[lo] + nth] = page;
+            a.counts[page] = 1;
+            if (nth == 0 && job_sm[lo] >= 0)
+                a.jobs[job_sm[lo]].y = page;
+        }
+        __syncthreads();
+    }
+}
+
+struct CopyArgs {
+    void *slab[kCompactLayers];
+    const int4 *jobs;                           // (from, to, rows)
+    const int32_t *num_jobs;
+    int64_t page_bytes;
+    int layers, row_vecs, pieces;               // 16-byte vectors of a row, pieces of a page
+};
+
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const CopyArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t all = (int64_t)*a.num_jobs * a.layers * a.pieces;
+    for (int64_t u = blockIdx.x; u < all; u += gridDim.x) {
+        const int piece = (int)(u % a.pieces);
+        const int layer = (int)(u / a.pieces % a.layers);
+        const int4 job = a.jobs[u / a.pieces / a.layers];
+        const int vecs = job.z * a.row_vecs, v0 = piece * kCopyPiece + (int)threadIdx.x;
+        if (piece * kCopyPiece >= vecs)
+            continue;
+        unsigned char *slab = static_cast<unsigned char *>(a.slab[layer]);
+        const uint4 *src = reinterpret_cast<const uint4 *>(slab + job.x * a.page_bytes);
+        uint4 *dst = reinterpret_cast<uint4 *>(slab + job.y * a.page_bytes);
+        uint4 v[kCopyVecs];
+#pragma unroll
+        for (int j = 0; j < kCopyVecs; ++j)
+            if (v0 + j * kCopyThreads < vecs)
+                v[j] = src[v0 + j * kCopyThreads];
+#pragma unroll
+        for (int j = 0; j < kCopyVecs; ++j)
+            if (v0 + j * kCopyThreads < vecs)
+                dst[v0 + j * kCopyThreads] = v[j];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream)
+{
+    fork_kernel<<<(unsigned)a.out_rows, kForkThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_free(const int32_t *table, int64_t ld, int64_t cols, int32_t *lens, int rows,
+                        int32_t *counts, int64_t num_pages, int32_t *status, cudaStream_t stream)
+{
+    free_kernel<<<(unsigned)rows, kForkThreads, 0, stream>>>(table, ld, cols, lens, counts,
+                                                            num_pages, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_reserve(const ReserveArgs &a, int num_layers, void *const *slabs, bool fp8,
+                           int64_t page_bytes, int sms, cudaStream_t stream)
+{
+    reserve_kernel<<<1, kReserveThreads, 0, stream>>>(a);
+    cudaError_t err = cudaGetLastError();
+    for (int l0 = 0; l0 < num_layers && err == cudaSuccess; l0 += kCompactLayers) {
+        CopyArgs c = {};
+        c.layers = num_layers - l0 < kCompactLayers ? num_layers - l0 : kCompactLayers;
+        for (int l = 0; l < c.layers; ++l)
+            c.slab[l] = slabs[l0 + l];
+        c.jobs = a.jobs;
+        c.num_jobs = a.num_jobs;
+        c.page_bytes = page_bytes;
+        c.row_vecs = (fp8 ? kRow : 2 * kRow) / 16;
+        c.pieces = (kPageTokens * c.row_vecs + kCopyPiece - 1) / kCopyPiece;
+        const int64_t most = (int64_t)a.num_reqs * c.layers * c.pieces;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(most < 8 * sms ? most : 8 * sms));
+        cfg.blockDim = dim3(kCopyThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = l0 == 0 ? 1 : 0;
+        err = cudaLaunchKernelEx(&cfg, page_copy_kernel, c);
+    }
+    return err;
+}
+
+}  // namespace plmla
