@@ -867,7 +867,57 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  *   35  no free page (the row, and those after it that need pages, are left as they are)
  *   36  a parent >= num_rows (the out row becomes empty)
  *   37  a page that a row holds but whose count is 0 (the count stays 0)
+ *   38  groups that are no partition of the requests
+ *   2 .. 15  a wait inside the decode timed out (its outputs are not valid)
  *
+ * mla_decode_shared -- mla_decode for a batch whose requests have prefixes in common: the
+ * tokens that a group of requests shares are read once, with the queries of all its
+ * members.  Same results as mla_decode, up to rounding.
+ *
+ * q_nope_absorbed, q_rope, gate, slab_base, page strides, seq_lens, n_q_per_req, out, lse
+ *               as in mla_decode; num_reqs 1 .. 1024, num_heads 1 .. 128 (any)
+ * page_table    page_table_cols (1 .. page_table_ld) columns a row; a history past them is cut
+ *               off there (status 33), an ID outside the pool reads another page (33)
+ * group_starts  int32 [num_groups + 1], device: group g is requests group_starts[g] ..
+ *               group_starts[g + 1] - 1; ascending from 0 to num_reqs (else status 38, and
+ *               the batch is decoded without sharing).  A group may be one request or
+ *               empty; num_groups 1 .. 1024
+ * shared_lens   int32 [num_groups], device: the first tokens that all members of the group
+ *               have in common, whatever pages hold them (they are read through the table row of the
+ *               group's first request); what exceeds a member's history is not used
+ * scale         finite and > 0
+ * workspace     device scratch of at least mla_shared_workspace_size(...) bytes (of the
+ *               current device; fp8 != 0 for mla_decode_shared_fp8), 256-byte aligned,
+ *               contents irrelevant; calls that may run at once need one each
+ * A row that sees no token gets 0 and -inf.  Groups, lengths and pages are device data, so a
+ * captured call serves changing ones of the same counts.  Deterministic.
+ *
+ * mla_decode_shared_fp8 takes E4M3 pages and kv_scale as mla_decode_fp8 does.  Its
+ * probabilities are multiplied in two E4M3 parts, within 2^-8 of themselves.
+ */
+size_t mla_shared_workspace_size(int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads,
+                                 int32_t num_groups, int32_t fp8);
+plmla_status mla_decode_shared(const void *q_nope_absorbed, const void *q_rope, const void *gate,
+                               const void *slab_base, int64_t num_pages,
+                               int64_t page_stride_elems, const int32_t *page_table,
+                               int64_t page_table_ld, int64_t page_table_cols,
+                               const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req,
+                               int32_t num_heads, const int32_t *group_starts,
+                               const int32_t *shared_lens, int32_t num_groups, float scale,
+                               void *out, float *lse, void *workspace, size_t workspace_bytes,
+                               int32_t *status, void *stream);
+plmla_status mla_decode_shared_fp8(const void *q_nope_absorbed, const void *q_rope,
+                                   const void *gate, const void *slab_base, int64_t num_pages,
+                                   int64_t page_stride_elems, float kv_scale,
+                                   const int32_t *page_table, int64_t page_table_ld,
+                                   int64_t page_table_cols, const int32_t *seq_lens,
+                                   int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads,
+                                   const int32_t *group_starts, const int32_t *shared_lens,
+                                   int32_t num_groups, float scale, void *out, float *lse,
+                                   void *workspace, size_t workspace_bytes, int32_t *status,
+                                   void *stream);
+
+/*
  * mla_pages_fork -- row i of out_table becomes the history of row parents[i] of
  * page_table (parents[i] < 0: an empty one), with the same pages: what the out row held
  * before is given up, as when one counted pointer is assigned to another.  No cache

@@ -82,6 +82,12 @@ SIGNATURES = {
     "mla_kv_compact_ex": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i64,
                                          _i64, _p, _i64, _p, _i32, _i32, _p, _i64, _i64, _p, _i64,
                                          _p, _p]),
+    "mla_shared_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "mla_decode_shared": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i32, _i32,
+                                         _i32, _p, _p, _i32, _f, _p, _p, _p, _sz, _p, _p]),
+    "mla_decode_shared_fp8": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _f, _p, _i64, _i64, _p,
+                                             _i32, _i32, _i32, _p, _p, _i32, _f, _p, _p, _p, _sz,
+                                             _p, _p]),
     "mla_pages_fork": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _p, _i32, _p, _i64, _p, _i64, _i64,
                                       _p, _p, _p]),
     "mla_pages_free": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _p, _i64, _p, _p]),

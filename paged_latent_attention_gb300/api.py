@@ -965,6 +965,104 @@ def _disjoint(a, b, message):
         _fail(message)
 
 
+def _shared_workspace_size(dev, num_reqs, n_q, num_heads, num_groups, fp8):
+    """The size depends on the device that the call will run on."""
+    size = _native.lib().mla_shared_workspace_size
+    if dev == torch._C._cuda_getDevice():
+        return size(num_reqs, n_q, num_heads, num_groups, fp8)
+    with torch.cuda.device(dev):
+        return size(num_reqs, n_q, num_heads, num_groups, fp8)
+
+
+def allocate_shared_workspace(num_reqs, n_q, num_heads, num_groups=None, fp8=False, device=None):
+    """A workspace tensor (uint8) of the size mla_decode_shared (or, with ``fp8``,
+    mla_decode_shared_fp8) needs, for up to num_groups groups (num_reqs by default)."""
+    device = torch.device(device or "cuda")
+    dev = torch.cuda.current_device() if device.index is None else device.index
+    n = _shared_workspace_size(dev, num_reqs, n_q, num_heads,
+                               num_reqs if num_groups is None else num_groups, bool(fp8))
+    if n == 0:
+        _fail("invalid shape for mla_shared_workspace_size")
+    return torch.empty(n, dtype=_U8, device=device)
+
+
+def mla_decode_shared(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens, group_starts,
+                      shared_lens, *, n_q=1, scale=DEFAULT_SCALE, out=None, lse=None,
+                      workspace=None, status=None, stream=None, with_lse=True):
+    """mla_decode for a batch whose requests have prefixes in common: the tokens that
+    a group shares are read once, with the queries of all its members.  Returns
+    (out, lse), mla_decode's up to rounding; arguments as there (any num_heads up to
+    128), and ``group_starts`` int32 [G+1]: group g is requests group_starts[g] ..
+    group_starts[g+1] - 1, ascending from 0 to R (a group may be one request);
+    ``shared_lens`` int32 [G]: the first tokens that its members have in common,
+    read through the first member's row of page_table, whatever pages of the others
+    hold them too.  The workspace comes from allocate_shared_workspace (a new one by
+    default); calls that may run at once need one each.  ``status``: optional CUDA
+    int32 tensor of one element, set to 33 (a history longer than its row of
+    page_table, which is cut off, or a page outside the pool), 38 (groups that are no
+    partition of the requests: nothing is shared) or the code of a wait that timed out.
+    Asynchronous."""
+    return _shared(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens, group_starts,
+                   shared_lens, n_q, scale, None, out, lse, workspace, status, stream, with_lse)
+
+
+def mla_decode_shared_fp8(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens, group_starts,
+                          shared_lens, *, kv_scale, n_q=1, scale=DEFAULT_SCALE, out=None, lse=None,
+                          workspace=None, status=None, stream=None, with_lse=True):
+    """mla_decode_shared over E4M3 pages (slab and kv_scale as in mla_decode_fp8).  The
+    workspace comes from allocate_shared_workspace(..., fp8=True)."""
+    return _shared(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens, group_starts,
+                   shared_lens, n_q, scale, _kv_scale(kv_scale), out, lse, workspace, status,
+                   stream, with_lse)
+
+
+def _shared(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens, group_starts, shared_lens,
+            n_q, scale, kv_scale, out, lse, workspace, status, stream, with_lse):
+    if torch.is_grad_enabled() and (q_nope_absorbed.requires_grad or q_rope.requires_grad
+                                    or gate.requires_grad or slab.requires_grad):
+        _fail("mla_decode_shared is not recorded by autograd: call it under torch.no_grad() or on "
+              "detached tensors")
+    fp8 = kv_scale is not None
+    base, pages, page_stride = _pool(slab, fp8)
+    dev, n_q = slab.get_device(), int(n_q)
+    shape = q_nope_absorbed.shape
+    if len(shape) != 3 or n_q < 1 or shape[0] % n_q != 0:
+        _fail("q_nope_absorbed must be [R*n_q, H, 512]")
+    T, H, _ = shape
+    R = T // n_q
+    wide = (T, H, LATENT)
+    head = (_dense(q_nope_absorbed, "q_nope_absorbed", dev, wide),
+            _dense(q_rope, "q_rope", dev, (T, H, ROPE)), _dense(gate, "gate", dev, wide), base,
+            pages, page_stride)
+    ids = _rows(page_table, "page_table", dev, _I32, R)
+    lens = _vector(seq_lens, "seq_lens", dev, R)
+    if shared_lens.dim() != 1:
+        _fail("shared_lens must be [G]")
+    G = shared_lens.shape[0]
+    groups = (_vector(group_starts, "group_starts", dev, G + 1),
+              _vector(shared_lens, "shared_lens", dev, G), G)
+    if out is None:
+        out = _empty(wide, _BF16, slab.device, stream)
+    if lse is None and with_lse:
+        lse = _empty((T, H), _F32, slab.device, stream)
+    outs = (_dense(out, "out", dev, wide),
+            None if lse is None else _dense(lse, "lse", dev, (T, H), _F32))
+    flag = _flag(status, dev)
+    if workspace is None:
+        workspace = _empty(_shared_workspace_size(dev, R, n_q, H, G, fp8), _U8, slab.device, stream)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _fail(f"workspace must be contiguous memory on cuda:{dev}")
+    tail = (*ids, lens, R, n_q, H, *groups, float(scale), *outs, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), flag)
+    lib = _native.lib()
+    if fp8:
+        _launch(dev, lib.mla_decode_shared_fp8, "mla_decode_shared_fp8", stream, *head, kv_scale,
+                *tail)
+    else:
+        _launch(dev, lib.mla_decode_shared, "mla_decode_shared", stream, *head, *tail)
+    return out, lse
+
+
 def mla_pages_fork(page_table, seq_lens, parents, ref_counts, out_table, out_lens, *, status=None,
                    stream=None):
     """Row i of out_table [N, columns] becomes the history of row parents[i] (int32

@@ -35,6 +35,7 @@ SOURCES = [
     "plmla_evict.cu",
     "plmla_pages.cu",
     "plmla_beam.cu",
+    "plmla_shared.cu",
     "plmla_branch_abi.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,5 +1,5 @@
 // plmla_branch_abi.cu -- host side of the entries for several continuations of one prompt
-// (page ownership, beam selection), declared in include/plmla.h.
+// (decode with shared prefixes, page ownership, beam selection), declared in include/plmla.h.
 //
 // Arguments are checked and the kernels enqueued on the caller's stream; nothing here
 // allocates device memory, synchronises, or reads device data back.
@@ -54,6 +54,149 @@ bool counts_ok(const int32_t *counts, int64_t num_pages, const int32_t *status)
 plmla_status result(cudaError_t err) { return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR; }
 
 }  // namespace
+
+namespace {
+
+bool shared_ok(int32_t num_reqs, int32_t n_q, int32_t num_heads, int32_t num_groups)
+{
+    return num_reqs >= 1 && num_reqs <= kMaxReqs && n_q >= 1 && n_q <= kMaxNq &&
+           num_heads >= 1 && num_heads <= 128 && num_groups >= 1 && num_groups <= kMaxReqs;
+}
+
+struct SharedLayout {
+    size_t total, group_of, parts, q8, qexp, lse_part, o_part, size;
+};
+
+SharedLayout shared_layout(int32_t num_reqs, int32_t rows, int32_t num_groups, bool fp8, int sms)
+{
+    const size_t slots = (size_t)shared_slots(num_reqs, rows, num_groups, sms);
+    const size_t all = (size_t)num_reqs * rows;
+    SharedLayout l;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align_up(bytes);
+        return here;
+    };
+    l.total = take(sizeof(int64_t));
+    l.group_of = take(4 * (size_t)num_reqs);
+    l.parts = take(sizeof(SharedPart) * ((size_t)num_groups + num_reqs));
+    l.q8 = take(fp8 ? 2 * (size_t)kRow * all : 0);
+    l.qexp = take(fp8 ? 4 * all : 0);
+    l.lse_part = take(4 * 128 * slots);
+    l.o_part = take(4 * 128 * (size_t)kLatent * slots);
+    l.size = at;
+    return l;
+}
+
+plmla_status shared_impl(const void *q_nope_absorbed, const void *q_rope, const void *gate,
+                         const void *slab_base, bool fp8, int64_t num_pages,
+                         int64_t page_stride_elems, float kv_scale, const int32_t *page_table,
+                         int64_t page_table_ld, int64_t page_table_cols, const int32_t *seq_lens,
+                         int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads,
+                         const int32_t *group_starts, const int32_t *shared_lens,
+                         int32_t num_groups, float scale, void *out, float *lse, void *workspace,
+                         size_t workspace_bytes, int32_t *status, void *stream)
+{
+    if (!shared_ok(num_reqs, n_q_per_req, num_heads, num_groups) ||
+        !table_ok(page_table, page_table_ld, page_table_cols, num_reqs) || num_pages < 1 ||
+        num_pages > INT32_MAX || page_stride_elems < (int64_t)kPageTokens * kRow ||
+        page_stride_elems % (fp8 ? 16 : 8) != 0 || !(isfinite(scale) && scale > 0.f) ||
+        !(isfinite(kv_scale) && kv_scale > 0.f))
+        return PLMLA_INVALID_ARGUMENT;
+    const void *rows16[] = {q_nope_absorbed, q_rope, gate, slab_base, out};
+    for (const void *p : rows16)
+        if (p == nullptr || !aligned(p, 16))
+            return PLMLA_INVALID_ARGUMENT;
+    if (!words_ok(seq_lens) || !words_ok(group_starts) || !words_ok(shared_lens) ||
+        (lse != nullptr && !aligned(lse, 4)) || (status != nullptr && !aligned(status, 4)) ||
+        workspace == nullptr || !aligned(workspace, kAlign))
+        return PLMLA_INVALID_ARGUMENT;
+    const int sms = device_sms();
+    if (sms < 2)
+        return PLMLA_CUDA_ERROR;
+    SharedArgs a = {};
+    a.rows = n_q_per_req * num_heads;
+    const SharedLayout l = shared_layout(num_reqs, a.rows, num_groups, fp8, sms);
+    if (workspace_bytes < l.size)
+        return PLMLA_WORKSPACE_TOO_SMALL;
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    a.q_nope = static_cast<const __nv_bfloat16 *>(q_nope_absorbed);
+    a.q_rope = static_cast<const __nv_bfloat16 *>(q_rope);
+    a.gate = static_cast<const __nv_bfloat16 *>(gate);
+    a.slab = slab_base;
+    a.num_pages = num_pages;
+    a.page_stride = page_stride_elems;
+    a.page_table = page_table;
+    a.table_ld = page_table_ld;
+    a.table_cols = page_table_cols;
+    a.seq_lens = seq_lens;
+    a.num_reqs = num_reqs;
+    a.n_q = n_q_per_req;
+    a.heads = num_heads;
+    a.group_starts = group_starts;
+    a.shared_lens = shared_lens;
+    a.num_groups = num_groups;
+    a.scale = scale;
+    a.kv_scale = kv_scale;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.lse = lse;
+    a.total = reinterpret_cast<int64_t *>(w + l.total);
+    a.group_of = reinterpret_cast<int32_t *>(w + l.group_of);
+    a.parts = reinterpret_cast<SharedPart *>(w + l.parts);
+    a.lse_part = reinterpret_cast<float *>(w + l.lse_part);
+    a.o_part = reinterpret_cast<float *>(w + l.o_part);
+    a.status = status;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (fp8) {
+        uint8_t *q8 = w + l.q8;
+        int32_t *qexp = reinterpret_cast<int32_t *>(w + l.qexp);
+        if (launch_quantize(a.q_nope, a.q_rope, num_reqs * a.rows, q8, qexp, s) != cudaSuccess)
+            return PLMLA_CUDA_ERROR;
+        a.q8 = q8;
+        a.qexp = qexp;
+    }
+    return result(launch_shared(a, sms, s));
+}
+
+}  // namespace
+
+extern "C" size_t mla_shared_workspace_size(int32_t num_reqs, int32_t n_q_per_req,
+                                            int32_t num_heads, int32_t num_groups, int32_t fp8)
+{
+    const int sms = device_sms();
+    if (!shared_ok(num_reqs, n_q_per_req, num_heads, num_groups) || sms < 2)
+        return 0;
+    return shared_layout(num_reqs, n_q_per_req * num_heads, num_groups, fp8 != 0, sms).size;
+}
+
+extern "C" plmla_status mla_decode_shared(
+    const void *q_nope_absorbed, const void *q_rope, const void *gate, const void *slab_base,
+    int64_t num_pages, int64_t page_stride_elems, const int32_t *page_table, int64_t page_table_ld,
+    int64_t page_table_cols, const int32_t *seq_lens, int32_t num_reqs, int32_t n_q_per_req,
+    int32_t num_heads, const int32_t *group_starts, const int32_t *shared_lens, int32_t num_groups,
+    float scale, void *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *status,
+    void *stream)
+{
+    return shared_impl(q_nope_absorbed, q_rope, gate, slab_base, false, num_pages,
+                       page_stride_elems, 1.f, page_table, page_table_ld, page_table_cols,
+                       seq_lens, num_reqs, n_q_per_req, num_heads, group_starts, shared_lens,
+                       num_groups, scale, out, lse, workspace, workspace_bytes, status, stream);
+}
+
+extern "C" plmla_status mla_decode_shared_fp8(
+    const void *q_nope_absorbed, const void *q_rope, const void *gate, const void *slab_base,
+    int64_t num_pages, int64_t page_stride_elems, float kv_scale, const int32_t *page_table,
+    int64_t page_table_ld, int64_t page_table_cols, const int32_t *seq_lens, int32_t num_reqs,
+    int32_t n_q_per_req, int32_t num_heads, const int32_t *group_starts,
+    const int32_t *shared_lens, int32_t num_groups, float scale, void *out, float *lse,
+    void *workspace, size_t workspace_bytes, int32_t *status, void *stream)
+{
+    return shared_impl(q_nope_absorbed, q_rope, gate, slab_base, true, num_pages,
+                       page_stride_elems, kv_scale, page_table, page_table_ld, page_table_cols,
+                       seq_lens, num_reqs, n_q_per_req, num_heads, group_starts, shared_lens,
+                       num_groups, scale, out, lse, workspace, workspace_bytes, status, stream);
+}
 
 extern "C" plmla_status mla_pages_fork(const int32_t *page_table, int64_t page_table_ld,
                                        int64_t page_table_cols, const int32_t *seq_lens,

@@ -187,6 +187,44 @@ cudaError_t launch_compact(int num_layers, void *const *slabs, bool fp8, int64_t
                            int64_t mass_ld, int64_t mass_cols, float *mass_out,
                            int64_t mass_out_ld, int32_t *status, cudaStream_t stream);
 
+// Decode with shared prefixes (plmla_shared.cu).
+constexpr int32_t kStatusGroups = 38;           // groups that are no partition of the requests
+struct SharedPart {                     // one attention problem: query rows over some tokens
+    int64_t base;                       // its first position in the order of all tiles
+    int tiles, blocks;                  // tiles of 128 tokens; blocks of 128 query rows
+    int block0;                         // its first block among all
+    int req;                            // the table row that its tokens are read through
+    int tok0, len;                      // first token, and the end of the history
+    int vis;                            // tokens below are visible to every row
+    int row0, rows;                     // its query rows
+    int pad;
+};
+struct SharedArgs {
+    const __nv_bfloat16 *q_nope, *q_rope, *gate;
+    const uint8_t *q8;                  // E4M3: [2, num_reqs * rows, 576], hi plane then lo
+    const int32_t *qexp;
+    const void *slab;                   // bf16 elements, or E4M3 bytes (q8 set)
+    int64_t num_pages, page_stride;
+    const int32_t *page_table;
+    int64_t table_ld, table_cols;
+    const int32_t *seq_lens;
+    int num_reqs, n_q, heads, rows;     // rows = n_q * heads
+    const int32_t *group_starts, *shared_lens;
+    int num_groups;
+    float scale, kv_scale;
+    float scale_log2;                   // set by the launch
+    __nv_bfloat16 *out;
+    float *lse;                         // may be null
+    SharedPart *parts;                  // workspace: [num_groups + num_reqs]
+    int64_t *total;                     // workspace: positions in all
+    int32_t *group_of;                  // workspace: [num_reqs]
+    float *o_part, *lse_part;           // workspace: [slots, 128, 512], [slots, 128]
+    int32_t *status;                    // may be null
+};
+// Partial outputs of 128 rows that a call may write.
+int64_t shared_slots(int num_reqs, int rows, int num_groups, int sms);
+cudaError_t launch_shared(const SharedArgs &a, int sms, cudaStream_t stream);
+
 // Page ownership (plmla_pages.cu).
 constexpr int32_t kStatusNoPage = 35;           // no free page left
 constexpr int32_t kStatusParent = 36;           // a parent that is no row

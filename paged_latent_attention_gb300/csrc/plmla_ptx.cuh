@@ -455,7 +455,7 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, int
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr)
         return false;
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     // out-of-range elements (the E4M3 rope block's columns past 576) read as zero
     return fn(map, dtype, rank, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

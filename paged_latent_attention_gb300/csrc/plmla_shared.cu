@@ -1,0 +1,1090 @@
+// plmla_shared.cu -- gated MLA decode of a batch whose requests share prefixes, on CTA pairs
+// of the 5th-generation tensor cores (tcgen05 + TMEM), for sm_103a.
+//
+//   out[r, j, h] = sigmoid(gate) sum_t w_t c_t,  w = softmax_t(scale q_{r,j,h} . x_t),  t < L_r - (n_q - 1 - j)
+//
+// The softmax over a history is the merge, by log-sum-exps, of the softmaxes over its
+// parts.  The tokens that a group of requests has in common are one part, read once: the
+// queries of all members are the rows of one attention problem over them (no causal limit
+// falls there).  What each request has of its own is the other part.
+//
+// Work.  A block is 128 query rows of one part.  plan_kernel lists the parts (groups' prefixes,
+// then requests' own tokens); the tiles of 128 tokens of all blocks, in order, are dealt to
+// CTA pairs in equal contiguous runs, a block's start counting kStart tiles more.  A pair's
+// run within a block is a segment: it leaves an unnormalised-to-1 partial output and its
+// log-sum-exp, and merge_kernel joins a row's partials in order and applies the gate.  There are
+// no atomics, and results depend on the arguments alone.
+//
+// A pair holds 64 rows in each CTA (cta_group::2, M = 128).  Per tile
+//   S = Q K^T      K split by tokens: each CTA loads 64 of them (N = 128)
+//   O += P V       V split by columns: each CTA loads its 2 x 128 of 512 (2 x N = 256)
+// so every byte that enters an SM serves 128 rows.  TMEM in each CTA: O takes 256 columns (lane =
+// row + 64 * half; columns of half h of each 256 in lanes 64 h ..), two score tiles 64 each.
+// Measured on this device: such MMAs issue at their full rate (32 and 64 cycles) when their
+// operands are warp-uniform and constant but for a base, against 110 cycles each from a
+// divergent thread with computed descriptors, so the issuing warp stays converged.
+//
+// Warps: 0 loads (TMA, one ring of 16 KB items in the order of use: K of tile g + 1, then V of
+// tile g), 1 issues the MMAs of the pair (in the even CTA), 4-7 softmax and epilogue, a
+// thread having half of a row's 128 scores in registers.  The running maximum lags: O is only
+// rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries in two E4M3 parts
+// (as in the FP8 decode) and the probabilities in two as well, hi + lo, so that they carry 8
+// bits like bf16 ones; a part each takes the rate that bf16 would.
+//
+// Every mbarrier wait is bounded; one that gives up sets the status word, and cluster
+// barriers keep both CTAs until neither can touch the other.
+#include <math.h>
+
+#include "plmla_ptx.cuh"
+
+namespace plmla {
+namespace {
+
+constexpr int kShThreads = 256;
+constexpr int kShSlots = 8, kShSlot = 16384;
+constexpr int kShRows = 128;                    // query rows of a block
+constexpr int kStart = 2;                       // cost of a block's start, in tiles
+constexpr int kShPlanThreads = 1024;
+constexpr int kMergeThreads = 128;
+constexpr int kColS = 256;                      // TMEM column of the first score tile
+constexpr int kNever = 0x7FFFFFFF;
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ int64_t scan64(int64_t v, int64_t *warp_sum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();
+    if (lane == 31)
+        warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = warp_sum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o)
+                s += y;
+        }
+        warp_sum[lane] = s;
+    }
+    __syncthreads();
+    return x - v + (warp == 0 ? 0 : warp_sum[warp - 1]);
+}
+
+// Parts 0 .. G - 1 are the groups' prefixes, G .. G + R - 1 the requests' own tokens.
+__global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const SharedArgs a)
+{
+    __shared__ int64_t warp_sum[32];
+    __shared__ int start[kMaxReqs + 1], least[kMaxReqs], eff[kMaxReqs];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int t = threadIdx.x, R = a.num_reqs, G = a.num_groups;
+    const int64_t cap = min(a.table_cols * kPageTokens, (int64_t)kNever);
+    bool bad = false;
+    for (int g = t; g <= G; g += kShPlanThreads)
+        start[g] = a.group_starts[g];
+    if (t < G)
+        least[t] = kNever;
+    int len = 0;
+    if (t < R) {
+        len = max(a.seq_lens[t], 0);
+        if (len > cap) {
+            len = (int)cap;
+            if (a.status != nullptr)
+                atomicExch(a.status, kStatusAppendPage);
+        }
+    }
+    __syncthreads();
+    for (int g = t; g <= G; g += kShPlanThreads)
+        bad |= (g == 0 && start[0] != 0) || (g == G && start[G] != R) ||
+               (g < G && start[g] > start[g + 1]);
+    // groups that are no partition of the requests: nothing is shared
+    bad = __syncthreads_or(bad) != 0;
+    if (bad && t == 0 && a.status != nullptr)
+        atomicExch(a.status, kStatusGroups);
+    int group = 0;
+    if (t < R && !bad) {
+        int hi = G - 1;                         // the last group that starts at or before t
+        while (group < hi) {
+            const int mid = (group + hi + 1) / 2;
+            if (start[mid] <= t)
+                group = mid;
+            else
+                hi = mid - 1;
+        }
+        atomicMin(&least[group], len - (a.n_q - 1));
+    }
+    __syncthreads();
+    SharedPart part = {};
+    if (t < G) {
+        const int members = bad ? 0 : start[t + 1] - start[t];
+        int64_t tiles = members > 1 ? max(0, min(a.shared_lens[t], least[t])) / kTile : 0;
+        // worth it where it saves more tiles than its blocks' starts cost
+        const int64_t blocks = ((int64_t)members * a.rows + kShRows - 1) / kShRows;
+        const int64_t alone = (int64_t)members * ((a.rows + kShRows - 1) / kShRows);
+        if (tiles * (alone - blocks) <= kStart * blocks)
+            tiles = 0;
+        part.tiles = (int)tiles;
+        part.blocks = tiles > 0 ? (int)blocks : 0;
+        part.req = bad ? 0 : start[t];
+        part.len = (int)tiles * kTile;
+        part.vis = kNever;
+        part.row0 = part.req * a.rows;
+        part.rows = members * a.rows;
+        eff[t] = part.len;
+    }
+    __syncthreads();
+    SharedPart mine = {};
+    if (t < R) {
+        mine.tok0 = bad ? 0 : eff[group];
+        mine.tiles = len > mine.tok0 ? (len - mine.tok0 - 1) / kTile + 1 : 0;
+        mine.blocks = mine.tiles > 0 ? (a.rows + kShRows - 1) / kShRows : 0;
+        mine.req = t;
+        mine.len = len;
+        mine.vis = len - (a.n_q - 1);
+        mine.row0 = t * a.rows;
+        mine.rows = a.rows;
+        a.group_of[t] = bad ? -1 : group;
+    }
+    const int64_t cost = (int64_t)part.blocks * (part.tiles + kStart);
+    const int64_t own = (int64_t)mine.blocks * (mine.tiles + kStart);
+    part.base = scan64(cost, warp_sum);
+    const int64_t prefixes = warp_sum[31];
+    mine.base = prefixes + scan64(own, warp_sum);
+    const int64_t total = prefixes + warp_sum[31];
+    part.block0 = (int)scan64(part.blocks, warp_sum);
+    const int before = (int)warp_sum[31];
+    mine.block0 = before + (int)scan64(mine.blocks, warp_sum);
+    if (t < G)
+        a.parts[t] = part;
+    if (t < R)
+        a.parts[G + t] = mine;
+    if (t == 0)
+        *a.total = total;
+}
+
+// ---------------------------------------------------------------------------
+// decode
+// ---------------------------------------------------------------------------
+
+struct ShBars {
+    uint64_t full[kShSlots], empty[kShSlots];
+    uint64_t rope_full, rope_empty, q_full, q_empty;
+    uint64_t s_full[2], s_free[2];
+    uint64_t p_full, pv_done, o_free, drain;
+};
+
+struct ShMisc {
+    ShBars bars;
+    uint32_t tmem;
+    int abort, status, first;
+    float half[3][128];                         // exchanged between the two halves of a row
+};
+
+template <bool F8>
+struct ShFmt {
+    static constexpr int k_items = F8 ? 2 : 4;  // of two blocks by 64 tokens
+    static constexpr int v_items = F8 ? 2 : 4;
+    static constexpr int rope_bytes = F8 ? 4096 : 8192;
+    static constexpr int q_part = F8 ? 64 * kRow : 128 * kRow;     // bytes of a query part
+    static constexpr int parts = F8 ? 2 : 1;
+};
+
+constexpr int kShQ = 64 * 2 * kRow;             // bytes of the queries: 64 rows
+constexpr int kShP = 16384;
+constexpr int kShRope = 8192;
+constexpr int kShSmem = kShQ + kShP + kShSlots * kShSlot + kShRope + (int)sizeof(ShMisc);
+static_assert(kShSmem <= 232448, "shared memory");
+
+__device__ __forceinline__ uint32_t bar_of(const uint64_t &b) { return smem_u32(&b); }
+
+// A pair's run of tiles, segment by segment; every role walks it alike.
+struct ShWalk {
+    const SharedPart *parts;
+    int64_t pos, end;
+    int e, blk;
+    SharedPart part;
+    int t0, t1;                                 // tiles of the segment
+    __device__ void begin(const SharedPart *p, int first, int64_t from, int64_t to)
+    {
+        parts = p;
+        pos = from;
+        end = to;
+        e = first;
+        blk = 0;
+        if (pos < end) {
+            part = parts[e];
+            blk = (int)((pos - part.base) / (part.tiles + kStart));
+        }
+    }
+    __device__ bool next()
+    {
+        while (pos < end) {
+            while (blk >= part.blocks) {
+                part = parts[++e];
+                blk = 0;
+            }
+            const int64_t at = part.base + (int64_t)blk * (part.tiles + kStart);
+            const int64_t stop = min(end, at + part.tiles + kStart);
+            t0 = max(0, (int)(pos - at) - kStart);
+            t1 = (int)(stop - at) - kStart;
+            slot_block = part.block0 + blk;
+            row0 = blk * kShRows;
+            pos = stop;
+            if (stop == at + part.tiles + kStart)
+                ++blk;
+            if (t1 > t0)
+                return true;
+        }
+        return false;
+    }
+    int slot_block, row0;
+};
+
+// Pairs with work: each has a position at least, so that every pair between the first and the
+// last of a block has a segment of it.
+__device__ __forceinline__ int64_t busy_pairs(int64_t total, int pairs)
+{
+    return total < pairs ? max(total, (int64_t)1) : pairs;
+}
+
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.b32 %0, 1, 0, e;\n\t}"
+                 : "=r"(r));
+    return r;
+}
+
+// The pair's MMA by the elected lane of a converged warp.
+template <bool F8>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t elected)
+{
+    if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected));
+}
+
+__device__ __forceinline__ void pair_commit(uint32_t bar, uint32_t elected)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3), "r"(elected)
+        : "memory");
+}
+
+// Arrive, with bytes to come, on a barrier of either CTA of the pair.
+__device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_4d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, int c3, uint32_t bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
+        "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_global_32(float *p, const uint32_t *v, float f)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                 "f"(__uint_as_float(v[0]) * f), "f"(__uint_as_float(v[1]) * f),
+                 "f"(__uint_as_float(v[2]) * f), "f"(__uint_as_float(v[3]) * f),
+                 "f"(__uint_as_float(v[4]) * f), "f"(__uint_as_float(v[5]) * f),
+                 "f"(__uint_as_float(v[6]) * f), "f"(__uint_as_float(v[7]) * f)
+                 : "memory");
+}
+
+struct ShMaps {
+    CUtensorMap k, v, rope, qn, qr, tail[7];
+};
+
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+template <bool F8>
+__global__ void __launch_bounds__(kShThreads, 1)
+shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
+{
+    using F = ShFmt<F8>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t s_q = smem_u32(smem), s_p = s_q + kShQ, s_ring = s_p + kShP;
+    const uint32_t s_rope = s_ring + kShSlots * kShSlot;
+    ShMisc &m = *reinterpret_cast<ShMisc *>(smem + kShQ + kShP + kShSlots * kShSlot + kShRope);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if ((s_q & 1023u) != 0u) {         // cannot be with no static shared memory
+        if (threadIdx.x == 0 && a.status != nullptr)
+            atomicExch(a.status, 12);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kShSlots; ++i) {
+            mbar_init(bar_of(m.bars.full[i]), 2);             // both CTAs' loads
+            mbar_init(bar_of(m.bars.empty[i]), 1);
+        }
+        mbar_init(bar_of(m.bars.rope_full), 2);
+        mbar_init(bar_of(m.bars.rope_empty), 1);
+        mbar_init(bar_of(m.bars.q_full), 2);
+        mbar_init(bar_of(m.bars.q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_of(m.bars.s_full[i]), 1);
+            mbar_init(bar_of(m.bars.s_free[i]), 8);           // the pair's softmax warps
+        }
+        mbar_init(bar_of(m.bars.p_full), 8);
+        mbar_init(bar_of(m.bars.pv_done), 1);
+        mbar_init(bar_of(m.bars.o_free), 8);
+        mbar_init(bar_of(m.bars.drain), 1);
+        m.abort = 0;
+        m.status = 0;
+        m.first = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&m.tmem)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    const uint32_t rank = cluster_rank();
+    const int pair = (int)blockIdx.x >> 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");        // the plan (and split queries)
+    const int64_t total = *a.total;
+    const int64_t pairs = busy_pairs(total, (int)gridDim.x >> 1);
+    const int64_t from = pair < pairs ? total * pair / pairs : total;
+    const int64_t to = pair < pairs ? total * (pair + 1) / pairs : total;
+    {
+        // the part that holds the run's first position: the last one that starts there or before
+        int mine = 0;
+        for (int e = threadIdx.x; e < a.num_groups + a.num_reqs; e += kShThreads)
+            if (a.parts[e].base <= from)
+                mine = e;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (mine != 0)
+            atomicMax(&m.first, mine);
+        __syncthreads();
+    }
+    cluster_sync();                             // the pair's barriers are initialised
+    const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
+    volatile int *abort_flag = &m.abort;
+    int32_t *status = &m.status;
+    auto lead = [&](const uint64_t &b) { return map_rank(bar_of(b), 0); };
+    ShWalk walk;
+    walk.begin(a.parts, m.first, from, to);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        // Two cursors: K runs a tile ahead of V.
+        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+        ShWalk vw = walk;
+        bool more = walk.next(), v_any = vw.next(), ok = true;
+        int kt = walk.t0, vt = vw.t0;
+        int slot = 0, ropes = 0, loads = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool fresh = true;                      // the K cursor is at a segment's start
+        auto page_at = [&](const SharedPart &p, int tok) -> int {
+            int page = a.page_table[(int64_t)p.req * a.table_ld + tok / kPageTokens];
+            if (page < 0 || (int64_t)page >= a.num_pages) {
+                if (lane == 0)
+                    atomicExch(status, kStatusAppendPage);
+                page = 0;
+            }
+            return page;
+        };
+        auto take = [&]() -> bool {
+            return all_ok(wait_bounded(bar_of(m.bars.empty[slot]), phase ^ 1, abort_flag, status, 2));
+        };
+        auto advance = [&]() {
+            ++issued;
+            if (++slot == kShSlots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        int k_col = -1, k_page = 0, v_col = -1, v_page = 0;
+        while (ok && v_any) {
+            if (more) {
+                if (fresh) {
+                    if (loads > 0 && !all_ok(wait_bounded(bar_of(m.bars.q_empty), (loads - 1) & 1,
+                                                          abort_flag, status, 1))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const uint32_t bar = lead(m.bars.q_full);
+                        arrive_expect_cluster(bar, kShQ);
+                        const int row = walk.part.row0 + walk.row0 + 64 * (int)rank;
+                        for (int p = 0; p < F::parts; ++p) {
+                            const uint32_t dst = s_q + p * F::q_part;
+                            const int at = p * a.num_reqs * a.rows + row;
+                            tma_3d_pair(dst, &maps.qn, 0, at, 0, bar);
+                            tma_3d_pair(dst + F::q_part - F::rope_bytes, &maps.qr,
+                                        F8 ? kLatent : 0, at, 0, bar);
+                        }
+                    }
+                    ++loads;
+                    fresh = false;
+                    k_col = -1;
+                }
+                const int tok = walk.part.tok0 + kt * kTile;
+                if (tok / kPageTokens != k_col) {
+                    k_col = tok / kPageTokens;
+                    k_page = page_at(walk.part, tok);
+                }
+                const int own = tok % kPageTokens + 64 * (int)rank;
+#pragma unroll 1
+                for (int i = 0; i < F::k_items && ok; ++i) {
+                    if (i == F::k_items / 2) {
+                        // the rope block in the middle of the products
+                        if (ropes > 0 && !all_ok(wait_bounded(bar_of(m.bars.rope_empty),
+                                                              (ropes - 1) & 1, abort_flag, status,
+                                                              3))) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            const uint32_t bar = lead(m.bars.rope_full);
+                            arrive_expect_cluster(bar, F::rope_bytes);
+                            tma_load_3d_pair(s_rope, &maps.rope, kLatent, own, k_page, bar,
+                                             walk.part.vis == kNever ? keep : once);
+                        }
+                        ++ropes;
+                    }
+                    if (!take()) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const uint32_t bar = lead(m.bars.full[slot]);
+                        arrive_expect_cluster(bar, kShSlot);
+                        tma_4d_pair(s_ring + slot * kShSlot, &maps.k, 0, own, 2 * i, k_page, bar,
+                                    keep);
+                    }
+                    advance();
+                }
+                if (!ok)
+                    break;
+                if (++kt == walk.t1) {
+                    more = walk.next();
+                    kt = walk.t0;
+                    fresh = true;
+                }
+                if (issued == F::k_items)       // the first K has no V before it
+                    if (more)
+                        continue;
+            }
+            // V of the tile behind
+            const int tok = vw.part.tok0 + vt * kTile;
+            if (tok / kPageTokens != v_col) {
+                v_col = tok / kPageTokens;
+                v_page = page_at(vw.part, tok);
+            }
+            const int in_page = tok % kPageTokens, valid = min(kTile, vw.part.len - tok);
+            // other pairs read a prefix too
+            const uint64_t v_use = vw.part.vis == kNever ? keep : once;
+#pragma unroll 1
+            for (int i = 0; i < F::v_items && ok; ++i) {
+                // bf16: (256 columns i / 2, 64 tokens i % 2); E4M3: (256 columns i)
+                const int t_off = F8 ? 0 : 64 * (i & 1), t_num = F8 ? 128 : 64;
+                const int block = F8 ? 2 * i + (int)rank : 4 * (i >> 1) + 2 * (int)rank;
+                if (!take()) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = s_ring + slot * kShSlot, bar = lead(m.bars.full[slot]);
+                const int n = min(t_num, max(0, valid - t_off));
+                if (n == t_num) {
+                    if (lane == 0) {
+                        arrive_expect_cluster(bar, kShSlot);
+                        tma_4d_pair(dst, &maps.v, 0, in_page + t_off, block, v_page, bar, v_use);
+                    }
+                } else {
+                    // a history's last tile: rows past it become zeros (they hold stale data,
+                    // and a weight of 0 times NaN is NaN), the others come in boxes of
+                    // 64, 32, .. 1 rows
+                    constexpr int kCols = F8 ? 1 : 2;         // 128-byte blocks of an item
+                    const int pitch = t_num * 128;
+                    for (int u = lane; u < kCols * (t_num - n) * 8; u += 32) {
+                        const int b = u / ((t_num - n) * 8), x = u % ((t_num - n) * 8);
+                        st_shared_16(dst + b * pitch + n * 128 + 16 * x, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive_expect_cluster(bar, kCols * n * 128);
+                        for (int b = 0; b < kCols; ++b)
+                            for (int w = 6, r0 = 0; w >= 0; --w)
+                                if (n >> w & 1) {
+                                    tma_4d_pair(dst + b * pitch + r0 * 128, &maps.tail[w], 0,
+                                                in_page + t_off + r0, block + b, v_page, bar, once);
+                                    r0 += 1 << w;
+                                }
+                    }
+                }
+                advance();
+            }
+            if (++vt == vw.t1) {
+                v_any = vw.next();
+                vt = vw.t0;
+                v_col = -1;
+            }
+        }
+        // both CTAs' copies complete on the even CTA's barriers: it waits for the last ones
+        if (rank == 0 && lane == 0) {
+            if (loads > 0)
+                wait_drain(bar_of(m.bars.q_full), (loads - 1) & 1);
+            if (ropes > 0)
+                wait_drain(bar_of(m.bars.rope_full), (ropes - 1) & 1);
+            for (int64_t it = issued > kShSlots ? issued - kShSlots : 0; it < issued; ++it)
+                wait_drain(bar_of(m.bars.full[it % kShSlots]), (uint32_t)(it / kShSlots) & 1u);
+        }
+    } else if (warp == 1 && rank == 0) {
+        // -------------------------------------------------------- MMA issue
+        const uint32_t el = elect_one();
+        constexpr uint32_t id_s = idesc_for<F8>(128, 128, false, false);
+        constexpr uint32_t id_o = idesc_for<F8>(128, 256, false, true);
+        const uint64_t dq0 = sdesc(s_q, 16, 1024, kSw128);
+        const uint64_t dq_rope = sdesc(s_q + F::q_part - F::rope_bytes, 16, F8 ? 512 : 1024,
+                                       F8 ? kSw64 : kSw128);
+        const uint64_t dk_rope = sdesc(s_rope, 16, F8 ? 512 : 1024, F8 ? kSw64 : kSw128);
+        const uint64_t dk0 = sdesc(s_ring, 16, 1024, kSw128);
+        // V: columns contiguous; two 64-column blocks 8 KB apart (bf16), 8-token groups 1 KB
+        const uint64_t dv0 = sdesc(s_ring, 8192, 1024, kSw128);
+        const uint64_t dp0 = sdesc(s_p, 16, 1024, kSw128);
+        constexpr uint64_t kPart = F::q_part >> 4;
+        ShWalk vw = walk;
+        bool more = walk.next(), v_any = vw.next(), ok = true, first_k = true, any = v_any;
+        int kt = walk.t0, vt = vw.t0, slot = 0, loads = 0;
+        uint32_t phase = 0;
+        int64_t g = 0, v = 0, segs = 0;         // tiles scored, tiles multiplied, segments done
+        auto advance = [&]() {
+            pair_commit(bar_of(m.bars.empty[slot]), el);
+            if (++slot == kShSlots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        auto wait = [&](const uint64_t &b, uint32_t parity, int code) -> bool {
+            const bool got = all_ok(wait_bounded(bar_of(b), parity, abort_flag, status, code));
+            tc_fence_after();
+            return got;
+        };
+        while (ok && v_any) {
+            if (more) {
+                if (kt == walk.t0) {
+                    if (!wait(m.bars.q_full, loads & 1, 4)) {
+                        ok = false;
+                        break;
+                    }
+                    ++loads;
+                }
+                const int buf = (int)(g & 1);
+                if (g >= 2 && !wait(m.bars.s_free[buf], (uint32_t)((g - 2) >> 1) & 1u, 5)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t d = tmem + kColS + 64 * buf;
+#pragma unroll
+                for (int i = 0; i < F::k_items; ++i) {
+                    if (i == F::k_items / 2) {
+                        if (!ok || !wait(m.bars.rope_full, (uint32_t)g & 1u, 6)) {
+                            ok = false;
+                            break;
+                        }
+                        constexpr int kSteps = F8 ? 2 : 4;
+#pragma unroll
+                        for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+                            for (int p = 0; p < F::parts; ++p)
+                                pair_mma<F8>(d, dq_rope + p * kPart + 2 * kk, dk_rope + 2 * kk,
+                                             id_s, 1, el);
+                        pair_commit(bar_of(m.bars.rope_empty), el);
+                    }
+                    if (!wait(m.bars.full[slot], phase, 7)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t dk = dk0 + (uint64_t)(slot * (kShSlot >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                        for (int p = 0; p < F::parts; ++p)
+                            pair_mma<F8>(d, dq0 + p * kPart + (2 * i + kk / 4) * 512 + 2 * (kk % 4),
+                                         dk + (kk / 4) * 512 + 2 * (kk % 4), id_s,
+                                         (i | kk | p) != 0, el);
+                    advance();
+                }
+                if (!ok)
+                    break;
+                pair_commit(bar_of(m.bars.s_full[buf]), el);
+                ++g;
+                if (++kt == walk.t1) {
+                    pair_commit(bar_of(m.bars.q_empty), el);
+                    more = walk.next();
+                    kt = walk.t0;
+                }
+                if (first_k) {
+                    first_k = false;
+                    if (more)
+                        continue;
+                }
+            }
+            // the segment before must have left O
+            if (vt == vw.t0 && segs > 0 &&
+                !wait(m.bars.o_free, (uint32_t)(segs - 1) & 1u, 8)) {
+                ok = false;
+                break;
+            }
+            if (!wait(m.bars.p_full, (uint32_t)v & 1u, 9)) {
+                ok = false;
+                break;
+            }
+            const uint32_t carry = vt != vw.t0 ? 1 : 0;
+#pragma unroll
+            for (int i = 0; i < F::v_items; ++i) {
+                if (!wait(m.bars.full[slot], phase, 10)) {
+                    ok = false;
+                    break;
+                }
+                const uint64_t dv = dv0 + (uint64_t)(slot * (kShSlot >> 4));
+                const int h = F8 ? i : i >> 1;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int p = 0; p < F::parts; ++p) {
+                        // bf16: 16 tokens a step, P in blocks of 64; E4M3: 32, hi and lo blocks
+                        const uint64_t dp = F8 ? dp0 + p * 512 + 2 * kk
+                                               : dp0 + (i & 1) * 512 + 2 * kk;
+                        const uint32_t acc =
+                            (F8 ? (kk | p) != 0 : (kk | (i & 1)) != 0) ? 1u : carry;
+                        pair_mma<F8>(tmem + 128 * h, dp, dv + (F8 ? 256 : 128) * kk, id_o, acc, el);
+                    }
+                advance();
+            }
+            if (!ok)
+                break;
+            pair_commit(bar_of(m.bars.pv_done), el);
+            ++v;
+            if (++vt == vw.t1) {
+                ++segs;
+                v_any = vw.next();
+                vt = vw.t0;
+            }
+        }
+        if (any) {
+            pair_commit(bar_of(m.bars.drain), el);
+            if (lane == 0)
+                wait_drain(bar_of(m.bars.drain), 0);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // the even CTA's commits arrive here too: the last of them comes after the others
+        if (walk.next())
+            wait_drain(bar_of(m.bars.drain), 0);
+    } else if (warp >= 4) {
+        // -------------------------------------------------- softmax, epilogue
+        // Thread (quad, lane): row 32 (quad % 2) + lane of this CTA, tokens 64 (quad / 2) .. + 63
+        // of a tile.  A wait that gives up clears `ok`: the loops run on without waiting or
+        // storing, so that every thread still meets the barriers.
+        const int quad = warp & 3, row = 32 * (quad & 1) + lane, side = quad >> 1;
+        const int tid = 32 * quad + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+        constexpr float kLag = F8 ? 4.f : 8.f, kUp = F8 ? 4.f : 0.f;
+        const uint32_t p_row = s_p + row * 128 + (F8 ? 0 : side * 8192);
+        bool ok = true;
+        int64_t g = 0;
+        auto wait = [&](const uint64_t &b, uint32_t parity, int code) {
+            ok = all_ok(ok && wait_bounded(bar_of(b), parity, abort_flag, status, code));
+            tc_fence_after();
+        };
+        auto arrive = [&](const uint64_t &b) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(lead(b));
+        };
+        while (walk.next()) {
+            const SharedPart &part = walk.part;
+            const int in_part = walk.row0 + 64 * (int)rank + row;
+            const bool real = in_part < part.rows;
+            // tokens that the row sees
+            int limit = part.len;
+            if (part.vis != kNever)
+                limit = min(part.len, part.vis + in_part / a.heads);
+            float f = a.scale_log2;
+            if constexpr (F8)
+                f = real ? ldexpf(f * a.kv_scale, a.qexp[part.row0 + in_part]) : 1.f;
+            float high = -INFINITY, sum = 0.f;  // in units of log2; of this thread's tokens
+            for (int t = walk.t0; t < walk.t1; ++t, ++g) {
+                const int buf = (int)(g & 1);
+                wait(m.bars.s_full[buf], (uint32_t)(g >> 1) & 1u, 11);
+                float x[64];
+                {
+                    uint32_t r[4][16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tmem_ld16(lanes + kColS + 64 * buf + 16 * i, r[i]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        x[i] = __uint_as_float(r[i / 16][i % 16]);
+                }
+                tc_fence_before();
+                arrive(m.bars.s_free[buf]);
+                const int tok = part.tok0 + t * kTile + 64 * side;
+                if (tok + 64 > limit) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        x[i] = tok + i < limit ? x[i] : -INFINITY;
+                }
+                float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int i = 4; i < 64; ++i)
+                    top[i % 4] = fmaxf(top[i % 4], x[i]);
+                float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                m.half[buf][tid] = best;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                best = fmaxf(best, m.half[buf][tid ^ 64]) * f;
+                float shrink = 1.f;
+                if (t == walk.t0) {
+                    high = best;
+                } else if (best > high + kLag) {
+                    shrink = fast_exp2(high - best);          // 0 where nothing was seen before
+                    high = best;
+                    sum *= shrink;
+                }
+                const float ref = high == -INFINITY ? 0.f : high - kUp;
+                float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    x[i] = fast_exp2(fmaf(x[i], f, -ref));
+                    add[i % 4] += x[i];
+                }
+                sum += (add[0] + add[1]) + (add[2] + add[3]);
+                // P is free, and O at rest, once the product of the tile before is done
+                if (g > 0)
+                    wait(m.bars.pv_done, (uint32_t)(g - 1) & 1u, 14);
+                if constexpr (F8) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            float h[4], l[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                // hi: four significant bits, rounded; lo: the rest
+                                const float p = x[16 * c + 4 * w + e];
+                                h[e] = __uint_as_float((__float_as_uint(p) + 0x00080000u) &
+                                                       0xFFF00000u);
+                                l[e] = p - h[e];
+                            }
+                            hi[w] = (uint32_t)e4m3x2(h[0], h[1]) | (uint32_t)e4m3x2(h[2], h[3]) << 16;
+                            lo[w] = (uint32_t)e4m3x2(l[0], l[1]) | (uint32_t)e4m3x2(l[2], l[3]) << 16;
+                        }
+                        const uint32_t at = p_row + (((4 * side + c) ^ (row & 7)) << 4);
+                        st_shared_16(at, hi[0], hi[1], hi[2], hi[3]);
+                        st_shared_16(at + 8192, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 b =
+                                __floats2bfloat162_rn(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        st_shared_16(p_row + ((c ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, shrink != 1.f)) {
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(lanes + c, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            r[i] = __float_as_uint(__uint_as_float(r[i]) * shrink);
+                        tmem_st16(lanes + c, r);
+                    }
+                    tmem_wait_st();
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                arrive(m.bars.p_full);
+            }
+            // the segment's partial
+            m.half[2][tid] = sum;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            sum += m.half[2][tid ^ 64];
+            wait(m.bars.pv_done, (uint32_t)(g - 1) & 1u, 15);
+            const int64_t slot = (int64_t)walk.slot_block + pair;
+            const bool store = real && ok && !*abort_flag;
+            float scale = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;    // NaN stays
+            if constexpr (F8)
+                scale *= a.kv_scale;
+            float *out = a.o_part + (slot * kShRows + 64 * (int)rank + row) * kLatent;
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(lanes + c, r);
+                tmem_wait_ld();
+                if (store) {
+                    float *to_col = out + (c >> 7) * 256 + 128 * side + (c & 127);
+                    st_global_32(to_col, r, scale);
+                    st_global_32(to_col + 8, r + 8, scale);
+                }
+            }
+            tc_fence_before();
+            arrive(m.bars.o_free);
+            if (store && side == 0)
+                a.lse_part[slot * kShRows + 64 * (int)rank + row] =
+                    sum == 0.f ? -INFINITY : (high - kUp + log2f(sum)) * kLn2;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // A pair leaves together: no copy or arrival of one CTA is on its way to the other, and
+    // each has waited for its own copy of the last commit.
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+    if (threadIdx.x == 0 && m.status != 0 && a.status != nullptr)
+        atomicExch(a.status, m.status);
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+
+// A block per row, a thread per four columns: the partials of the group's prefix, then those of
+// the request's own tokens, in the order of their tokens.
+__global__ void __launch_bounds__(kMergeThreads)
+shared_merge_kernel(const SharedArgs a, const int pairs)
+{
+    __shared__ float weight[kMergeThreads];
+    __shared__ int64_t first_slot[2];
+    __shared__ int count[2], row_in[2];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t row = blockIdx.x;
+    const int t = threadIdx.x, r = (int)(row / a.rows), lane = t & 31;
+    const uint2 graw = reinterpret_cast<const uint2 *>(a.gate + row * kLatent)[t];
+    if (t < 2) {
+        const int g = a.group_of[r];
+        const int e = t == 1 ? a.num_groups + r : g;
+        int n = 0;
+        if (e >= 0) {
+            const SharedPart part = a.parts[e];
+            if (part.blocks > 0) {
+                const int64_t total = *a.total, busy = busy_pairs(total, pairs);
+                const int at = (int)(row - part.row0), blk = at / kShRows;
+                // positions of the block's tiles, and the pairs that have them
+                const int64_t v0 = part.base + (int64_t)blk * (part.tiles + kStart) + kStart;
+                const int p0 = (int)(((v0 + 1) * busy - 1) / total);
+                const int p1 = (int)(((v0 + part.tiles) * busy - 1) / total);
+                n = p1 - p0 + 1;
+                first_slot[t] = (int64_t)part.block0 + blk + p0;
+                row_in[t] = at % kShRows;
+            }
+        }
+        count[t] = n;
+    }
+    __syncthreads();
+    const int n0 = count[0], n = n0 + count[1];
+    auto part_row = [&](int i) -> int64_t {
+        const int s = i < n0 ? 0 : 1;
+        return (first_slot[s] + (s == 0 ? i : i - n0)) * kShRows + row_in[s];
+    };
+    // the row's maximum: every warp alike
+    float high = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+        high = fmaxf(high, __ldcg(a.lse_part + part_row(i)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+    const float ref = high == -INFINITY ? 0.f : high;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int i0 = 0; i0 < n; i0 += kMergeThreads) {
+        __syncthreads();
+        if (i0 + t < n)
+            weight[t] = expf(__ldcg(a.lse_part + part_row(i0 + t)) - ref);
+        __syncthreads();
+        const int here = min(kMergeThreads, n - i0);
+#pragma unroll 8
+        for (int i = 0; i < here; ++i) {
+            const float w = weight[i];
+            const float4 v = __ldcg(
+                reinterpret_cast<const float4 *>(a.o_part + part_row(i0 + i) * kLatent) + t);
+            sum += w;
+            if (w != 0.f) {                     // a part that the row does not see holds zeros
+                acc.x = fmaf(w, v.x, acc.x);
+                acc.y = fmaf(w, v.y, acc.y);
+                acc.z = fmaf(w, v.z, acc.z);
+                acc.w = fmaf(w, v.w, acc.w);
+            }
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float2 g01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw.x));
+    const float2 g23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw.y));
+    const __nv_bfloat162 p01 = __floats2bfloat162_rn(acc.x * inv / (1.f + expf(-g01.x)),
+                                                     acc.y * inv / (1.f + expf(-g01.y)));
+    const __nv_bfloat162 p23 = __floats2bfloat162_rn(acc.z * inv / (1.f + expf(-g23.x)),
+                                                     acc.w * inv / (1.f + expf(-g23.y)));
+    uint2 packed;
+    packed.x = *reinterpret_cast<const uint32_t *>(&p01);
+    packed.y = *reinterpret_cast<const uint32_t *>(&p23);
+    reinterpret_cast<uint2 *>(a.out + row * kLatent)[t] = packed;
+    if (t == 0 && a.lse != nullptr)
+        a.lse[row] = sum == 0.f ? -INFINITY : high + logf(sum);
+}
+
+template <bool F8>
+cudaError_t launch_decode(const SharedArgs &a, int sms, cudaStream_t stream)
+{
+    const CUtensorMapDataType dt = F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t es = F8 ? 1 : 2, wide = F8 ? 128 : 64;
+    const cuuint64_t blocks = F8 ? 4 : 9, rows = (cuuint64_t)a.num_reqs * a.rows;
+    ShMaps m;
+    // (column in a 128-byte block, token, block, page)
+    const cuuint64_t dims[4] = {wide, (cuuint64_t)kPageTokens, blocks, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {kRow * es, 128, (cuuint64_t)a.page_stride * es};
+    const cuuint32_t w32 = (cuuint32_t)wide;
+    const cuuint32_t k_box[4] = {w32, 64, 2, 1};
+    const cuuint32_t v_box[4] = {w32, F8 ? 128u : 64u, F8 ? 1u : 2u, 1};
+    bool ok = make_map(&m.k, dt, a.slab, 4, dims, strides, k_box) &&
+              make_map(&m.v, dt, a.slab, 4, dims, strides, v_box);
+    for (int b = 0; b < 7; ++b) {
+        const cuuint32_t box[4] = {w32, 1u << b, 1, 1};
+        ok = ok && make_map(&m.tail[b], dt, a.slab, 4, dims, strides, box);
+    }
+    // the 64 rope columns: 128-byte rows (bf16), or 64-byte ones with their swizzle
+    const cuuint64_t r_dims[3] = {(cuuint64_t)kRow, (cuuint64_t)kPageTokens, (cuuint64_t)a.num_pages};
+    const cuuint64_t r_str[2] = {kRow * es, (cuuint64_t)a.page_stride * es};
+    const cuuint32_t r_box[3] = {64, 64, 1};
+    const CUtensorMapSwizzle r_sw = F8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    ok = ok && make_map(&m.rope, dt, a.slab, 3, r_dims, r_str, r_box, r_sw);
+    if (F8) {
+        // [hi rows | lo rows] of 576 bytes: (column in a block, row, block)
+        const cuuint64_t n_dims[3] = {128, 2 * rows, 4}, n_str[2] = {kRow, 128};
+        const cuuint64_t o_dims[3] = {kRow, 2 * rows, 1}, o_str[2] = {kRow, kRow};
+        const cuuint32_t n_box[3] = {128, 64, 4}, o_box[3] = {64, 64, 1};
+        ok = ok && make_map(&m.qn, dt, a.q8, 3, n_dims, n_str, n_box) &&
+             make_map(&m.qr, dt, a.q8, 3, o_dims, o_str, o_box, r_sw);
+    } else {
+        const cuuint64_t n_dims[3] = {64, rows, 8}, n_str[2] = {kLatent * 2, 128};
+        const cuuint64_t o_dims[3] = {kRope, rows, 1}, o_str[2] = {kRope * 2, kRope * 2};
+        const cuuint32_t n_box[3] = {64, 64, 8}, o_box[3] = {64, 64, 1};
+        ok = ok && make_map(&m.qn, dt, a.q_nope, 3, n_dims, n_str, n_box) &&
+             make_map(&m.qr, dt, a.q_rope, 3, o_dims, o_str, o_box);
+    }
+    if (!ok)
+        return cudaErrorInvalidValue;
+    cudaError_t err = cudaFuncSetAttribute(shared_decode_kernel<F8>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kShSmem);
+    if (err != cudaSuccess)
+        return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+    cfg.blockDim = dim3(kShThreads);
+    cfg.dynamicSmemBytes = (size_t)kShSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    SharedArgs b = a;
+    // the accumulator's truncation is given back (see plmla_mass.cu): 4 units of 2^-23 for a
+    // chain of 36 bf16 MMAs, 1 for E4M3's
+    b.scale_log2 = (float)((double)a.scale * kLog2e * (1.0 + (F8 ? 1.0 : 4.0) * 0x1p-23));
+    err = cudaLaunchKernelEx(&cfg, shared_decode_kernel<F8>, m, b);
+    if (err != cudaSuccess)
+        return err;
+    cudaLaunchConfig_t mc = {};
+    mc.gridDim = dim3((unsigned)rows);
+    mc.blockDim = dim3(kMergeThreads);
+    mc.stream = stream;
+    mc.attrs = attr + 1;
+    mc.numAttrs = 1;
+    return cudaLaunchKernelEx(&mc, shared_merge_kernel, b, sms / 2);
+}
+
+}  // namespace
+
+int64_t shared_slots(int num_reqs, int rows, int num_groups, int sms)
+{
+    const int64_t total = (int64_t)num_reqs * rows;
+    return total / kShRows + num_groups + (int64_t)num_reqs * ((rows + kShRows - 1) / kShRows) +
+           sms / 2;
+}
+
+cudaError_t launch_shared(const SharedArgs &a, int sms, cudaStream_t stream)
+{
+    shared_plan_kernel<<<1, kShPlanThreads, 0, stream>>>(a);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess)
+        return err;
+    return a.q8 != nullptr ? launch_decode<true>(a, sms, stream)
+                           : launch_decode<false>(a, sms, stream);
+}
+
+}  // namespace plmla
