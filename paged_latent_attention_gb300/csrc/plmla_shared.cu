@@ -24,9 +24,9 @@
 // operands are warp-uniform and constant but for a base, against 110 cycles each from a
 // divergent thread with computed descriptors, so the issuing warp stays converged.
 //
-// Warps: 0 loads (TMA, one ring of 16 KB items in the order of use: K of tile g + 1, then V of
-// tile g), 1 issues the MMAs of the pair (in the even CTA), 4-7 softmax and epilogue, a
-// thread having half of a row's 128 scores in registers.  The running maximum lags: O is only
+// Warps: 0 loads K, 2 loads V (TMA, a ring of four 16 KB items each), 3 Q and K's rope block, 1 issues the MMAs of
+// the pair (in the even CTA), K a tile ahead of V, 4-7 softmax and epilogue, a thread
+// having half of a row's 128 scores in registers.  The running maximum lags: O is only
 // rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries in two E4M3 parts
 // (as in the FP8 decode) and the probabilities in two as well, hi + lo, so that they carry 8
 // bits like bf16 ones; a part each takes the rate that bf16 would.
@@ -41,7 +41,7 @@ namespace plmla {
 namespace {
 
 constexpr int kShThreads = 256;
-constexpr int kShSlots = 8, kShSlot = 16384;
+constexpr int kShSlots = 4, kShSlot = 16384;    // of the K ring, and of the V ring
 constexpr int kShRows = 128;                    // query rows of a block
 constexpr int kStart = 2;                       // cost of a block's start, in tiles
 constexpr int kShPlanThreads = 1024;
@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const Share
 // ---------------------------------------------------------------------------
 
 struct ShBars {
-    uint64_t full[kShSlots], empty[kShSlots];
+    uint64_t k_full[kShSlots], k_empty[kShSlots], v_full[kShSlots], v_empty[kShSlots];
     uint64_t rope_full, rope_empty, q_full, q_empty;
+    uint64_t zeros[2];                          // by the half of the V ring (E4M3)
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, pv_done, o_free, drain;
 };
@@ -204,7 +205,8 @@ struct ShFmt {
 constexpr int kShQ = 64 * 2 * kRow;             // bytes of the queries: 64 rows
 constexpr int kShP = 16384;
 constexpr int kShRope = 8192;
-constexpr int kShSmem = kShQ + kShP + kShSlots * kShSlot + kShRope + (int)sizeof(ShMisc);
+constexpr int kShRing = kShSlots * kShSlot;
+constexpr int kShSmem = kShQ + kShP + 2 * kShRing + kShRope + (int)sizeof(ShMisc);
 static_assert(kShSmem <= 232448, "shared memory");
 
 __device__ __forceinline__ uint32_t bar_of(const uint64_t &b) { return smem_u32(&b); }
@@ -293,32 +295,46 @@ __device__ __forceinline__ void pair_commit(uint32_t bar, uint32_t elected)
         : "memory");
 }
 
-// Arrive, with bytes to come, on a barrier of either CTA of the pair.
-__device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t bytes)
+// Arrive on a barrier of either CTA, releasing to this CTA: what the softmax warps hand over
+// (the probabilities, behind a proxy fence; TMEM) is used by their own SM's tensor core.
+__device__ __forceinline__ void arrive_pair(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tma_4d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                            int c2, int c3, uint32_t bar, uint64_t policy)
+// Expect bytes on one of the even CTA's barriers, and loads that complete there, by the lane
+// of a converged warp with `go` set (in a divergent branch every operand costs a move to
+// the uniform registers: some 200 cycles a load).
+__device__ __forceinline__ void expect_if(uint32_t bar, uint32_t bytes, uint32_t go)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
-        "l"(policy)
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(go)
         : "memory");
 }
 
-__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                            int c2, uint32_t bar)
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap *map, int c1, int c2, int c3,
+                                        uint32_t bar, uint64_t policy, uint32_t go)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+        "@e cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {0, %2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy),
+        "r"(go)
+        : "memory");
+}
+
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                        uint32_t bar, uint64_t policy, uint32_t go)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+        "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy),
+        "r"(go)
         : "memory");
 }
 
@@ -346,15 +362,25 @@ struct ShMaps {
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
+// The page of a part's column, 0 (reported) where the table has none of the pool.
+__device__ __forceinline__ int page_at(const SharedArgs &a, int req, int col, int32_t *status)
+{
+    const int page = a.page_table[(int64_t)req * a.table_ld + col];
+    if (page >= 0 && (int64_t)page < a.num_pages)
+        return page;
+    atomicExch(status, kStatusAppendPage);
+    return 0;
+}
+
 template <bool F8>
 __global__ void __launch_bounds__(kShThreads, 1)
 shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
 {
     using F = ShFmt<F8>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    const uint32_t s_q = smem_u32(smem), s_p = s_q + kShQ, s_ring = s_p + kShP;
-    const uint32_t s_rope = s_ring + kShSlots * kShSlot;
-    ShMisc &m = *reinterpret_cast<ShMisc *>(smem + kShQ + kShP + kShSlots * kShSlot + kShRope);
+    const uint32_t s_q = smem_u32(smem), s_p = s_q + kShQ, s_k = s_p + kShP, s_v = s_k + kShRing;
+    const uint32_t s_rope = s_v + kShRing;
+    ShMisc &m = *reinterpret_cast<ShMisc *>(smem + kShQ + kShP + 2 * kShRing + kShRope);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;");
     if ((s_q & 1023u) != 0u) {         // cannot be with no static shared memory
@@ -364,14 +390,17 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kShSlots; ++i) {
-            mbar_init(bar_of(m.bars.full[i]), 2);             // both CTAs' loads
-            mbar_init(bar_of(m.bars.empty[i]), 1);
+            mbar_init(bar_of(m.bars.k_full[i]), 1);           // the even CTA expects for both
+            mbar_init(bar_of(m.bars.k_empty[i]), 1);
+            mbar_init(bar_of(m.bars.v_full[i]), 1);
+            mbar_init(bar_of(m.bars.v_empty[i]), 1);
         }
-        mbar_init(bar_of(m.bars.rope_full), 2);
+        mbar_init(bar_of(m.bars.rope_full), 1);
         mbar_init(bar_of(m.bars.rope_empty), 1);
-        mbar_init(bar_of(m.bars.q_full), 2);
+        mbar_init(bar_of(m.bars.q_full), 1);
         mbar_init(bar_of(m.bars.q_empty), 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_of(m.bars.zeros[i]), 2);            // both CTAs wrote them
             mbar_init(bar_of(m.bars.s_full[i]), 1);
             mbar_init(bar_of(m.bars.s_free[i]), 8);           // the pair's softmax warps
         }
@@ -420,174 +449,166 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
     walk.begin(a.parts, m.first, from, to);
 
     if (warp == 0) {
-        // ------------------------------------------------------------ loads
-        // Two cursors: K runs a tile ahead of V.
-        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
-        ShWalk vw = walk;
-        bool more = walk.next(), v_any = vw.next(), ok = true;
-        int kt = walk.t0, vt = vw.t0;
-        int slot = 0, ropes = 0, loads = 0;
-        uint32_t phase = 0;
-        int64_t issued = 0;
-        bool fresh = true;                      // the K cursor is at a segment's start
-        auto page_at = [&](const SharedPart &p, int tok) -> int {
-            int page = a.page_table[(int64_t)p.req * a.table_ld + tok / kPageTokens];
-            if (page < 0 || (int64_t)page >= a.num_pages) {
-                if (lane == 0)
-                    atomicExch(status, kStatusAppendPage);
-                page = 0;
-            }
-            return page;
-        };
-        auto take = [&]() -> bool {
-            return all_ok(wait_bounded(bar_of(m.bars.empty[slot]), phase ^ 1, abort_flag, status, 2));
-        };
-        auto advance = [&]() {
-            ++issued;
-            if (++slot == kShSlots) {
-                slot = 0;
-                phase ^= 1;
-            }
-        };
-        int k_col = -1, k_page = 0, v_col = -1, v_page = 0;
-        while (ok && v_any) {
-            if (more) {
-                if (fresh) {
-                    if (loads > 0 && !all_ok(wait_bounded(bar_of(m.bars.q_empty), (loads - 1) & 1,
-                                                          abort_flag, status, 1))) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        const uint32_t bar = lead(m.bars.q_full);
-                        arrive_expect_cluster(bar, kShQ);
-                        const int row = walk.part.row0 + walk.row0 + 64 * (int)rank;
-                        for (int p = 0; p < F::parts; ++p) {
-                            const uint32_t dst = s_q + p * F::q_part;
-                            const int at = p * a.num_reqs * a.rows + row;
-                            tma_3d_pair(dst, &maps.qn, 0, at, 0, bar);
-                            tma_3d_pair(dst + F::q_part - F::rope_bytes, &maps.qr,
-                                        F8 ? kLatent : 0, at, 0, bar);
-                        }
-                    }
-                    ++loads;
-                    fresh = false;
-                    k_col = -1;
-                }
-                const int tok = walk.part.tok0 + kt * kTile;
-                if (tok / kPageTokens != k_col) {
-                    k_col = tok / kPageTokens;
-                    k_page = page_at(walk.part, tok);
+        // ------------------------------------------------------------ K loads
+        const uint64_t keep = l2_policy_evict_last();
+        const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0;
+        const uint32_t full = lead(m.bars.k_full[0]), empty = bar_of(m.bars.k_empty[0]);
+        int64_t g = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            int col = -1, page = 0;
+#pragma unroll 1
+            for (int t = walk.t0; t < walk.t1 && ok; ++t, ++g) {
+                const int tok = walk.part.tok0 + t * kTile;
+                if (tok / kPageTokens != col) {
+                    col = tok / kPageTokens;
+                    page = page_at(a, walk.part.req, col, status);
                 }
                 const int own = tok % kPageTokens + 64 * (int)rank;
-#pragma unroll 1
-                for (int i = 0; i < F::k_items && ok; ++i) {
-                    if (i == F::k_items / 2) {
-                        // the rope block in the middle of the products
-                        if (ropes > 0 && !all_ok(wait_bounded(bar_of(m.bars.rope_empty),
-                                                              (ropes - 1) & 1, abort_flag, status,
-                                                              3))) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) {
-                            const uint32_t bar = lead(m.bars.rope_full);
-                            arrive_expect_cluster(bar, F::rope_bytes);
-                            tma_load_3d_pair(s_rope, &maps.rope, kLatent, own, k_page, bar,
-                                             walk.part.vis == kNever ? keep : once);
-                        }
-                        ++ropes;
-                    }
-                    if (!take()) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        const uint32_t bar = lead(m.bars.full[slot]);
-                        arrive_expect_cluster(bar, kShSlot);
-                        tma_4d_pair(s_ring + slot * kShSlot, &maps.k, 0, own, 2 * i, k_page, bar,
-                                    keep);
-                    }
-                    advance();
+                const int half = F8 ? 2 * (int)(g & 1) : 0;
+                const uint32_t phase = (uint32_t)(F8 ? g >> 1 : g) & 1u;
+#pragma unroll
+                for (int i = 0; i < F::k_items; ++i) {
+                    const uint32_t at = 8 * (half + i);
+                    ok &= wait_bounded(empty + at, phase ^ 1, abort_flag, status, 2);
+                    expect_if(full + at, 2 * kShSlot, ok ? el0 : 0);
+                    load_4d(s_k + (half + i) * kShSlot, &maps.k, own, 2 * i, page, full + at, keep,
+                            ok ? el : 0);
                 }
-                if (!ok)
-                    break;
-                if (++kt == walk.t1) {
-                    more = walk.next();
-                    kt = walk.t0;
-                    fresh = true;
-                }
-                if (issued == F::k_items)       // the first K has no V before it
-                    if (more)
-                        continue;
-            }
-            // V of the tile behind
-            const int tok = vw.part.tok0 + vt * kTile;
-            if (tok / kPageTokens != v_col) {
-                v_col = tok / kPageTokens;
-                v_page = page_at(vw.part, tok);
-            }
-            const int in_page = tok % kPageTokens, valid = min(kTile, vw.part.len - tok);
-            // other pairs read a prefix too
-            const uint64_t v_use = vw.part.vis == kNever ? keep : once;
-#pragma unroll 1
-            for (int i = 0; i < F::v_items && ok; ++i) {
-                // bf16: (256 columns i / 2, 64 tokens i % 2); E4M3: (256 columns i)
-                const int t_off = F8 ? 0 : 64 * (i & 1), t_num = F8 ? 128 : 64;
-                const int block = F8 ? 2 * i + (int)rank : 4 * (i >> 1) + 2 * (int)rank;
-                if (!take()) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = s_ring + slot * kShSlot, bar = lead(m.bars.full[slot]);
-                const int n = min(t_num, max(0, valid - t_off));
-                if (n == t_num) {
-                    if (lane == 0) {
-                        arrive_expect_cluster(bar, kShSlot);
-                        tma_4d_pair(dst, &maps.v, 0, in_page + t_off, block, v_page, bar, v_use);
-                    }
-                } else {
-                    // a history's last tile: rows past it become zeros (they hold stale data,
-                    // and a weight of 0 times NaN is NaN), the others come in boxes of
-                    // 64, 32, .. 1 rows
-                    constexpr int kCols = F8 ? 1 : 2;         // 128-byte blocks of an item
-                    const int pitch = t_num * 128;
-                    for (int u = lane; u < kCols * (t_num - n) * 8; u += 32) {
-                        const int b = u / ((t_num - n) * 8), x = u % ((t_num - n) * 8);
-                        st_shared_16(dst + b * pitch + n * 128 + 16 * x, 0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        arrive_expect_cluster(bar, kCols * n * 128);
-                        for (int b = 0; b < kCols; ++b)
-                            for (int w = 6, r0 = 0; w >= 0; --w)
-                                if (n >> w & 1) {
-                                    tma_4d_pair(dst + b * pitch + r0 * 128, &maps.tail[w], 0,
-                                                in_page + t_off + r0, block + b, v_page, bar, once);
-                                    r0 += 1 << w;
-                                }
-                    }
-                }
-                advance();
-            }
-            if (++vt == vw.t1) {
-                v_any = vw.next();
-                vt = vw.t0;
-                v_col = -1;
+                ok = all_ok(ok);
             }
         }
         // both CTAs' copies complete on the even CTA's barriers: it waits for the last ones
         if (rank == 0 && lane == 0) {
+            const int64_t items = g * F::k_items;
+            for (int64_t it = items > kShSlots ? items - kShSlots : 0; it < items; ++it)
+                wait_drain(bar_of(m.bars.k_full[it % kShSlots]), (uint32_t)(it / kShSlots) & 1u);
+        }
+    } else if (warp == 3) {
+        // --------------------------------------- Q, and the rope block of K
+        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+        const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0;
+        const uint32_t rope_full = lead(m.bars.rope_full), q_full = lead(m.bars.q_full);
+        int64_t g = 0;
+        int loads = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            if (loads > 0)
+                ok = all_ok(wait_bounded(bar_of(m.bars.q_empty), (loads - 1) & 1, abort_flag, status,
+                                         1));
+            if (!ok)
+                break;
+            expect_if(q_full, 2 * kShQ, el0);
+            const int row = walk.part.row0 + walk.row0 + 64 * (int)rank;
+#pragma unroll
+            for (int p = 0; p < F::parts; ++p) {
+                const uint32_t dst = s_q + p * F::q_part;
+                const int at = p * a.num_reqs * a.rows + row;
+                load_3d(dst, &maps.qn, 0, at, 0, q_full, keep, el);
+                load_3d(dst + F::q_part - F::rope_bytes, &maps.qr, F8 ? kLatent : 0, at, 0, q_full,
+                        keep, el);
+            }
+            ++loads;
+            // other pairs read a prefix too
+            const uint64_t use = walk.part.vis == kNever ? keep : once;
+            int col = -1, page = 0;
+#pragma unroll 1
+            for (int t = walk.t0; t < walk.t1 && ok; ++t, ++g) {
+                const int tok = walk.part.tok0 + t * kTile;
+                if (tok / kPageTokens != col) {
+                    col = tok / kPageTokens;
+                    page = page_at(a, walk.part.req, col, status);
+                }
+                if (g > 0)
+                    ok = all_ok(wait_bounded(bar_of(m.bars.rope_empty), (uint32_t)(g - 1) & 1u,
+                                             abort_flag, status, 3));
+                expect_if(rope_full, 2 * F::rope_bytes, ok ? el0 : 0);
+                load_3d(s_rope, &maps.rope, kLatent, tok % kPageTokens + 64 * (int)rank, page,
+                        rope_full, use, ok ? el : 0);
+            }
+        }
+        if (rank == 0 && lane == 0) {
             if (loads > 0)
                 wait_drain(bar_of(m.bars.q_full), (loads - 1) & 1);
-            if (ropes > 0)
-                wait_drain(bar_of(m.bars.rope_full), (ropes - 1) & 1);
-            for (int64_t it = issued > kShSlots ? issued - kShSlots : 0; it < issued; ++it)
-                wait_drain(bar_of(m.bars.full[it % kShSlots]), (uint32_t)(it / kShSlots) & 1u);
+            if (g > 0)
+                wait_drain(bar_of(m.bars.rope_full), (uint32_t)(g - 1) & 1u);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ V loads
+        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+        const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0;
+        const uint32_t full = lead(m.bars.v_full[0]), empty = bar_of(m.bars.v_empty[0]);
+        int64_t g = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            const uint64_t use = walk.part.vis == kNever ? keep : once;
+            int col = -1, page = 0;
+#pragma unroll 1
+            for (int t = walk.t0; t < walk.t1 && ok; ++t, ++g) {
+                const int tok = walk.part.tok0 + t * kTile;
+                if (tok / kPageTokens != col) {
+                    col = tok / kPageTokens;
+                    page = page_at(a, walk.part.req, col, status);
+                }
+                const int in_page = tok % kPageTokens, valid = walk.part.len - tok;
+                const int half = F8 ? 2 * (int)(g & 1) : 0;
+                const uint32_t phase = (uint32_t)(F8 ? g >> 1 : g) & 1u;
+                // item i: bf16 (256 columns i / 2, 64 tokens i % 2); E4M3 (256 columns i)
+                if (valid >= kTile) {
+#pragma unroll
+                    for (int i = 0; i < F::v_items; ++i) {
+                        const uint32_t at = 8 * (half + i);
+                        const int block = F8 ? 2 * i + (int)rank : 4 * (i >> 1) + 2 * (int)rank;
+                        ok &= wait_bounded(empty + at, phase ^ 1, abort_flag, status, 2);
+                        expect_if(full + at, 2 * kShSlot, ok ? el0 : 0);
+                        load_4d(s_v + (half + i) * kShSlot, &maps.v, in_page + (F8 ? 0 : 64 * (i & 1)),
+                                block, page, full + at, use, ok ? el : 0);
+                    }
+                    ok = all_ok(ok);
+                    continue;
+                }
+                // a history's last tile: rows past it become zeros (they hold stale data, and
+                // a weight of 0 times NaN is NaN), the others come in boxes of 64, 32, .. 1
+                // rows
+                constexpr int kCols = F8 ? 1 : 2;             // 128-byte blocks of an item
+                constexpr int t_num = F8 ? 128 : 64, pitch = t_num * 128;
+                for (int i = 0; i < F::v_items; ++i) {
+                    const int n = min(t_num, max(0, valid - (F8 ? 0 : 64 * (i & 1))));
+                    ok = all_ok(ok && wait_bounded(empty + 8 * (half + i), phase ^ 1, abort_flag,
+                                                   status, 2));
+                    for (int b = 0; b < kCols && ok; ++b)
+                        for (int x = n * 128 + 16 * lane; x < pitch; x += 512)
+                            st_shared_16(s_v + (half + i) * kShSlot + b * pitch + x, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(lead(m.bars.zeros[half >> 1]));
+                for (int i = 0; i < F::v_items && ok; ++i) {
+                    const int t_off = F8 ? 0 : 64 * (i & 1), n = min(t_num, max(0, valid - t_off));
+                    const int block = F8 ? 2 * i + (int)rank : 4 * (i >> 1) + 2 * (int)rank;
+                    const uint32_t bar = full + 8 * (half + i);
+                    expect_if(bar, 2 * kCols * n * 128, el0);
+                    for (int b = 0; b < kCols; ++b)
+                        for (int w = 6, r0 = 0; w >= 0; --w)
+                            if (n >> w & 1) {
+                                load_4d(s_v + (half + i) * kShSlot + b * pitch + r0 * 128,
+                                        &maps.tail[w], in_page + t_off + r0, block + b, page, bar,
+                                        use, el);
+                                r0 += 1 << w;
+                            }
+                }
+            }
+        }
+        if (rank == 0 && lane == 0) {
+            const int64_t items = g * F::v_items;
+            for (int64_t it = items > kShSlots ? items - kShSlots : 0; it < items; ++it)
+                wait_drain(bar_of(m.bars.v_full[it % kShSlots]), (uint32_t)(it / kShSlots) & 1u);
         }
     } else if (warp == 1 && rank == 0) {
         // -------------------------------------------------------- MMA issue
+        // K runs a tile ahead of V.  A wait that gives up is noticed at the tile's end: MMAs on
+        // what had not arrived stay within the pair's memory, and nothing is stored.
         const uint32_t el = elect_one();
         constexpr uint32_t id_s = idesc_for<F8>(128, 128, false, false);
         constexpr uint32_t id_o = idesc_for<F8>(128, 256, false, true);
@@ -595,50 +616,36 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         const uint64_t dq_rope = sdesc(s_q + F::q_part - F::rope_bytes, 16, F8 ? 512 : 1024,
                                        F8 ? kSw64 : kSw128);
         const uint64_t dk_rope = sdesc(s_rope, 16, F8 ? 512 : 1024, F8 ? kSw64 : kSw128);
-        const uint64_t dk0 = sdesc(s_ring, 16, 1024, kSw128);
+        const uint64_t dk0 = sdesc(s_k, 16, 1024, kSw128);
         // V: columns contiguous; two 64-column blocks 8 KB apart (bf16), 8-token groups 1 KB
-        const uint64_t dv0 = sdesc(s_ring, 8192, 1024, kSw128);
+        const uint64_t dv0 = sdesc(s_v, 8192, 1024, kSw128);
         const uint64_t dp0 = sdesc(s_p, 16, 1024, kSw128);
         constexpr uint64_t kPart = F::q_part >> 4;
         ShWalk vw = walk;
-        bool more = walk.next(), v_any = vw.next(), ok = true, first_k = true, any = v_any;
-        int kt = walk.t0, vt = vw.t0, slot = 0, loads = 0;
-        uint32_t phase = 0;
+        bool more = walk.next(), v_any = vw.next(), ok = true, any = v_any;
+        int kt = walk.t0, vt = vw.t0, loads = 0;
+        uint32_t tails = 0;                     // phases of the zeros
         int64_t g = 0, v = 0, segs = 0;         // tiles scored, tiles multiplied, segments done
-        auto advance = [&]() {
-            pair_commit(bar_of(m.bars.empty[slot]), el);
-            if (++slot == kShSlots) {
-                slot = 0;
-                phase ^= 1;
-            }
-        };
-        auto wait = [&](const uint64_t &b, uint32_t parity, int code) -> bool {
-            const bool got = all_ok(wait_bounded(bar_of(b), parity, abort_flag, status, code));
+        auto wait = [&](uint32_t bar, uint32_t parity, int code) {
+            ok &= wait_bounded(bar, parity, abort_flag, status, code);
             tc_fence_after();
-            return got;
         };
-        while (ok && v_any) {
+        while (v_any) {
             if (more) {
                 if (kt == walk.t0) {
-                    if (!wait(m.bars.q_full, loads & 1, 4)) {
-                        ok = false;
-                        break;
-                    }
+                    wait(bar_of(m.bars.q_full), loads & 1, 4);
                     ++loads;
                 }
                 const int buf = (int)(g & 1);
-                if (g >= 2 && !wait(m.bars.s_free[buf], (uint32_t)((g - 2) >> 1) & 1u, 5)) {
-                    ok = false;
-                    break;
-                }
+                if (g >= 2)
+                    wait(bar_of(m.bars.s_free[buf]), (uint32_t)((g - 2) >> 1) & 1u, 5);
                 const uint32_t d = tmem + kColS + 64 * buf;
+                const uint32_t phase = (uint32_t)(F8 ? g >> 1 : g) & 1u;
+                const int half = F8 ? 2 * buf : 0;
 #pragma unroll
                 for (int i = 0; i < F::k_items; ++i) {
                     if (i == F::k_items / 2) {
-                        if (!ok || !wait(m.bars.rope_full, (uint32_t)g & 1u, 6)) {
-                            ok = false;
-                            break;
-                        }
+                        wait(bar_of(m.bars.rope_full), (uint32_t)g & 1u, 6);
                         constexpr int kSteps = F8 ? 2 : 4;
 #pragma unroll
                         for (int kk = 0; kk < kSteps; ++kk)
@@ -648,11 +655,8 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                                              id_s, 1, el);
                         pair_commit(bar_of(m.bars.rope_empty), el);
                     }
-                    if (!wait(m.bars.full[slot], phase, 7)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint64_t dk = dk0 + (uint64_t)(slot * (kShSlot >> 4));
+                    wait(bar_of(m.bars.k_full[0]) + 8 * (half + i), phase, 7);
+                    const uint64_t dk = dk0 + (uint64_t)((half + i) * (kShSlot >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
@@ -660,10 +664,8 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                             pair_mma<F8>(d, dq0 + p * kPart + (2 * i + kk / 4) * 512 + 2 * (kk % 4),
                                          dk + (kk / 4) * 512 + 2 * (kk % 4), id_s,
                                          (i | kk | p) != 0, el);
-                    advance();
+                    pair_commit(bar_of(m.bars.k_empty[0]) + 8 * (half + i), el);
                 }
-                if (!ok)
-                    break;
                 pair_commit(bar_of(m.bars.s_full[buf]), el);
                 ++g;
                 if (++kt == walk.t1) {
@@ -671,30 +673,26 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                     more = walk.next();
                     kt = walk.t0;
                 }
-                if (first_k) {
-                    first_k = false;
-                    if (more)
-                        continue;
-                }
+                if (!all_ok(ok))
+                    break;
+                if (g == 1 && more)
+                    continue;
             }
             // the segment before must have left O
-            if (vt == vw.t0 && segs > 0 &&
-                !wait(m.bars.o_free, (uint32_t)(segs - 1) & 1u, 8)) {
-                ok = false;
-                break;
+            if (vt == vw.t0 && segs > 0)
+                wait(bar_of(m.bars.o_free), (uint32_t)(segs - 1) & 1u, 8);
+            const int half = F8 ? 2 * (int)(v & 1) : 0;
+            if (vw.part.tok0 + (vt + 1) * kTile > vw.part.len) {
+                wait(bar_of(m.bars.zeros[half >> 1]), tails >> (half >> 1) & 1u, 12);
+                tails ^= 1u << (half >> 1);
             }
-            if (!wait(m.bars.p_full, (uint32_t)v & 1u, 9)) {
-                ok = false;
-                break;
-            }
+            wait(bar_of(m.bars.p_full), (uint32_t)v & 1u, 9);
             const uint32_t carry = vt != vw.t0 ? 1 : 0;
+            const uint32_t phase = (uint32_t)(F8 ? v >> 1 : v) & 1u;
 #pragma unroll
             for (int i = 0; i < F::v_items; ++i) {
-                if (!wait(m.bars.full[slot], phase, 10)) {
-                    ok = false;
-                    break;
-                }
-                const uint64_t dv = dv0 + (uint64_t)(slot * (kShSlot >> 4));
+                wait(bar_of(m.bars.v_full[0]) + 8 * (half + i), phase, 10);
+                const uint64_t dv = dv0 + (uint64_t)((half + i) * (kShSlot >> 4));
                 const int h = F8 ? i : i >> 1;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -707,10 +705,8 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                             (F8 ? (kk | p) != 0 : (kk | (i & 1)) != 0) ? 1u : carry;
                         pair_mma<F8>(tmem + 128 * h, dp, dv + (F8 ? 256 : 128) * kk, id_o, acc, el);
                     }
-                advance();
+                pair_commit(bar_of(m.bars.v_empty[0]) + 8 * (half + i), el);
             }
-            if (!ok)
-                break;
             pair_commit(bar_of(m.bars.pv_done), el);
             ++v;
             if (++vt == vw.t1) {
@@ -718,6 +714,8 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 v_any = vw.next();
                 vt = vw.t0;
             }
+            if (!all_ok(ok))
+                break;
         }
         if (any) {
             pair_commit(bar_of(m.bars.drain), el);
@@ -747,7 +745,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         auto arrive = [&](const uint64_t &b) {
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_cluster(lead(b));
+                arrive_pair(lead(b));
         };
         while (walk.next()) {
             const SharedPart &part = walk.part;
