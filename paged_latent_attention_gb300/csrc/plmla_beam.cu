@@ -13,8 +13,9 @@
 // shared memory, and the list is ranked by counting.  A row's order by logits is its order
 // by candidates, so no more than `beams` of a slice can matter.  merge_kernel: a block per
 // batch entry joins each row's sorted lists by bitonic merges in registers (a warp per
-// row), then the rows'.  Sums over slices, logarithms and candidates are held in 64 bits there:
-// candidates of different rows are compared, and a rounding must not change their order.
+// row), then the rows'.  Sums over slices, logarithms and candidates are held in pairs of
+// floats there: candidates of different rows are compared, and a rounding must not change
+// their order.
 //
 // Bound: HBM for the logits of a large batch; else latency of two launches.
 #include <math.h>
@@ -41,200 +42,169 @@ __device__ __forceinline__ float value_of(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// 16 bytes of logits as floats.
+// 32 bits of logits, kept as they came: 16-bit ones in pairs, compared as pairs (a bound is
+// one of the logits, so it has their type) and unpacked for the exponentials alone.
 template <typename T>
-struct Vec;
+struct Word;
 template <>
-struct Vec<float> {
-    static constexpr int n = 4;
-    __device__ static void load(const float *p, float (&x)[4])
+struct Word<float> {
+    static constexpr int n = 1;
+    static constexpr uint32_t none = 0xFF800000u;             // -inf in every element
+    __device__ static uint32_t max(uint32_t a, uint32_t b)
     {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
     }
-    __device__ static float one(const float *p) { return *p; }
+    __device__ static float get(uint32_t w, int) { return __uint_as_float(w); }
+    __device__ static uint32_t both(float x) { return __float_as_uint(x); }
+    // bit e: element e reaches x
+    __device__ static uint32_t reach(uint32_t w, uint32_t x)
+    {
+        return __uint_as_float(w) >= __uint_as_float(x) ? 1u : 0u;
+    }
 };
 template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int n = 8;
-    __device__ static void load(const __nv_bfloat16 *p, float (&x)[8])
+struct Word<__nv_bfloat16> {
+    static constexpr int n = 2;
+    static constexpr uint32_t none = 0xFF80FF80u;
+    __device__ static __nv_bfloat162 as(uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); }
+    __device__ static uint32_t max(uint32_t a, uint32_t b)
     {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        const __nv_bfloat162 m = __hmax2(as(a), as(b));
+        return *reinterpret_cast<const uint32_t *>(&m);
     }
-    __device__ static float one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    __device__ static float get(uint32_t w, int e)
+    {
+        return __uint_as_float(e ? w & 0xFFFF0000u : w << 16);
+    }
+    __device__ static uint32_t both(float x)
+    {
+        const uint32_t b = __float_as_uint(x) >> 16;          // x is a bf16
+        return b << 16 | b;
+    }
+    __device__ static uint32_t reach(uint32_t w, uint32_t x)
+    {
+        const uint32_t m = __hge2_mask(as(w), as(x));
+        return (m & 1u) | (m >> 31 << 1);
+    }
 };
 template <>
-struct Vec<__half> {
-    static constexpr int n = 8;
-    __device__ static void load(const __half *p, float (&x)[8])
+struct Word<__half> {
+    static constexpr int n = 2;
+    static constexpr uint32_t none = 0xFC00FC00u;
+    __device__ static __half2 as(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+    __device__ static uint32_t max(uint32_t a, uint32_t b)
     {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+        const __half2 m = __hmax2(as(a), as(b));
+        return *reinterpret_cast<const uint32_t *>(&m);
     }
-    __device__ static float one(const __half *p) { return __half2float(*p); }
+    __device__ static float get(uint32_t w, int e)
+    {
+        const float2 f = __half22float2(as(w));
+        return e ? f.y : f.x;
+    }
+    __device__ static uint32_t both(float x)
+    {
+        const __half2 h = __float2half2_rn(x);                // x is a fp16
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    __device__ static uint32_t reach(uint32_t w, uint32_t x)
+    {
+        const uint32_t m = __hge2_mask(as(w), as(x));
+        return (m & 1u) | (m >> 31 << 1);
+    }
 };
+
+// Two floats in one register pair, added and multiplied by one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 struct SliceOut {
     float *high, *sum;                  // [rows, slices]
-    uint32_t *keys;                     // [rows, slices, beams], descending
-    int32_t *ids;
+    uint64_t *lists;                    // [rows, slices, beams] entries, descending
     int slices;
 };
 
-// E logits a thread, in groups of 16 bytes: group g of thread t starts at element
-// (g * threads + t) * n of the slice, so that element order is (group, thread, element).
-template <typename T, int E>
-__global__ void __launch_bounds__(kSliceThreads)
-slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int vocab, int vec_ok,
-             SliceOut o)
+// A logit and its token as one number: the larger logit first, then the lower token.  0 is none.
+__device__ __forceinline__ uint64_t entry_of(float x, int v)
 {
-    constexpr int N = Vec<T>::n, G = E / N, kSlice = E * kSliceThreads;
-    constexpr int kCap = 2048 + 4 * kMaxBeams;
-    __shared__ uint32_t keys[kCap];
-    __shared__ int32_t ids[kCap];
-    __shared__ alignas(16) uint32_t tops[kSliceThreads];
-    __shared__ float warp_f[kSliceThreads / 32];
-    __shared__ int warp_i[kSliceThreads / 32];
-    __shared__ uint32_t bound;
-    __shared__ int count, ties;
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int row = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t at = (int64_t)row * o.slices + blockIdx.x;
-    if (ended != nullptr && ended[row] != 0)
-        return;                                 // its logits count nothing
-    const int v0 = blockIdx.x * kSlice, left = vocab - v0;
-    const T *src = logits + (int64_t)row * ld + v0;
-    float x[E];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int e0 = (g * kSliceThreads + t) * N;
-        float v[N];
-        if (vec_ok && e0 + N <= left) {
-            Vec<T>::load(src + e0, v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                v[e] = e0 + e < left ? Vec<T>::one(src + e0 + e) : -INFINITY;
+    return (uint64_t)key_of(x) << 32 | (uint32_t)~v;
+}
+
+// What a block shares.
+struct SliceShared {
+    static constexpr int kFew = 512;            // a list that is ranked by counting
+    uint64_t list[kFew];
+    uint32_t tops[kSliceThreads];
+    float warp_sum[kSliceThreads / 32];
+    uint32_t warp_high[kSliceThreads / 32], warp_least[kSliceThreads / 32];
+    int warp_i[kSliceThreads / 32];
+    uint32_t bound;
+    int count;
+};
+
+// Slices in which more elements reach the first bound than the list holds: equal logits (masked
+// ones, say), or few threads with many.  A tighter bound is the beams'th largest of all
+// threads' maxima.  What exceeds it, if that is few, and of what equals it the first in
+// element order fill the list; else the block takes the largest out one by one.  The logits
+// are read again.  Returns the list's length.
+template <typename T, int G>
+__device__ __noinline__ int pick_list(const T *head, int v0, int lo, int left, float top, int beams,
+                                      SliceShared &s)
+{
+    constexpr int N = 16 / sizeof(T), kEach = G * N;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    auto id_at = [&](int e) { return (e / N * kSliceThreads + t) * N + e % N; };
+    auto in_row = [&](int id) { return id >= lo && id < left; };
+    auto logit = [&](int id) { return in_row(id) ? (float)head[v0 + id] : -INFINITY; };
+    const uint32_t mine = key_of(top);
+    s.tops[t] = mine;
+    __syncthreads();                            // and count has been read
+    int before = 0;
+    for (int j = 0; j < kSliceThreads; ++j)
+        before += s.tops[j] > mine || (s.tops[j] == mine && j < t);
+    if (before == beams - 1)
+        s.bound = mine;
+    if (t == 0)
+        s.count = 0;
+    __syncthreads();
+    const uint32_t least = s.bound;
+    const float reach = value_of(least);
+    for (int e = 0; e < kEach; ++e) {
+        const float x = logit(id_at(e));
+        if (x > reach) {                        // (-inf past the row)
+            const int i = atomicAdd(&s.count, 1);
+            if (i < SliceShared::kFew)
+                s.list[i] = entry_of(x, v0 + id_at(e));
         }
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            x[g * N + e] = v[e];
-    }
-    // the slice's maximum and sum; elements past the row are -inf and add nothing
-    float high = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        high = fmaxf(high, x[e]);
-    const uint32_t top = key_of(high);
-    float m = high;
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    if (lane == 0)
-        warp_f[warp] = m;
-    tops[t] = top;
-    if (t == 0) {
-        count = ties = 0;
-        bound = 0;
     }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSliceThreads / 32; ++w)
-        m = fmaxf(m, warp_f[w]);
-    // the beams'th largest of the threads' maxima: at least that many elements reach it
-    {
-        int above = 0;
-        const uint4 *p = reinterpret_cast<const uint4 *>(tops);
-#pragma unroll 8
-        for (int j = 0; j < kSliceThreads / 4; ++j) {
-            const uint4 k = p[j];
-            above += (k.x > top || (k.x == top && 4 * j < t)) +
-                     (k.y > top || (k.y == top && 4 * j + 1 < t)) +
-                     (k.z > top || (k.z == top && 4 * j + 2 < t)) +
-                     (k.w > top || (k.w == top && 4 * j + 3 < t));
-        }
-        if (above == beams - 1)
-            bound = top;
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        sum += fast_exp2((x[e] - ref) * kLog2e);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    __syncthreads();                            // the maxima have been read, the bound is set
-    if (lane == 0)
-        warp_f[warp] = sum;
-    const uint32_t least = bound;
-    // elements above the bound: at most beams - 1 threads have any, so at most
-    // (kMaxBeams - 1) * E <= kCap of them (more only in a row with NaN, which counts nothing)
-    if (top >= least) {
-        int equal = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t k = key_of(x[e]);
-            const int id = ((e / N) * kSliceThreads + t) * N + e % N;
-            if (k > least && id < left) {
-                const int i = atomicAdd(&count, 1);
-                if (i < kCap) {
-                    keys[i] = k;
-                    ids[i] = v0 + id;
-                }
-            }
-            equal += k == least && id < left ? 1 : 0;
-        }
-        if (equal != 0)
-            atomicAdd(&ties, equal);
-    }
-    __syncthreads();
-    if (t == 0) {
-        float s = 0.f;
-        for (int w = 0; w < kSliceThreads / 32; ++w)
-            s += warp_f[w];
-        o.high[at] = m;
-        o.sum[at] = s;
-    }
-    // elements at the bound fill the list up: all of them where they are few (the ranking
-    // puts them in order), else the first ones in element order
-    const int above = min(count, kCap), equal = ties;
-    int n = above;
-    if (above < beams && equal <= 4 * kMaxBeams) {
-        __syncthreads();                        // count has been read
-        if (top >= least) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int id = ((e / N) * kSliceThreads + t) * N + e % N;
-                if (key_of(x[e]) == least && id < left) {
-                    const int i = atomicAdd(&count, 1);
-                    keys[i] = least;
-                    ids[i] = v0 + id;
-                }
-            }
-        }
-        n = above + equal;
-    } else if (above < beams) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            int mine = 0;
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                mine += key_of(x[g * N + e]) == least && (g * kSliceThreads + t) * N + e < left;
-            int y = mine;
-#pragma unroll
+    int n = s.count;
+    if (n <= SliceShared::kFew) {
+        for (int g = 0; g < G && n < beams; ++g) {
+            int equal = 0;
+            for (int e = g * N; e < g * N + N; ++e)
+                equal += logit(id_at(e)) == reach && in_row(id_at(e));
+            int y = equal;
             for (int w = 1; w < 32; w <<= 1) {
                 const int z = __shfl_up_sync(0xffffffffu, y, w);
                 if (lane >= w)
@@ -242,94 +212,313 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
             }
             __syncthreads();                    // the last group's sums have been read
             if (lane == 31)
-                warp_i[warp] = y;
+                s.warp_i[warp] = y;
             __syncthreads();
-            int i = n + y - mine;
+            int i = n + y - equal;
             for (int w = 0; w < kSliceThreads / 32; ++w) {
-                i += w < warp ? warp_i[w] : 0;
-                n += warp_i[w];
+                i += w < warp ? s.warp_i[w] : 0;
+                n += s.warp_i[w];
             }
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const int id = (g * kSliceThreads + t) * N + e;
-                if (key_of(x[g * N + e]) == least && id < left) {
-                    if (i < beams) {
-                        keys[i] = least;
-                        ids[i] = v0 + id;
-                    }
+            for (int e = g * N; e < g * N + N; ++e)
+                if (logit(id_at(e)) == reach && in_row(id_at(e))) {
+                    if (i < beams)
+                        s.list[i] = entry_of(reach, v0 + id_at(e));
                     ++i;
+                }
+        }
+        __syncthreads();
+        return n < beams ? n : s.count > beams ? s.count : beams;
+    }
+    uint64_t last = ~0ull;
+    for (int i = 0; i < beams; ++i) {
+        uint64_t best = 0;                      // the first behind the last one taken
+        for (int e = 0; e < kEach; ++e) {
+            const float x = logit(id_at(e));
+            if (x == x && in_row(id_at(e))) {
+                const uint64_t k = entry_of(x, v0 + id_at(e));
+                best = k < last && k > best ? k : best;
+            }
+        }
+        for (int w = 16; w > 0; w >>= 1) {
+            const uint64_t k = __shfl_xor_sync(0xffffffffu, best, w);
+            best = k > best ? k : best;
+        }
+        __syncthreads();                        // the last round's entries have been read
+        if (lane == 0) {
+            s.tops[2 * warp] = (uint32_t)(best >> 32);
+            s.tops[2 * warp + 1] = (uint32_t)best;
+        }
+        __syncthreads();
+        last = 0;
+        for (int w = 0; w < kSliceThreads / 32; ++w) {
+            const uint64_t k = (uint64_t)s.tops[2 * w] << 32 | s.tops[2 * w + 1];
+            last = k > last ? k : last;
+        }
+        if (t == 0)
+            s.list[i] = last;
+    }
+    __syncthreads();
+    return beams;
+}
+
+// G groups of 16 bytes a thread: group g of thread t starts at element (g * threads + t) * n of
+// the slice (n elements in 16 bytes), so that element order is (group, thread, element).
+// Latency-bound: five blocks an SM hide the loads and barriers (with three, and the rare
+// path's copy of the logits in local memory, 128 rows of 150,001 took 28 us).
+template <typename T, int G>
+__global__ void __launch_bounds__(kSliceThreads, 5)
+slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int vocab, SliceOut o)
+{
+    using W = Word<T>;
+    constexpr int N = 4 * W::n, kSlice = G * N * kSliceThreads, kWarps = kSliceThreads / 32;
+    __shared__ SliceShared s;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int row = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int64_t at = (int64_t)row * o.slices + blockIdx.x;
+    if (ended != nullptr && ended[row] != 0)
+        return;                                 // its logits count nothing
+    // 16-byte groups at aligned addresses, whatever the row's own: element 0 of the first slice
+    // lies up to N - 1 elements before the row.  Groups across either end are read by
+    // elements.
+    const T *head = logits + (int64_t)row * ld;
+    const int skip = (int)(reinterpret_cast<uintptr_t>(head) % 16 / sizeof(T));
+    const int v0 = blockIdx.x * kSlice - skip, left = vocab - v0, lo = max(0, -v0);
+    const T *src = head + v0;
+    auto in_row = [&](int id) { return id >= lo && id < left; };
+    uint32_t raw[G][4];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int e0 = (g * kSliceThreads + t) * N;
+        if (e0 >= lo && e0 + N <= left) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + e0);
+            raw[g][0] = v.x, raw[g][1] = v.y, raw[g][2] = v.z, raw[g][3] = v.w;
+        } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                raw[g][w] = W::none;
+#pragma unroll
+                for (int e = 0; e < W::n; ++e) {
+                    const int i = e0 + W::n * w + e;
+                    if (in_row(i)) {
+                        if constexpr (W::n == 1) {
+                            raw[g][w] = *reinterpret_cast<const uint32_t *>(src + i);
+                        } else {
+                            const uint32_t b = *reinterpret_cast<const uint16_t *>(src + i);
+                            raw[g][w] = e ? (raw[g][w] & 0xFFFFu) | b << 16
+                                          : (raw[g][w] & 0xFFFF0000u) | b;
+                        }
+                    }
                 }
             }
         }
-        n = min(n, beams);
+    }
+    if (t == 0)
+        s.count = 0;
+    // this thread's maximum; elements past the row are -inf
+    uint32_t most = raw[0][0];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            most = W::max(most, raw[g][w]);
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < W::n; ++e)
+        top = fmaxf(top, W::get(most, e));      // (a NaN is left out)
+    const uint32_t top_key = key_of(top), warp_top = __reduce_max_sync(0xffffffffu, top_key);
+    // A bound that at least `beams` elements reach: the least of the warps' share'th largest
+    // thread maxima.  Only warps count whose every thread has an element (a slice that the
+    // row does not fill has fewer; with too few, all of its elements are taken).
+    const int skipped = (lo + 32 * N - 1) / (32 * N);
+    const int whole = min(left, kSliceThreads * N) / (32 * N) - skipped;
+    const int share = whole > 0 ? (beams + whole - 1) / whole : 33;
+    uint32_t warp_key = share > 32 ? key_of(-INFINITY) : warp_top;
+    {
+        uint32_t rest = top_key;
+        for (int j = 1; j < share && share <= 32; ++j) {
+            const uint32_t first = __ballot_sync(0xffffffffu, rest == warp_key);
+            if (lane == __ffs(first) - 1)
+                rest = 0;                       // below every key
+            warp_key = __reduce_max_sync(0xffffffffu, rest);
+        }
+    }
+    if (lane == 0) {
+        s.warp_high[warp] = warp_top;
+        s.warp_least[warp] = warp >= skipped && warp < skipped + whole ? warp_key : 0xFFFFFFFFu;
     }
     __syncthreads();
+    uint32_t high_key = 0, least = whole > 0 ? 0xFFFFFFFFu : key_of(-INFINITY);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        high_key = max(high_key, s.warp_high[w]);
+        least = min(least, s.warp_least[w]);
+    }
+    const float reach = value_of(least);
+    if (top >= reach) {
+        const uint32_t x = W::both(reach);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t hit = W::reach(raw[g][w], x);
+                if (hit != 0)
+#pragma unroll
+                    for (int e = 0; e < W::n; ++e) {
+                        const int id = (g * kSliceThreads + t) * N + W::n * w + e;
+                        if ((hit >> e & 1u) != 0 && in_row(id)) {
+                            const int i = atomicAdd(&s.count, 1);
+                            if (i < SliceShared::kFew)
+                                s.list[i] = entry_of(W::get(raw[g][w], e), v0 + id);
+                        }
+                    }
+            }
+    }
+    const float high = value_of(high_key), ref = high == -INFINITY ? 0.f : high;
+    float sum;
+    {
+        const uint64_t shift = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
+        uint64_t acc[2] = {0, 0};               // two pairs of zeros
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int w = 0; w < 4; w += 2 / W::n) {
+                const float a = W::get(raw[g][w], 0);
+                const float b = W::n == 2 ? W::get(raw[g][w], 1) : W::get(raw[g][w + 1], 0);
+                float x, y;
+                unpack2(mul2(add2(pack2(a, b), shift), scale), x, y);
+                acc[g & 1] = add2(acc[g & 1], pack2(fast_exp2(x), fast_exp2(y)));
+            }
+        float x, y;
+        unpack2(add2(acc[0], acc[1]), x, y);
+        sum = x + y;
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    if (lane == 0)
+        s.warp_sum[warp] = sum;
+    __syncthreads();
+    if (t == 0) {
+        float all = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            all += s.warp_sum[w];
+        o.high[at] = high;
+        o.sum[at] = all;
+    }
+    int n = s.count;
+    if (n > SliceShared::kFew)
+        n = pick_list<T, G>(head, v0, lo, left, top, beams, s);
     for (int i = t; i < max(n, beams); i += kSliceThreads) {
-        int rank = i;
-        uint32_t k = 0;
-        int id = 0x7FFFFFFF;
-        if (i < n) {
-            k = keys[i];
-            id = ids[i];
-            rank = 0;
+        const uint64_t k = i < n ? s.list[i] : 0;
+        int rank = i < n ? 0 : i;
+        if (i < n)
+#pragma unroll 8
             for (int j = 0; j < n; ++j)
-                rank += keys[j] > k || (keys[j] == k && ids[j] < id);
-        }
-        if (rank < beams) {
-            o.keys[at * beams + rank] = k;
-            o.ids[at * beams + rank] = id;
-        }
+                rank += s.list[j] > k;
+        if (rank < beams)
+            o.lists[at * beams + rank] = k;
     }
 }
 
-// Lists of 32 P entries in descending order, entry p * 32 + lane in register p of a lane.
-// An entry is (key, id): the larger key first, then the lower id.
-template <typename K>
-__device__ __forceinline__ bool before(K k, int id, K k2, int id2)
+// Lists of 32 P entries in descending order, entry p * 32 + lane in register p of a lane: the
+// upper 32 P of this list and another, whose entries come in ascending order (a bitonic
+// merge).  An entry is a number, or (key, id): the larger key first, then the lower id.
+template <typename A>
+__device__ __forceinline__ bool before(A a, A b)
 {
-    return k > k2 || (k == k2 && id < id2);
+    return a > b;
+}
+struct Candidate {
+    unsigned long long key;
+    int id;
+};
+__device__ __forceinline__ bool before(Candidate a, Candidate b)
+{
+    return a.key > b.key || (a.key == b.key && a.id < b.id);
+}
+__device__ __forceinline__ uint64_t shuffle_xor(uint64_t a, int w)
+{
+    return __shfl_xor_sync(0xffffffffu, a, w);
+}
+__device__ __forceinline__ Candidate shuffle_xor(Candidate a, int w)
+{
+    return {__shfl_xor_sync(0xffffffffu, a.key, w), __shfl_xor_sync(0xffffffffu, a.id, w)};
 }
 
-// The upper 32 P of this list and another, whose entries come in ascending order.
-template <int P, typename K>
-__device__ __forceinline__ void join(K (&k)[P], int (&id)[P], const K (&k2)[P], const int (&id2)[P])
+template <int P, typename A>
+__device__ __forceinline__ void join(A (&list)[P], const A (&other)[P])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int p = 0; p < P; ++p)
-        if (before(k2[p], id2[p], k[p], id[p])) {
-            k[p] = k2[p];
-            id[p] = id2[p];
-        }
+        if (before(other[p], list[p]))
+            list[p] = other[p];
     if constexpr (P == 2) {
-        if (before(k[1], id[1], k[0], id[0])) {
-            const K x = k[0];
-            const int y = id[0];
-            k[0] = k[1], id[0] = id[1];
-            k[1] = x, id[1] = y;
+        if (before(list[1], list[0])) {
+            const A x = list[0];
+            list[0] = list[1];
+            list[1] = x;
         }
     }
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1)
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const K x = __shfl_xor_sync(0xffffffffu, k[p], w);
-            const int y = __shfl_xor_sync(0xffffffffu, id[p], w);
-            if (before(x, y, k[p], id[p]) == ((lane & w) == 0)) {
-                k[p] = x;
-                id[p] = y;
-            }
+            const A x = shuffle_xor(list[p], w);
+            if (before(x, list[p]) == ((lane & w) == 0))
+                list[p] = x;
         }
 }
 
-__device__ __forceinline__ unsigned long long wide_key(double x)
+// A number as the unevaluated sum of two floats, hi = hi + lo rounded (error-free transforms:
+// Dekker, 1971; Knuth, The Art of Computer Programming 2, 4.2.2).  48 bits are plenty here,
+// and this device's 64-bit unit is so slow that with it the merge took 25 us.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b)
 {
-    const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
-    return b >> 63 ? ~b : b | 1ull << 63;
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ double wide_value(unsigned long long k)
+__device__ __forceinline__ Pair add(Pair a, float b)
 {
-    return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k));
+    const Pair s = two_sum(a.hi, b);
+    const float lo = __fadd_rn(s.lo, a.lo), hi = __fadd_rn(s.hi, lo);
+    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b)
+{
+    const Pair s = two_sum(a.hi, b.hi);
+    const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
+    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+
+// ln s of a positive sum: s = 2^e m with m around 1; ln 2 in a part whose products with e are
+// exact and a rest.  Off by some 2^-25.
+__device__ __forceinline__ Pair ln(float s)
+{
+    constexpr double kLn2 = 0.69314718055994530942;
+    constexpr float kLn2Hi = 2839.f / 4096.f, kLn2Lo = (float)(kLn2 - 2839.0 / 4096.0);
+    int e;
+    float m = frexpf(s, &e);                    // [1/2, 1)
+    if (m < 0.70710678f) {
+        m *= 2.f;
+        --e;
+    }
+    return add(two_sum((float)e * kLn2Hi, logf(m)), (float)e * kLn2Lo);
+}
+
+// Keys in the order of pairs.  -inf, alone in hi, is above 0, which stands for no candidate.
+__device__ __forceinline__ unsigned long long wide_key(Pair x)
+{
+    return (unsigned long long)key_of(x.hi) << 32 | key_of(x.lo);
+}
+__device__ __forceinline__ float wide_value(unsigned long long k)
+{
+    return value_of((uint32_t)(k >> 32));       // lo is below half a unit of hi
 }
 
 template <int P>
@@ -341,21 +530,27 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
     const int K = a.beams, per_row = K >= kWarps ? 1 : kWarps / K;
     const int part = warp % per_row;
-    unsigned long long best[P];
-    int flat[P];
+    const Candidate none = {0, 0x7FFFFFFF};     // below -inf
+    Candidate best[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        best[p] = 0;                            // no candidate: below -inf
-        flat[p] = 0x7FFFFFFF;
-    }
+    for (int p = 0; p < P; ++p)
+        best[p] = none;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int k = warp / per_row; k < K; k += kWarps / per_row) {
         const int64_t row = (int64_t)b * K + k;
-        const double score = (double)a.scores[row];
+        // this warp's first list of the row is on its way while the sum is taken
+        uint64_t next[P];
+        auto fetch = [&](int s) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int i = kList - 1 - (32 * p + lane);          // ascending for join
+                next[p] = s < o.slices && i < K ? o.lists[(row * o.slices + s) * K + i] : 0;
+            }
+        };
+        fetch(part);
+        const float score = a.scores[row];
         const bool ended = a.ended != nullptr && a.ended[row] != 0;
-        unsigned long long wk[P];
-        int wi[P];
-        double shift = score;
+        Pair shift = {score, 0.f};
         if (!ended) {
             float high = -INFINITY;
             for (int s = lane; s < o.slices; s += 32)
@@ -363,63 +558,66 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1)
                 high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, w));
-            double sum = 0.0;
+            Pair sum = {0.f, 0.f};
             for (int s = lane; s < o.slices; s += 32) {
                 const float h = o.high[row * o.slices + s];
                 // (a NaN among the logits is in the sum, not in the maximum)
-                const double e = h == high ? 1.0 : exp((double)h - (double)high);
-                sum += e * (double)o.sum[row * o.slices + s];
+                const float e = h == high ? 1.f : expf(h - high);
+                sum = add(sum, e * o.sum[row * o.slices + s]);
             }
 #pragma unroll
-            for (int w = 16; w > 0; w >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, w);
-            shift = score - ((double)high + log(sum));
+            for (int w = 16; w > 0; w >>= 1) {
+                const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, w);
+                const float lo = __shfl_xor_sync(0xffffffffu, sum.lo, w);
+                sum = add(sum, Pair{hi, lo});                 // the same in both lanes
+            }
+            const float s = sum.hi;
+            const Pair l = ln(s);
+            shift = add(add(two_sum(score, -high), -l.hi), -(l.lo + sum.lo / s));
+            if (!isfinite(s) || s <= 0.f)
+                shift.hi = -INFINITY;
         }
-        if (!isfinite(shift) || ended) {
+        Candidate mine[P];
+        if (!isfinite(shift.hi) || ended) {
             // its first tokens in order, at -inf; an ended beam's end token before them
-            const bool end = ended && isfinite(shift);
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int i = kList - 1 - (32 * p + lane);          // ascending for join
-                const bool is_end = end && i == 0;
-                const int v = is_end ? a.end_token : end && i - 1 < a.end_token ? i - 1 : i;
-                const bool in = part == 0 && i < K && v < a.vocab;
-                wk[p] = !in ? 0 : wide_key(is_end ? score : -(double)INFINITY);
-                wi[p] = !in ? 0x7FFFFFFF : k * a.vocab + v;
-            }
-            join<P>(best, flat, wk, wi);
-            continue;
-        }
-        // this warp's slices of the row by logits (a part in each warp of the row)
-        uint32_t key[P];
-        int id[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            key[p] = 0;
-            id[p] = 0x7FFFFFFF;
-        }
-        for (int s = part; s < o.slices; s += per_row) {
-            const int64_t at = (row * o.slices + s) * K;
-            uint32_t k2[P];
-            int id2[P];
+            const bool end = ended && isfinite(score);
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 const int i = kList - 1 - (32 * p + lane);
-                k2[p] = i < K ? o.keys[at + i] : 0;
-                id2[p] = i < K ? o.ids[at + i] : 0x7FFFFFFF;
+                const bool is_end = end && i == 0;
+                const int v = is_end ? a.end_token : end && i - 1 < a.end_token ? i - 1 : i;
+                mine[p] = none;
+                if (part == 0 && i < K && v < a.vocab)
+                    mine[p] = {wide_key({is_end ? score : -INFINITY, 0.f}), k * a.vocab + v};
             }
-            join<P>(key, id, k2, id2);
-        }
-        // as candidates, in ascending order: entry i comes from kList - 1 - i
+        } else {
+            // its slices by logits (a part in each warp of the row)
+            uint64_t list[P];
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const uint32_t x = __shfl_sync(0xffffffffu, key[P - 1 - p], 31 - lane);
-            const int v = __shfl_sync(0xffffffffu, id[P - 1 - p], 31 - lane);
-            const bool in = x != 0 && v < a.vocab;
-            wk[p] = in ? wide_key((double)value_of(x) + shift) : 0;
-            wi[p] = in ? k * a.vocab + v : 0x7FFFFFFF;
+            for (int p = 0; p < P; ++p)
+                list[p] = 0;
+            for (int s = part; s < o.slices; s += per_row) {
+                uint64_t now[P];
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    now[p] = next[p];
+                fetch(s + per_row);
+                join<P>(list, now);
+            }
+            // as candidates, in ascending order: entry i comes from kList - 1 - i
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const uint64_t x = __shfl_sync(0xffffffffu, list[P - 1 - p], 31 - lane);
+                const int v = (int)~(uint32_t)x;
+                Pair c = add(shift, value_of((uint32_t)(x >> 32)));
+                if (!isfinite(c.hi))
+                    c = {-INFINITY, 0.f};       // a masked token
+                mine[p] = none;
+                if (x != 0)
+                    mine[p] = {wide_key(c), k * a.vocab + v};
+            }
         }
-        join<P>(best, flat, wk, wi);
+        join<P>(best, mine);
     }
     // the warps' lists: the upper half hands its lists to the lower half
 #pragma unroll 1
@@ -427,20 +625,18 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
         if (warp >= half && warp < 2 * half)
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                keys[(warp - half) * kList + 32 * p + lane] = best[p];
-                ids[(warp - half) * kList + 32 * p + lane] = flat[p];
+                keys[(warp - half) * kList + 32 * p + lane] = best[p].key;
+                ids[(warp - half) * kList + 32 * p + lane] = best[p].id;
             }
         __syncthreads();
         if (warp < half) {
-            unsigned long long wk[P];
-            int wi[P];
+            Candidate other[P];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 const int i = kList - 1 - (32 * p + lane);
-                wk[p] = keys[warp * kList + i];
-                wi[p] = ids[warp * kList + i];
+                other[p] = {keys[warp * kList + i], ids[warp * kList + i]};
             }
-            join<P>(best, flat, wk, wi);
+            join<P>(best, other);
         }
         __syncthreads();
     }
@@ -449,38 +645,38 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
         for (int p = 0; p < P; ++p)
             if (32 * p + lane < K) {
                 const int64_t at = (int64_t)b * K + 32 * p + lane;
-                a.tokens[at] = flat[p] % a.vocab;
-                a.parents[at] = b * K + flat[p] / a.vocab;
-                a.out_scores[at] = (float)wide_value(best[p]);
+                a.tokens[at] = best[p].id % a.vocab;
+                a.parents[at] = b * K + best[p].id / a.vocab;
+                a.out_scores[at] = wide_value(best[p].key);
             }
 }
 
-// Logits a thread: slices of 8,192 where they fill the device, else of 2,048, so that a few
+// Groups of 16 bytes a thread: four where such slices fill the device, else one, so that a few
 // rows are read by more SMs.
-int thread_logits(int64_t rows, int vocab, int sms)
+int thread_groups(int64_t rows, int vocab, int type, int sms)
 {
-    constexpr int wide = 32 * kSliceThreads;
-    return rows * ((vocab + wide - 1) / wide) >= sms ? 32 : 8;
+    const int wide = 4 * (type == kRopeFp32 ? 4 : 8) * kSliceThreads;
+    return rows * ((vocab + wide - 1) / wide) >= sms ? 4 : 1;
 }
 
-int slice_count(int64_t rows, int vocab, int sms)
+int slice_count(int64_t rows, int vocab, int type, int sms)
 {
-    const int slice = thread_logits(rows, vocab, sms) * kSliceThreads;
-    return (vocab + slice - 1) / slice;
+    const int group = type == kRopeFp32 ? 4 : 8;
+    const int slice = thread_groups(rows, vocab, type, sms) * group * kSliceThreads;
+    return (vocab + group - 1 + slice - 1) / slice;           // a row may start inside a group
 }
 
 template <typename T>
-void launch_slices(const BeamArgs &a, int wide, const SliceOut &o, cudaStream_t stream)
+void launch_slices(const BeamArgs &a, int groups, const SliceOut &o, cudaStream_t stream)
 {
     const T *x = static_cast<const T *>(a.logits);
-    const int vec_ok = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && a.ld * sizeof(T) % 16 == 0;
     const dim3 grid((unsigned)o.slices, (unsigned)(a.batch * a.beams));
-    if (wide)
-        slice_kernel<T, 32><<<grid, kSliceThreads, 0, stream>>>(x, a.ld, a.ended, a.beams, a.vocab,
-                                                                vec_ok, o);
+    if (groups == 4)
+        slice_kernel<T, 4><<<grid, kSliceThreads, 0, stream>>>(x, a.ld, a.ended, a.beams, a.vocab,
+                                                               o);
     else
-        slice_kernel<T, 8><<<grid, kSliceThreads, 0, stream>>>(x, a.ld, a.ended, a.beams, a.vocab,
-                                                               vec_ok, o);
+        slice_kernel<T, 1><<<grid, kSliceThreads, 0, stream>>>(x, a.ld, a.ended, a.beams, a.vocab,
+                                                               o);
 }
 
 }  // namespace
@@ -488,26 +684,26 @@ void launch_slices(const BeamArgs &a, int wide, const SliceOut &o, cudaStream_t 
 size_t beam_workspace(int batch, int beams, int vocab, int sms)
 {
     const size_t rows = (size_t)batch * beams;
-    return rows * slice_count((int64_t)rows, vocab, sms) * 8 * (1 + (size_t)beams);
+    // fp32 logits have the most slices
+    return rows * slice_count((int64_t)rows, vocab, kRopeFp32, sms) * 8 * (1 + (size_t)beams);
 }
 
 cudaError_t launch_beams(const BeamArgs &a, void *workspace, int sms, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)a.batch * a.beams;
     SliceOut o;
-    o.slices = slice_count(rows, a.vocab, sms);
+    o.slices = slice_count(rows, a.vocab, a.type, sms);
     const int64_t lists = rows * o.slices;
-    o.high = static_cast<float *>(workspace);
+    o.lists = static_cast<uint64_t *>(workspace);
+    o.high = reinterpret_cast<float *>(o.lists + lists * a.beams);
     o.sum = o.high + lists;
-    o.keys = reinterpret_cast<uint32_t *>(o.sum + lists);
-    o.ids = reinterpret_cast<int32_t *>(o.keys + lists * a.beams);
-    const int wide = thread_logits(rows, a.vocab, sms) == 32;
+    const int groups = thread_groups(rows, a.vocab, a.type, sms);
     if (a.type == kRopeBf16)
-        launch_slices<__nv_bfloat16>(a, wide, o, stream);
+        launch_slices<__nv_bfloat16>(a, groups, o, stream);
     else if (a.type == kRopeFp16)
-        launch_slices<__half>(a, wide, o, stream);
+        launch_slices<__half>(a, groups, o, stream);
     else
-        launch_slices<float>(a, wide, o, stream);
+        launch_slices<float>(a, groups, o, stream);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess)
         return err;
