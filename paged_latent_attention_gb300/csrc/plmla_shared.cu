@@ -35,6 +35,8 @@
 // barriers keep both CTAs until neither can touch the other.
 #include <math.h>
 
+#include <atomic>
+
 #include "plmla_ptx.cuh"
 
 namespace plmla {
@@ -45,7 +47,7 @@ constexpr int kShSlots = 4, kShSlot = 16384;    // of the K ring, and of the V r
 constexpr int kShRows = 128;                    // query rows of a block
 constexpr int kStart = 2;                       // cost of a block's start, in tiles
 constexpr int kShPlanThreads = 1024;
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
 constexpr int kColS = 256;                      // TMEM column of the first score tile
 constexpr int kNever = 0x7FFFFFFF;
 constexpr double kLog2e = 1.4426950408889634074;
@@ -55,44 +57,44 @@ constexpr float kLn2 = 0.69314718055994531f;
 // plan
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ int64_t scan64(int64_t v, int64_t *warp_sum)
+// Positions and blocks, of prefixes and of requests' own parts, summed together.
+struct PlanSum {
+    int64_t cost[2];
+    int blocks[2];
+};
+__device__ __forceinline__ PlanSum operator+(const PlanSum &a, const PlanSum &b)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
+    return {{a.cost[0] + b.cost[0], a.cost[1] + b.cost[1]},
+            {a.blocks[0] + b.blocks[0], a.blocks[1] + b.blocks[1]}};
+}
+__device__ __forceinline__ PlanSum scan_warp(PlanSum x)
+{
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    __syncthreads();
-    if (lane == 31)
-        warp_sum[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t s = warp_sum[lane];
+        PlanSum y;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o)
-                s += y;
+        for (int i = 0; i < 2; ++i) {
+            y.cost[i] = __shfl_up_sync(0xffffffffu, x.cost[i], o);
+            y.blocks[i] = __shfl_up_sync(0xffffffffu, x.blocks[i], o);
         }
-        warp_sum[lane] = s;
+        if ((threadIdx.x & 31) >= o)
+            x = x + y;
     }
-    __syncthreads();
-    return x - v + (warp == 0 ? 0 : warp_sum[warp - 1]);
+    return x;
 }
 
 // Parts 0 .. G - 1 are the groups' prefixes, G .. G + R - 1 the requests' own tokens.
 __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const SharedArgs a)
 {
-    __shared__ int64_t warp_sum[32];
+    __shared__ PlanSum warp_sum[32];
     __shared__ int start[kMaxReqs + 1], least[kMaxReqs], eff[kMaxReqs];
+    // the decode, and the merge behind it, may start once all work before this call is done
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int t = threadIdx.x, R = a.num_reqs, G = a.num_groups;
     const int64_t cap = min(a.table_cols * kPageTokens, (int64_t)kNever);
     bool bad = false;
-    for (int g = t; g <= G; g += kShPlanThreads)
+    for (int g = t; g <= G; g += blockDim.x)
         start[g] = a.group_starts[g];
     if (t < G)
         least[t] = kNever;
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const Share
         }
     }
     __syncthreads();
-    for (int g = t; g <= G; g += kShPlanThreads)
+    for (int g = t; g <= G; g += blockDim.x)
         bad |= (g == 0 && start[0] != 0) || (g == G && start[G] != R) ||
                (g < G && start[g] > start[g + 1]);
     // groups that are no partition of the requests: nothing is shared
@@ -157,21 +159,39 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const Share
         mine.rows = a.rows;
         a.group_of[t] = bad ? -1 : group;
     }
-    const int64_t cost = (int64_t)part.blocks * (part.tiles + kStart);
-    const int64_t own = (int64_t)mine.blocks * (mine.tiles + kStart);
-    part.base = scan64(cost, warp_sum);
-    const int64_t prefixes = warp_sum[31];
-    mine.base = prefixes + scan64(own, warp_sum);
-    const int64_t total = prefixes + warp_sum[31];
-    part.block0 = (int)scan64(part.blocks, warp_sum);
-    const int before = (int)warp_sum[31];
-    mine.block0 = before + (int)scan64(mine.blocks, warp_sum);
+    const PlanSum own = {{(int64_t)part.blocks * (part.tiles + kStart),
+                          (int64_t)mine.blocks * (mine.tiles + kStart)},
+                         {part.blocks, mine.blocks}};
+    const PlanSum to_here = scan_warp(own);
+    const int lane = t & 31, warp = t >> 5;
+    if (lane == 31)
+        warp_sum[warp] = to_here;
+    __syncthreads();
+    PlanSum all = lane < (int)blockDim.x / 32 ? warp_sum[lane] : PlanSum{};
+    all = scan_warp(all);
+    PlanSum before = {}, total;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int from = max(warp - 1, 0);
+        before.cost[i] = __shfl_sync(0xffffffffu, all.cost[i], from);
+        before.blocks[i] = __shfl_sync(0xffffffffu, all.blocks[i], from);
+        before.cost[i] = warp == 0 ? 0 : before.cost[i];
+        before.blocks[i] = warp == 0 ? 0 : before.blocks[i];
+        total.cost[i] = __shfl_sync(0xffffffffu, all.cost[i], 31);
+        total.blocks[i] = __shfl_sync(0xffffffffu, all.blocks[i], 31);
+        before.cost[i] += to_here.cost[i] - own.cost[i];
+        before.blocks[i] += to_here.blocks[i] - own.blocks[i];
+    }
+    part.base = before.cost[0];
+    part.block0 = before.blocks[0];
+    mine.base = total.cost[0] + before.cost[1];
+    mine.block0 = total.blocks[0] + before.blocks[1];
     if (t < G)
         a.parts[t] = part;
     if (t < R)
         a.parts[G + t] = mine;
     if (t == 0)
-        *a.total = total;
+        *a.total = total.cost[0] + total.cost[1];
 }
 
 // ---------------------------------------------------------------------------
@@ -182,6 +202,7 @@ struct ShBars {
     uint64_t k_full[kShSlots], k_empty[kShSlots], v_full[kShSlots], v_empty[kShSlots];
     uint64_t rope_full, rope_empty, q_full, q_empty;
     uint64_t zeros[2];                          // by the half of the V ring (E4M3)
+    uint64_t tail;
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, pv_done, o_free, drain;
 };
@@ -357,7 +378,7 @@ __device__ __forceinline__ void st_global_32(float *p, const uint32_t *v, float 
 }
 
 struct ShMaps {
-    CUtensorMap k, v, rope, qn, qr, tail[7];
+    CUtensorMap k, v, rope, qn, qr;
 };
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
@@ -395,6 +416,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             mbar_init(bar_of(m.bars.v_full[i]), 1);
             mbar_init(bar_of(m.bars.v_empty[i]), 1);
         }
+        mbar_init(bar_of(m.bars.tail), 1);
         mbar_init(bar_of(m.bars.rope_full), 1);
         mbar_init(bar_of(m.bars.rope_empty), 1);
         mbar_init(bar_of(m.bars.q_full), 1);
@@ -538,7 +560,9 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
         const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0;
         const uint32_t full = lead(m.bars.v_full[0]), empty = bar_of(m.bars.v_empty[0]);
+        const uint32_t own_tail = map_rank(bar_of(m.bars.tail), rank);
         int64_t g = 0;
+        uint32_t tails = 0;
         bool ok = true;
         while (ok && walk.next()) {
             const uint64_t use = walk.part.vis == kNever ? keep : once;
@@ -567,16 +591,27 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                     ok = all_ok(ok);
                     continue;
                 }
-                // a history's last tile: rows past it become zeros (they hold stale data, and
-                // a weight of 0 times NaN is NaN), the others come in boxes of 64, 32, .. 1
-                // rows
+                // A history's last tile: its rows past the history hold stale data, and a weight
+                // of 0 times NaN is NaN.  It is loaded on a barrier of this CTA's own, and
+                // those rows become zeros before the MMAs hear of it.
+                for (int i = 0; i < F::v_items; ++i)
+                    ok &= wait_bounded(empty + 8 * (half + i), phase ^ 1, abort_flag, status, 2);
+                ok = all_ok(ok);
+                if (!ok)
+                    break;
+                expect_if(bar_of(m.bars.tail), F::v_items * kShSlot, el);
+#pragma unroll
+                for (int i = 0; i < F::v_items; ++i)
+                    load_4d(s_v + (half + i) * kShSlot, &maps.v, in_page + (F8 ? 0 : 64 * (i & 1)),
+                            F8 ? 2 * i + (int)rank : 4 * (i >> 1) + 2 * (int)rank, page, own_tail,
+                            use, el);
+                ok = all_ok(wait_bounded(bar_of(m.bars.tail), tails & 1u, abort_flag, status, 13));
+                ++tails;
                 constexpr int kCols = F8 ? 1 : 2;             // 128-byte blocks of an item
                 constexpr int t_num = F8 ? 128 : 64, pitch = t_num * 128;
                 for (int i = 0; i < F::v_items; ++i) {
                     const int n = min(t_num, max(0, valid - (F8 ? 0 : 64 * (i & 1))));
-                    ok = all_ok(ok && wait_bounded(empty + 8 * (half + i), phase ^ 1, abort_flag,
-                                                   status, 2));
-                    for (int b = 0; b < kCols && ok; ++b)
+                    for (int b = 0; b < kCols; ++b)
                         for (int x = n * 128 + 16 * lane; x < pitch; x += 512)
                             st_shared_16(s_v + (half + i) * kShSlot + b * pitch + x, 0u, 0u, 0u, 0u);
                 }
@@ -584,20 +619,9 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster(lead(m.bars.zeros[half >> 1]));
-                for (int i = 0; i < F::v_items && ok; ++i) {
-                    const int t_off = F8 ? 0 : 64 * (i & 1), n = min(t_num, max(0, valid - t_off));
-                    const int block = F8 ? 2 * i + (int)rank : 4 * (i >> 1) + 2 * (int)rank;
-                    const uint32_t bar = full + 8 * (half + i);
-                    expect_if(bar, 2 * kCols * n * 128, el0);
-                    for (int b = 0; b < kCols; ++b)
-                        for (int w = 6, r0 = 0; w >= 0; --w)
-                            if (n >> w & 1) {
-                                load_4d(s_v + (half + i) * kShSlot + b * pitch + r0 * 128,
-                                        &maps.tail[w], in_page + t_off + r0, block + b, page, bar,
-                                        use, el);
-                                r0 += 1 << w;
-                            }
-                }
+                if (rank == 0 && lane == 0)
+                    for (int i = 0; i < F::v_items; ++i)
+                        mbar_arrive(bar_of(m.bars.v_full[half + i]));
             }
         }
         if (rank == 0 && lane == 0) {
@@ -805,43 +829,38 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                     add[i % 4] += x[i];
                 }
                 sum += (add[0] + add[1]) + (add[2] + add[3]);
+                uint32_t hi[F8 ? 16 : 32], lo[F8 ? 16 : 1];
+                if constexpr (F8) {
+#pragma unroll
+                    for (int w = 0; w < 16; ++w) {
+                        float h[4], l[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // hi: four significant bits, rounded; lo: the rest
+                            const float p = x[4 * w + e];
+                            h[e] = __uint_as_float((__float_as_uint(p) + 0x00080000u) & 0xFFF00000u);
+                            l[e] = p - h[e];
+                        }
+                        hi[w] = (uint32_t)e4m3x2(h[0], h[1]) | (uint32_t)e4m3x2(h[2], h[3]) << 16;
+                        lo[w] = (uint32_t)e4m3x2(l[0], l[1]) | (uint32_t)e4m3x2(l[2], l[3]) << 16;
+                    }
+                } else {
+                    lo[0] = 0;
+#pragma unroll
+                    for (int w = 0; w < 32; ++w) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * w], x[2 * w + 1]);
+                        hi[w] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                }
                 // P is free, and O at rest, once the product of the tile before is done
                 if (g > 0)
                     wait(m.bars.pv_done, (uint32_t)(g - 1) & 1u, 14);
-                if constexpr (F8) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            float h[4], l[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                // hi: four significant bits, rounded; lo: the rest
-                                const float p = x[16 * c + 4 * w + e];
-                                h[e] = __uint_as_float((__float_as_uint(p) + 0x00080000u) &
-                                                       0xFFF00000u);
-                                l[e] = p - h[e];
-                            }
-                            hi[w] = (uint32_t)e4m3x2(h[0], h[1]) | (uint32_t)e4m3x2(h[2], h[3]) << 16;
-                            lo[w] = (uint32_t)e4m3x2(l[0], l[1]) | (uint32_t)e4m3x2(l[2], l[3]) << 16;
-                        }
-                        const uint32_t at = p_row + (((4 * side + c) ^ (row & 7)) << 4);
-                        st_shared_16(at, hi[0], hi[1], hi[2], hi[3]);
-                        st_shared_16(at + 8192, lo[0], lo[1], lo[2], lo[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 b =
-                                __floats2bfloat162_rn(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
-                            w[e] = *reinterpret_cast<const uint32_t *>(&b);
-                        }
-                        st_shared_16(p_row + ((c ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-                    }
+                for (int c = 0; c < (F8 ? 4 : 8); ++c) {
+                    const uint32_t at = p_row + (((F8 ? 4 * side + c : c) ^ (row & 7)) << 4);
+                    st_shared_16(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                    if constexpr (F8)
+                        st_shared_16(at + 8192, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
                 }
                 if (__any_sync(0xffffffffu, shrink != 1.f)) {
 #pragma unroll 1
@@ -907,86 +926,99 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
 // merge
 // ---------------------------------------------------------------------------
 
-// A block per row, a thread per four columns: the partials of the group's prefix, then those of
-// the request's own tokens, in the order of their tokens.
+// SPLIT warps a row, a lane having 4 / SPLIT groups of four columns: the partials of the group's
+// prefix, then those of the request's own tokens, in the order of their tokens.  Reads of
+// partials (2 KB each, mostly in L2) bound it; few rows take four warps each.
+template <int SPLIT>
 __global__ void __launch_bounds__(kMergeThreads)
 shared_merge_kernel(const SharedArgs a, const int pairs)
 {
-    __shared__ float weight[kMergeThreads];
-    __shared__ int64_t first_slot[2];
-    __shared__ int count[2], row_in[2];
+    constexpr int KG = 4 / SPLIT;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int lane = threadIdx.x & 31;
+    const int64_t wid = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row = wid / SPLIT;
+    if (row >= (int64_t)a.num_reqs * a.rows)
+        return;
+    const int f0 = (int)(wid % SPLIT) * 32 * KG + lane;       // this lane's first float4 of the row
+    const int r = (int)(row / a.rows);
+    uint2 graw[KG];
+#pragma unroll
+    for (int k = 0; k < KG; ++k)
+        graw[k] = reinterpret_cast<const uint2 *>(a.gate + row * kLatent)[f0 + 32 * k];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = blockIdx.x;
-    const int t = threadIdx.x, r = (int)(row / a.rows), lane = t & 31;
-    const uint2 graw = reinterpret_cast<const uint2 *>(a.gate + row * kLatent)[t];
-    if (t < 2) {
-        const int g = a.group_of[r];
-        const int e = t == 1 ? a.num_groups + r : g;
-        int n = 0;
-        if (e >= 0) {
-            const SharedPart part = a.parts[e];
-            if (part.blocks > 0) {
-                const int64_t total = *a.total, busy = busy_pairs(total, pairs);
-                const int at = (int)(row - part.row0), blk = at / kShRows;
-                // positions of the block's tiles, and the pairs that have them
-                const int64_t v0 = part.base + (int64_t)blk * (part.tiles + kStart) + kStart;
-                const int p0 = (int)(((v0 + 1) * busy - 1) / total);
-                const int p1 = (int)(((v0 + part.tiles) * busy - 1) / total);
-                n = p1 - p0 + 1;
-                first_slot[t] = (int64_t)part.block0 + blk + p0;
-                row_in[t] = at % kShRows;
-            }
+    // lane 0: the prefix's partials, lane 1: the own tokens'
+    const int g = a.group_of[r], e = (lane & 1) != 0 ? a.num_groups + r : g;
+    int n = 0;
+    int64_t first = 0;                          // the first partial's row
+    if (e >= 0) {
+        const SharedPart part = a.parts[e];
+        if (part.blocks > 0) {
+            const int64_t total = *a.total, busy = busy_pairs(total, pairs);
+            const int at = (int)(row - part.row0), blk = at / kShRows;
+            // positions of the block's tiles, and the pairs that have them
+            const int64_t v0 = part.base + (int64_t)blk * (part.tiles + kStart) + kStart;
+            const int p0 = (int)(((v0 + 1) * busy - 1) / total);
+            const int p1 = (int)(((v0 + part.tiles) * busy - 1) / total);
+            n = p1 - p0 + 1;
+            first = ((int64_t)part.block0 + blk + p0) * kShRows + at % kShRows;
         }
-        count[t] = n;
     }
-    __syncthreads();
-    const int n0 = count[0], n = n0 + count[1];
-    auto part_row = [&](int i) -> int64_t {
-        const int s = i < n0 ? 0 : 1;
-        return (first_slot[s] + (s == 0 ? i : i - n0)) * kShRows + row_in[s];
-    };
-    // the row's maximum: every warp alike
+    const int n0 = __shfl_sync(0xffffffffu, n, 0), all = n0 + __shfl_sync(0xffffffffu, n, 1);
+    const int64_t first0 = __shfl_sync(0xffffffffu, first, 0);
+    const int64_t first1 = __shfl_sync(0xffffffffu, first, 1) - (int64_t)n0 * kShRows;
+    auto part_row = [&](int i) -> int64_t { return (i < n0 ? first0 : first1) + (int64_t)i * kShRows; };
     float high = -INFINITY;
-    for (int i = lane; i < n; i += 32)
+    for (int i = lane; i < all; i += 32)
         high = fmaxf(high, __ldcg(a.lse_part + part_row(i)));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
     const float ref = high == -INFINITY ? 0.f : high;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[KG];
+#pragma unroll
+    for (int k = 0; k < KG; ++k)
+        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int i0 = 0; i0 < n; i0 += kMergeThreads) {
-        __syncthreads();
-        if (i0 + t < n)
-            weight[t] = expf(__ldcg(a.lse_part + part_row(i0 + t)) - ref);
-        __syncthreads();
-        const int here = min(kMergeThreads, n - i0);
-#pragma unroll 8
+    for (int i0 = 0; i0 < all; i0 += 32) {
+        const float mine = i0 + lane < all ? expf(__ldcg(a.lse_part + part_row(i0 + lane)) - ref) : 0.f;
+        sum += mine;
+        const int here = min(32, all - i0);
+#pragma unroll 4
         for (int i = 0; i < here; ++i) {
-            const float w = weight[i];
-            const float4 v = __ldcg(
-                reinterpret_cast<const float4 *>(a.o_part + part_row(i0 + i) * kLatent) + t);
-            sum += w;
-            if (w != 0.f) {                     // a part that the row does not see holds zeros
-                acc.x = fmaf(w, v.x, acc.x);
-                acc.y = fmaf(w, v.y, acc.y);
-                acc.z = fmaf(w, v.z, acc.z);
-                acc.w = fmaf(w, v.w, acc.w);
+            const float w = __shfl_sync(0xffffffffu, mine, i);
+            const float4 *src =
+                reinterpret_cast<const float4 *>(a.o_part + part_row(i0 + i) * kLatent) + f0;
+#pragma unroll
+            for (int k = 0; k < KG; ++k) {
+                float4 v = __ldcg(src + 32 * k);
+                if (w == 0.f)                   // not seen by the row: may hold 0 times NaN
+                    v = make_float4(0.f, 0.f, 0.f, 0.f);
+                acc[k].x = fmaf(w, v.x, acc[k].x);
+                acc[k].y = fmaf(w, v.y, acc[k].y);
+                acc[k].z = fmaf(w, v.z, acc[k].z);
+                acc[k].w = fmaf(w, v.w, acc[k].w);
             }
         }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float2 g01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw.x));
-    const float2 g23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw.y));
-    const __nv_bfloat162 p01 = __floats2bfloat162_rn(acc.x * inv / (1.f + expf(-g01.x)),
-                                                     acc.y * inv / (1.f + expf(-g01.y)));
-    const __nv_bfloat162 p23 = __floats2bfloat162_rn(acc.z * inv / (1.f + expf(-g23.x)),
-                                                     acc.w * inv / (1.f + expf(-g23.y)));
-    uint2 packed;
-    packed.x = *reinterpret_cast<const uint32_t *>(&p01);
-    packed.y = *reinterpret_cast<const uint32_t *>(&p23);
-    reinterpret_cast<uint2 *>(a.out + row * kLatent)[t] = packed;
-    if (t == 0 && a.lse != nullptr)
+#pragma unroll
+    for (int k = 0; k < KG; ++k) {
+        const float2 g01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw[k].x));
+        const float2 g23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw[k].y));
+        const __nv_bfloat162 p01 = __floats2bfloat162_rn(acc[k].x * inv / (1.f + expf(-g01.x)),
+                                                         acc[k].y * inv / (1.f + expf(-g01.y)));
+        const __nv_bfloat162 p23 = __floats2bfloat162_rn(acc[k].z * inv / (1.f + expf(-g23.x)),
+                                                         acc[k].w * inv / (1.f + expf(-g23.y)));
+        uint2 packed;
+        packed.x = *reinterpret_cast<const uint32_t *>(&p01);
+        packed.y = *reinterpret_cast<const uint32_t *>(&p23);
+        reinterpret_cast<uint2 *>(a.out + row * kLatent)[f0 + 32 * k] = packed;
+    }
+    if (lane == 0 && wid % SPLIT == 0 && a.lse != nullptr)
         a.lse[row] = sum == 0.f ? -INFINITY : high + logf(sum);
 }
 
@@ -1003,13 +1035,11 @@ cudaError_t launch_decode(const SharedArgs &a, int sms, cudaStream_t stream)
     const cuuint64_t strides[3] = {kRow * es, 128, (cuuint64_t)a.page_stride * es};
     const cuuint32_t w32 = (cuuint32_t)wide;
     const cuuint32_t k_box[4] = {w32, 64, 2, 1};
-    const cuuint32_t v_box[4] = {w32, F8 ? 128u : 64u, F8 ? 1u : 2u, 1};
-    bool ok = make_map(&m.k, dt, a.slab, 4, dims, strides, k_box) &&
-              make_map(&m.v, dt, a.slab, 4, dims, strides, v_box);
-    for (int b = 0; b < 7; ++b) {
-        const cuuint32_t box[4] = {w32, 1u << b, 1, 1};
-        ok = ok && make_map(&m.tail[b], dt, a.slab, 4, dims, strides, box);
-    }
+    const cuuint32_t v_box[4] = {w32, 128, 1, 1};
+    bool ok = make_map(&m.k, dt, a.slab, 4, dims, strides, k_box);
+    m.v = m.k;
+    if (F8)
+        ok = ok && make_map(&m.v, dt, a.slab, 4, dims, strides, v_box);
     // the 64 rope columns: 128-byte rows (bf16), or 64-byte ones with their swizzle
     const cuuint64_t r_dims[3] = {(cuuint64_t)kRow, (cuuint64_t)kPageTokens, (cuuint64_t)a.num_pages};
     const cuuint64_t r_str[2] = {kRow * es, (cuuint64_t)a.page_stride * es};
@@ -1032,10 +1062,20 @@ cudaError_t launch_decode(const SharedArgs &a, int sms, cudaStream_t stream)
     }
     if (!ok)
         return cudaErrorInvalidValue;
-    cudaError_t err = cudaFuncSetAttribute(shared_decode_kernel<F8>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kShSmem);
+    // once per device: the attribute stays with the function
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess)
         return err;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit == 0 || (set.load(std::memory_order_relaxed) & bit) == 0) {
+        err = cudaFuncSetAttribute(shared_decode_kernel<F8>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kShSmem);
+        if (err != cudaSuccess)
+            return err;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
     cfg.blockDim = dim3(kShThreads);
@@ -1057,13 +1097,17 @@ cudaError_t launch_decode(const SharedArgs &a, int sms, cudaStream_t stream)
     err = cudaLaunchKernelEx(&cfg, shared_decode_kernel<F8>, m, b);
     if (err != cudaSuccess)
         return err;
+    // about eight warps an SM at least
+    const bool few = rows < (cuuint64_t)8 * sms;
+    const cuuint64_t warps = rows * (few ? 4 : 1), per_block = kMergeThreads / 32;
     cudaLaunchConfig_t mc = {};
-    mc.gridDim = dim3((unsigned)rows);
+    mc.gridDim = dim3((unsigned)((warps + per_block - 1) / per_block));
     mc.blockDim = dim3(kMergeThreads);
     mc.stream = stream;
     mc.attrs = attr + 1;
     mc.numAttrs = 1;
-    return cudaLaunchKernelEx(&mc, shared_merge_kernel, b, sms / 2);
+    return few ? cudaLaunchKernelEx(&mc, shared_merge_kernel<4>, b, sms / 2)
+               : cudaLaunchKernelEx(&mc, shared_merge_kernel<1>, b, sms / 2);
 }
 
 }  // namespace
@@ -1077,8 +1121,17 @@ int64_t shared_slots(int num_reqs, int rows, int num_groups, int sms)
 
 cudaError_t launch_shared(const SharedArgs &a, int sms, cudaStream_t stream)
 {
-    shared_plan_kernel<<<1, kShPlanThreads, 0, stream>>>(a);
-    const cudaError_t err = cudaGetLastError();
+    const int most = a.num_reqs > a.num_groups ? a.num_reqs : a.num_groups;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3((unsigned)((most + 31) / 32 * 32));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
     if (err != cudaSuccess)
         return err;
     return a.q8 != nullptr ? launch_decode<true>(a, sms, stream)
