@@ -950,6 +950,13 @@ def mla_kv_compact(slabs, page_table, seq_lens, out_table, kept, kept_lens, *, m
 # ---------------------------------------------------------------------------
 
 
+def _scratch(workspace, dev):
+    """(address, bytes) of a workspace."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _fail(f"workspace must be contiguous memory on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _counts(ref_counts, dev):
     """(address, pages) of a pool's counts."""
     if not (ref_counts.dtype is _I32 and ref_counts.get_device() == dev
@@ -1043,17 +1050,21 @@ def _shared(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens, group_sta
               _vector(shared_lens, "shared_lens", dev, G), G)
     if out is None:
         out = _empty(wide, _BF16, slab.device, stream)
-    if lse is None and with_lse:
+        outs = out.data_ptr()
+    else:
+        outs = _dense(out, "out", dev, wide)
+    if lse is not None:
+        sums = _dense(lse, "lse", dev, (T, H), _F32)
+    elif with_lse:
         lse = _empty((T, H), _F32, slab.device, stream)
-    outs = (_dense(out, "out", dev, wide),
-            None if lse is None else _dense(lse, "lse", dev, (T, H), _F32))
+        sums = lse.data_ptr()
+    else:
+        sums = None
     flag = _flag(status, dev)
     if workspace is None:
         workspace = _empty(_shared_workspace_size(dev, R, n_q, H, G, fp8), _U8, slab.device, stream)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        _fail(f"workspace must be contiguous memory on cuda:{dev}")
-    tail = (*ids, lens, R, n_q, H, *groups, float(scale), *outs, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), flag)
+    tail = (*ids, lens, R, n_q, H, *groups, float(scale), outs, sums, *_scratch(workspace, dev),
+            flag)
     lib = _native.lib()
     if fp8:
         _launch(dev, lib.mla_decode_shared_fp8, "mla_decode_shared_fp8", stream, *head, kv_scale,
@@ -1150,12 +1161,9 @@ def mla_pages_reserve(slabs, page_table, seq_lens, n_new, ref_counts, *, workspa
     lib = _native.lib()
     if workspace is None:
         workspace = _empty(lib.mla_pages_workspace_size(R), _U8, first.device, stream)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        _fail(f"workspace must be contiguous memory on cuda:{dev}")
     _launch(dev, lib.mla_pages_reserve, "mla_pages_reserve", stream, layers, bases,
             1 if fp8 else 2, pages, page_stride, *ids, lens, R, each, new, counts,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _flag(status, dev))
+            *_scratch(workspace, dev), _flag(status, dev))
     return page_table
 
 
@@ -1207,21 +1215,20 @@ def mla_beam_select(logits, scores, *, ended=None, end_token=-1, tokens=None, pa
         if ended.dtype is not torch.bool and ended.dtype is not _U8:
             _fail("ended must be a bool (or uint8) tensor")
         flags = _dense(ended, "ended", dev, shape, ended.dtype)
-    if tokens is None:
-        tokens = _empty(shape, _I32, logits.device, stream)
-    if parents is None:
-        parents = _empty(shape, _I32, logits.device, stream)
-    if out_scores is None:
-        out_scores = _empty(shape, _F32, logits.device, stream)
-    else:
+    if out_scores is not None:
         _disjoint(scores, out_scores, "out_scores must not overlap scores")
-    out = (_dense(tokens, "tokens", dev, shape, _I32), _dense(parents, "parents", dev, shape, _I32),
-           _dense(out_scores, "out_scores", dev, shape, _F32))
+    device, out = logits.device, []
+    for t, name, dtype in ((tokens, "tokens", _I32), (parents, "parents", _I32),
+                           (out_scores, "out_scores", _F32)):
+        if t is None:
+            t = _empty(shape, dtype, device, stream)
+        else:
+            _dense(t, name, dev, shape, dtype)
+        out.append(t)
+    tokens, parents, out_scores = out
     if workspace is None:
-        workspace = _empty(_beam_workspace_size(dev, B, K, rows[2]), _U8, logits.device, stream)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        _fail(f"workspace must be contiguous memory on cuda:{dev}")
+        workspace = _empty(_beam_workspace_size(dev, B, K, rows[2]), _U8, device, stream)
     _launch(dev, _native.lib().mla_beam_select, "mla_beam_select", stream, rows[0], rows[1], kind,
-            have, flags, int(end_token), B, K, rows[2], *out, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            have, flags, int(end_token), B, K, rows[2], tokens.data_ptr(), parents.data_ptr(),
+            out_scores.data_ptr(), *_scratch(workspace, dev))
     return tokens, parents, out_scores

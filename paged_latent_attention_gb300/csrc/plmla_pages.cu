@@ -172,13 +172,16 @@ __device__ __forceinline__ uint32_t free_bits(const int32_t *counts, int64_t fir
 __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveArgs a)
 {
     __shared__ int warp_sum[32];
-    __shared__ int last_sm[kMaxReqs];           // shared last page of a row, or -1
+    __shared__ alignas(16) int last_sm[kMaxReqs];             // shared last page of a row, or -1
     __shared__ int end_sm[kMaxReqs];            // pages that rows 0 .. r need together
     __shared__ int col_sm[kMaxReqs];            // column of the row's first page needed
     __shared__ int job_sm[kMaxReqs];            // the row's copy, or -1
+    __shared__ int window[kReserveThreads];
     __shared__ int granted;
     asm volatile("griddepcontrol.launch_dependents;");
     const int r = threadIdx.x;
+    // the first sweep's counts are on their way while the rows' needs are worked out
+    uint32_t bits = free_bits(a.counts, 16 * r, a.num_pages);
     int need = 0, part = 0, last = -1, holders = 0, col = 0;
     bool parts = false;                         // the last page has other holders
     if (r < a.num_reqs) {
@@ -210,8 +213,13 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
     last_sm[r] = parts ? last : -1;
     if (__syncthreads_or(parts) && parts) {
         int earlier = 0;
-        for (int j = 0; j < r; ++j)
-            earlier += last_sm[j] == last ? 1 : 0;
+        const int4 *rows = reinterpret_cast<const int4 *>(last_sm);
+#pragma unroll 4
+        for (int j = 0; j < (r + 3) / 4; ++j) {
+            const int4 v = rows[j];
+            earlier += (v.x == last && 4 * j < r) + (v.y == last && 4 * j + 1 < r) +
+                       (v.z == last && 4 * j + 2 < r) + (v.w == last && 4 * j + 3 < r);
+        }
         parts = holders - earlier > 1;          // the last holder keeps the page
     }
     need += parts ? 1 : 0;
@@ -226,11 +234,11 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
     __syncthreads();
 
     // the free pages that there are, as far as they are needed
-    uint32_t bits = 0;
     int found = 0, rank = 0;
     int64_t base = 0;
     for (; base < a.num_pages && found < total; base += kSweep) {
-        bits = free_bits(a.counts, base + 16 * r, a.num_pages);
+        if (base > 0)
+            bits = free_bits(a.counts, base + 16 * r, a.num_pages);
         int here;
         rank = found + block_scan(__popc(bits), warp_sum, &here);
         found += here;
@@ -250,35 +258,44 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
         *a.num_jobs = copies;                   // served rows come first
     const int most = granted;
 
-    // page number q of them belongs to the row whose pages end past q
+    // Page number q of them belongs to the row whose pages end past q.  The sweep's free pages
+    // are listed a window at a time, and a thread places one: pages in a row often lie in few
+    // threads' 16, which one by one took 5 us for 64 rows.
     const bool once = base <= kSweep;           // one sweep: its bits are at hand
     int before = 0;
     for (int64_t at = 0; at < base && before < most; at += kSweep) {
+        int here = found;
         if (!once) {
             bits = free_bits(a.counts, at + 16 * r, a.num_pages);
-            int here;
             rank = before + block_scan(__popc(bits), warp_sum, &here);
-            before += here;
-        } else {
-            before = most;
         }
-        for (int q = rank; bits != 0 && q < most; ++q, bits &= bits - 1) {
-            const int page = (int)(at + 16 * r) + __ffs(bits) - 1;
-            int lo = 0, hi = a.num_reqs - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (end_sm[mid] > q)
-                    hi = mid;
-                else
-                    lo = mid + 1;
+        const int upto = min(before + here, most);
+        for (int q0 = before; q0 < upto; q0 += kReserveThreads) {
+            __syncthreads();                    // the last window has been placed
+            int q = rank;
+            for (uint32_t left = bits; left != 0; left &= left - 1, ++q)
+                if (q >= q0 && q < q0 + kReserveThreads)
+                    window[q - q0] = (int)(at + 16 * r) + __ffs(left) - 1;
+            __syncthreads();
+            q = q0 + r;
+            if (q < upto) {
+                const int page = window[r];
+                int lo = 0, hi = a.num_reqs - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (end_sm[mid] > q)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                const int nth = q - (lo == 0 ? 0 : end_sm[lo - 1]);
+                a.table[(int64_t)lo * a.ld + col_sm[lo] + nth] = page;
+                a.counts[page] = 1;
+                if (nth == 0 && job_sm[lo] >= 0)
+                    a.jobs[job_sm[lo]].y = page;
             }
-            const int nth = q - (lo == 0 ? 0 : end_sm[lo - 1]);
-            a.table[(int64_t)lo * a.ld + col_sm[lo] + nth] = page;
-            a.counts[page] = 1;
-            if (nth == 0 && job_sm[lo] >= 0)
-                a.jobs[job_sm[lo]].y = page;
         }
-        __syncthreads();
+        before += here;
     }
 }
 
