@@ -64,7 +64,7 @@ bool shared_ok(int32_t num_reqs, int32_t n_q, int32_t num_heads, int32_t num_gro
 }
 
 struct SharedLayout {
-    size_t total, group_of, parts, q8, qexp, lse_part, o_part, size;
+    size_t total, sources, parts, q8, qexp, lse_part, o_part, size;
 };
 
 SharedLayout shared_layout(int32_t num_reqs, int32_t rows, int32_t num_groups, bool fp8, int sms)
@@ -79,7 +79,7 @@ SharedLayout shared_layout(int32_t num_reqs, int32_t rows, int32_t num_groups, b
         return here;
     };
     l.total = take(sizeof(int64_t));
-    l.group_of = take(4 * (size_t)num_reqs);
+    l.sources = take(sizeof(SharedSource) * (size_t)num_reqs);
     l.parts = take(sizeof(SharedPart) * ((size_t)num_groups + num_reqs));
     l.q8 = take(fp8 ? 2 * (size_t)kRow * all : 0);
     l.qexp = take(fp8 ? 4 * all : 0);
@@ -142,7 +142,7 @@ plmla_status shared_impl(const void *q_nope_absorbed, const void *q_rope, const 
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     a.total = reinterpret_cast<int64_t *>(w + l.total);
-    a.group_of = reinterpret_cast<int32_t *>(w + l.group_of);
+    a.sources = reinterpret_cast<SharedSource *>(w + l.sources);
     a.parts = reinterpret_cast<SharedPart *>(w + l.parts);
     a.lse_part = reinterpret_cast<float *>(w + l.lse_part);
     a.o_part = reinterpret_cast<float *>(w + l.o_part);

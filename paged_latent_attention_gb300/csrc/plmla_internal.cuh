@@ -199,6 +199,10 @@ struct SharedPart {                     // one attention problem: query rows ove
     int row0, rows;                     // its query rows
     int pad;
 };
+struct SharedSource {                   // where a request's partials come from: its group's prefix
+    int64_t base[2];                    // (0, of no tiles where nothing is shared) and its own
+    int tiles[2], block0[2], row0[2];   // tokens (1)
+};
 struct SharedArgs {
     const __nv_bfloat16 *q_nope, *q_rope, *gate;
     const uint8_t *q8;                  // E4M3: [2, num_reqs * rows, 576], hi plane then lo
@@ -217,8 +221,8 @@ struct SharedArgs {
     float *lse;                         // may be null
     SharedPart *parts;                  // workspace: [num_groups + num_reqs]
     int64_t *total;                     // workspace: positions in all
-    int32_t *group_of;                  // workspace: [num_reqs]
-    float *o_part, *lse_part;           // workspace: [slots, 128, 512], [slots, 128]
+    SharedSource *sources;              // workspace: [num_reqs]
+    float *o_part, *lse_part;           // workspace: [slots, 128 x 512], [slots, 128]
     int32_t *status;                    // may be null
 };
 // Partial outputs of 128 rows that a call may write.

@@ -47,7 +47,7 @@ constexpr int kShSlots = 4, kShSlot = 16384;    // of the K ring, and of the V r
 constexpr int kShRows = 128;                    // query rows of a block
 constexpr int kStart = 2;                       // cost of a block's start, in tiles
 constexpr int kShPlanThreads = 1024;
-constexpr int kMergeThreads = 256;
+constexpr int kKept = 64;                       // log-sum-exps of a row that the merge keeps
 constexpr int kColS = 256;                      // TMEM column of the first score tile
 constexpr int kNever = 0x7FFFFFFF;
 constexpr double kLog2e = 1.4426950408889634074;
@@ -88,6 +88,8 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const Share
 {
     __shared__ PlanSum warp_sum[32];
     __shared__ int start[kMaxReqs + 1], least[kMaxReqs], eff[kMaxReqs];
+    __shared__ int64_t base[kMaxReqs];          // of the groups' prefixes, for the requests
+    __shared__ int block0[kMaxReqs], blocks[kMaxReqs];
     // the decode, and the merge behind it, may start once all work before this call is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -157,7 +159,6 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const Share
         mine.vis = len - (a.n_q - 1);
         mine.row0 = t * a.rows;
         mine.rows = a.rows;
-        a.group_of[t] = bad ? -1 : group;
     }
     const PlanSum own = {{(int64_t)part.blocks * (part.tiles + kStart),
                           (int64_t)mine.blocks * (mine.tiles + kStart)},
@@ -186,10 +187,26 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const Share
     part.block0 = before.blocks[0];
     mine.base = total.cost[0] + before.cost[1];
     mine.block0 = total.blocks[0] + before.blocks[1];
-    if (t < G)
+    if (t < G) {
         a.parts[t] = part;
+        base[t] = part.base;
+        block0[t] = part.block0;
+        blocks[t] = part.blocks;
+    }
     if (t < R)
         a.parts[G + t] = mine;
+    __syncthreads();
+    if (t < R) {
+        SharedSource from = {};
+        if (!bad && blocks[group] > 0)
+            from = {{base[group], 0}, {eff[group] / kTile, 0}, {block0[group], 0},
+                    {start[group] * a.rows, 0}};
+        from.base[1] = mine.base;
+        from.tiles[1] = mine.tiles;
+        from.block0[1] = mine.block0;
+        from.row0[1] = mine.row0;
+        a.sources[t] = from;
+    }
     if (t == 0)
         *a.total = total.cost[0] + total.cost[1];
 }
@@ -282,6 +299,14 @@ __device__ __forceinline__ int64_t busy_pairs(int64_t total, int pairs)
     return total < pairs ? max(total, (int64_t)1) : pairs;
 }
 
+// All threads of the pair, without the memory ordering of cluster_sync, whose release waits for
+// every store of the CTA.
+__device__ __forceinline__ void pair_sync()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t r;
@@ -367,16 +392,6 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t
                  : "memory");
 }
 
-__device__ __forceinline__ void st_global_32(float *p, const uint32_t *v, float f)
-{
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
-                 "f"(__uint_as_float(v[0]) * f), "f"(__uint_as_float(v[1]) * f),
-                 "f"(__uint_as_float(v[2]) * f), "f"(__uint_as_float(v[3]) * f),
-                 "f"(__uint_as_float(v[4]) * f), "f"(__uint_as_float(v[5]) * f),
-                 "f"(__uint_as_float(v[6]) * f), "f"(__uint_as_float(v[7]) * f)
-                 : "memory");
-}
-
 struct ShMaps {
     CUtensorMap k, v, rope, qn, qr;
 };
@@ -445,14 +460,16 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
     const uint32_t rank = cluster_rank();
     const int pair = (int)blockIdx.x >> 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");        // the plan (and split queries)
+    const int num_parts = a.num_groups + a.num_reqs;
+    const int64_t base0 = (int)threadIdx.x < num_parts ? a.parts[threadIdx.x].base : 0;
     const int64_t total = *a.total;
     const int64_t pairs = busy_pairs(total, (int)gridDim.x >> 1);
     const int64_t from = pair < pairs ? total * pair / pairs : total;
     const int64_t to = pair < pairs ? total * (pair + 1) / pairs : total;
     {
         // the part that holds the run's first position: the last one that starts there or before
-        int mine = 0;
-        for (int e = threadIdx.x; e < a.num_groups + a.num_reqs; e += kShThreads)
+        int mine = (int)threadIdx.x < num_parts && base0 <= from ? (int)threadIdx.x : 0;
+        for (int e = threadIdx.x + kShThreads; e < num_parts; e += kShThreads)
             if (a.parts[e].base <= from)
                 mine = e;
         tc_fence_before();
@@ -462,7 +479,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             atomicMax(&m.first, mine);
         __syncthreads();
     }
-    cluster_sync();                             // the pair's barriers are initialised
+    pair_sync();                                // the pair's barriers are initialised (and fenced)
     const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
     volatile int *abort_flag = &m.abort;
     int32_t *status = &m.status;
@@ -889,17 +906,22 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             float scale = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;    // NaN stays
             if constexpr (F8)
                 scale *= a.kv_scale;
-            float *out = a.o_part + (slot * kShRows + 64 * (int)rank + row) * kLatent;
+            // lane by lane, so that a store covers 512 bytes (rows of their own, 32 bytes of each
+            // a store, took 7 us to drain at the kernel's end)
+            float4 *out = reinterpret_cast<float4 *>(a.o_part) +
+                          ((slot * 2 + (int)rank) * 4 + quad) * 64 * 32 + lane;
 #pragma unroll 1
             for (int c = 0; c < 256; c += 16) {
                 uint32_t r[16];
                 tmem_ld16(lanes + c, r);
                 tmem_wait_ld();
-                if (store) {
-                    float *to_col = out + (c >> 7) * 256 + 128 * side + (c & 127);
-                    st_global_32(to_col, r, scale);
-                    st_global_32(to_col + 8, r + 8, scale);
-                }
+                if (store)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        out[(c / 4 + i) * 32] = make_float4(
+                            __uint_as_float(r[4 * i]) * scale, __uint_as_float(r[4 * i + 1]) * scale,
+                            __uint_as_float(r[4 * i + 2]) * scale,
+                            __uint_as_float(r[4 * i + 3]) * scale);
             }
             tc_fence_before();
             arrive(m.bars.o_free);
@@ -913,7 +935,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
     __syncthreads();
     // A pair leaves together: no copy or arrival of one CTA is on its way to the other, and
     // each has waited for its own copy of the last commit.
-    cluster_sync();
+    pair_sync();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
@@ -926,100 +948,150 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
 // merge
 // ---------------------------------------------------------------------------
 
-// SPLIT warps a row, a lane having 4 / SPLIT groups of four columns: the partials of the group's
-// prefix, then those of the request's own tokens, in the order of their tokens.  Reads of
-// partials (2 KB each, mostly in L2) bound it; few rows take four warps each.
-template <int SPLIT>
-__global__ void __launch_bounds__(kMergeThreads)
+// The sigmoid, within 2^-21 of itself; the merge of many rows is bound by instructions, which
+// the exact division and exponential were half of.
+__device__ __forceinline__ float gate_of(float x)
+{
+    return __fdividef(1.f, 1.f + fast_exp2(-x * (float)kLog2e));
+}
+
+// A block takes 32 rows by 8 C columns: a warp C of the columns of every PARTS'th partial, a lane
+// a row, as the partials lie ([slot, CTA, TMEM quadrant, four columns, lane]), and the block
+// writes its outputs in whole pieces of rows.  A row's partials are those of the group's
+// prefix, then those of the request's own tokens, in the order of their tokens.  Many rows are
+// bound by the reads and take 16 columns a warp; with few, each of many partials, latency
+// counts, and two warps share them (512 rows of 20 partials: 3 us less).
+template <int C, int PARTS>
+__global__ void __launch_bounds__(256 * PARTS)
 shared_merge_kernel(const SharedArgs a, const int pairs)
 {
-    constexpr int KG = 4 / SPLIT;
+    constexpr int kThreads = 256 * PARTS, kWarps = kThreads / 32, kBlocks = kLatent / (8 * C);
+    constexpr int kOut = 32 * 2 * C / kThreads;               // groups of 4 columns of a thread
+    __shared__ float tile[PARTS][32][8 * C + 1], sums[PARTS][32];
+    __shared__ float lses[kKept][32], highs[kWarps][32];
     asm volatile("griddepcontrol.launch_dependents;");
-    const int lane = threadIdx.x & 31;
-    const int64_t wid = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-    const int64_t row = wid / SPLIT;
-    if (row >= (int64_t)a.num_reqs * a.rows)
-        return;
-    const int f0 = (int)(wid % SPLIT) * 32 * KG + lane;       // this lane's first float4 of the row
-    const int r = (int)(row / a.rows);
-    uint2 graw[KG];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 3;
+    const int64_t rows = (int64_t)a.num_reqs * a.rows, row0 = (int64_t)(blockIdx.x / kBlocks) * 32;
+    const int64_t row = min(row0 + lane, rows - 1);
+    const int col0 = (int)(blockIdx.x % kBlocks) * 8 * C, col = col0 + C * (warp & 7);
+    uint2 gate[kOut];
 #pragma unroll
-    for (int k = 0; k < KG; ++k)
-        graw[k] = reinterpret_cast<const uint2 *>(a.gate + row * kLatent)[f0 + 32 * k];
+    for (int q = 0; q < kOut; ++q) {
+        const int u = threadIdx.x + q * kThreads;
+        gate[q] = make_uint2(0u, 0u);
+        if (row0 + u / (2 * C) < rows)
+            gate[q] = *reinterpret_cast<const uint2 *>(a.gate + (row0 + u / (2 * C)) * kLatent +
+                                                       col0 + 4 * (u % (2 * C)));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // lane 0: the prefix's partials, lane 1: the own tokens'
-    const int g = a.group_of[r], e = (lane & 1) != 0 ? a.num_groups + r : g;
-    int n = 0;
-    int64_t first = 0;                          // the first partial's row
-    if (e >= 0) {
-        const SharedPart part = a.parts[e];
-        if (part.blocks > 0) {
-            const int64_t total = *a.total, busy = busy_pairs(total, pairs);
-            const int at = (int)(row - part.row0), blk = at / kShRows;
-            // positions of the block's tiles, and the pairs that have them
-            const int64_t v0 = part.base + (int64_t)blk * (part.tiles + kStart) + kStart;
-            const int p0 = (int)(((v0 + 1) * busy - 1) / total);
-            const int p1 = (int)(((v0 + part.tiles) * busy - 1) / total);
-            n = p1 - p0 + 1;
-            first = ((int64_t)part.block0 + blk + p0) * kShRows + at % kShRows;
+    // the row's partials: of the prefix (0) and of its own tokens (1)
+    const int64_t total = *a.total, busy = busy_pairs(total, pairs);
+    const SharedSource from = a.sources[row / a.rows];
+    // the pair that has position x: (the last p with p total / busy, rounded down, <= x)
+    auto pair_of = [&](int64_t x) -> int {
+        return total < 1 << 24 ? (int)(((uint32_t)(x + 1) * (uint32_t)busy - 1) / (uint32_t)total)
+                               : (int)(((x + 1) * busy - 1) / total);
+    };
+    int n[2], at[2];
+    int64_t first[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int in_part = (int)(row - from.row0[i]), blk = in_part / kShRows;
+        // positions of the block's tiles
+        const int64_t v0 = from.base[i] + (int64_t)blk * (from.tiles[i] + kStart) + kStart;
+        n[i] = at[i] = 0;
+        first[i] = 0;
+        if (from.tiles[i] > 0) {
+            const int p0 = pair_of(v0);
+            n[i] = pair_of(v0 + from.tiles[i] - 1) - p0 + 1;
+            first[i] = (int64_t)from.block0[i] + blk + p0;
+            at[i] = in_part % kShRows;
         }
     }
-    const int n0 = __shfl_sync(0xffffffffu, n, 0), all = n0 + __shfl_sync(0xffffffffu, n, 1);
-    const int64_t first0 = __shfl_sync(0xffffffffu, first, 0);
-    const int64_t first1 = __shfl_sync(0xffffffffu, first, 1) - (int64_t)n0 * kShRows;
-    auto part_row = [&](int i) -> int64_t { return (i < n0 ? first0 : first1) + (int64_t)i * kShRows; };
+    // their log-sum-exps, each by one of the warps
+    const int all = n[0] + n[1];
     float high = -INFINITY;
-    for (int i = lane; i < all; i += 32)
-        high = fmaxf(high, __ldcg(a.lse_part + part_row(i)));
+    auto lse_at = [&](int k) -> float {
+        const int64_t slot = k < n[0] ? first[0] + k : first[1] + k - n[0];
+        return __ldcg(a.lse_part + slot * kShRows + (k < n[0] ? at[0] : at[1]));
+    };
+    for (int k = warp; k < all; k += kWarps) {
+        const float l = lse_at(k);
+        if (k < kKept)
+            lses[k][lane] = l;
+        high = fmaxf(high, l);
+    }
+    highs[warp][lane] = high;
+    __syncthreads();
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+    for (int w = 0; w < kWarps; ++w)
+        high = fmaxf(high, highs[w][lane]);
     const float ref = high == -INFINITY ? 0.f : high;
-    float4 acc[KG];
+    float acc[C] = {}, sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < KG; ++k)
-        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int i0 = 0; i0 < all; i0 += 32) {
-        const float mine = i0 + lane < all ? expf(__ldcg(a.lse_part + part_row(i0 + lane)) - ref) : 0.f;
-        sum += mine;
-        const int here = min(32, all - i0);
-#pragma unroll 4
-        for (int i = 0; i < here; ++i) {
-            const float w = __shfl_sync(0xffffffffu, mine, i);
-            const float4 *src =
-                reinterpret_cast<const float4 *>(a.o_part + part_row(i0 + i) * kLatent) + f0;
+    for (int i = 0; i < 2; ++i) {
+        // CTA, quadrant (rows, side of 128 columns), four columns, lane
+        const int quad = (at[i] >> 5 & 1) + 2 * (col >> 7 & 1);
+        const float4 *src = reinterpret_cast<const float4 *>(a.o_part) +
+                            (((first[i] * 2 + (at[i] >> 6)) * 4 + quad) * 64 +
+                             (col >> 8) * 32 + (col & 127) / 4) * 32 + (at[i] & 31);
+        const int before = i == 0 ? 0 : n[0], kept = min(n[i], kKept - min(before, kKept));
+        auto take = [&](int k, float l) {
+            float4 x[C / 4];
 #pragma unroll
-            for (int k = 0; k < KG; ++k) {
-                float4 v = __ldcg(src + 32 * k);
+            for (int j = 0; j < C / 4; ++j)
+                x[j] = __ldcg(src + (int64_t)k * kShRows * kLatent / 4 + 32 * j);
+            const float w = fast_exp2((l - ref) * (float)kLog2e);
+            sum += w;
+#pragma unroll
+            for (int j = 0; j < C / 4; ++j) {
                 if (w == 0.f)                   // not seen by the row: may hold 0 times NaN
-                    v = make_float4(0.f, 0.f, 0.f, 0.f);
-                acc[k].x = fmaf(w, v.x, acc[k].x);
-                acc[k].y = fmaf(w, v.y, acc[k].y);
-                acc[k].z = fmaf(w, v.z, acc[k].z);
-                acc[k].w = fmaf(w, v.w, acc[k].w);
+                    x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                acc[4 * j] = fmaf(w, x[j].x, acc[4 * j]);
+                acc[4 * j + 1] = fmaf(w, x[j].y, acc[4 * j + 1]);
+                acc[4 * j + 2] = fmaf(w, x[j].z, acc[4 * j + 2]);
+                acc[4 * j + 3] = fmaf(w, x[j].w, acc[4 * j + 3]);
             }
-        }
+        };
+#pragma unroll (64 / C)
+        for (int k = part; k < kept; k += PARTS)
+            take(k, lses[before + k][lane]);
+        for (int k = kept + (kept + part) % PARTS; k < n[i]; k += PARTS)
+            take(k, lse_at(before + k));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int k = 0; k < KG; ++k) {
-        const float2 g01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw[k].x));
-        const float2 g23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&graw[k].y));
-        const __nv_bfloat162 p01 = __floats2bfloat162_rn(acc[k].x * inv / (1.f + expf(-g01.x)),
-                                                         acc[k].y * inv / (1.f + expf(-g01.y)));
-        const __nv_bfloat162 p23 = __floats2bfloat162_rn(acc[k].z * inv / (1.f + expf(-g23.x)),
-                                                         acc[k].w * inv / (1.f + expf(-g23.y)));
-        uint2 packed;
-        packed.x = *reinterpret_cast<const uint32_t *>(&p01);
-        packed.y = *reinterpret_cast<const uint32_t *>(&p23);
-        reinterpret_cast<uint2 *>(a.out + row * kLatent)[f0 + 32 * k] = packed;
-    }
-    if (lane == 0 && wid % SPLIT == 0 && a.lse != nullptr)
+    for (int j = 0; j < C; ++j)
+        tile[part][lane][C * (warp & 7) + j] = acc[j];
+    if ((warp & 7) == 0)
+        sums[part][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && col0 == 0 && row0 + lane < rows && a.lse != nullptr) {
+        sum = PARTS == 2 ? sums[0][lane] + sums[PARTS - 1][lane] : sums[0][lane];
         a.lse[row] = sum == 0.f ? -INFINITY : high + logf(sum);
+    }
+#pragma unroll
+    for (int q = 0; q < kOut; ++q) {
+        const int u = threadIdx.x + q * kThreads, i = u / (2 * C), c = 4 * (u % (2 * C));
+        if (row0 + i >= rows)
+            continue;
+        float s = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            s += sums[p][i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] += tile[p][i][c + j];
+        }
+        const float inv = s == 0.f ? 0.f : 1.f / s;
+        const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&gate[q].x));
+        const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&gate[q].y));
+        const __nv_bfloat162 o0 = __floats2bfloat162_rn(v[0] * inv * gate_of(g0.x),
+                                                        v[1] * inv * gate_of(g0.y));
+        const __nv_bfloat162 o1 = __floats2bfloat162_rn(v[2] * inv * gate_of(g1.x),
+                                                        v[3] * inv * gate_of(g1.y));
+        *reinterpret_cast<uint2 *>(a.out + (row0 + i) * kLatent + col0 + c) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&o0), *reinterpret_cast<const uint32_t *>(&o1));
+    }
 }
 
 template <bool F8>
@@ -1097,17 +1169,17 @@ cudaError_t launch_decode(const SharedArgs &a, int sms, cudaStream_t stream)
     err = cudaLaunchKernelEx(&cfg, shared_decode_kernel<F8>, m, b);
     if (err != cudaSuccess)
         return err;
-    // about eight warps an SM at least
-    const bool few = rows < (cuuint64_t)8 * sms;
-    const cuuint64_t warps = rows * (few ? 4 : 1), per_block = kMergeThreads / 32;
+    // (blocks of the form for few rows: an SM holds two)
+    const unsigned groups = (unsigned)((rows + 31) / 32);
+    const bool few = groups * 8 <= 2u * (unsigned)sms;
     cudaLaunchConfig_t mc = {};
-    mc.gridDim = dim3((unsigned)((warps + per_block - 1) / per_block));
-    mc.blockDim = dim3(kMergeThreads);
+    mc.gridDim = dim3(groups * (few ? 8 : 4));
+    mc.blockDim = dim3(few ? 512 : 256);
     mc.stream = stream;
     mc.attrs = attr + 1;
     mc.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&mc, shared_merge_kernel<4>, b, sms / 2)
-               : cudaLaunchKernelEx(&mc, shared_merge_kernel<1>, b, sms / 2);
+    return few ? cudaLaunchKernelEx(&mc, shared_merge_kernel<8, 2>, b, sms / 2)
+               : cudaLaunchKernelEx(&mc, shared_merge_kernel<16, 1>, b, sms / 2);
 }
 
 }  // namespace
