@@ -147,16 +147,11 @@ plmla_status shared_impl(const void *q_nope_absorbed, const void *q_rope, const 
     a.lse_part = reinterpret_cast<float *>(w + l.lse_part);
     a.o_part = reinterpret_cast<float *>(w + l.o_part);
     a.status = status;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (fp8) {
-        uint8_t *q8 = w + l.q8;
-        int32_t *qexp = reinterpret_cast<int32_t *>(w + l.qexp);
-        if (launch_quantize(a.q_nope, a.q_rope, num_reqs * a.rows, q8, qexp, s) != cudaSuccess)
-            return PLMLA_CUDA_ERROR;
-        a.q8 = q8;
-        a.qexp = qexp;
+        a.q8 = w + l.q8;
+        a.qexp = reinterpret_cast<int32_t *>(w + l.qexp);
     }
-    return result(launch_shared(a, sms, s));
+    return result(launch_shared(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

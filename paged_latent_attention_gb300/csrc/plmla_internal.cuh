@@ -205,8 +205,8 @@ struct SharedSource {                   // where a request's partials come from:
 };
 struct SharedArgs {
     const __nv_bfloat16 *q_nope, *q_rope, *gate;
-    const uint8_t *q8;                  // E4M3: [2, num_reqs * rows, 576], hi plane then lo
-    const int32_t *qexp;
+    uint8_t *q8;                        // workspace, E4M3: [2, num_reqs * rows, 576], hi plane
+    int32_t *qexp;                      // then lo, and exponents
     const void *slab;                   // bf16 elements, or E4M3 bytes (q8 set)
     int64_t num_pages, page_stride;
     const int32_t *page_table;

@@ -25,8 +25,8 @@
 // divergent thread with computed descriptors, so the issuing warp stays converged.
 //
 // Warps: 0 loads K, 2 loads V (TMA, a ring of four 16 KB items each), 3 Q and K's rope block, 1 issues the MMAs of
-// the pair (in the even CTA), K a tile ahead of V, 4-7 softmax and epilogue, a thread
-// having half of a row's 128 scores in registers.  The running maximum lags: O is only
+// the pair (in the even CTA), K a tile ahead of V, 4-11 softmax and epilogue, a thread
+// having a quarter of a row's 128 scores in registers.  The running maximum lags: O is only
 // rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries in two E4M3 parts
 // (as in the FP8 decode) and the probabilities in two as well, hi + lo, so that they carry 8
 // bits like bf16 ones; a part each takes the rate that bf16 would.
@@ -38,11 +38,12 @@
 #include <atomic>
 
 #include "plmla_ptx.cuh"
+#include "plmla_quantize.cuh"
 
 namespace plmla {
 namespace {
 
-constexpr int kShThreads = 256;
+constexpr int kShThreads = 384;
 constexpr int kShSlots = 4, kShSlot = 16384;    // of the K ring, and of the V ring
 constexpr int kShRows = 128;                    // query rows of a block
 constexpr int kStart = 2;                       // cost of a block's start, in tiles
@@ -83,8 +84,10 @@ __device__ __forceinline__ PlanSum scan_warp(PlanSum x)
     return x;
 }
 
-// Parts 0 .. G - 1 are the groups' prefixes, G .. G + R - 1 the requests' own tokens.
-__global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const SharedArgs a)
+// Parts 0 .. G - 1 are the groups' prefixes, G .. G + R - 1 the requests' own tokens.  The blocks
+// behind the first split E4M3's queries meanwhile, a warp a row.
+__global__ void __launch_bounds__(kShPlanThreads)
+shared_plan_kernel(const SharedArgs a, const PlanBuffers queries)
 {
     __shared__ PlanSum warp_sum[32];
     __shared__ int start[kMaxReqs + 1], least[kMaxReqs], eff[kMaxReqs];
@@ -93,6 +96,12 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const Share
     // the decode, and the merge behind it, may start once all work before this call is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    if (blockIdx.x > 0) {
+        const int row = ((int)blockIdx.x - 1) * (int)(blockDim.x / 32) + ((int)threadIdx.x >> 5);
+        if (row < queries.q_rows)
+            quantize_row(queries, row);
+        return;
+    }
     const int t = threadIdx.x, R = a.num_reqs, G = a.num_groups;
     const int64_t cap = min(a.table_cols * kPageTokens, (int64_t)kNever);
     bool bad = false;
@@ -228,7 +237,7 @@ struct ShMisc {
     ShBars bars;
     uint32_t tmem;
     int abort, status, first;
-    float half[3][128];                         // exchanged between the two halves of a row
+    float quarter[2][256];                      // exchanged between the quarters of a row
 };
 
 template <bool F8>
@@ -439,11 +448,11 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_of(m.bars.zeros[i]), 2);            // both CTAs wrote them
             mbar_init(bar_of(m.bars.s_full[i]), 1);
-            mbar_init(bar_of(m.bars.s_free[i]), 8);           // the pair's softmax warps
+            mbar_init(bar_of(m.bars.s_free[i]), 16);          // the pair's softmax warps
         }
-        mbar_init(bar_of(m.bars.p_full), 8);
+        mbar_init(bar_of(m.bars.p_full), 16);
         mbar_init(bar_of(m.bars.pv_done), 1);
-        mbar_init(bar_of(m.bars.o_free), 8);
+        mbar_init(bar_of(m.bars.o_free), 16);
         mbar_init(bar_of(m.bars.drain), 1);
         m.abort = 0;
         m.status = 0;
@@ -769,16 +778,19 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             wait_drain(bar_of(m.bars.drain), 0);
     } else if (warp >= 4) {
         // -------------------------------------------------- softmax, epilogue
-        // Thread (quad, lane): row 32 (quad % 2) + lane of this CTA, tokens 64 (quad / 2) .. + 63
-        // of a tile.  A wait that gives up clears `ok`: the loops run on without waiting or
-        // storing, so that every thread still meets the barriers.
+        // Thread (warp group, quad, lane): row 32 (quad % 2) + lane of this CTA, and of a tile the 32
+        // tokens from 64 (quad / 2) + 32 group on: a quarter of the row.  A wait that gives up
+        // clears `ok`: the loops run on without waiting or storing, so that every thread still
+        // meets the barriers.
         const int quad = warp & 3, row = 32 * (quad & 1) + lane, side = quad >> 1;
-        const int tid = 32 * quad + lane;
+        const int group = (warp - 4) >> 2, tid = 32 * quad + lane + 128 * group;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         constexpr float kLag = F8 ? 4.f : 8.f, kUp = F8 ? 4.f : 0.f;
+        constexpr int kChunks = F8 ? 2 : 4;     // 16-byte chunks of P (of each part)
         const uint32_t p_row = s_p + row * 128 + (F8 ? 0 : side * 8192);
         bool ok = true;
         int64_t g = 0;
+        int exchange = 0;
         auto wait = [&](const uint64_t &b, uint32_t parity, int code) {
             ok = all_ok(ok && wait_bounded(bar_of(b), parity, abort_flag, status, code));
             tc_fence_after();
@@ -800,36 +812,38 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             if constexpr (F8)
                 f = real ? ldexpf(f * a.kv_scale, a.qexp[part.row0 + in_part]) : 1.f;
             float high = -INFINITY, sum = 0.f;  // in units of log2; of this thread's tokens
-            for (int t = walk.t0; t < walk.t1; ++t, ++g) {
+            for (int t = walk.t0; t < walk.t1; ++t, ++g, ++exchange) {
                 const int buf = (int)(g & 1);
                 wait(m.bars.s_full[buf], (uint32_t)(g >> 1) & 1u, 11);
-                float x[64];
+                float x[32];
                 {
-                    uint32_t r[4][16];
+                    uint32_t r[2][16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tmem_ld16(lanes + kColS + 64 * buf + 16 * i, r[i]);
+                    for (int i = 0; i < 2; ++i)
+                        tmem_ld16(lanes + kColS + 64 * buf + 32 * group + 16 * i, r[i]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
+                    for (int i = 0; i < 32; ++i)
                         x[i] = __uint_as_float(r[i / 16][i % 16]);
                 }
                 tc_fence_before();
                 arrive(m.bars.s_free[buf]);
-                const int tok = part.tok0 + t * kTile + 64 * side;
-                if (tok + 64 > limit) {
+                const int tok = part.tok0 + t * kTile + 64 * side + 32 * group;
+                if (tok + 32 > limit) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
+                    for (int i = 0; i < 32; ++i)
                         x[i] = tok + i < limit ? x[i] : -INFINITY;
                 }
                 float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int i = 4; i < 64; ++i)
+                for (int i = 4; i < 32; ++i)
                     top[i % 4] = fmaxf(top[i % 4], x[i]);
                 float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                m.half[buf][tid] = best;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                best = fmaxf(best, m.half[buf][tid ^ 64]) * f;
+                float(&quarter)[256] = m.quarter[exchange & 1];
+                quarter[tid] = best;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                best = fmaxf(fmaxf(best, quarter[tid ^ 64]),
+                             fmaxf(quarter[tid ^ 128], quarter[tid ^ 192])) * f;
                 float shrink = 1.f;
                 if (t == walk.t0) {
                     high = best;
@@ -841,15 +855,15 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 const float ref = high == -INFINITY ? 0.f : high - kUp;
                 float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
+                for (int i = 0; i < 32; ++i) {
                     x[i] = fast_exp2(fmaf(x[i], f, -ref));
                     add[i % 4] += x[i];
                 }
                 sum += (add[0] + add[1]) + (add[2] + add[3]);
-                uint32_t hi[F8 ? 16 : 32], lo[F8 ? 16 : 1];
+                uint32_t hi[4 * kChunks], lo[F8 ? 4 * kChunks : 1];
                 if constexpr (F8) {
 #pragma unroll
-                    for (int w = 0; w < 16; ++w) {
+                    for (int w = 0; w < 8; ++w) {
                         float h[4], l[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -864,7 +878,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 } else {
                     lo[0] = 0;
 #pragma unroll
-                    for (int w = 0; w < 32; ++w) {
+                    for (int w = 0; w < 16; ++w) {
                         const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * w], x[2 * w + 1]);
                         hi[w] = *reinterpret_cast<const uint32_t *>(&b);
                     }
@@ -873,15 +887,16 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 if (g > 0)
                     wait(m.bars.pv_done, (uint32_t)(g - 1) & 1u, 14);
 #pragma unroll
-                for (int c = 0; c < (F8 ? 4 : 8); ++c) {
-                    const uint32_t at = p_row + (((F8 ? 4 * side + c : c) ^ (row & 7)) << 4);
+                for (int c = 0; c < kChunks; ++c) {
+                    const int chunk = (F8 ? 4 * side : 0) + kChunks * group + c;
+                    const uint32_t at = p_row + ((chunk ^ (row & 7)) << 4);
                     st_shared_16(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
                     if constexpr (F8)
                         st_shared_16(at + 8192, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
                 }
                 if (__any_sync(0xffffffffu, shrink != 1.f)) {
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 16) {
+                    for (int c = 128 * group; c < 128 * group + 128; c += 16) {
                         uint32_t r[16];
                         tmem_ld16(lanes + c, r);
                         tmem_wait_ld();
@@ -897,21 +912,23 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 arrive(m.bars.p_full);
             }
             // the segment's partial
-            m.half[2][tid] = sum;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            sum += m.half[2][tid ^ 64];
+            float(&quarter)[256] = m.quarter[exchange++ & 1];
+            quarter[tid] = sum;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // (in one order, so that all four agree)
+            const int q0 = tid & 63;
+            sum = (quarter[q0] + quarter[q0 + 64]) + (quarter[q0 + 128] + quarter[q0 + 192]);
             wait(m.bars.pv_done, (uint32_t)(g - 1) & 1u, 15);
             const int64_t slot = (int64_t)walk.slot_block + pair;
             const bool store = real && ok && !*abort_flag;
             float scale = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;    // NaN stays
             if constexpr (F8)
                 scale *= a.kv_scale;
-            // lane by lane, so that a store covers 512 bytes (rows of their own, 32 bytes of each
-            // a store, took 7 us to drain at the kernel's end)
+            // lane by lane, so that a store covers 512 bytes
             float4 *out = reinterpret_cast<float4 *>(a.o_part) +
                           ((slot * 2 + (int)rank) * 4 + quad) * 64 * 32 + lane;
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 16) {
+            for (int c = 128 * group; c < 128 * group + 128; c += 16) {
                 uint32_t r[16];
                 tmem_ld16(lanes + c, r);
                 tmem_wait_ld();
@@ -925,7 +942,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             }
             tc_fence_before();
             arrive(m.bars.o_free);
-            if (store && side == 0)
+            if (store && side == 0 && group == 0)
                 a.lse_part[slot * kShRows + 64 * (int)rank + row] =
                     sum == 0.f ? -INFINITY : (high - kUp + log2f(sum)) * kLn2;
         }
@@ -1194,16 +1211,27 @@ int64_t shared_slots(int num_reqs, int rows, int num_groups, int sms)
 cudaError_t launch_shared(const SharedArgs &a, int sms, cudaStream_t stream)
 {
     const int most = a.num_reqs > a.num_groups ? a.num_reqs : a.num_groups;
+    PlanBuffers queries = {};
+    int threads = (most + 31) / 32 * 32, blocks = 1;
+    if (a.q8 != nullptr) {
+        queries.q_nope = a.q_nope;
+        queries.q_rope = a.q_rope;
+        queries.q8 = a.q8;
+        queries.qexp = a.qexp;
+        queries.q_rows = a.num_reqs * a.rows;
+        threads = threads < 256 ? 256 : threads;
+        blocks += (queries.q_rows + threads / 32 - 1) / (threads / 32);
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3((unsigned)((most + 31) / 32 * 32));
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, shared_plan_kernel, a, queries);
     if (err != cudaSuccess)
         return err;
     return a.q8 != nullptr ? launch_decode<true>(a, sms, stream)
