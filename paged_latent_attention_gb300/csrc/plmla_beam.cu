@@ -19,6 +19,7 @@
 //
 // Bound: HBM for the logits of a large batch; else latency of two launches.
 #include <math.h>
+#include <algorithm>
 
 #include <cuda_fp16.h>
 
@@ -684,8 +685,10 @@ void launch_slices(const BeamArgs &a, int groups, const SliceOut &o, cudaStream_
 size_t beam_workspace(int batch, int beams, int vocab, int sms)
 {
     const size_t rows = (size_t)batch * beams;
-    // fp32 logits have the most slices
-    return rows * slice_count((int64_t)rows, vocab, kRopeFp32, sms) * 8 * (1 + (size_t)beams);
+    // fp32 slices are half as long, but fill the device, and so grow, at half the rows
+    const int slices = std::max(slice_count((int64_t)rows, vocab, kRopeFp32, sms),
+                                slice_count((int64_t)rows, vocab, kRopeBf16, sms));
+    return rows * slices * 8 * (1 + (size_t)beams);
 }
 
 cudaError_t launch_beams(const BeamArgs &a, void *workspace, int sms, cudaStream_t stream)

@@ -111,6 +111,16 @@ def test_views_outputs_and_workspace():
     assert torch.equal(tokens, api.mla_beam_select(logits, scores)[0])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B,K,V", [(8, 4, 32_000), (10, 5, 20_000), (100, 1, 8000), (1, 64, 9000)])
+def test_nothing_behind_the_workspace_is_written(B, K, V, dtype):
+    """Also where 16-bit rows are cut shorter than fp32 rows of the same length."""
+    size = api.allocate_beam_workspace(B, K, V).numel()
+    room = torch.full((2 * size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    _check(*_inputs(B, K, V, dtype, K), workspace=room[:size])
+    assert bool((room[size:] == 0xA5).all())
+
+
 def test_other_stream_and_graph_replay():
     logits, scores = _inputs(4, 4, 30_000, torch.float32, 2)
     side = torch.cuda.Stream()
