@@ -889,8 +889,10 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  * workspace     device scratch of at least mla_shared_workspace_size(...) bytes (of the
  *               current device; fp8 != 0 for mla_decode_shared_fp8), 256-byte aligned,
  *               contents irrelevant; calls that may run at once need one each
- * A row that sees no token gets 0 and -inf.  Groups, lengths and pages are device data, so a
- * captured call serves changing ones of the same counts.  Deterministic.
+ * A row that sees no token gets 0 and -inf.  Cache rows behind a history may hold anything;
+ * those within it should be finite (NaN or infinity in a draft's row may reach the request's
+ * other drafts).  Groups, lengths and pages are device data, so a captured call serves
+ * changing ones of the same counts.  Deterministic.
  *
  * mla_decode_shared_fp8 takes E4M3 pages and kv_scale as mla_decode_fp8 does.  Its
  * probabilities are multiplied in two E4M3 parts, within 2^-8 of themselves.
@@ -982,12 +984,13 @@ plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base, int32
  * tokens       int32 [batch * beams]: v
  * parents      int32 [batch * beams]: the row b * beams + k it goes on from (as
  *              mla_pages_fork takes it)
- * out_scores   fp32 [batch * beams]: the candidates; must not be scores
+ * out_scores   fp32 [batch * beams]: the candidates; the outputs must not overlap scores or one
+ *              another
  * workspace    device scratch of at least mla_beam_workspace_size(...) bytes (of the current
  *              device), 256-byte aligned, contents irrelevant; calls that may run at once
  *              need one each
- * Log-sum-exps and candidates are held in 64 bits, so the order is that of the formula
- * wherever candidates differ by 1e-6 or more.  Deterministic.
+ * Log-sum-exps and candidates are held in pairs of floats, so the order is that of the
+ * formula wherever candidates differ by 1e-6 or more.  Deterministic.
  */
 size_t mla_beam_workspace_size(int32_t batch, int32_t beams, int32_t vocab);
 plmla_status mla_beam_select(const void *logits, int64_t logits_ld, int32_t dtype,

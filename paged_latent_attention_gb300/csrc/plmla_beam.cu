@@ -264,10 +264,10 @@ __device__ __noinline__ int pick_list(const T *head, int v0, int lo, int left, f
 
 // G groups of 16 bytes a thread: group g of thread t starts at element (g * threads + t) * n of
 // the slice (n elements in 16 bytes), so that element order is (group, thread, element).
-// Latency-bound: five blocks an SM hide the loads and barriers (with three, and the rare
-// path's copy of the logits in local memory, 128 rows of 150,001 took 28 us).
+// Latency-bound: four or five blocks an SM hide each other's loads and barriers (four blocks that
+// go on to further slices, whose logits they load ahead: 256 rows of 50,000 bf16 25 us, not 18).
 template <typename T, int G>
-__global__ void __launch_bounds__(kSliceThreads, 5)
+__global__ void __launch_bounds__(kSliceThreads, G == 8 ? 4 : 5)
 slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int vocab, SliceOut o)
 {
     using W = Word<T>;
@@ -283,7 +283,9 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
     // elements.
     const T *head = logits + (int64_t)row * ld;
     const int skip = (int)(reinterpret_cast<uintptr_t>(head) % 16 / sizeof(T));
-    const int v0 = blockIdx.x * kSlice - skip, left = vocab - v0, lo = max(0, -v0);
+    // (a last slice that no token reaches is empty)
+    const int v0 = (int)min((int64_t)blockIdx.x * kSlice - skip, (int64_t)vocab);
+    const int left = vocab - v0, lo = max(0, -v0);
     const T *src = head + v0;
     auto in_row = [&](int id) { return id >= lo && id < left; };
     uint32_t raw[G][4];
@@ -652,19 +654,23 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
             }
 }
 
-// Groups of 16 bytes a thread: four where such slices fill the device, else one, so that a few
-// rows are read by more SMs.
+// Groups of 16 bytes a thread: one where eight or four would leave SMs without a slice, so that
+// a few rows are read by more of them (4 beams of 32,000 bf16 tokens in 8.9 us), and where it
+// holds a row (2,000 rows of 2,000 bf16 tokens: 30 us; of four groups 35); else four, and eight
+// for rows that four do not hold (2,000 rows of 7,000 bf16 tokens: four 34.6, eight 44; 64 of
+// 100,000: 19.5 and 15.4; 512 fp32 rows of 32,000: 23.0 and 20.3).
 int thread_groups(int64_t rows, int vocab, int type, int sms)
 {
-    const int wide = 4 * (type == kRopeFp32 ? 4 : 8) * kSliceThreads;
-    return rows * ((vocab + wide - 1) / wide) >= sms ? 4 : 1;
+    const int one = (type == kRopeFp32 ? 4 : 8) * kSliceThreads;
+    auto slices = [&](int groups) { return rows * ((vocab - 1) / (groups * one) + 1); };
+    return vocab > 4 * one && slices(8) >= 2 * sms ? 8 : vocab > one && slices(4) >= sms ? 4 : 1;
 }
 
 int slice_count(int64_t rows, int vocab, int type, int sms)
 {
     const int group = type == kRopeFp32 ? 4 : 8;
     const int slice = thread_groups(rows, vocab, type, sms) * group * kSliceThreads;
-    return (vocab + group - 1 + slice - 1) / slice;           // a row may start inside a group
+    return (int)(((int64_t)vocab + group - 2) / slice + 1);   // a row may start inside a group
 }
 
 template <typename T>
@@ -672,7 +678,10 @@ void launch_slices(const BeamArgs &a, int groups, const SliceOut &o, cudaStream_
 {
     const T *x = static_cast<const T *>(a.logits);
     const dim3 grid((unsigned)o.slices, (unsigned)(a.batch * a.beams));
-    if (groups == 4)
+    if (groups == 8)
+        slice_kernel<T, 8><<<grid, kSliceThreads, 0, stream>>>(x, a.ld, a.ended, a.beams, a.vocab,
+                                                               o);
+    else if (groups == 4)
         slice_kernel<T, 4><<<grid, kSliceThreads, 0, stream>>>(x, a.ld, a.ended, a.beams, a.vocab,
                                                                o);
     else

@@ -302,7 +302,9 @@ extern "C" plmla_status mla_beam_select(const void *logits, int64_t logits_ld, i
         logits == nullptr || !aligned(logits, dtype == PLMLA_FP32 ? 4 : 2) || scores == nullptr ||
         !aligned(scores, 4) || (ended != nullptr && (end_token < 0 || end_token >= vocab)) ||
         !words_ok(tokens) || !words_ok(parents) || out_scores == nullptr ||
-        !aligned(out_scores, 4) || out_scores == scores || workspace == nullptr ||
+        !aligned(out_scores, 4) || out_scores == scores || tokens == parents ||
+        static_cast<void *>(out_scores) == tokens || static_cast<void *>(out_scores) == parents ||
+        workspace == nullptr ||
         !aligned(workspace, kAlign))
         return PLMLA_INVALID_ARGUMENT;
     const int sms = device_sms();

@@ -79,8 +79,8 @@ def test_shapes_that_no_workspace_serves(lib):
 
 
 def test_beam_arguments(lib):
-    base = dict(x=FAKE, ld=50, dt=0, scores=FAKE, ended=None, end=-1, B=2, K=3, V=50, tok=FAKE,
-                par=FAKE, out=2 * FAKE, work=FAKE, size=1 << 30)
+    base = dict(x=FAKE, ld=50, dt=0, scores=FAKE, ended=None, end=-1, B=2, K=3, V=50, tok=3 * FAKE,
+                par=4 * FAKE, out=2 * FAKE, work=FAKE, size=1 << 30)
 
     def call(**a):
         return lib.mla_beam_select(a["x"], a["ld"], a["dt"], a["scores"], a["ended"], a["end"],
@@ -91,7 +91,8 @@ def test_beam_arguments(lib):
         dict(scores=None), dict(scores=FAKE + 2), dict(ended=FAKE), dict(ended=FAKE, end=50),
         dict(B=0), dict(K=0), dict(K=65), dict(V=0), dict(B=30000), dict(V=1 << 30, ld=1 << 30),
         dict(tok=None), dict(par=FAKE + 1), dict(out=None), dict(out=FAKE), dict(work=None),
-        dict(work=FAKE + 128)])
+        dict(work=FAKE + 128), dict(tok=4 * FAKE), dict(par=3 * FAKE), dict(out=3 * FAKE),
+        dict(out=4 * FAKE)])
 
 
 @pytest.mark.parametrize("fp8", [False, True])
