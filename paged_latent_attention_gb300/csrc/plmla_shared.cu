@@ -1,7 +1,8 @@
 // plmla_shared.cu -- gated MLA decode of a batch whose requests share prefixes, on CTA pairs
 // of the 5th-generation tensor cores (tcgen05 + TMEM), for sm_103a.
 //
-//   out[r, j, h] = sigmoid(gate) sum_t w_t c_t,  w = softmax_t(scale q_{r,j,h} . x_t),  t < L_r - (n_q - 1 - j)
+//   out[r, j, h] = sigmoid(gate) sum_t w_t c_t,  w = softmax_t(scale q_{r,j,h} . x_t),
+//                  t < L_r - (n_q - 1 - j)
 //
 // The softmax over a history is the merge, by log-sum-exps, of the softmaxes over its
 // parts.  The tokens that a group of requests has in common are one part, read once: the
@@ -11,9 +12,9 @@
 // Work.  A block is 128 query rows of one part.  plan_kernel lists the parts (groups' prefixes,
 // then requests' own tokens); the tiles of 128 tokens of all blocks, in order, are dealt to
 // CTA pairs in equal contiguous runs, a block's start counting kStart tiles more.  A pair's
-// run within a block is a segment: it leaves an unnormalised-to-1 partial output and its
-// log-sum-exp, and merge_kernel joins a row's partials in order and applies the gate.  There are
-// no atomics, and results depend on the arguments alone.
+// run within a block is a segment: it leaves a partial output and its log-sum-exp, and
+// merge_kernel joins a row's partials in order and applies the gate.  There are no atomics,
+// and results depend on the arguments alone.
 //
 // A pair holds 64 rows in each CTA (cta_group::2, M = 128).  Per tile
 //   S = Q K^T      K split by tokens: each CTA loads 64 of them (N = 128)
@@ -24,10 +25,10 @@
 // operands are warp-uniform and constant but for a base, against 110 cycles each from a
 // divergent thread with computed descriptors, so the issuing warp stays converged.
 //
-// Warps: 0 loads K, 2 loads V (TMA, a ring of four 16 KB items each), 3 Q and K's rope block, 1 issues the MMAs of
-// the pair (in the even CTA), K a tile ahead of V, 4-11 softmax and epilogue, a thread
-// having a quarter of a row's 128 scores in registers.  The running maximum lags: O is only
-// rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries in two E4M3 parts
+// Warps: 0 loads K, 2 loads V (TMA, a ring of four 16 KB items each), 3 Q and K's rope block,
+// 1 issues the MMAs of the pair (in the even CTA), K a tile ahead of V, 4-11 softmax and
+// epilogue, a thread having a quarter of a row's 128 scores in registers.  The running maximum
+// lags: O is only rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries in two E4M3 parts
 // (as in the FP8 decode) and the probabilities in two as well, hi + lo, so that they carry 8
 // bits like bf16 ones; a part each takes the rate that bf16 would.
 //
@@ -732,7 +733,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             if (vt == vw.t0 && segs > 0)
                 wait(bar_of(m.bars.o_free), (uint32_t)(segs - 1) & 1u, 8);
             const int half = F8 ? 2 * (int)(v & 1) : 0;
-            if (vw.part.tok0 + (vt + 1) * kTile > vw.part.len) {
+            if (vw.part.len - (vw.part.tok0 + vt * kTile) < kTile) {
                 wait(bar_of(m.bars.zeros[half >> 1]), tails >> (half >> 1) & 1u, 12);
                 tails ^= 1u << (half >> 1);
             }
@@ -772,10 +773,6 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             if (lane == 0)
                 wait_drain(bar_of(m.bars.drain), 0);
         }
-    } else if (warp == 1 && lane == 0) {
-        // the even CTA's commits arrive here too: the last of them comes after the others
-        if (walk.next())
-            wait_drain(bar_of(m.bars.drain), 0);
     } else if (warp >= 4) {
         // -------------------------------------------------- softmax, epilogue
         // Thread (warp group, quad, lane): row 32 (quad % 2) + lane of this CTA, and of a tile the 32
@@ -828,11 +825,11 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 }
                 tc_fence_before();
                 arrive(m.bars.s_free[buf]);
-                const int tok = part.tok0 + t * kTile + 64 * side + 32 * group;
-                if (tok + 32 > limit) {
+                const int seen = limit - (part.tok0 + t * kTile + 64 * side + 32 * group);
+                if (seen < 32) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        x[i] = tok + i < limit ? x[i] : -INFINITY;
+                        x[i] = i < seen ? x[i] : -INFINITY;
                 }
                 float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -950,6 +947,10 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
 
     tc_fence_before();
     __syncthreads();
+    // the even CTA's commits arrive in the odd one too: the last of them comes after the others
+    if (warp == 1 && rank == 1 && lane == 0 && walk.next())
+        wait_drain(bar_of(m.bars.drain), 0);
+    __syncwarp();
     // A pair leaves together: no copy or arrival of one CTA is on its way to the other, and
     // each has waited for its own copy of the last commit.
     pair_sync();
