@@ -406,6 +406,20 @@ struct ShMaps {
     CUtensorMap k, v, rope, qn, qr;
 };
 
+// Waits through the whole run; once another warp has given up (their waits are bounded), as
+// wait_drain.
+__device__ __noinline__ void wait_last(uint32_t bar, volatile int *abort_flag)
+{
+    unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(bar, 0)) {
+        const unsigned long long now = global_ns();
+        if (!*abort_flag)
+            t0 = now;
+        else if (now - t0 > kDrainLimitNs)
+            return;
+    }
+}
+
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 // The page of a part's column, 0 (reported) where the table has none of the pool.
@@ -773,6 +787,10 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             if (lane == 0)
                 wait_drain(bar_of(m.bars.drain), 0);
         }
+    } else if (warp == 1 && lane == 0) {
+        // the even CTA's commits arrive here too: the last of them comes after the others
+        if (walk.next())
+            wait_last(bar_of(m.bars.drain), abort_flag);
     } else if (warp >= 4) {
         // -------------------------------------------------- softmax, epilogue
         // Thread (warp group, quad, lane): row 32 (quad % 2) + lane of this CTA, and of a tile the 32
@@ -947,10 +965,6 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
 
     tc_fence_before();
     __syncthreads();
-    // the even CTA's commits arrive in the odd one too: the last of them comes after the others
-    if (warp == 1 && rank == 1 && lane == 0 && walk.next())
-        wait_drain(bar_of(m.bars.drain), 0);
-    __syncwarp();
     // A pair leaves together: no copy or arrival of one CTA is on its way to the other, and
     // each has waited for its own copy of the last commit.
     pair_sync();
