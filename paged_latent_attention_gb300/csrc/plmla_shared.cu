@@ -108,9 +108,11 @@ shared_plan_kernel(const SharedArgs a, const PlanBuffers queries)
     bool bad = false;
     for (int g = t; g <= G; g += blockDim.x)
         start[g] = a.group_starts[g];
-    if (t < G)
+    int len = 0, common = 0;
+    if (t < G) {
+        common = a.shared_lens[t];
         least[t] = kNever;
-    int len = 0;
+    }
     if (t < R) {
         len = max(a.seq_lens[t], 0);
         if (len > cap) {
@@ -143,7 +145,7 @@ shared_plan_kernel(const SharedArgs a, const PlanBuffers queries)
     SharedPart part = {};
     if (t < G) {
         const int members = bad ? 0 : start[t + 1] - start[t];
-        int64_t tiles = members > 1 ? max(0, min(a.shared_lens[t], least[t])) / kTile : 0;
+        int64_t tiles = members > 1 ? max(0, min(common, least[t])) / kTile : 0;
         // worth it where it saves more tiles than its blocks' starts cost
         const int64_t blocks = ((int64_t)members * a.rows + kShRows - 1) / kShRows;
         const int64_t alone = (int64_t)members * ((a.rows + kShRows - 1) / kShRows);
@@ -238,6 +240,7 @@ struct ShMisc {
     ShBars bars;
     uint32_t tmem;
     int abort, status, first;
+    SharedPart part;                            // the first
     float quarter[2][256];                      // exchanged between the quarters of a row
 };
 
@@ -266,17 +269,15 @@ struct ShWalk {
     int e, blk;
     SharedPart part;
     int t0, t1;                                 // tiles of the segment
-    __device__ void begin(const SharedPart *p, int first, int64_t from, int64_t to)
+    __device__ void begin(const SharedPart *p, const SharedPart &at_from, int first, int64_t from,
+                          int64_t to)
     {
         parts = p;
         pos = from;
         end = to;
         e = first;
-        blk = 0;
-        if (pos < end) {
-            part = parts[e];
-            blk = (int)((pos - part.base) / (part.tiles + kStart));
-        }
+        part = at_from;
+        blk = pos < end ? (int)((pos - part.base) / (part.tiles + kStart)) : 0;
     }
     __device__ bool next()
     {
@@ -485,14 +486,16 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
     const int pair = (int)blockIdx.x >> 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");        // the plan (and split queries)
     const int num_parts = a.num_groups + a.num_reqs;
-    const int64_t base0 = (int)threadIdx.x < num_parts ? a.parts[threadIdx.x].base : 0;
+    SharedPart own = {};
+    if ((int)threadIdx.x < num_parts)
+        own = a.parts[threadIdx.x];
     const int64_t total = *a.total;
     const int64_t pairs = busy_pairs(total, (int)gridDim.x >> 1);
     const int64_t from = pair < pairs ? total * pair / pairs : total;
     const int64_t to = pair < pairs ? total * (pair + 1) / pairs : total;
     {
         // the part that holds the run's first position: the last one that starts there or before
-        int mine = (int)threadIdx.x < num_parts && base0 <= from ? (int)threadIdx.x : 0;
+        int mine = (int)threadIdx.x < num_parts && own.base <= from ? (int)threadIdx.x : 0;
         for (int e = threadIdx.x + kShThreads; e < num_parts; e += kShThreads)
             if (a.parts[e].base <= from)
                 mine = e;
@@ -502,6 +505,12 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         if (mine != 0)
             atomicMax(&m.first, mine);
         __syncthreads();
+        // (another read of it from L2 would be on the way to the first loads)
+        if (m.first == (int)threadIdx.x)
+            m.part = own;
+        else if (threadIdx.x == 0 && m.first >= kShThreads)
+            m.part = a.parts[m.first];
+        __threadfence_block();                  // (the barrier below orders nothing by itself)
     }
     pair_sync();                                // the pair's barriers are initialised (and fenced)
     const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
@@ -509,7 +518,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
     int32_t *status = &m.status;
     auto lead = [&](const uint64_t &b) { return map_rank(bar_of(b), 0); };
     ShWalk walk;
-    walk.begin(a.parts, m.first, from, to);
+    walk.begin(a.parts, m.part, m.first, from, to);
 
     if (warp == 0) {
         // ------------------------------------------------------------ K loads
