@@ -457,6 +457,9 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             atomicExch(a.status, 12);
         return;
     }
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + sizeof(ShMaps) / sizeof(CUtensorMap))
+        asm volatile("prefetch.tensormap [%0];" ::"l"(
+            reinterpret_cast<uint64_t>(&maps.k + (threadIdx.x - 64))) : "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < kShSlots; ++i) {
             mbar_init(bar_of(m.bars.k_full[i]), 1);           // the even CTA expects for both
@@ -959,18 +962,22 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             // lane by lane, so that a store covers 512 bytes
             float4 *out = reinterpret_cast<float4 *>(a.o_part) +
                           ((slot * 2 + (int)rank) * 4 + quad) * 64 * 32 + lane;
-#pragma unroll 1
-            for (int c = 128 * group; c < 128 * group + 128; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(lanes + c, r);
+            uint32_t r[2][16];                  // the next columns are read while these are stored
+            tmem_ld16(lanes + 128 * group, r[0]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = 128 * group + 16 * j;
                 tmem_wait_ld();
+                if (j < 7)
+                    tmem_ld16(lanes + c + 16, r[(j + 1) & 1]);
+                const uint32_t(&x)[16] = r[j & 1];
                 if (store)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         out[(c / 4 + i) * 32] = make_float4(
-                            __uint_as_float(r[4 * i]) * scale, __uint_as_float(r[4 * i + 1]) * scale,
-                            __uint_as_float(r[4 * i + 2]) * scale,
-                            __uint_as_float(r[4 * i + 3]) * scale);
+                            __uint_as_float(x[4 * i]) * scale, __uint_as_float(x[4 * i + 1]) * scale,
+                            __uint_as_float(x[4 * i + 2]) * scale,
+                            __uint_as_float(x[4 * i + 3]) * scale);
             }
             tc_fence_before();
             arrive(m.bars.o_free);
