@@ -276,6 +276,7 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
     using W = Word<T>;
     constexpr int N = 4 * W::n, kSlice = G * N * kSliceThreads, kWarps = kSliceThreads / 32;
     __shared__ SliceShared s;
+    __shared__ uint4 copies[G][kSliceThreads];   // of threads that have candidates
     asm volatile("griddepcontrol.launch_dependents;");
     const int row = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t at = (int64_t)row * o.slices + blockIdx.x;
@@ -362,22 +363,42 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
     const float reach = value_of(least);
     if (top >= reach) {
         const uint32_t x = W::both(reach);
-#pragma unroll
-        for (int g = 0; g < G; ++g)
+        auto offer = [&](float logit, int id) {
+            const int i = atomicAdd(&s.count, 1);
+            if (i < SliceShared::kFew)
+                s.list[i] = entry_of(logit, v0 + id);
+        };
+        if constexpr (G == 1) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const uint32_t hit = W::reach(raw[g][w], x);
-                if (hit != 0)
+                const uint32_t hit = W::reach(raw[0][w], x);
 #pragma unroll
-                    for (int e = 0; e < W::n; ++e) {
-                        const int id = (g * kSliceThreads + t) * N + W::n * w + e;
-                        if ((hit >> e & 1u) != 0 && in_row(id)) {
-                            const int i = atomicAdd(&s.count, 1);
-                            if (i < SliceShared::kFew)
-                                s.list[i] = entry_of(W::get(raw[g][w], e), v0 + id);
-                        }
-                    }
+                for (int e = 0; e < W::n; ++e) {
+                    const int id = t * N + W::n * w + e;
+                    if ((hit >> e & 1u) != 0 && in_row(id))
+                        offer(W::get(raw[0][w], e), id);
+                }
             }
+        } else {
+            // A bit for each element, then a loop over those set: with the offers unrolled over all
+            // elements the blocks waited for instructions (128 rows of 150,001 18.2 us, not 16.2;
+            // a single group is faster unrolled, 8.9 us, not 9.8, for 4 rows of 32,000 fp32).
+            unsigned long long hits = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                copies[g][t] = make_uint4(raw[g][0], raw[g][1], raw[g][2], raw[g][3]);
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    hits |= (unsigned long long)W::reach(raw[g][w], x) << (g * N + w * W::n);
+            }
+#pragma unroll 1
+            for (; hits != 0; hits &= hits - 1) {
+                const int bit = __ffsll((long long)hits) - 1, g = bit / N, e = bit % N;
+                const int id = (g * kSliceThreads + t) * N + e;
+                if (in_row(id))
+                    offer((float)reinterpret_cast<const T *>(&copies[g][t])[e], id);
+            }
+        }
     }
     const float high = value_of(high_key), ref = high == -INFINITY ? 0.f : high;
     float sum;
