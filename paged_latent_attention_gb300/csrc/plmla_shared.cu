@@ -1028,7 +1028,7 @@ shared_merge_kernel(const SharedArgs a, const int pairs)
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 3;
     const int64_t rows = (int64_t)a.num_reqs * a.rows, row0 = (int64_t)(blockIdx.x / kBlocks) * 32;
-    const int64_t row = min(row0 + lane, rows - 1);
+    const int row = (int)min(row0 + lane, rows - 1), req = row / a.rows;  // (2^25 rows at most)
     const int col0 = (int)(blockIdx.x % kBlocks) * 8 * C, col = col0 + C * (warp & 7);
     uint2 gate[kOut];
 #pragma unroll
@@ -1042,7 +1042,7 @@ shared_merge_kernel(const SharedArgs a, const int pairs)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // the row's partials: of the prefix (0) and of its own tokens (1)
     const int64_t total = *a.total, busy = busy_pairs(total, pairs);
-    const SharedSource from = a.sources[row / a.rows];
+    const SharedSource from = a.sources[req];
     // the pair that has position x: (the last p with p total / busy, rounded down, <= x)
     auto pair_of = [&](int64_t x) -> int {
         return total < 1 << 24 ? (int)(((uint32_t)(x + 1) * (uint32_t)busy - 1) / (uint32_t)total)
@@ -1052,7 +1052,7 @@ shared_merge_kernel(const SharedArgs a, const int pairs)
     int64_t first[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int in_part = (int)(row - from.row0[i]), blk = in_part / kShRows;
+        const int in_part = row - from.row0[i], blk = in_part / kShRows;
         // positions of the block's tiles
         const int64_t v0 = from.base[i] + (int64_t)blk * (from.tiles[i] + kStart) + kStart;
         n[i] = at[i] = 0;
