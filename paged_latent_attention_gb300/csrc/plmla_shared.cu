@@ -1016,9 +1016,10 @@ __device__ __forceinline__ float gate_of(float x)
 // writes its outputs in whole pieces of rows.  A row's partials are those of the group's
 // prefix, then those of the request's own tokens, in the order of their tokens.  Many rows are
 // bound by the reads and take 16 columns a warp; with few, each of many partials, latency
-// counts, and two warps share them (512 rows of 20 partials: 3 us less).
+// counts, and two warps share them (512 rows of 20 partials: 3 us less), two blocks an SM (0.7 us
+// less than with one; the form for many rows is slower with any minimum: 1-13%).
 template <int C, int PARTS>
-__global__ void __launch_bounds__(256 * PARTS)
+__global__ void __launch_bounds__(256 * PARTS, PARTS == 1 ? 0 : 2)
 shared_merge_kernel(const SharedArgs a, const int pairs)
 {
     constexpr int kThreads = 256 * PARTS, kWarps = kThreads / 32, kBlocks = kLatent / (8 * C);
