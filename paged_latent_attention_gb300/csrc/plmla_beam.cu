@@ -17,10 +17,9 @@
 // floats there: candidates of different rows are compared, and a rounding must not change
 // their order.
 //
-// Bound: latencies, of two launches and of a block's chain (loads, two barriers, the list, whose
-// code is long enough to wait for the instruction cache too); the logits' bytes are a fifth to
-// a third of it.  128 rows of 150,001 bf16 logits 18.1 us (5.7 us of HBM), 128 of 100,257 fp16
-// 21.0 (3.8; lists of 32), 4 of 32,000 fp32 8.9.
+// Bound: latencies, of two launches and of a block's chain (loads, two barriers, the list); the
+// logits' bytes are a fifth to a third of it.  128 rows of 150,001 bf16 logits 16.1 us (5.7 us of
+// HBM), 128 of 100,257 fp16 20.0 (3.8; lists of 32), 4 of 32,000 fp32 8.9.
 #include <math.h>
 #include <algorithm>
 
@@ -268,7 +267,8 @@ __device__ __noinline__ int pick_list(const T *head, int v0, int lo, int left, f
 // G groups of 16 bytes a thread: group g of thread t starts at element (g * threads + t) * n of
 // the slice (n elements in 16 bytes), so that element order is (group, thread, element).
 // Latency-bound: four or five blocks an SM hide each other's loads and barriers (four blocks that
-// go on to further slices, whose logits they load ahead: 128 rows of 150,001 bf16 25 us, not 18).
+// go on to further slices, whose logits they load ahead: 128 rows of 150,001 bf16 25 us instead of
+// the 18 it took then).
 template <typename T, int G>
 __global__ void __launch_bounds__(kSliceThreads, G == 8 ? 4 : 5)
 slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int vocab, SliceOut o)

@@ -35,8 +35,8 @@
 // Measured: 64 requests x 64 heads over 32,768 shared and 300-4,000 own tokens, bf16: 200 us, the
 // decode kernel 188, 1.66 PFLOP/s (87% of a library product's burst, tensor pipe busy 79% of
 // the time; each SM takes in 139 KB a tile, at 80% of what the L2 gives it).  4-draft verification
-// over 48 E4M3 histories: 148 us, the decode 125.  8 answers to 20,011 tokens: 33 us, 2 requests of
-// 1,500: 15.6 us, both latency: three launches, a block's start, a partial's way out and back.
+// over 48 E4M3 histories: 148 us, the decode 125.  8 answers to 20,011 tokens: 32 us, 2 requests of
+// 1,500: 14.6 us, both latency: three launches, a block's start, a partial's way out and back.
 // Against the plain decode, which reads a prefix once per request: 64 requests of 66,048 + 2,000
 // tokens 360 us, not 684.
 //
