@@ -986,9 +986,8 @@ plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base, int32
  *              mla_pages_fork takes it)
  * out_scores   fp32 [batch * beams]: the candidates; the outputs must not overlap scores or one
  *              another
- * workspace    device scratch of at least mla_beam_workspace_size(...) bytes (of the current
- *              device), 256-byte aligned, contents irrelevant; calls that may run at once
- *              need one each
+ * workspace    device scratch of at least mla_beam_workspace_size(...) bytes, 256-byte
+ *              aligned, contents irrelevant; calls that may run at once need one each
  * Log-sum-exps and candidates are held in pairs of floats, so the order is that of the
  * formula wherever candidates differ by 1e-6 or more.  Deterministic.
  */

@@ -1167,23 +1167,12 @@ def mla_pages_reserve(slabs, page_table, seq_lens, n_new, ref_counts, *, workspa
     return page_table
 
 
-def _beam_workspace_size(dev, batch, beams, vocab):
-    """The size depends on the device that the call will run on."""
-    size = _native.lib().mla_beam_workspace_size
-    if dev == torch._C._cuda_getDevice():
-        return size(batch, beams, vocab)
-    with torch.cuda.device(dev):
-        return size(batch, beams, vocab)
-
-
 def allocate_beam_workspace(batch, beams, vocab, device=None):
     """A workspace tensor (uint8) of the size mla_beam_select needs."""
-    device = torch.device(device or "cuda")
-    dev = torch.cuda.current_device() if device.index is None else device.index
-    n = _beam_workspace_size(dev, batch, beams, vocab)
+    n = _native.lib().mla_beam_workspace_size(batch, beams, vocab)
     if n == 0:
         _fail("invalid shape for mla_beam_workspace_size")
-    return torch.empty(n, dtype=_U8, device=device)
+    return torch.empty(n, dtype=_U8, device=device or "cuda")
 
 
 def mla_beam_select(logits, scores, *, ended=None, end_token=-1, tokens=None, parents=None,
@@ -1226,9 +1215,10 @@ def mla_beam_select(logits, scores, *, ended=None, end_token=-1, tokens=None, pa
             _dense(t, name, dev, shape, dtype)
         out.append(t)
     tokens, parents, out_scores = out
+    lib = _native.lib()
     if workspace is None:
-        workspace = _empty(_beam_workspace_size(dev, B, K, rows[2]), _U8, device, stream)
-    _launch(dev, _native.lib().mla_beam_select, "mla_beam_select", stream, rows[0], rows[1], kind,
+        workspace = _empty(lib.mla_beam_workspace_size(B, K, rows[2]), _U8, device, stream)
+    _launch(dev, lib.mla_beam_select, "mla_beam_select", stream, rows[0], rows[1], kind,
             have, flags, int(end_token), B, K, rows[2], tokens.data_ptr(), parents.data_ptr(),
             out_scores.data_ptr(), *_scratch(workspace, dev))
     return tokens, parents, out_scores

@@ -19,7 +19,7 @@
 //
 // Bound: latencies, of two launches and of a block's chain (loads, two barriers, the list); the
 // logits' bytes are a fifth to a third of it.  128 rows of 150,001 bf16 logits 16.1 us (5.7 us of
-// HBM), 128 of 100,257 fp16 20.0 (3.8; lists of 32), 4 of 32,000 fp32 8.9.
+// HBM), 128 of 100,257 fp16 20.0 (3.8; lists of 32), 4 of 32,000 fp32 8.1.
 #include <math.h>
 #include <algorithm>
 
@@ -678,22 +678,21 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
             }
 }
 
-// Groups of 16 bytes a thread: one where eight or four would leave SMs without a slice, so that
-// a few rows are read by more of them (4 beams of 32,000 bf16 tokens in 8.9 us), and where it
-// holds a row (2,000 rows of 2,000 bf16 tokens: 30 us; of four groups 35); else four, and eight
-// for rows that four do not hold (2,000 rows of 7,000 bf16 tokens: four 34.6, eight 44; 64 of
-// 100,000: 19.5 and 15.4; 512 fp32 rows of 32,000: 23.0 and 20.3).
-int thread_groups(int64_t rows, int vocab, int type, int sms)
+// Groups of 16 bytes a thread: one where that holds a row (2,000 rows of 2,000 bf16 tokens: 30
+// us; of four groups 34), four where those do (7,000: 33; one 47, eight 41), else eight (512
+// fp32 rows of 32,000: 20; four 25, one 60).  With few rows shorter slices on more SMs gain nothing,
+// since the merge has more lists: 4 rows of 150,000 bf16 tokens 9.2 us, in slices of four
+// groups 9.5, of one 12.2.
+int thread_groups(int vocab, int type)
 {
     const int one = (type == kRopeFp32 ? 4 : 8) * kSliceThreads;
-    auto slices = [&](int groups) { return rows * ((vocab - 1) / (groups * one) + 1); };
-    return vocab > 4 * one && slices(8) >= 2 * sms ? 8 : vocab > one && slices(4) >= sms ? 4 : 1;
+    return vocab > 4 * one ? 8 : vocab > one ? 4 : 1;
 }
 
-int slice_count(int64_t rows, int vocab, int type, int sms)
+int slice_count(int vocab, int type)
 {
     const int group = type == kRopeFp32 ? 4 : 8;
-    const int slice = thread_groups(rows, vocab, type, sms) * group * kSliceThreads;
+    const int slice = thread_groups(vocab, type) * group * kSliceThreads;
     return (int)(((int64_t)vocab + group - 2) / slice + 1);   // a row may start inside a group
 }
 
@@ -715,25 +714,24 @@ void launch_slices(const BeamArgs &a, int groups, const SliceOut &o, cudaStream_
 
 }  // namespace
 
-size_t beam_workspace(int batch, int beams, int vocab, int sms)
+size_t beam_workspace(int batch, int beams, int vocab)
 {
     const size_t rows = (size_t)batch * beams;
-    // fp32 slices are half as long, but fill the device, and so grow, at half the rows
-    const int slices = std::max(slice_count((int64_t)rows, vocab, kRopeFp32, sms),
-                                slice_count((int64_t)rows, vocab, kRopeBf16, sms));
+    // fp32 slices are half as long, but hold rows of a length that 16-bit ones cut at less
+    const int slices = std::max(slice_count(vocab, kRopeFp32), slice_count(vocab, kRopeBf16));
     return rows * slices * 8 * (1 + (size_t)beams);
 }
 
-cudaError_t launch_beams(const BeamArgs &a, void *workspace, int sms, cudaStream_t stream)
+cudaError_t launch_beams(const BeamArgs &a, void *workspace, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)a.batch * a.beams;
     SliceOut o;
-    o.slices = slice_count(rows, a.vocab, a.type, sms);
+    o.slices = slice_count(a.vocab, a.type);
     const int64_t lists = rows * o.slices;
     o.lists = static_cast<uint64_t *>(workspace);
     o.high = reinterpret_cast<float *>(o.lists + lists * a.beams);
     o.sum = o.high + lists;
-    const int groups = thread_groups(rows, a.vocab, a.type, sms);
+    const int groups = thread_groups(a.vocab, a.type);
     if (a.type == kRopeBf16)
         launch_slices<__nv_bfloat16>(a, groups, o, stream);
     else if (a.type == kRopeFp16)

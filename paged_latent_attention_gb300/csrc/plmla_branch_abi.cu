@@ -286,8 +286,7 @@ bool beams_ok(int32_t batch, int32_t beams, int32_t vocab)
 
 extern "C" size_t mla_beam_workspace_size(int32_t batch, int32_t beams, int32_t vocab)
 {
-    const int sms = device_sms();
-    return beams_ok(batch, beams, vocab) && sms > 0 ? beam_workspace(batch, beams, vocab, sms) : 0;
+    return beams_ok(batch, beams, vocab) ? beam_workspace(batch, beams, vocab) : 0;
 }
 
 extern "C" plmla_status mla_beam_select(const void *logits, int64_t logits_ld, int32_t dtype,
@@ -307,12 +306,9 @@ extern "C" plmla_status mla_beam_select(const void *logits, int64_t logits_ld, i
         workspace == nullptr ||
         !aligned(workspace, kAlign))
         return PLMLA_INVALID_ARGUMENT;
-    const int sms = device_sms();
-    if (sms <= 0)
-        return PLMLA_CUDA_ERROR;
-    if (workspace_bytes < beam_workspace(batch, beams, vocab, sms))
+    if (workspace_bytes < beam_workspace(batch, beams, vocab))
         return PLMLA_WORKSPACE_TOO_SMALL;
     const BeamArgs a = {logits, logits_ld, dtype, scores, ended, end_token, batch,
                         beams,  vocab,     tokens, parents, out_scores};
-    return result(launch_beams(a, workspace, sms, static_cast<cudaStream_t>(stream)));
+    return result(launch_beams(a, workspace, static_cast<cudaStream_t>(stream)));
 }

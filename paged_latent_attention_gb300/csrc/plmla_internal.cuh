@@ -277,8 +277,8 @@ struct BeamArgs {
     int32_t *tokens, *parents;          // [batch * beams]
     float *out_scores;
 };
-size_t beam_workspace(int batch, int beams, int vocab, int sms);
-cudaError_t launch_beams(const BeamArgs &a, void *workspace, int sms, cudaStream_t stream);
+size_t beam_workspace(int batch, int beams, int vocab);
+cudaError_t launch_beams(const BeamArgs &a, void *workspace, cudaStream_t stream);
 
 // Shared by the query quantiser (plan grid) and the FP8 append: one E4M3 byte
 // pair from two floats, round to nearest even, saturating to +-448.

@@ -112,7 +112,8 @@ def test_views_outputs_and_workspace():
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("B,K,V", [(8, 4, 32_000), (10, 5, 20_000), (100, 1, 8000), (1, 64, 9000)])
+@pytest.mark.parametrize("B,K,V", [(8, 4, 32_000), (10, 5, 20_000), (100, 1, 8000), (1, 64, 9000),
+                                   (3, 4, 2048), (2, 8, 2043), (2, 2, 16_384)])
 def test_nothing_behind_the_workspace_is_written(B, K, V, dtype):
     """Also where 16-bit rows are cut shorter than fp32 rows of the same length."""
     size = api.allocate_beam_workspace(B, K, V).numel()

@@ -74,6 +74,7 @@ def test_shapes_that_no_workspace_serves(lib):
     for shape in ((0, 1, 64, 1, 0), (1025, 1, 64, 1, 0), (1, 0, 64, 1, 0), (1, 257, 64, 1, 0),
                   (1, 1, 0, 1, 0), (1, 1, 129, 1, 0), (1, 1, 64, 0, 0), (1, 1, 64, 1025, 1)):
         assert lib.mla_shared_workspace_size(*shape) == 0
+    assert lib.mla_beam_workspace_size(1, 1, 1) > 0            # (the same on any)
     for shape in ((0, 4, 10), (1, 0, 10), (1, 65, 10), (1, 4, 0), (16384, 4, 10), (1, 64, 1 << 30)):
         assert lib.mla_beam_workspace_size(*shape) == 0
 
