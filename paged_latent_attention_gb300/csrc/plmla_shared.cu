@@ -55,7 +55,7 @@ namespace {
 constexpr int kShThreads = 384;
 constexpr int kShSlots = 4, kShSlot = 16384;    // of the K ring, and of the V ring
 constexpr int kShRows = 128;                    // query rows of a block
-constexpr int kStart = 5;                       // cost of a block's start, in tiles (2: 7% slower, 8: 2%)
+constexpr int kStart = 5;                       // cost of a block's start, in tiles (3: 6% slower, 6: 1%)
 constexpr int kShPlanThreads = 1024;
 constexpr int kKept = 64;                       // log-sum-exps of a row that the merge keeps
 constexpr int kColS = 256;                      // TMEM column of the first score tile
