@@ -18,8 +18,8 @@
 // their order.
 //
 // Bound: latencies, of two launches and of a block's chain (loads, two barriers, the list); the
-// logits' bytes are a fifth to a third of it.  128 rows of 150,001 bf16 logits 16.1 us (5.7 us of
-// HBM), 128 of 100,257 fp16 20.0 (3.8; lists of 32), 4 of 32,000 fp32 8.1.
+// logits' bytes are a fifth to a third of it.  128 rows of 150,001 bf16 logits 15.3 us (5.7 us of
+// HBM), 128 of 100,257 fp16 20.0 (3.8; lists of 32), 4 of 32,000 fp32 6.2.
 #include <math.h>
 #include <algorithm>
 
@@ -31,7 +31,6 @@ namespace plmla {
 namespace {
 
 constexpr int kSliceThreads = 256;
-constexpr int kMergeThreads = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A 32-bit key in the order of the floats (-0 as 0, so that equal logits tie).
@@ -548,10 +547,10 @@ __device__ __forceinline__ float wide_value(unsigned long long k)
     return value_of((uint32_t)(k >> 32));       // lo is below half a unit of hi
 }
 
-template <int P>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, const SliceOut o)
+template <int P, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, const SliceOut o)
 {
-    constexpr int kWarps = kMergeThreads / 32, kList = 32 * P;
+    constexpr int kWarps = WARPS, kList = 32 * P;
     __shared__ unsigned long long keys[kWarps * kList / 2];
     __shared__ int ids[kWarps * kList / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
@@ -741,17 +740,21 @@ cudaError_t launch_beams(const BeamArgs &a, void *workspace, cudaStream_t stream
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess)
         return err;
+    // Eight warps where each has one beam at most and few lists, else 32: fewer levels of joins,
+    // and more blocks an SM (4 beams of 2,000 tokens 5.2 us, not 7.3, 500 times 4 of 1,000 14, not
+    // 29, 4 of 150,000 8.0, not 9.2; 32 of 1,000 12.4, not 9.4, 64 lists of 32 beams 14, not 11).
+    const bool few = a.beams <= 8 && a.beams * (int64_t)o.slices <= 64;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.batch);
-    cfg.blockDim = dim3(kMergeThreads);
+    cfg.blockDim = dim3(few ? 256 : 1024);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return a.beams <= 32 ? cudaLaunchKernelEx(&cfg, merge_kernel<1>, a, o)
-                         : cudaLaunchKernelEx(&cfg, merge_kernel<2>, a, o);
+    auto kernel = few ? merge_kernel<1, 8> : a.beams <= 32 ? merge_kernel<1, 32> : merge_kernel<2, 32>;
+    return cudaLaunchKernelEx(&cfg, kernel, a, o);
 }
 
 }  // namespace plmla
