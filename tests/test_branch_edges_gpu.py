@@ -215,3 +215,47 @@ def test_new_tokens_past_every_table_are_refused():
         status.zero_()
         api.mla_pages_reserve([slab], table, _ints([length]), n, counts, status=status)
         assert int(status.item()) == 33 and counts.tolist() == [1, 0] and table.tolist() == [[0]]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_past_four_gigabytes(fp8):
+    """Pages at the end of a pool larger than 2^32 bytes: read, and copied into."""
+    pages = 4900 if fp8 else 2450
+    b = make_batch([(2000, [2100, 2300]), (0, [1000])], 1, 16, fp8, seed=6, spare=0)
+    small, bits = b["slab"].shape[0], torch.uint8 if fp8 else torch.int16
+    pool = torch.empty(pages, PT * ROW, dtype=b["slab"].dtype, device="cuda")
+    assert pool.numel() * pool.element_size() > 2 ** 32
+    pool.view(bits)[pages - small:] = b["slab"].view(bits)
+    table = torch.where(b["table"] >= 0, b["table"] + (pages - small), b["table"])
+    want = _decode(b)
+    got = _decode({**b, "slab": pool, "table": table})
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # page 1 is held twice; the only free page is the last
+    counts = torch.ones(pages, dtype=torch.int32, device="cuda")
+    counts[1], counts[pages - 1] = 2, 0
+    pool.view(bits)[1] = torch.randint(0, 100, (PT * ROW,), dtype=bits, device="cuda")
+    rows, status = _ints([[1], [1]]), _ints([0])
+    api.mla_pages_reserve([pool], rows, _ints([1400, 1400]), 1, counts, status=status)
+    assert int(status.item()) == 0 and rows.tolist() == [[pages - 1], [1]]
+    assert torch.equal(pool.view(bits)[pages - 1, :1400 * ROW], pool.view(bits)[1, :1400 * ROW])
+
+
+def test_calls_refuse_nothing_that_a_view_allows():
+    """Tables, counts and lengths that start anywhere in a buffer, rows of logits at any stride."""
+    b = make_batch([(1600, [1700, 1650]), (0, [40])], 2, 5, seed=8)
+    want = _decode(b)
+    shift = {}
+    for k in ("lens", "starts", "shared"):
+        buf = torch.full((b[k].numel() + 7,), -1, dtype=torch.int32, device="cuda")
+        shift[k] = buf[3:3 + b[k].numel()].copy_(b[k])
+    wide = torch.full((b["table"].shape[0], b["table"].shape[1] + 5), -1, dtype=torch.int32,
+                      device="cuda")
+    shift["table"] = wide[:, 1:1 + b["table"].shape[1]].copy_(b["table"])
+    got = _decode({**b, **shift})
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    counts = torch.zeros(9, dtype=torch.int32, device="cuda")[1:]        # not 16-byte aligned
+    slab = torch.zeros(8, PT * ROW, dtype=torch.uint8, device="cuda")
+    table = torch.full((3, 9), -1, dtype=torch.int32, device="cuda")[:, 2:5]
+    api.mla_pages_reserve([slab], table, _ints([0, 0, 0]), _ints([PT + 1, 0, 5]), counts)
+    assert table.tolist() == [[0, 1, -1], [-1] * 3, [2, -1, -1]]
+    assert counts.tolist() == [1, 1, 1, 0, 0, 0, 0, 0]
