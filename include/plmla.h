@@ -889,10 +889,10 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  * workspace     device scratch of at least mla_shared_workspace_size(...) bytes (of the
  *               current device; fp8 != 0 for mla_decode_shared_fp8), 256-byte aligned,
  *               contents irrelevant; calls that may run at once need one each
- * A row that sees no token gets 0 and -inf.  Cache rows behind a history may hold anything;
- * those within it should be finite (NaN or infinity in a draft's row may reach the request's
- * other drafts).  Groups, lengths and pages are device data, so a captured call serves
- * changing ones of the same counts.  Deterministic.
+ * A row that sees no token gets 0 and -inf.  Cache rows that a query does not see, behind its
+ * history or of later drafts, may hold anything.  (What is not finite in a draft's row
+ * counts as 0 where its weight is 0: where the score is -inf.)  Groups, lengths and pages are
+ * device data, so a captured call serves changing ones of the same counts.  Deterministic.
  *
  * mla_decode_shared_fp8 takes E4M3 pages and kv_scale as mla_decode_fp8 does.  Its
  * probabilities are multiplied in two E4M3 parts, within 2^-8 of themselves.

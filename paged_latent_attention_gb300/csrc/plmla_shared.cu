@@ -411,6 +411,31 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t
                  : "memory");
 }
 
+// 16 bytes of V: what is not finite becomes 0.
+template <bool F8>
+__device__ __forceinline__ void finite_16(uint32_t addr)
+{
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // a mask of the elements whose exponent (bf16), or all of them but the sign (E4M3), is ones
+        const uint32_t bad = F8 ? __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu)
+                                : __vcmpeq2(w[i] & 0x7F807F80u, 0x7F807F80u);
+        any |= bad;
+        w[i] &= ~bad;
+    }
+    if (any != 0)
+        st_shared_16(addr, w[0], w[1], w[2], w[3]);
+}
+
+// The end of the tokens that every row of the part sees.
+__device__ __forceinline__ int tokens_to_all(const SharedPart &part) { return min(part.len, part.vis); }
+
 struct ShMaps {
     CUtensorMap k, v, rope, qn, qr;
 };
@@ -636,10 +661,11 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                     page = page_at(a, walk.part.req, col, status);
                 }
                 const int in_page = tok % kPageTokens, valid = walk.part.len - tok;
+                const int seen = tokens_to_all(walk.part) - tok;
                 const int half = F8 ? 2 * (int)(g & 1) : 0;
                 const uint32_t phase = (uint32_t)(F8 ? g >> 1 : g) & 1u;
                 // item i: bf16 (256 columns i / 2, 64 tokens i % 2); E4M3 (256 columns i)
-                if (valid >= kTile) {
+                if (seen >= kTile) {
 #pragma unroll
                     for (int i = 0; i < F::v_items; ++i) {
                         const uint32_t at = 8 * (half + i);
@@ -652,9 +678,11 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                     ok = all_ok(ok);
                     continue;
                 }
-                // A history's last tile: its rows past the history hold stale data, and a weight
-                // of 0 times NaN is NaN.  It is loaded on a barrier of this CTA's own, and
-                // those rows become zeros before the MMAs hear of it.
+                // A history's last tiles.  Rows past the history hold stale data, those of drafts are
+                // not seen by all of its queries, and a weight of 0 times NaN is NaN.  The tile
+                // is loaded on a barrier of this CTA's own; before the MMAs hear of it, rows past the
+                // history become zeros, and so does what is not finite in a draft's row (the
+                // queries that see it have it in their scores).
                 for (int i = 0; i < F::v_items; ++i)
                     ok &= wait_bounded(empty + 8 * (half + i), phase ^ 1, abort_flag, status, 2);
                 ok = all_ok(ok);
@@ -672,9 +700,15 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 constexpr int t_num = F8 ? 128 : 64, pitch = t_num * 128;
                 for (int i = 0; i < F::v_items; ++i) {
                     const int n = min(t_num, max(0, valid - (F8 ? 0 : 64 * (i & 1))));
-                    for (int b = 0; b < kCols; ++b)
+                    const int m = min(n, max(0, seen - (F8 ? 0 : 64 * (i & 1))));
+                    for (int b = 0; b < kCols; ++b) {
+                        const uint32_t block = s_v + (half + i) * kShSlot + b * pitch;
+#pragma unroll 4
+                        for (int x = m * 128 + 16 * lane; x < n * 128; x += 512)
+                            finite_16<F8>(block + x);
                         for (int x = n * 128 + 16 * lane; x < pitch; x += 512)
-                            st_shared_16(s_v + (half + i) * kShSlot + b * pitch + x, 0u, 0u, 0u, 0u);
+                            st_shared_16(block + x, 0u, 0u, 0u, 0u);
+                    }
                 }
                 fence_proxy_async();
                 __syncwarp();
@@ -767,7 +801,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             if (vt == vw.t0 && segs > 0)
                 wait(bar_of(m.bars.o_free), (uint32_t)(segs - 1) & 1u, 8);
             const int half = F8 ? 2 * (int)(v & 1) : 0;
-            if (vw.part.len - (vw.part.tok0 + vt * kTile) < kTile) {
+            if (tokens_to_all(vw.part) - (vw.part.tok0 + vt * kTile) < kTile) {
                 wait(bar_of(m.bars.zeros[half >> 1]), tails >> (half >> 1) & 1u, 12);
                 tails ^= 1u << (half >> 1);
             }

@@ -206,6 +206,37 @@ def test_not_a_number_stays_in_its_request():
     check(b, out, lse, rows=rest)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n_q,H,lens", [
+    (2, 64, [129, 640, 1537, 1]), (4, 16, [2, 131, 1538, 4000]), (3, 5, [1536, 1537, 1664, 258]),
+    (130, 8, [129, 400, 1600]), (256, 3, [300, 1792])])
+def test_drafts_that_see_no_bad_token_stay_clean(n_q, H, lens, fp8):
+    """NaN (and infinities) in the cache rows of the last tokens reach the drafts that see them."""
+    b = make_batch([(0, [n]) for n in lens], n_q, H, fp8, seed=n_q)
+    slab = b["slab"].view(torch.uint8).view(b["slab"].shape[0], PT, -1)
+    first = []                                      # the first bad token of each request
+    for r, n in enumerate(lens):
+        bad = [n - 1] if n_q == 2 else [n - 1, max(n - n_q // 2, 0)]
+        for t in bad:
+            page, row = int(b["table"][r, t // PT]), t % PT
+            x = slab[page, row]
+            if fp8:
+                x[7 * t % 500], x[t % 512] = 0x7F, 0xFF
+            else:
+                v = x.view(torch.bfloat16)
+                v[7 * t % 500], v[t % 512], v[511] = math.inf, math.nan, -math.inf
+        first.append(min(bad))
+    out, lse = _run(b)
+    clean = [r * n_q + j for r, n in enumerate(lens) for j in range(n_q) if n - (n_q - 1 - j) <= first[r]]
+    check(b, out, lse, rows=clean)
+    hit = sorted(set(range(len(lens) * n_q)) - set(clean))
+    # A score with NaN or +inf among the visible ones leaves no number; one of -inf (two infinities
+    # at the same token, by the signs of q) has no weight.
+    want = torch.isfinite(reference(b)[1][hit])
+    assert torch.equal(torch.isfinite(lse[hit]), want) and not bool(want.all())
+    assert torch.equal(torch.isnan(out[hit]), ~want[..., None].expand(-1, -1, 512))
+
+
 def test_views_and_outputs():
     b = make_batch([(700, [800, 900]), (0, [2000])], 1, 64, seed=2)
     want = _run(b)
