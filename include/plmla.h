@@ -883,8 +883,8 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  *               the batch is decoded without sharing).  A group may be one request or
  *               empty; num_groups 1 .. 1024
  * shared_lens   int32 [num_groups], device: the first tokens that all members of the group
- *               have in common, whatever pages hold them (they are read through the table row of the
- *               group's first request); what exceeds a member's history is not used
+ *               have in common, whatever pages hold them (they are read through the table
+ *               row of the group's first request); what exceeds a member's history is not used
  * scale         finite and > 0
  * workspace     device scratch of at least mla_shared_workspace_size(...) bytes (of the
  *               current device; fp8 != 0 for mla_decode_shared_fp8), 256-byte aligned,

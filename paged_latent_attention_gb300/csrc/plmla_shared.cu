@@ -28,9 +28,9 @@
 // Warps: 0 loads K, 2 loads V (TMA, a ring of four 16 KB items each), 3 Q and K's rope block,
 // 1 issues the MMAs of the pair (in the even CTA), K a tile ahead of V, 4-11 softmax and
 // epilogue, a thread having a quarter of a row's 128 scores in registers.  The running maximum
-// lags: O is only rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries in two E4M3 parts
-// (as in the FP8 decode) and the probabilities in two as well, hi + lo, so that they carry 8
-// bits like bf16 ones; a part each takes the rate that bf16 would.
+// lags: O is only rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries
+// in two E4M3 parts (as in the FP8 decode) and the probabilities in two as well, hi + lo, so that
+// they carry 8 bits like bf16 ones; both parts together take the time that bf16 would.
 //
 // Measured: 64 requests x 64 heads over 32,768 shared and 300-4,000 own tokens, bf16: 200 us, the
 // decode kernel 188, 1.66 PFLOP/s (87% of a library product's burst, tensor pipe busy 79% of
@@ -55,7 +55,7 @@ namespace {
 constexpr int kShThreads = 384;
 constexpr int kShSlots = 4, kShSlot = 16384;    // of the K ring, and of the V ring
 constexpr int kShRows = 128;                    // query rows of a block
-constexpr int kStart = 5;                       // cost of a block's start, in tiles (3: 6% slower, 6: 1%)
+constexpr int kStart = 5;                       // a block's start, in tiles (3: 6% slower, 6: 1%)
 constexpr int kShPlanThreads = 1024;
 constexpr int kKept = 64;                       // log-sum-exps of a row that the merge keeps
 constexpr int kColS = 256;                      // TMEM column of the first score tile
@@ -678,11 +678,11 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                     ok = all_ok(ok);
                     continue;
                 }
-                // A history's last tiles.  Rows past the history hold stale data, those of drafts are
-                // not seen by all of its queries, and a weight of 0 times NaN is NaN.  The tile
-                // is loaded on a barrier of this CTA's own; before the MMAs hear of it, rows past the
-                // history become zeros, and so does what is not finite in a draft's row (the
-                // queries that see it have it in their scores).
+                // A history's last tiles.  Rows past the history hold stale data, those of
+                // drafts are not seen by all of its queries, and a weight of 0 times NaN is NaN.
+                // The tile is loaded on a barrier of this CTA's own; before the MMAs hear of it,
+                // rows past the history become zeros, and so does what is not finite in a
+                // draft's row (the queries that see it have it in their scores).
                 for (int i = 0; i < F::v_items; ++i)
                     ok &= wait_bounded(empty + 8 * (half + i), phase ^ 1, abort_flag, status, 2);
                 ok = all_ok(ok);
