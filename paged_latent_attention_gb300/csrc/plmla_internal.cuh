@@ -289,6 +289,14 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
     return r;
 }
 
+// The same as E5M2.
+__device__ __forceinline__ uint16_t e5m2x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Merge of chunk partials + sigmoid gate.  Row rw of request r (rw = j*H + h)
 // lives in group g = rw / group_rows at row rw % group_rows of the partials
 // of segments [g*stride + indptr[r], g*stride + indptr[r + 1]), where stride is

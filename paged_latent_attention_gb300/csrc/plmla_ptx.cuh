@@ -258,6 +258,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major,
            ((uint32_t)(M >> 4) << 24);
 }
 
+// The same with E5M2 A (the kind takes the types of A and B apart).
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N, bool a_mn_major,
+                                                       bool b_mn_major)
+{
+    return idesc_e4m3(M, N, a_mn_major, b_mn_major) | (1u << 7);
+}
+
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate)
 {

@@ -29,8 +29,13 @@
 // 1 issues the MMAs of the pair (in the even CTA), K a tile ahead of V, 4-11 softmax and
 // epilogue, a thread having a quarter of a row's 128 scores in registers.  The running maximum
 // lags: O is only rescaled when a score exceeds it by 2^8 (2^4 for E4M3).  E4M3 pages: queries
-// in two E4M3 parts (as in the FP8 decode) and the probabilities in two as well, hi + lo, so that
-// they carry 8 bits like bf16 ones; both parts together take the time that bf16 would.
+// in two E4M3 parts (as in the FP8 decode) and the probabilities in two as well, E4M3 and the
+// rest as E5M2 (the MMA takes the types of A and B apart); both parts together take the time that
+// bf16 would.  Together they carry 8 bits like bf16 ones down to 2^-6, and steps of 2^-14 and less
+// below, so there the reference follows the history down too: once a row's largest in a tile
+// falls 2^6 below it, O is scaled up.  A weight is off by 2^-8 of itself, or 2^-12 of the largest of its
+// tile.  (With one reference for the whole history, the tokens behind one that takes half of
+// the weight lost a third of theirs; 148.2 us there in the 4-draft case, 149 so.)
 //
 // Measured: 64 requests x 64 heads over 32,768 shared and 300-4,000 own tokens, bf16: 200 us, the
 // decode kernel 188, 1.66 PFLOP/s (87% of a library product's burst, tensor pipe busy 79% of
@@ -731,6 +736,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         const uint32_t el = elect_one();
         constexpr uint32_t id_s = idesc_for<F8>(128, 128, false, false);
         constexpr uint32_t id_o = idesc_for<F8>(128, 256, false, true);
+        constexpr uint32_t id_o_lo = F8 ? idesc_e5m2_e4m3(128, 256, false, true) : id_o;
         const uint64_t dq0 = sdesc(s_q, 16, 1024, kSw128);
         const uint64_t dq_rope = sdesc(s_q + F::q_part - F::rope_bytes, 16, F8 ? 512 : 1024,
                                        F8 ? kSw64 : kSw128);
@@ -822,7 +828,8 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                                                : dp0 + (i & 1) * 512 + 2 * kk;
                         const uint32_t acc =
                             (F8 ? (kk | p) != 0 : (kk | (i & 1)) != 0) ? 1u : carry;
-                        pair_mma<F8>(tmem + 128 * h, dp, dv + (F8 ? 256 : 128) * kk, id_o, acc, el);
+                        pair_mma<F8>(tmem + 128 * h, dp, dv + (F8 ? 256 : 128) * kk,
+                                     p == 0 ? id_o : id_o_lo, acc, el);
                     }
                 pair_commit(bar_of(m.bars.v_empty[0]) + 8 * (half + i), el);
             }
@@ -855,6 +862,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         const int group = (warp - 4) >> 2, tid = 32 * quad + lane + 128 * group;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         constexpr float kLag = F8 ? 4.f : 8.f, kUp = F8 ? 4.f : 0.f;
+        constexpr float kFall = 6.f, kMost = 40.f;            // (E4M3)
         constexpr int kChunks = F8 ? 2 : 4;     // 16-byte chunks of P (of each part)
         const uint32_t p_row = s_p + row * 128 + (F8 ? 0 : side * 8192);
         bool ok = true;
@@ -880,7 +888,8 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
             float f = a.scale_log2;
             if constexpr (F8)
                 f = real ? ldexpf(f * a.kv_scale, a.qexp[part.row0 + in_part]) : 1.f;
-            float high = -INFINITY, sum = 0.f;  // in units of log2; of this thread's tokens
+            // in units of log2, of all tokens; of this thread's tokens
+            float high = -INFINITY, top_most = -INFINITY, sum = 0.f;
             for (int t = walk.t0; t < walk.t1; ++t, ++g, ++exchange) {
                 const int buf = (int)(g & 1);
                 wait(m.bars.s_full[buf], (uint32_t)(g >> 1) & 1u, 11);
@@ -916,11 +925,14 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 float shrink = 1.f;
                 if (t == walk.t0) {
                     high = best;
-                } else if (best > high + kLag) {
-                    shrink = fast_exp2(high - best);          // 0 where nothing was seen before
-                    high = best;
+                } else if (best > high + kLag || (F8 && best < high - kFall && best > -INFINITY)) {
+                    // (kMost octaves below the largest a weight does not count any more)
+                    const float next = F8 ? fmaxf(best, top_most - kMost) : best;
+                    shrink = fast_exp2(high - next);          // 0 where nothing was seen before
+                    high = next;
                     sum *= shrink;
                 }
+                top_most = fmaxf(top_most, best);
                 const float ref = high == -INFINITY ? 0.f : high - kUp;
                 float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -933,16 +945,13 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
                 if constexpr (F8) {
 #pragma unroll
                     for (int w = 0; w < 8; ++w) {
-                        float h[4], l[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // hi: four significant bits, rounded; lo: the rest
-                            const float p = x[4 * w + e];
-                            h[e] = __uint_as_float((__float_as_uint(p) + 0x00080000u) & 0xFFF00000u);
-                            l[e] = p - h[e];
-                        }
-                        hi[w] = (uint32_t)e4m3x2(h[0], h[1]) | (uint32_t)e4m3x2(h[2], h[3]) << 16;
-                        lo[w] = (uint32_t)e4m3x2(l[0], l[1]) | (uint32_t)e4m3x2(l[2], l[3]) << 16;
+                        // hi: four significant bits, rounded; lo: the rest, in three
+                        const uint16_t h0 = e4m3x2(x[4 * w], x[4 * w + 1]);
+                        const uint16_t h1 = e4m3x2(x[4 * w + 2], x[4 * w + 3]);
+                        const float2 f0 = e4m3x2_to_float2(h0), f1 = e4m3x2_to_float2(h1);
+                        hi[w] = (uint32_t)h0 | (uint32_t)h1 << 16;
+                        lo[w] = (uint32_t)e5m2x2(x[4 * w] - f0.x, x[4 * w + 1] - f0.y) |
+                                (uint32_t)e5m2x2(x[4 * w + 2] - f1.x, x[4 * w + 3] - f1.y) << 16;
                     }
                 } else {
                     lo[0] = 0;
