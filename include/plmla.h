@@ -952,7 +952,8 @@ plmla_status mla_pages_free(const int32_t *page_table, int64_t page_table_ld,
  * may write them: rows in order take free pages (the lowest first) for columns
  * ceil(L / 1536) .. ceil((L + n) / 1536) - 1, and a row whose last page is partly filled
  * and held by others too takes one more, into which the page's rows (of every layer) are copied
- * first.  Of several rows that share such a page the last keeps it.
+ * first.  Of several rows that share such a page the last keeps it (where the earlier ones
+ * got theirs).
  *
  * slab_base, elem_bytes, page_stride_elems   the layers' pools as in mla_kv_compact
  * seq_lens     int32 [num_reqs]: the histories BEFORE the new tokens (num_reqs 1 .. 1024)
@@ -961,6 +962,11 @@ plmla_status mla_pages_free(const int32_t *page_table, int64_t page_table_ld,
  * workspace    device scratch of at least mla_pages_workspace_size(num_reqs) bytes, 256-byte
  *              aligned, contents irrelevant; calls that may run at once need one each
  * A row whose pages cannot be had (35) must not be appended to: its last page may be shared.
+ *
+ * mla_pages_reserve_ex also says which rows those are: granted, int32 [num_reqs] on the
+ * device (NULL: not wanted), becomes the number of new tokens that the row has room for: all
+ * of them, or 0 (32, 33, 35).  A row's history then grows by that.  It must not overlap the
+ * other arguments, but may be n_new_of.
  */
 size_t mla_pages_workspace_size(int32_t num_reqs);
 plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base, int32_t elem_bytes,
@@ -969,6 +975,13 @@ plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base, int32
                                const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
                                const int32_t *n_new_of, int32_t *ref_counts, void *workspace,
                                size_t workspace_bytes, int32_t *status, void *stream);
+plmla_status mla_pages_reserve_ex(int32_t num_layers, void *const *slab_base, int32_t elem_bytes,
+                                  int64_t num_pages, int64_t page_stride_elems,
+                                  int32_t *page_table, int64_t page_table_ld,
+                                  int64_t page_table_cols, const int32_t *seq_lens,
+                                  int32_t num_reqs, int32_t n_new, const int32_t *n_new_of,
+                                  int32_t *granted, int32_t *ref_counts, void *workspace,
+                                  size_t workspace_bytes, int32_t *status, void *stream);
 
 /*
  * mla_beam_select -- beam search's step: of the candidates

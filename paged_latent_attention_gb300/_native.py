@@ -94,6 +94,8 @@ SIGNATURES = {
     "mla_pages_workspace_size": (_sz, [_i32]),
     "mla_pages_reserve": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _i64, _p, _i32, _i32,
                                          _p, _p, _p, _sz, _p, _p]),
+    "mla_pages_reserve_ex": (ctypes.c_int, [_i32, _p, _i32, _i64, _i64, _p, _i64, _i64, _p, _i32,
+                                            _i32, _p, _p, _p, _p, _sz, _p, _p]),
     "mla_beam_workspace_size": (_sz, [_i32, _i32, _i32]),
     "mla_beam_select": (ctypes.c_int, [_p, _i64, _i32, _p, _p, _i32, _i32, _i32, _i32, _p, _p, _p,
                                        _p, _sz, _p]),

@@ -1118,8 +1118,8 @@ def mla_pages_free(page_table, seq_lens, ref_counts, *, status=None, stream=None
             _flag(status, dev))
 
 
-def mla_pages_reserve(slabs, page_table, seq_lens, n_new, ref_counts, *, workspace=None,
-                      status=None, stream=None):
+def mla_pages_reserve(slabs, page_table, seq_lens, n_new, ref_counts, *, granted=None,
+                      workspace=None, status=None, stream=None):
     """Room for ``n_new`` tokens (an int, or int32 [R]) behind every history, so that
     an append may write them: free pages, the lowest first, go into page_table's next
     columns, and a partly filled last page that other rows hold too is copied (in
@@ -1128,7 +1128,10 @@ def mla_pages_reserve(slabs, page_table, seq_lens, n_new, ref_counts, *, workspa
     the histories before the new tokens, and stays.  ``status``: optional CUDA int32
     tensor of one element, set to 32 (a negative length or count), 33 (a table too
     short, or a page outside the pool), 35 (no free page: this row and the later ones
-    that need pages are left as they are and must not be appended to) or 37.  The
+    that need pages are left as they are and must not be appended to) or 37.
+    ``granted`` (int32 [R], optional; may be n_new) is set to the new tokens that each row
+    has room for: all of them, or 0 for a row that status is about.  Add it to the lengths
+    instead of n_new.  The
     workspace (uint8, mla_pages_workspace_size; a new one by default) must not be shared by
     calls that may run at once.  Returns page_table.  Asynchronous."""
     if not isinstance(slabs, (list, tuple)) or not slabs:
@@ -1158,11 +1161,15 @@ def mla_pages_reserve(slabs, page_table, seq_lens, n_new, ref_counts, *, workspa
     counts, have = _counts(ref_counts, dev)
     if have != pages:
         _fail(f"ref_counts must have an entry for each of the pool's {pages} pages")
+    room = None
+    if granted is not None:
+        room = _vector(granted, "granted", dev, R)
+        _disjoint(seq_lens, granted, "granted must not overlap seq_lens")
     lib = _native.lib()
     if workspace is None:
         workspace = _empty(lib.mla_pages_workspace_size(R), _U8, first.device, stream)
-    _launch(dev, lib.mla_pages_reserve, "mla_pages_reserve", stream, layers, bases,
-            1 if fp8 else 2, pages, page_stride, *ids, lens, R, each, new, counts,
+    _launch(dev, lib.mla_pages_reserve_ex, "mla_pages_reserve", stream, layers, bases,
+            1 if fp8 else 2, pages, page_stride, *ids, lens, R, each, new, room, counts,
             *_scratch(workspace, dev), _flag(status, dev))
     return page_table
 

@@ -230,14 +230,14 @@ extern "C" size_t mla_pages_workspace_size(int32_t num_reqs)
     return kAlign + align_up(sizeof(int4) * (size_t)num_reqs);
 }
 
-extern "C" plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base,
-                                          int32_t elem_bytes, int64_t num_pages,
-                                          int64_t page_stride_elems, int32_t *page_table,
-                                          int64_t page_table_ld, int64_t page_table_cols,
-                                          const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
-                                          const int32_t *n_new_of, int32_t *ref_counts,
-                                          void *workspace, size_t workspace_bytes, int32_t *status,
-                                          void *stream)
+extern "C" plmla_status mla_pages_reserve_ex(int32_t num_layers, void *const *slab_base,
+                                             int32_t elem_bytes, int64_t num_pages,
+                                             int64_t page_stride_elems, int32_t *page_table,
+                                             int64_t page_table_ld, int64_t page_table_cols,
+                                             const int32_t *seq_lens, int32_t num_reqs,
+                                             int32_t n_new, const int32_t *n_new_of,
+                                             int32_t *granted, int32_t *ref_counts, void *workspace,
+                                             size_t workspace_bytes, int32_t *status, void *stream)
 {
     if (num_layers < 1 || num_layers > kMaxLayers || slab_base == nullptr ||
         (elem_bytes != 1 && elem_bytes != 2) ||
@@ -245,6 +245,7 @@ extern "C" plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_
         page_stride_elems % (elem_bytes == 1 ? 16 : 8) != 0 ||
         !table_ok(page_table, page_table_ld, page_table_cols, num_reqs) || !words_ok(seq_lens) ||
         (n_new_of == nullptr ? n_new < 0 : !aligned(n_new_of, 4)) ||
+        (granted != nullptr && (!aligned(granted, 4) || granted == seq_lens)) ||
         !counts_ok(ref_counts, num_pages, status) || workspace == nullptr ||
         !aligned(workspace, kAlign))
         return PLMLA_INVALID_ARGUMENT;
@@ -268,10 +269,26 @@ extern "C" plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_
     a.num_pages = num_pages;
     a.num_jobs = static_cast<int32_t *>(workspace);
     a.jobs = reinterpret_cast<int4 *>(static_cast<unsigned char *>(workspace) + kAlign);
+    a.granted = granted;
     a.status = status;
     return result(launch_reserve(a, num_layers, slab_base, elem_bytes == 1,
                                  page_stride_elems * elem_bytes, sms,
                                  static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" plmla_status mla_pages_reserve(int32_t num_layers, void *const *slab_base,
+                                          int32_t elem_bytes, int64_t num_pages,
+                                          int64_t page_stride_elems, int32_t *page_table,
+                                          int64_t page_table_ld, int64_t page_table_cols,
+                                          const int32_t *seq_lens, int32_t num_reqs, int32_t n_new,
+                                          const int32_t *n_new_of, int32_t *ref_counts,
+                                          void *workspace, size_t workspace_bytes, int32_t *status,
+                                          void *stream)
+{
+    return mla_pages_reserve_ex(num_layers, slab_base, elem_bytes, num_pages, page_stride_elems,
+                                page_table, page_table_ld, page_table_cols, seq_lens, num_reqs,
+                                n_new, n_new_of, nullptr, ref_counts, workspace, workspace_bytes,
+                                status, stream);
 }
 
 namespace {

@@ -259,6 +259,7 @@ struct ReserveArgs {
     int64_t num_pages;
     int4 *jobs;                         // workspace: [num_reqs] copies (from, to, rows)
     int32_t *num_jobs;                  // workspace: how many
+    int32_t *granted;                   // [num_reqs] new tokens that a row has room for, may be null
     int32_t *status;                    // may be null
 };
 cudaError_t launch_reserve(const ReserveArgs &a, int num_layers, void *const *slabs, bool fp8,

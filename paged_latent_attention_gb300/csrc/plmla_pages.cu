@@ -180,22 +180,23 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
     __shared__ int col_sm[kMaxReqs];            // column of the row's first page needed
     __shared__ int job_sm[kMaxReqs];            // the row's copy, or -1
     __shared__ int window[kReserveThreads];
-    __shared__ int granted;
+    __shared__ int placed, refused;             // pages given out; the first row without its pages
     asm volatile("griddepcontrol.launch_dependents;");
     const int r = threadIdx.x;
     // the first sweep's counts are on their way while the rows' needs are worked out
     uint32_t bits = free_bits(a.counts, 16 * r, a.num_pages);
-    int need = 0, part = 0, last = -1, holders = 0, col = 0;
-    bool parts = false;                         // the last page has other holders
+    int need = 0, part = 0, last = -1, holders = 0, col = 0, add = 0;
+    bool valid = false, parts = false;          // the last page has other holders
     if (r < a.num_reqs) {
         const int len = a.lens[r];
-        const int add = a.n_new_of != nullptr ? a.n_new_of[r] : a.n_new;
+        add = a.n_new_of != nullptr ? a.n_new_of[r] : a.n_new;
         const int64_t want = ((int64_t)len + add + kPageTokens - 1) / kPageTokens;
         if (len < 0 || add < 0) {
             report(a.status, kStatusAppendPosition);
         } else if (want > a.cols) {
             report(a.status, kStatusAppendPage);
         } else if (add > 0) {
+            valid = true;
             part = len % kPageTokens;
             col = pages_of(len);
             need = (int)want - col;
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
                 if (last < 0 || last >= a.num_pages) {
                     report(a.status, kStatusAppendPage);
                     need = 0;
+                    valid = false;
                 } else {
                     holders = a.counts[last];
                     parts = holders > 1;
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
         }
     }
     last_sm[r] = parts ? last : -1;
+    const bool shares = parts;
     if (__syncthreads_or(parts) && parts) {
         int earlier = 0;
         const int4 *rows = reinterpret_cast<const int4 *>(last_sm);
@@ -232,8 +235,10 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
     end_sm[r] = first + need;
     col_sm[r] = col - (parts ? 1 : 0);
     job_sm[r] = parts ? job : -1;
-    if (r == 0)
-        granted = 0;
+    if (r == 0) {
+        placed = 0;
+        refused = kReserveThreads;
+    }
     __syncthreads();
 
     // the free pages that there are, as far as they are needed
@@ -248,9 +253,9 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
     }
     const bool served = need > 0 && first + need <= found;
     if (need > 0 && !served)
-        report(a.status, kStatusNoPage);
+        atomicMin(&refused, r);
     if (served)
-        atomicMax(&granted, first + need);
+        atomicMax(&placed, first + need);
     if (parts && served) {
         a.jobs[job].x = last;
         a.jobs[job].z = part;
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
     const int copies = __syncthreads_count(parts && served);
     if (r == 0)
         *a.num_jobs = copies;                   // served rows come first
-    const int most = granted;
+    const int most = placed;
 
     // Page number q of them belongs to the row whose pages end past q.  The sweep's free pages
     // are listed a window at a time, and a thread places one: pages in a row often lie in few
@@ -300,6 +305,20 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
         }
         before += here;
     }
+
+    bool denied = need > 0 && !served;
+    if (r > refused && shares && need == 0) {
+        // the page was to be its own, but earlier holders had to stay: it would need one too
+        int left = holders;
+#pragma unroll 1
+        for (int j = 0; j < refused; ++j)
+            left -= last_sm[j] == last;
+        denied = left > 1;
+    }
+    if (denied)
+        report(a.status, kStatusNoPage);
+    if (a.granted != nullptr && r < a.num_reqs)
+        a.granted[r] = valid && !denied ? add : 0;
 }
 
 struct CopyArgs {
