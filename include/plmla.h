@@ -866,7 +866,9 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  *       its table (a source row counts as empty, a row that gives up pages gives up those it has)
  *   35  no free page (the row, and those after it that need pages, are left as they are)
  *   36  a parent >= num_rows (the out row becomes empty)
- *   37  a page that a row holds but whose count is 0 (the count stays 0)
+ *   37  a page that a row holds but whose count is 0 (giving it up leaves the count at 0; a row to
+ *       be appended to is left as it is, but its page is free to be taken).  Full pages of a row
+ *       are not looked at until it gives them up
  *   38  groups that are no partition of the requests
  *   2 .. 15  a wait inside the decode timed out (its outputs are not valid)
  *
@@ -965,7 +967,7 @@ plmla_status mla_pages_free(const int32_t *page_table, int64_t page_table_ld,
  *
  * mla_pages_reserve_ex also says which rows those are: granted, int32 [num_reqs] on the
  * device (NULL: not wanted), becomes the number of new tokens that the row has room for: all
- * of them, or 0 (32, 33, 35).  A row's history then grows by that.  It must not overlap the
+ * of them, or 0 (32, 33, 35, 37).  A row's history then grows by that.  It must not overlap the
  * other arguments, but may be n_new_of.
  */
 size_t mla_pages_workspace_size(int32_t num_reqs);

@@ -36,6 +36,9 @@ def pages_reserve(slabs, table, lens, n_new, counts):
     for r, (L, new) in enumerate(zip(lens, n_new)):
         L, new = int(L), int(new)
         have, want = -(-L // PAGE_TOKENS), -(-(L + new) // PAGE_TOKENS)
+        if new > 0 and L % PAGE_TOKENS != 0 and c[out[r, have - 1]] < 1:
+            served.append(False)            # a page that no one is counted to hold
+            continue
         shared = new > 0 and L % PAGE_TOKENS != 0 and c[out[r, have - 1]] > 1
         need = (want - have + (1 if shared else 0)) if new > 0 else 0
         if need > len(free):

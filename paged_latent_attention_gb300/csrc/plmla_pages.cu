@@ -209,8 +209,11 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const ReserveA
                 } else {
                     holders = a.counts[last];
                     parts = holders > 1;
-                    if (holders < 1)
+                    if (holders < 1) {          // it may go to another row
                         report(a.status, kStatusPageCount);
+                        need = 0;
+                        valid = false;
+                    }
                 }
             }
         }

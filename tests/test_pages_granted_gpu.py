@@ -104,3 +104,18 @@ def test_a_search_goes_on_without_the_rows_that_have_no_room():
             got = slab.view(pages, PT, ROW)[table[r].long()[t // PT], t % PT]
             assert torch.equal(got[:, 0].float().cpu(), torch.tensor(h)) and bool((got == got[:, :1]).all())
     assert int(status.item()) == 35 and lens.tolist() == [PT, PT - 2, PT - 2, 14]
+
+
+def test_a_row_on_a_page_without_holders_is_left_alone():
+    """Its page looks free, and may go to another row."""
+    slab = _slab(4)
+    for table, lens, new, counts in (
+            ([[0, 9], [1, 9]], [7, PT], [1, 1], [0, 1, 1, 1]),
+            ([[2, 9], [1, 9]], [PT - 1, 8], [PT, 1], [1, 1, 0, 0]),
+            ([[3, 9], [3, 9], [0, 9]], [5, 6, 7], [1, 1, 1], [2, 1, 0, 0])):
+        t, c, st, got = _ints(table), _ints(counts), _ints([0]), _ints([0] * len(lens))
+        _, want, left, served = oracle.pages_reserve([], table, lens, new, counts)
+        api.mla_pages_reserve([slab], t, _ints(lens), _ints(new), c, status=st, granted=got)
+        assert int(st.item()) == 37 and not served[0]
+        assert got.tolist() == [n if ok else 0 for n, ok in zip(new, served)]
+        assert np.array_equal(t.cpu().numpy(), want) and np.array_equal(c.cpu().numpy(), left)
