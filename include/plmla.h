@@ -860,8 +860,10 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  * at once: they belong on one stream, or ordered by events.  Results depend on
  * the arguments alone.
  *
- * status, in these calls, is an optional device int32 as in mla_kv_append:
- *   32  a negative length or number of new tokens (the row is left as it is)
+ * status, in these calls, is an optional device int32 as in mla_kv_append (of several codes
+ * of a call on pages the largest stays):
+ *   32  a negative length or number of new tokens (the row, in a fork the out row, is left as
+ *       it is; a decode takes it as 0 without a report)
  *   33  a page outside the pool (it is not counted), or a history longer than a row of
  *       its table (a source row counts as empty, a row that gives up pages gives up those it has)
  *   35  no free page (the row, and those after it that need pages, are left as they are)

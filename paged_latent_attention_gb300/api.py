@@ -1082,8 +1082,8 @@ def mla_pages_fork(page_table, seq_lens, parents, ref_counts, out_table, out_len
     the rows that hold each page (0: free).  out_lens int32 [N] must hold the out
     rows' lengths on entry, 0 where they hold nothing (zeros, at first).  No cache
     row moves: mla_pages_reserve copies the partly filled page before the histories
-    grow apart.  ``status``: optional CUDA int32 tensor of one element, set to 33
-    (a page outside the pool, or a table too short), 36 (a parent that is no row) or 37 (a
+    grow apart.  ``status``: optional CUDA int32 tensor of one element, set to 32 (a
+    negative length: the out row is left as it is), 33 (a page outside the pool, or a table too short), 36 (a parent that is no row) or 37 (a
     held page whose count is 0).  Returns (out_table, out_lens).  Asynchronous; calls
     on one pool belong on one stream."""
     dev = page_table.get_device()
@@ -1106,7 +1106,7 @@ def mla_pages_fork(page_table, seq_lens, parents, ref_counts, out_table, out_len
 
 def mla_pages_free(page_table, seq_lens, ref_counts, *, status=None, stream=None):
     """Every row of page_table [R, columns] gives up its pages: their ref_counts go
-    down by one and seq_lens becomes 0.  ``status`` as in mla_pages_fork (33, 37).
+    down by one and seq_lens becomes 0.  ``status`` as in mla_pages_fork (32, 33, 37).
     Asynchronous."""
     dev = page_table.get_device()
     if dev < 0 or seq_lens.dim() != 1:

@@ -35,10 +35,11 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;                    // 16-byte vectors of a thread in flight
 constexpr int kCopyPiece = kCopyThreads * kCopyVecs;
 
+// (of several codes the largest stays, whichever row comes first)
 __device__ __forceinline__ void report(int32_t *status, int32_t code)
 {
     if (status != nullptr)
-        atomicExch(status, code);
+        atomicMax(status, code);
 }
 
 __device__ __forceinline__ void hold(int32_t *counts, int64_t num_pages, int page, int32_t *status)
@@ -68,16 +69,21 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a)
 {
     const int i = blockIdx.x;
     int32_t *out = a.out_table + (int64_t)i * a.out_ld;
-    const int parent = a.parents[i];
-    int old = pages_of(a.out_lens[i]), len = 0;
+    const int parent = a.parents[i], held = a.out_lens[i];
+    int old = pages_of(held), len = 0;
+    if (parent >= 0 && parent < a.rows)
+        len = a.lens[parent];
+    if (held < 0 || len < 0) {
+        if (threadIdx.x == 0)
+            report(a.status, kStatusAppendPosition);
+        return;
+    }
     if (old > a.out_cols) {
         old = (int)a.out_cols;
         if (threadIdx.x == 0)
             report(a.status, kStatusAppendPage);
     }
-    if (parent >= 0 && parent < a.rows)
-        len = max(0, a.lens[parent]);
-    else if (parent >= a.rows && threadIdx.x == 0)
+    if (parent >= a.rows && threadIdx.x == 0)
         report(a.status, kStatusParent);
     int pages = pages_of(len);
     if (pages > a.cols || pages > a.out_cols) {
@@ -107,7 +113,13 @@ free_kernel(const int32_t *table, int64_t ld, int64_t cols, int32_t *lens, int32
             int64_t num_pages, int32_t *status)
 {
     const int r = blockIdx.x;
-    int pages = pages_of(lens[r]);
+    const int len = lens[r];
+    int pages = pages_of(len);
+    if (len < 0) {
+        if (threadIdx.x == 0)
+            report(status, kStatusAppendPosition);
+        return;
+    }
     if (pages > cols) {
         pages = (int)cols;
         if (threadIdx.x == 0)
