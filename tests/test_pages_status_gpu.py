@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from paged_latent_attention_gb300 import api
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,47 @@ def test_of_several_codes_the_largest_stays():
         st, n = _ints([0]), _ints(np.where(np.arange(rows) % 2 == 0, -1, 3 * PT))
         api.mla_pages_free(_ints(table), n, _ints([2 * rows]), status=st)
         assert int(st.item()) == 33
+
+
+@pytest.mark.parametrize("rows", [2, 8, 10, 64, 66, 1000])
+def test_counts_of_an_under_counted_fork_do_not_depend_on_the_order_of_rows(rows):
+    """A count becomes what was counted, plus what is taken, less what is given up, or 0."""
+    rng = np.random.default_rng(rows)
+    table, out = rng.permutation(rows)[:, None], rng.permutation(rows)[:, None]
+    parents = rng.permutation(rows)
+    half = rows // 2
+    twice = np.concatenate([np.arange(half), np.arange(half)])[:, None]
+    to = np.where(np.arange(rows) < half, np.arange(rows), -1)
+    for have in (0, 1, 2):
+        for _ in range(10):
+            # each page loses a holder and gains one
+            status, o, n, c = _fork(table, [1] * rows, parents, [have] * rows, out, [1] * rows)
+            assert c == [have] * rows and status == 0
+            assert o == table[parents].tolist() and n == [1] * rows
+            # each page loses two and gains one
+            status, _, _, c = _fork(np.roll(np.arange(half), 1)[:, None], [1] * half, to, [have] * half,
+                                    twice, [1] * rows)
+            assert c == [max(0, have - 1)] * half and status == (0 if have else 37)
+
+
+@pytest.mark.parametrize("rows", [3, 8, 9, 57, 64, 65])
+def test_forks_around_the_sizes_of_a_cluster(rows):
+    """Rows of more columns than threads, some left as they are, some emptied."""
+    rng = np.random.default_rng(rows)
+    cols, pages = 300, 400_000
+    table = rng.permutation(pages)[:rows * cols].reshape(rows, cols)
+    lens = rng.integers(0, cols * PT + 1, rows)
+    parents = rng.integers(-1, rows, rows)
+    counts = np.zeros(pages, np.int64)
+    out, n = np.full((rows, cols), 7), np.zeros(rows, np.int64)
+    for r in range(rows):
+        counts[table[r, :-(-lens[r] // PT)]] += 1
+    d = [_ints(x) for x in (table, lens, counts, out, n)]
+    st = _ints([0])
+    for _ in range(3):
+        out, n, counts = oracle.pages_fork(table, lens, parents, counts, out, n)
+        api.mla_pages_fork(d[0], d[1], _ints(parents), d[2], d[3], d[4], status=st)
+        for got, want in zip(d[2:], (counts, out, n)):
+            assert np.array_equal(got.cpu().numpy(), want)
+        parents = rng.integers(-1, rows, rows)
+    assert int(st.item()) == 0
