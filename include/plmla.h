@@ -879,7 +879,8 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  * members.  Same results as mla_decode, up to rounding.
  *
  * q_nope_absorbed, q_rope, gate, slab_base, page strides, seq_lens, n_q_per_req, out, lse
- *               as in mla_decode; num_reqs 1 .. 1024, num_heads 1 .. 128 (any)
+ *               as in mla_decode; num_reqs 1 .. 1024, num_heads 1 .. 128 (any).  out may be
+ *               gate, and else does not overlap it; lse overlaps neither
  * page_table    page_table_cols (1 .. page_table_ld) columns a row; a history past them is cut
  *               off there (status 33), an ID outside the pool reads another page (33)
  * group_starts  int32 [num_groups + 1], device: group g is requests group_starts[g] ..
@@ -1002,8 +1003,8 @@ plmla_status mla_pages_reserve_ex(int32_t num_layers, void *const *slab_base, in
  * tokens       int32 [batch * beams]: v
  * parents      int32 [batch * beams]: the row b * beams + k it goes on from (as
  *              mla_pages_fork takes it)
- * out_scores   fp32 [batch * beams]: the candidates; the outputs must not overlap scores or one
- *              another
+ * out_scores   fp32 [batch * beams]: the candidates; the outputs must not overlap scores, ended
+ *              or one another
  * workspace    device scratch of at least mla_beam_workspace_size(...) bytes, 256-byte
  *              aligned, contents irrelevant; calls that may run at once need one each
  * Log-sum-exps and candidates are held in pairs of floats, so the order is that of the

@@ -51,6 +51,30 @@ bool counts_ok(const int32_t *counts, int64_t num_pages, const int32_t *status)
            (status == nullptr || aligned(status, 4));
 }
 
+// Whether two ranges of bytes share none.
+bool apart(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a == nullptr || b == nullptr || x + na <= y || y + nb <= x;
+}
+
+// Whether two tables share no entry: their ranges do not meet, or their rows lie in different
+// columns of one grid (of the shorter stride, of which the other is a multiple).
+bool tables_apart(const int32_t *a, int64_t lda, int64_t na, int32_t rows_a, const int32_t *b,
+                  int64_t ldb, int64_t nb, int32_t rows_b)
+{
+    if (apart(a, 4 * (size_t)((rows_a - 1) * lda + na), b, 4 * (size_t)((rows_b - 1) * ldb + nb)))
+        return true;
+    const int64_t step = rows_a == 1 ? (rows_b == 1 ? 0 : ldb)
+                         : rows_b == 1 || lda < ldb ? lda : ldb;
+    if (step == 0 || (rows_a > 1 && lda % step != 0) || (rows_b > 1 && ldb % step != 0))
+        return false;
+    int64_t off = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 4 % step;
+    if (off < 0)
+        off += step;
+    return na <= off && off <= step - nb;
+}
+
 plmla_status result(cudaError_t err) { return err == cudaSuccess ? PLMLA_OK : PLMLA_CUDA_ERROR; }
 
 }  // namespace
@@ -111,6 +135,12 @@ plmla_status shared_impl(const void *q_nope_absorbed, const void *q_rope, const 
     if (!words_ok(seq_lens) || !words_ok(group_starts) || !words_ok(shared_lens) ||
         (lse != nullptr && !aligned(lse, 4)) || (status != nullptr && !aligned(status, 4)) ||
         workspace == nullptr || !aligned(workspace, kAlign))
+        return PLMLA_INVALID_ARGUMENT;
+    // a block of the merge reads its part of the gate before it writes the same part of out
+    const size_t all_rows = (size_t)num_reqs * n_q_per_req * num_heads;
+    if ((out != gate && !apart(out, 2 * kLatent * all_rows, gate, 2 * kLatent * all_rows)) ||
+        !apart(lse, 4 * all_rows, out, 2 * kLatent * all_rows) ||
+        !apart(lse, 4 * all_rows, gate, 2 * kLatent * all_rows))
         return PLMLA_INVALID_ARGUMENT;
     const int sms = device_sms();
     if (sms < 2)
@@ -203,7 +233,9 @@ extern "C" plmla_status mla_pages_fork(const int32_t *page_table, int64_t page_t
     if (!table_ok(page_table, page_table_ld, page_table_cols, num_rows) ||
         !table_ok(out_table, out_table_ld, out_table_cols, out_rows) || !words_ok(seq_lens) ||
         !words_ok(parents) || !words_ok(out_lens) || !counts_ok(ref_counts, num_pages, status) ||
-        out_table == page_table || out_lens == seq_lens)
+        !tables_apart(page_table, page_table_ld, page_table_cols, num_rows, out_table, out_table_ld,
+                      out_table_cols, out_rows) ||
+        !apart(seq_lens, 4 * (size_t)num_rows, out_lens, 4 * (size_t)out_rows))
         return PLMLA_INVALID_ARGUMENT;
     const ForkArgs a = {page_table, page_table_ld, page_table_cols, seq_lens, num_rows,
                         parents,    out_rows,      out_table,       out_table_ld, out_table_cols,
@@ -245,7 +277,10 @@ extern "C" plmla_status mla_pages_reserve_ex(int32_t num_layers, void *const *sl
         page_stride_elems % (elem_bytes == 1 ? 16 : 8) != 0 ||
         !table_ok(page_table, page_table_ld, page_table_cols, num_reqs) || !words_ok(seq_lens) ||
         (n_new_of == nullptr ? n_new < 0 : !aligned(n_new_of, 4)) ||
-        (granted != nullptr && (!aligned(granted, 4) || granted == seq_lens)) ||
+        (granted != nullptr &&
+         (!aligned(granted, 4) || !apart(granted, 4 * (size_t)num_reqs, seq_lens, 4 * (size_t)num_reqs) ||
+          (granted != n_new_of &&
+           !apart(granted, 4 * (size_t)num_reqs, n_new_of, 4 * (size_t)num_reqs)))) ||
         !counts_ok(ref_counts, num_pages, status) || workspace == nullptr ||
         !aligned(workspace, kAlign))
         return PLMLA_INVALID_ARGUMENT;
@@ -318,11 +353,14 @@ extern "C" plmla_status mla_beam_select(const void *logits, int64_t logits_ld, i
         logits == nullptr || !aligned(logits, dtype == PLMLA_FP32 ? 4 : 2) || scores == nullptr ||
         !aligned(scores, 4) || (ended != nullptr && (end_token < 0 || end_token >= vocab)) ||
         !words_ok(tokens) || !words_ok(parents) || out_scores == nullptr ||
-        !aligned(out_scores, 4) || out_scores == scores || tokens == parents ||
-        static_cast<void *>(out_scores) == tokens || static_cast<void *>(out_scores) == parents ||
-        workspace == nullptr ||
-        !aligned(workspace, kAlign))
+        !aligned(out_scores, 4) || workspace == nullptr || !aligned(workspace, kAlign))
         return PLMLA_INVALID_ARGUMENT;
+    const size_t words = 4 * (size_t)batch * beams;
+    const void *outs[] = {tokens, parents, out_scores};
+    for (int i = 0; i < 3; ++i)
+        if (!apart(outs[i], words, outs[(i + 1) % 3], words) || !apart(outs[i], words, scores, words) ||
+            !apart(outs[i], words, ended, words / 4))
+            return PLMLA_INVALID_ARGUMENT;
     if (workspace_bytes < beam_workspace(batch, beams, vocab))
         return PLMLA_WORKSPACE_TOO_SMALL;
     const BeamArgs a = {logits, logits_ld, dtype, scores, ended, end_token, batch,
