@@ -10,6 +10,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native
 
@@ -965,6 +966,15 @@ def _counts(ref_counts, dev):
     return ref_counts.data_ptr(), ref_counts.shape[0]
 
 
+def _no_derivatives(where, *tensors):
+    """Refuses tensors that autograd follows, backward or forward: the call would lose it."""
+    if (torch.is_grad_enabled() and any(t.requires_grad for t in tensors)) or (
+            forward_ad._current_level >= 0
+            and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)):
+        _fail(f"{where} is not recorded by autograd: call it under torch.no_grad() or on "
+              "detached tensors without tangents")
+
+
 def _disjoint(a, b, message):
     """Refuses two contiguous vectors that share bytes."""
     a0, b0 = a.data_ptr(), b.data_ptr()
@@ -1025,10 +1035,7 @@ def mla_decode_shared_fp8(q_nope_absorbed, q_rope, gate, slab, page_table, seq_l
 
 def _shared(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens, group_starts, shared_lens,
             n_q, scale, kv_scale, out, lse, workspace, status, stream, with_lse):
-    if torch.is_grad_enabled() and (q_nope_absorbed.requires_grad or q_rope.requires_grad
-                                    or gate.requires_grad or slab.requires_grad):
-        _fail("mla_decode_shared is not recorded by autograd: call it under torch.no_grad() or on "
-              "detached tensors")
+    _no_derivatives("mla_decode_shared", q_nope_absorbed, q_rope, gate, slab)
     fp8 = kv_scale is not None
     base, pages, page_stride = _pool(slab, fp8)
     dev, n_q = slab.get_device(), int(n_q)
@@ -1192,16 +1199,14 @@ def mla_beam_select(logits, scores, *, ended=None, end_token=-1, tokens=None, pa
     them (parents.view(-1)).  ``ended`` bool [B, K] marks beams that offer
     ``end_token`` alone, at their score; a beam whose score is -inf, or whose logits
     hold NaN, offers nothing.  K is at most 64.  Tensors that require grad are
-    refused while gradients are recorded.  The workspace comes from
+    refused while gradients are recorded, as are those with tangents.  The workspace comes from
     allocate_beam_workspace (a new one by default); calls that may run at once need
     one each.  Asynchronous."""
+    _no_derivatives("mla_beam_select", logits, scores)
     kind = _ROPE_TYPES.get(logits.dtype)
     dev = logits.get_device()
     if kind is None or dev < 0 or logits.dim() != 2 or scores.dim() != 2:
         _fail("logits must be a CUDA bf16, fp16 or fp32 tensor [B*K, vocab], scores [B, K]")
-    if torch.is_grad_enabled() and (logits.requires_grad or scores.requires_grad):
-        _fail("mla_beam_select is not recorded by autograd: call it under torch.no_grad() or on "
-              "detached tensors")
     B, K = scores.shape
     shape = (B, K)
     rows = _rows(logits, "logits", dev, logits.dtype, B * K)
