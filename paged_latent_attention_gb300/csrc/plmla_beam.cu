@@ -288,7 +288,7 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
     const int skip = (int)(reinterpret_cast<uintptr_t>(head) % 16 / sizeof(T));
     // (a last slice that no token reaches is empty)
     const int v0 = (int)min((int64_t)blockIdx.x * kSlice - skip, (int64_t)vocab);
-    const int left = vocab - v0, lo = max(0, -v0);
+    const int left = (int)min((int64_t)vocab - v0, (int64_t)kSlice), lo = max(0, -v0);
     const T *src = head + v0;
     auto in_row = [&](int id) { return id >= lo && id < left; };
     uint32_t raw[G][4];
