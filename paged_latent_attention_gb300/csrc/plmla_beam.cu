@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kSliceThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kCentre = 8.f, kFixed = 0x1p36f, kUnfixed = 0x1p-44f;   // of a slice's terms
 
 // A 32-bit key in the order of the floats (-0 as 0, so that equal logits tie).
 __device__ __forceinline__ uint32_t key_of(float x)
@@ -133,11 +134,47 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
+{
+    return fma2(b, pack2(-1.f, -1.f), a);
+}
+
+// What the sum of a and b lost (as in two_sum).
+__device__ __forceinline__ uint64_t lost2(uint64_t a, uint64_t b, uint64_t sum)
+{
+    const uint64_t t = sub2(sum, a);
+    return add2(sub2(a, sub2(sum, t)), sub2(b, t));
+}
+
+// A number as the unevaluated sum of two floats, hi = hi + lo rounded (error-free transforms:
+// Dekker, 1971; Knuth, The Art of Computer Programming 2, 4.2.2).  48 bits are plenty here,
+// and this device's 64-bit unit is so slow that with it the merge took 25 us.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair add(Pair a, float b)
+{
+    const Pair s = two_sum(a.hi, b);
+    const float lo = __fadd_rn(s.lo, a.lo), hi = __fadd_rn(s.hi, lo);
+    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b)
+{
+    const Pair s = two_sum(a.hi, b.hi);
+    const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
+    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
 }
 
 struct SliceOut {
@@ -157,7 +194,7 @@ struct SliceShared {
     static constexpr int kFew = 512;            // a list that is ranked by counting
     uint64_t list[kFew];
     uint32_t tops[kSliceThreads];
-    float warp_sum[kSliceThreads / 32];
+    long long warp_sum[kSliceThreads / 32];
     uint32_t warp_high[kSliceThreads / 32], warp_least[kSliceThreads / 32];
     int warp_i[kSliceThreads / 32];
     uint32_t bound;
@@ -399,38 +436,68 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
             }
         }
     }
+    // Sum of exponentials of d = x - high, each 2^kCentre times itself: the argument d log2 e + kCentre
+    // is then near 0, where its rounding is small, for the terms that a large vocabulary is
+    // made of (d = -11: half a step of 2^-22 instead of 2^-20, which many equal logits, all
+    // rounded alike, would carry into the sum).  Added as a tree for the same reason; across threads
+    // in fixed point, without a rounding.
     const float high = value_of(high_key), ref = high == -INFINITY ? 0.f : high;
-    float sum;
+    float own;
     {
         const uint64_t shift = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
-        uint64_t acc[2] = {0, 0};               // two pairs of zeros
+        const uint64_t centre = pack2(kCentre, kCentre);
+        uint64_t sums[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int g = 0; g < G; ++g) {
+            uint64_t e[4];
 #pragma unroll
-            for (int w = 0; w < 4; w += 2 / W::n) {
-                const float a = W::get(raw[g][w], 0);
-                const float b = W::n == 2 ? W::get(raw[g][w], 1) : W::get(raw[g][w + 1], 0);
+            for (int w = 0; w < 2 * W::n; ++w) {
+                const uint64_t v = W::n == 2 ? pack2(W::get(raw[g][w], 0), W::get(raw[g][w], 1))
+                                             : pack2(W::get(raw[g][2 * w % 4], 0),
+                                                     W::get(raw[g][(2 * w + 1) % 4], 0));
+                const uint64_t d = add2(v, shift);
+                uint64_t p = fma2(d, scale, centre);
                 float x, y;
-                unpack2(mul2(add2(pack2(a, b), shift), scale), x, y);
-                acc[g & 1] = add2(acc[g & 1], pack2(fast_exp2(x), fast_exp2(y)));
+                if constexpr (W::n == 1) {
+                    // what d lost (16-bit logits differ exactly, but for those next to 0); it is not a
+                    // number where d is -inf
+                    unpack2(lost2(v, shift, d), x, y);
+                    p = fma2(pack2(fminf(x, 0x1p-18f), fminf(y, 0x1p-18f)), scale, p);
+                }
+                unpack2(p, x, y);
+                e[w] = pack2(fast_exp2(x), fast_exp2(y));
             }
-        float x, y;
-        unpack2(add2(acc[0], acc[1]), x, y);
-        sum = x + y;
-    }
+            sums[g] = add2(e[0], e[1]);
+            if constexpr (W::n == 2)
+                sums[g] = add2(sums[g], add2(e[2], e[3]));
+        }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        for (int w = 1; w < G; w *= 2)
+#pragma unroll
+            for (int g = 0; g < G; g += 2 * w)
+                sums[g] = add2(sums[g], sums[g + w]);
+        float x, y;
+        unpack2(sums[0], x, y);
+        own = x + y;
+    }
+    // (a thread's sum is 2^14 at most: 23 bits above the lower 27)
+    const unsigned long long fixed = __float2ull_rn(own * kFixed);
+    const uint32_t sum_lo = __reduce_add_sync(0xffffffffu, (uint32_t)fixed & 0x7FFFFFFu);
+    const uint32_t sum_hi = __reduce_add_sync(0xffffffffu, (uint32_t)(fixed >> 27));
+    const bool nan = __any_sync(0xffffffffu, own != own);
     if (lane == 0)
-        s.warp_sum[warp] = sum;
+        s.warp_sum[warp] = nan ? -1 : ((long long)sum_hi << 27) + sum_lo;
     __syncthreads();
     if (t == 0) {
-        float all = 0.f;
+        bool bad = false;
+        long long sum = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            all += s.warp_sum[w];
+        for (int w = 0; w < kWarps; ++w) {
+            sum += s.warp_sum[w];
+            bad |= s.warp_sum[w] < 0;
+        }
         o.high[at] = high;
-        o.sum[at] = all;
+        o.sum[at] = bad ? NAN : __ll2float_rn(sum) * kUnfixed;
     }
     int n = s.count;
     if (n > SliceShared::kFew)
@@ -497,37 +564,18 @@ __device__ __forceinline__ void join(A (&list)[P], const A (&other)[P])
         }
 }
 
-// A number as the unevaluated sum of two floats, hi = hi + lo rounded (error-free transforms:
-// Dekker, 1971; Knuth, The Art of Computer Programming 2, 4.2.2).  48 bits are plenty here,
-// and this device's 64-bit unit is so slow that with it the merge took 25 us.
-struct Pair {
-    float hi, lo;
-};
-__device__ __forceinline__ Pair two_sum(float a, float b)
+__device__ __forceinline__ Pair product(float a, float b)
 {
-    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
-}
-__device__ __forceinline__ Pair add(Pair a, float b)
-{
-    const Pair s = two_sum(a.hi, b);
-    const float lo = __fadd_rn(s.lo, a.lo), hi = __fadd_rn(s.hi, lo);
-    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
-}
-
-__device__ __forceinline__ Pair add(Pair a, Pair b)
-{
-    const Pair s = two_sum(a.hi, b.hi);
-    const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
-    return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+    const float hi = __fmul_rn(a, b);
+    return {hi, fmaf(a, b, -hi)};
 }
 
 // ln s of a positive sum: s = 2^e m with m around 1; ln 2 in a part whose products with e are
 // exact and a rest.  Off by some 2^-25.
 __device__ __forceinline__ Pair ln(float s)
 {
-    constexpr double kLn2 = 0.69314718055994530942;
-    constexpr float kLn2Hi = 2839.f / 4096.f, kLn2Lo = (float)(kLn2 - 2839.0 / 4096.0);
+    constexpr float kLn2Hi = 2839.f / 4096.f;
+    constexpr float kLn2Lo = (float)(0.69314718055994530942 - 2839.0 / 4096.0);
     int e;
     float m = frexpf(s, &e);                    // [1/2, 1)
     if (m < 0.70710678f) {
@@ -588,8 +636,10 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
             for (int s = lane; s < o.slices; s += 32) {
                 const float h = o.high[row * o.slices + s];
                 // (a NaN among the logits is in the sum, not in the maximum)
+                const Pair d = two_sum(h, -high);
                 const float e = h == high ? 1.f : expf(h - high);
-                sum = add(sum, e * o.sum[row * o.slices + s]);
+                const float more = h == high || e == 0.f ? 0.f : d.lo;
+                sum = add(sum, product(fmaf(e, more, e), o.sum[row * o.slices + s]));
             }
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) {
