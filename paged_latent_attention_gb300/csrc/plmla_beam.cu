@@ -177,6 +177,8 @@ __device__ __forceinline__ Pair add(Pair a, Pair b)
     return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
 }
 
+constexpr float kSameSum = 3e-6f;               // what two logarithms of the same sum may differ by
+
 struct SliceOut {
     float *high, *sum;                  // [rows, slices]
     uint64_t *lists;                    // [rows, slices, beams] entries, descending
@@ -601,6 +603,8 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
     constexpr int kWarps = WARPS, kList = 32 * P;
     __shared__ unsigned long long keys[kWarps * kList / 2];
     __shared__ int ids[kWarps * kList / 2];
+    __shared__ Pair logs[kMaxBeams];            // of the rows' sums
+    __shared__ float tops[kMaxBeams];           // their largest logits; NaN: no candidates
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
     const int K = a.beams, per_row = K >= kWarps ? 1 : kWarps / K;
     const int part = warp % per_row;
@@ -610,29 +614,27 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
     for (int p = 0; p < P; ++p)
         best[p] = none;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int k = warp / per_row; k < K; k += kWarps / per_row) {
-        const int64_t row = (int64_t)b * K + k;
-        // this warp's first list of the row is on its way while the sum is taken
-        uint64_t next[P];
-        auto fetch = [&](int s) {
+    uint64_t next[P];
+    auto fetch = [&](int64_t row, int s) {
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int i = kList - 1 - (32 * p + lane);          // ascending for join
-                next[p] = s < o.slices && i < K ? o.lists[(row * o.slices + s) * K + i] : 0;
-            }
-        };
-        fetch(part);
-        const float score = a.scores[row];
-        const bool ended = a.ended != nullptr && a.ended[row] != 0;
-        Pair shift = {score, 0.f};
-        if (!ended) {
-            float high = -INFINITY;
+        for (int p = 0; p < P; ++p) {
+            const int i = kList - 1 - (32 * p + lane);        // ascending for join
+            next[p] = s < o.slices && i < K ? o.lists[(row * o.slices + s) * K + i] : 0;
+        }
+    };
+    // this warp's first list is on its way while the sums are taken, a warp a row
+    if (warp / per_row < K)
+        fetch((int64_t)b * K + warp / per_row, part);
+    for (int k = warp; k < K; k += kWarps) {
+        const int64_t row = (int64_t)b * K + k;
+        float high = -INFINITY;
+        Pair sum = {0.f, 0.f};
+        if (a.ended == nullptr || a.ended[row] == 0) {
             for (int s = lane; s < o.slices; s += 32)
                 high = fmaxf(high, o.high[row * o.slices + s]);
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1)
                 high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, w));
-            Pair sum = {0.f, 0.f};
             for (int s = lane; s < o.slices; s += 32) {
                 const float h = o.high[row * o.slices + s];
                 // (a NaN among the logits is in the sum, not in the maximum)
@@ -647,12 +649,37 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
                 const float lo = __shfl_xor_sync(0xffffffffu, sum.lo, w);
                 sum = add(sum, Pair{hi, lo});                 // the same in both lanes
             }
-            const float s = sum.hi;
-            const Pair l = ln(s);
-            shift = add(add(two_sum(score, -high), -l.hi), -(l.lo + sum.lo / s));
-            if (!isfinite(s) || s <= 0.f)
-                shift.hi = -INFINITY;
         }
+        if (lane == 0) {
+            const Pair l = ln(sum.hi);
+            logs[k] = {l.hi, l.lo + sum.lo / sum.hi};
+            tops[k] = isfinite(sum.hi) && sum.hi > 0.f ? high : NAN;
+        }
+    }
+    __syncthreads();
+    for (int k = warp / per_row; k < K; k += kWarps / per_row) {
+        const int64_t row = (int64_t)b * K + k;
+        if (k >= kWarps / per_row)
+            fetch(row, part);
+        const float score = a.scores[row], high = tops[k];
+        const bool ended = a.ended != nullptr && a.ended[row] != 0;
+        // Rows with the same logits have to have the same sum, so that ties stay ties, but what is
+        // added first depends on where they start within 16 bytes: the first one's is taken.
+        Pair l = logs[k];
+        int same = K;
+#pragma unroll
+        for (int j0 = 0; j0 < 32 * P; j0 += 32) {
+            const int j = min(j0 + lane, k);
+            const bool alike = tops[j] == high &&
+                               fabsf((logs[j].hi - l.hi) + (logs[j].lo - l.lo)) <= kSameSum;
+            const uint32_t found = __ballot_sync(0xffffffffu, alike);
+            if (same == K && found != 0)
+                same = min(j0 + __ffs(found) - 1, k);
+        }
+        l = logs[min(same, k)];
+        Pair shift = add(add(two_sum(score, -high), -l.hi), -l.lo);
+        if (!isfinite(high))
+            shift.hi = -INFINITY;
         Candidate mine[P];
         if (!isfinite(shift.hi) || ended) {
             // its first tokens in order, at -inf; an ended beam's end token before them
@@ -677,7 +704,7 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     now[p] = next[p];
-                fetch(s + per_row);
+                fetch(row, s + per_row);
                 join<P>(list, now);
             }
             // as candidates, in ascending order: entry i comes from kList - 1 - i
