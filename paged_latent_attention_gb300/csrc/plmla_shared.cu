@@ -1047,11 +1047,14 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
 // merge
 // ---------------------------------------------------------------------------
 
-// The sigmoid, within 2^-21 of itself; the merge of many rows is bound by instructions, which
-// the exact division and exponential were half of.
+// The sigmoid times 2^8; the merge of many rows is bound by instructions, which the exact
+// division and exponential were half of.  Within 2^-20 of itself for gates above -16, 2^-17 down to
+// -92.8 (the exponent's rounding), 0 below: the quotient takes divisors up to 2^126, which the
+// factor brings to where a bf16 product with at most 1 ends.
+constexpr float kGateScale = 256.f;
 __device__ __forceinline__ float gate_of(float x)
 {
-    return __fdividef(1.f, 1.f + fast_exp2(-x * (float)kLog2e));
+    return __fdividef(1.f, 1.f / kGateScale + fast_exp2(fmaf(-x, (float)kLog2e, -8.f)));
 }
 
 // A block takes 32 rows by 8 C columns: a warp C of the columns of every PARTS'th partial, a lane
@@ -1182,7 +1185,7 @@ shared_merge_kernel(const SharedArgs a, const int pairs)
             for (int j = 0; j < 4; ++j)
                 v[j] += tile[p][i][c + j];
         }
-        const float inv = s == 0.f ? 0.f : 1.f / s;
+        const float inv = s == 0.f ? 0.f : 1.f / (s * kGateScale);
         const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&gate[q].x));
         const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&gate[q].y));
         const __nv_bfloat162 o0 = __floats2bfloat162_rn(v[0] * inv * gate_of(g0.x),
