@@ -45,8 +45,9 @@
 // Against the plain decode, which reads a prefix once per request: 64 requests of 66,048 + 2,000
 // tokens 360 us, not 684.
 //
-// Every mbarrier wait is bounded; one that gives up sets the status word, and cluster
-// barriers keep both CTAs until neither can touch the other.
+// Every mbarrier wait is bounded (the odd CTA's for the last commit from when its other warps are
+// through); one that gives up sets the status word, and cluster barriers keep both CTAs until
+// neither can touch the other.
 #include <math.h>
 
 #include <atomic>
@@ -252,7 +253,7 @@ struct ShBars {
 struct ShMisc {
     ShBars bars;
     uint32_t tmem;
-    int abort, status, first;
+    int abort, status, first, done;             // warps that are through with their run
     SharedPart part;                            // the first
     float quarter[2][256];                      // exchanged between the quarters of a row
 };
@@ -445,17 +446,20 @@ struct ShMaps {
     CUtensorMap k, v, rope, qn, qr;
 };
 
-// Waits through the whole run; once another warp has given up (their waits are bounded), as
-// wait_drain.
-__device__ __noinline__ void wait_last(uint32_t bar, volatile int *abort_flag)
+// Waits through the whole run: while the CTA's other warps go on (their waits are bounded), and
+// then as wait_drain.
+__device__ __noinline__ void wait_last(uint32_t bar, volatile int *abort_flag, volatile int *done,
+                                       int others, int32_t *status)
 {
     unsigned long long t0 = global_ns();
     while (!mbar_try_wait(bar, 0)) {
         const unsigned long long now = global_ns();
-        if (!*abort_flag)
+        if (!*abort_flag && *done < others) {
             t0 = now;
-        else if (now - t0 > kDrainLimitNs)
+        } else if (now - t0 > kDrainLimitNs) {
+            atomicCAS(status, 0, 15);
             return;
+        }
     }
 }
 
@@ -514,6 +518,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         m.abort = 0;
         m.status = 0;
         m.first = 0;
+        m.done = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
@@ -851,7 +856,7 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
     } else if (warp == 1 && lane == 0) {
         // the even CTA's commits arrive here too: the last of them comes after the others
         if (walk.next())
-            wait_last(bar_of(m.bars.drain), abort_flag);
+            wait_last(bar_of(m.bars.drain), abort_flag, &m.done, kShThreads / 32 - 1, status);
     } else if (warp >= 4) {
         // -------------------------------------------------- softmax, epilogue
         // Thread (warp group, quad, lane): row 32 (quad % 2) + lane of this CTA, and of a tile the 32
@@ -1030,6 +1035,8 @@ shared_decode_kernel(const __grid_constant__ ShMaps maps, const SharedArgs a)
         }
     }
 
+    if (warp != 1 && lane == 0)
+        atomicAdd(&m.done, 1);
     tc_fence_before();
     __syncthreads();
     // A pair leaves together: no copy or arrival of one CTA is on its way to the other, and
