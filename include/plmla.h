@@ -875,8 +875,10 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  *   2 .. 15  a wait inside the decode timed out (its outputs are not valid)
  *
  * mla_decode_shared -- mla_decode for a batch whose requests have prefixes in common: the
- * tokens that a group of requests shares are read once, with the queries of all its
- * members.  Same results as mla_decode, up to rounding.
+ * tokens that a group of requests shares are read with the queries of all its members, once for
+ * every 128 of their n_q_per_req * num_heads rows each.  Where that saves nothing (those are a
+ * multiple of 128, or the prefix is short) every member reads them for itself.  Same results as
+ * mla_decode, up to rounding.
  *
  * q_nope_absorbed, q_rope, gate, slab_base, page strides, seq_lens, n_q_per_req, out, lse
  *               as in mla_decode; num_reqs 1 .. 1024, num_heads 1 .. 128 (any).  out may be
@@ -1010,7 +1012,7 @@ plmla_status mla_pages_reserve_ex(int32_t num_layers, void *const *slab_base, in
  * A log-sum-exp is within 1.5e-6 of the exact one (4e-7 in all that was measured, for logits
  * that are all rounded alike; 1e-7 for random ones), and candidates are held in pairs of
  * floats, so the order is that of the formula wherever candidates of different beams differ by
- * 3e-6 or more, and always within a beam.  Beams whose largest logits are equal and whose
+ * 3e-6 or more (within a beam, by 2^-45 of their size).  Beams whose largest logits are equal and whose
  * log-sum-exps come within 3e-6 count as having the same one, that of the first: ties between beams
  * with the same logits stay ties, wherever their rows start.  Deterministic.
  */

@@ -1007,8 +1007,9 @@ def mla_decode_shared(q_nope_absorbed, q_rope, gate, slab, page_table, seq_lens,
                       shared_lens, *, n_q=1, scale=DEFAULT_SCALE, out=None, lse=None,
                       workspace=None, status=None, stream=None, with_lse=True):
     """mla_decode for a batch whose requests have prefixes in common: the tokens that
-    a group shares are read once, with the queries of all its members.  Returns
-    (out, lse), mla_decode's up to rounding; arguments as there (any num_heads up to
+    a group shares are read with the queries of all its members, once for every 128 of
+    their n_q * H rows each (by each member where that is no fewer times, as it is for
+    multiples of 128).  Returns (out, lse), mla_decode's up to rounding; arguments as there (any num_heads up to
     128), and ``group_starts`` int32 [G+1]: group g is requests group_starts[g] ..
     group_starts[g+1] - 1, ascending from 0 to R (a group may be one request);
     ``shared_lens`` int32 [G]: the first tokens that its members have in common,

@@ -18,8 +18,8 @@
 // their order.
 //
 // Bound: latencies, of two launches and of a block's chain (loads, two barriers, the list); the
-// logits' bytes are a fifth to a third of it.  128 rows of 150,001 bf16 logits 15.3 us (5.7 us of
-// HBM), 128 of 100,257 fp16 20.0 (3.8; lists of 32), 4 of 32,000 fp32 6.2.
+// logits' bytes are a fifth to a third of it.  128 rows of 150,001 bf16 logits 15.4-16.5 us (5.7 us
+// of HBM), 128 of 100,257 fp16 20.6 (3.8; lists of 32), 4 of 32,000 fp32 6.6.
 #include <math.h>
 #include <algorithm>
 
@@ -754,11 +754,11 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
             }
 }
 
-// Groups of 16 bytes a thread: one where that holds a row (2,000 rows of 2,000 bf16 tokens: 30
-// us; of four groups 34), four where those do (7,000: 33; one 47, eight 41), else eight (512
-// fp32 rows of 32,000: 20; four 25, one 60).  With few rows shorter slices on more SMs gain nothing,
-// since the merge has more lists: 4 rows of 150,000 bf16 tokens 9.2 us, in slices of four
-// groups 9.5, of one 12.2.
+// Groups of 16 bytes a thread: one where that holds a row (2,000 rows of 2,000 bf16 tokens: 14.6
+// us; of four groups 19, of eight 26), four where those do (7,000: 18.3; one 34, eight 26), else
+// eight (512 fp32 rows of 32,000: 21.4; four 25.5, one 46).  With few rows shorter slices on more
+// SMs gain nothing, since the merge has more lists: 4 rows of 150,000 bf16 tokens 8.4 us, in
+// slices of four groups 9.6, of one 12.5.
 int thread_groups(int vocab, int type)
 {
     const int one = (type == kRopeFp32 ? 4 : 8) * kSliceThreads;
@@ -818,8 +818,8 @@ cudaError_t launch_beams(const BeamArgs &a, void *workspace, cudaStream_t stream
     if (err != cudaSuccess)
         return err;
     // Eight warps where each has one beam at most and few lists, else 32: fewer levels of joins,
-    // and more blocks an SM (4 beams of 2,000 tokens 5.2 us, not 7.3, 500 times 4 of 1,000 14, not
-    // 29, 4 of 150,000 8.0, not 9.2; 32 of 1,000 12.4, not 9.4, 64 lists of 32 beams 14, not 11).
+    // and more blocks an SM (4 beams of 2,000 tokens 6.0 us, not 7.8, 500 times 4 of 1,000 14, not
+    // 30, 4 of 150,000 8.4, not 9.6; but 32 of 1,000 12.8, not 9.8, 32 of 30,000 15.8, not 11.7).
     const bool few = a.beams <= 8 && a.beams * (int64_t)o.slices <= 64;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.batch);

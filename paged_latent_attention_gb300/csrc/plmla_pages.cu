@@ -14,15 +14,16 @@
 //
 // Fork and free: one block per row, a page per thread; atomics on counts add up to the
 // same whole numbers in any order.  A page that an out row already holds in the same place
-// stays without touching its count (continuations share all but their last pages).  Both
-// are latency-bound: three dependent loads and an atomic (1,024 rows of up to 330 pages 2.7 us,
-// four rows 1.8).
+// stays without touching its count.  Both are latency-bound: three dependent loads and an
+// atomic.  A fork into the emptied double of a table and the release of the old rows, so every
+// page's count goes up and down: 1,024 rows with 196,306 pages 9.5 us, four rows 4.4; a fork of rows
+// that are there already 4.0 and 1.9.
 //
 // Reserve: one block plans (rows in threads, prefix sums, 16,384 counts a sweep), then a grid
 // of blocks copies the planned pages, one contiguous piece per (row, layer), at the copy
 // rate of HBM.  The copy is launched programmatically behind the plan.  Eight E4M3 prompts' 64
-// continuations in four layers: 36 us with the fork before it, of which the bytes take 31; two
-// rows and one page 9 us, latency.
+// continuations in four layers: 35.5-37 us with the fork before it, of which the bytes take 31; two
+// rows and one page 9-10 us, latency.
 #include "plmla_internal.cuh"
 
 namespace plmla {

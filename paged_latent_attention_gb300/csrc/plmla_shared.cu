@@ -34,14 +34,16 @@
 // bf16 would.  Together they carry 8 bits like bf16 ones down to 2^-6, and steps of 2^-14 and less
 // below, so there the reference follows the history down too: once a row's largest in a tile
 // falls 2^6 below it, O is scaled up.  A weight is off by 2^-8 of itself, or 2^-12 of the largest of its
-// tile.  (With one reference for the whole history, the tokens behind one that takes half of
-// the weight lost a third of theirs; 148.2 us there in the 4-draft case, 149 so.)
+// tile.  (Two E4M3 parts under a reference that only rises lose what is below 2^-14 of the row's
+// largest weight: a third of the output behind a token that takes 0.62 of the weight.  This
+// costs 0.7% of the 4-draft case below, 3% with scores four times as large.)
 //
-// Measured: 64 requests x 64 heads over 32,768 shared and 300-4,000 own tokens, bf16: 200 us, the
-// decode kernel 188, 1.66 PFLOP/s (87% of a library product's burst, tensor pipe busy 79% of
-// the time; each SM takes in 139 KB a tile, at 80% of what the L2 gives it).  4-draft verification
-// over 48 E4M3 histories: 148 us, the decode 125.  8 answers to 20,011 tokens: 32 us, 2 requests of
-// 1,500: 14.6 us, both latency: three launches, a block's start, a partial's way out and back.
+// Measured (over several boxes): 64 requests x 64 heads over 32,768 shared and 300-4,000 own tokens,
+// bf16: 194-207 us, the decode kernel 188 of 200, 1.66 PFLOP/s (87% of a library product's burst,
+// tensor pipe busy 79% of the time; each SM takes in 139 KB a tile, at 80% of what the L2 gives
+// it).  4-draft verification over 48 E4M3 histories, whose prefixes nothing is saved by sharing:
+// 144-151 us, the decode 125.  8 answers to 20,011 tokens: 32-36 us, 2 requests of 1,500: 14.6-15.6 us,
+// both latency: three launches, a block's start, a partial's way out and back.
 // Against the plain decode, which reads a prefix once per request: 64 requests of 66,048 + 2,000
 // tokens 360 us, not 684.
 //
