@@ -940,7 +940,7 @@ plmla_status mla_decode_shared_fp8(const void *q_nope_absorbed, const void *q_ro
  * out_table, out_lens     rows and lengths, updated; out_lens must hold valid lengths on
  *                         entry (0 for rows without pages).  Columns past a
  *                         history's pages are not written.  They must not overlap
- *                         page_table and seq_lens.
+ *                         page_table, seq_lens or each other.
  */
 plmla_status mla_pages_fork(const int32_t *page_table, int64_t page_table_ld,
                             int64_t page_table_cols, const int32_t *seq_lens, int32_t num_rows,

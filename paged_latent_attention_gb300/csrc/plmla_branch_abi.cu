@@ -59,7 +59,8 @@ bool apart(const void *a, size_t na, const void *b, size_t nb)
 }
 
 // Whether two tables share no entry: their ranges do not meet, or their rows lie in different
-// columns of one grid (of the shorter stride, of which the other is a multiple).
+// columns of one grid (of the shorter stride, of which the other is a multiple).  A vector is a
+// table of one row.
 bool tables_apart(const int32_t *a, int64_t lda, int64_t na, int32_t rows_a, const int32_t *b,
                   int64_t ldb, int64_t nb, int32_t rows_b)
 {
@@ -235,7 +236,13 @@ extern "C" plmla_status mla_pages_fork(const int32_t *page_table, int64_t page_t
         !words_ok(parents) || !words_ok(out_lens) || !counts_ok(ref_counts, num_pages, status) ||
         !tables_apart(page_table, page_table_ld, page_table_cols, num_rows, out_table, out_table_ld,
                       out_table_cols, out_rows) ||
-        !apart(seq_lens, 4 * (size_t)num_rows, out_lens, 4 * (size_t)out_rows))
+        !apart(seq_lens, 4 * (size_t)num_rows, out_lens, 4 * (size_t)out_rows) ||
+        !tables_apart(page_table, page_table_ld, page_table_cols, num_rows, out_lens, out_rows,
+                      out_rows, 1) ||
+        !tables_apart(out_table, out_table_ld, out_table_cols, out_rows, seq_lens, num_rows, num_rows,
+                      1) ||
+        !tables_apart(out_table, out_table_ld, out_table_cols, out_rows, out_lens, out_rows, out_rows,
+                      1))
         return PLMLA_INVALID_ARGUMENT;
     const ForkArgs a = {page_table, page_table_ld, page_table_cols, seq_lens, num_rows,
                         parents,    out_rows,      out_table,       out_table_ld, out_table_cols,
@@ -280,8 +287,12 @@ extern "C" plmla_status mla_pages_reserve_ex(int32_t num_layers, void *const *sl
         (granted != nullptr &&
          (!aligned(granted, 4) || !apart(granted, 4 * (size_t)num_reqs, seq_lens, 4 * (size_t)num_reqs) ||
           (granted != n_new_of &&
-           !apart(granted, 4 * (size_t)num_reqs, n_new_of, 4 * (size_t)num_reqs)))) ||
-        !counts_ok(ref_counts, num_pages, status) || workspace == nullptr ||
+           !apart(granted, 4 * (size_t)num_reqs, n_new_of, 4 * (size_t)num_reqs)) ||
+          !tables_apart(page_table, page_table_ld, page_table_cols, num_reqs, granted, num_reqs,
+                        num_reqs, 1))) ||
+        !counts_ok(ref_counts, num_pages, status) ||
+        !apart(granted, 4 * (size_t)num_reqs, ref_counts, 4 * (size_t)num_pages) ||
+        !apart(granted, 4 * (size_t)num_reqs, status, 4) || workspace == nullptr ||
         !aligned(workspace, kAlign))
         return PLMLA_INVALID_ARGUMENT;
     for (int32_t l = 0; l < num_layers; ++l)

@@ -51,6 +51,12 @@ def test_granted_of_a_reservation(lib):
         assert call(7 * FAKE + off, 7 * FAKE) == (NO_ROOM if off == 0 else REFUSED)
     for off in (-16, 16):
         assert call(3 * FAKE + off) == call(7 * FAKE + off, 7 * FAKE) == NO_ROOM
+    # the counts (8) and the table (4 rows of 3 columns)
+    for off in (-12, 0, 28):
+        assert call(4 * FAKE + off) == REFUSED
+    for off in (-12, 0, 8, 40, 56):
+        assert call(2 * FAKE + off) == REFUSED
+    assert call(4 * FAKE + 32) == call(2 * FAKE + 60) == call(2 * FAKE - 16) == NO_ROOM
 
 
 # (a fork has no workspace to be refused for: where nothing else stops it, its launch fails for
@@ -78,6 +84,14 @@ def test_fork_outputs(lib):
     for off in (-4, 0, 4, 8):
         assert call(out_lens=2 * FAKE + off) == REFUSED
     assert call(out_lens=2 * FAKE + 12) == fine and call(out_lens=2 * FAKE - 8) == fine
+    # lengths inside a table, or between its rows
+    for base in (FAKE, 3 * FAKE):
+        for off in (-1, 0, 3, 9, 10, 20):
+            assert call(out_lens=base + 4 * off) == (fine if base == 3 * FAKE and off == 20 else REFUSED)
+        assert call(out_lens=base + 4 * 6) == call(out_lens=base - 8) == fine
+    for off in (-8, 0, 12, 8 * 4, 10 * 4):
+        assert call(lens=3 * FAKE + off) == REFUSED
+    assert call(lens=3 * FAKE + 16) == call(lens=3 * FAKE - 12) == fine
 
 
 @no_gpu
