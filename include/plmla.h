@@ -903,7 +903,8 @@ plmla_status mla_kv_compact_ex(int32_t num_layers, void *const *slab_base, int32
  *
  * mla_decode_shared_fp8 takes E4M3 pages and kv_scale as mla_decode_fp8 does.  Its
  * probabilities are multiplied in two parts, E4M3 and E5M2: each is within 2^-8 of itself,
- * or within 2^-12 of the row's largest among the same 128 tokens.
+ * or within 2^-12 of the row's largest among the same 128 tokens (or 2^-50 of its largest of
+ * all).
  */
 size_t mla_shared_workspace_size(int32_t num_reqs, int32_t n_q_per_req, int32_t num_heads,
                                  int32_t num_groups, int32_t fp8);
