@@ -1013,9 +1013,9 @@ plmla_status mla_pages_reserve_ex(int32_t num_layers, void *const *slab_base, in
  * A log-sum-exp is within 1.5e-6 of the exact one (4e-7 in all that was measured, for logits
  * that are all rounded alike; 1e-7 for random ones), and candidates are held in pairs of
  * floats, so the order is that of the formula wherever candidates of different beams differ by
- * 3e-6 or more (within a beam, by 2^-45 of their size).  Beams whose largest logits are equal and whose
- * log-sum-exps come within 3e-6 count as having the same one, that of the first: ties between beams
- * with the same logits stay ties, wherever their rows start.  Deterministic.
+ * 3e-6 or more (within a beam, by 2^-45 of their size).  Beams with the same logits have the
+ * same log-sum-exp, so that ties between them stay ties, wherever their rows start.
+ * Deterministic.
  */
 size_t mla_beam_workspace_size(int32_t batch, int32_t beams, int32_t vocab);
 plmla_status mla_beam_select(const void *logits, int64_t logits_ld, int32_t dtype,

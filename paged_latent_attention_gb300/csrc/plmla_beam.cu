@@ -19,7 +19,7 @@
 //
 // Bound: latencies, of two launches and of a block's chain (loads, two barriers, the list); the
 // logits' bytes are a fifth to a third of it.  128 rows of 150,001 bf16 logits 15.4-16.5 us (5.7 us
-// of HBM), 128 of 100,257 fp16 20.6 (3.8; lists of 32), 4 of 32,000 fp32 6.6.
+// of HBM), 128 of 100,257 fp16 20.9 (3.8; lists of 32), 4 of 32,000 fp32 6.8.
 #include <math.h>
 #include <algorithm>
 
@@ -58,6 +58,8 @@ struct Word<float> {
         return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
     }
     __device__ static float get(uint32_t w, int) { return __uint_as_float(w); }
+    // of all elements, in any order, added up
+    __device__ static uint32_t mark(uint32_t w, uint32_t sum) { return sum + w; }
     __device__ static uint32_t both(float x) { return __float_as_uint(x); }
     // bit e: element e reaches x
     __device__ static uint32_t reach(uint32_t w, uint32_t x)
@@ -79,6 +81,7 @@ struct Word<__nv_bfloat16> {
     {
         return __uint_as_float(e ? w & 0xFFFF0000u : w << 16);
     }
+    __device__ static uint32_t mark(uint32_t w, uint32_t sum) { return __dp4a(w, 0xFB01FB01u, sum); }
     __device__ static uint32_t both(float x)
     {
         const uint32_t b = __float_as_uint(x) >> 16;          // x is a bf16
@@ -105,6 +108,7 @@ struct Word<__half> {
         const float2 f = __half22float2(as(w));
         return e ? f.y : f.x;
     }
+    __device__ static uint32_t mark(uint32_t w, uint32_t sum) { return __dp4a(w, 0xFB01FB01u, sum); }
     __device__ static uint32_t both(float x)
     {
         const __half2 h = __float2half2_rn(x);                // x is a fp16
@@ -181,6 +185,7 @@ constexpr float kSameSum = 3e-6f;               // what two logarithms of the sa
 
 struct SliceOut {
     float *high, *sum;                  // [rows, slices]
+    uint32_t *mark;                     // the same
     uint64_t *lists;                    // [rows, slices, beams] entries, descending
     int slices;
 };
@@ -197,6 +202,7 @@ struct SliceShared {
     uint64_t list[kFew];
     uint32_t tops[kSliceThreads];
     long long warp_sum[kSliceThreads / 32];
+    uint32_t warp_mark[kSliceThreads / 32];
     uint32_t warp_high[kSliceThreads / 32], warp_least[kSliceThreads / 32];
     int warp_i[kSliceThreads / 32];
     uint32_t bound;
@@ -445,6 +451,7 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
     // in fixed point, without a rounding.
     const float high = value_of(high_key), ref = high == -INFINITY ? 0.f : high;
     float own;
+    uint32_t mark = 0;
     {
         const uint64_t shift = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
         const uint64_t centre = pack2(kCentre, kCentre);
@@ -469,6 +476,9 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
                 unpack2(p, x, y);
                 e[w] = pack2(fast_exp2(x), fast_exp2(y));
             }
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                mark = W::mark(raw[g][w], mark);
             sums[g] = add2(e[0], e[1]);
             if constexpr (W::n == 2)
                 sums[g] = add2(sums[g], add2(e[2], e[3]));
@@ -487,18 +497,24 @@ slice_kernel(const T *logits, int64_t ld, const uint8_t *ended, int beams, int v
     const uint32_t sum_lo = __reduce_add_sync(0xffffffffu, (uint32_t)fixed & 0x7FFFFFFu);
     const uint32_t sum_hi = __reduce_add_sync(0xffffffffu, (uint32_t)(fixed >> 27));
     const bool nan = __any_sync(0xffffffffu, own != own);
-    if (lane == 0)
+    mark = __reduce_add_sync(0xffffffffu, mark);
+    if (lane == 0) {
+        s.warp_mark[warp] = mark;
         s.warp_sum[warp] = nan ? -1 : ((long long)sum_hi << 27) + sum_lo;
+    }
     __syncthreads();
     if (t == 0) {
         bool bad = false;
         long long sum = 0;
+        mark = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
+            mark += s.warp_mark[w];
             sum += s.warp_sum[w];
             bad |= s.warp_sum[w] < 0;
         }
         o.high[at] = high;
+        o.mark[at] = mark;
         o.sum[at] = bad ? NAN : __ll2float_rn(sum) * kUnfixed;
     }
     int n = s.count;
@@ -605,6 +621,7 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
     __shared__ int ids[kWarps * kList / 2];
     __shared__ Pair logs[kMaxBeams];            // of the rows' sums
     __shared__ float tops[kMaxBeams];           // their largest logits; NaN: no candidates
+    __shared__ uint32_t marks[kMaxBeams];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
     const int K = a.beams, per_row = K >= kWarps ? 1 : kWarps / K;
     const int part = warp % per_row;
@@ -629,9 +646,13 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
         const int64_t row = (int64_t)b * K + k;
         float high = -INFINITY;
         Pair sum = {0.f, 0.f};
+        uint32_t mark = 0;
         if (a.ended == nullptr || a.ended[row] == 0) {
-            for (int s = lane; s < o.slices; s += 32)
+            for (int s = lane; s < o.slices; s += 32) {
                 high = fmaxf(high, o.high[row * o.slices + s]);
+                mark += o.mark[row * o.slices + s];
+            }
+            mark = __reduce_add_sync(0xffffffffu, mark);
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1)
                 high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, w));
@@ -653,6 +674,7 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
         if (lane == 0) {
             const Pair l = ln(sum.hi);
             logs[k] = {l.hi, l.lo + sum.lo / sum.hi};
+            marks[k] = mark;
             tops[k] = isfinite(sum.hi) && sum.hi > 0.f ? high : NAN;
         }
     }
@@ -665,12 +687,14 @@ __global__ void __launch_bounds__(32 * WARPS) merge_kernel(const BeamArgs a, con
         const bool ended = a.ended != nullptr && a.ended[row] != 0;
         // Rows with the same logits have to have the same sum, so that ties stay ties, but what is
         // added first depends on where they start within 16 bytes: the first one's is taken.
+        // (Known by their marks: the largest logit and the sum alone can be close in rows of
+        // nearly equal logits.)
         Pair l = logs[k];
         int same = K;
 #pragma unroll
         for (int j0 = 0; j0 < 32 * P; j0 += 32) {
             const int j = min(j0 + lane, k);
-            const bool alike = tops[j] == high &&
+            const bool alike = marks[j] == marks[k] && tops[j] == high &&
                                fabsf((logs[j].hi - l.hi) + (logs[j].lo - l.lo)) <= kSameSum;
             const uint32_t found = __ballot_sync(0xffffffffu, alike);
             if (same == K && found != 0)
@@ -795,7 +819,7 @@ size_t beam_workspace(int batch, int beams, int vocab)
     const size_t rows = (size_t)batch * beams;
     // fp32 slices are half as long, but hold rows of a length that 16-bit ones cut at less
     const int slices = std::max(slice_count(vocab, kRopeFp32), slice_count(vocab, kRopeBf16));
-    return rows * slices * 8 * (1 + (size_t)beams);
+    return rows * slices * (8 * (size_t)beams + 12);
 }
 
 cudaError_t launch_beams(const BeamArgs &a, void *workspace, cudaStream_t stream)
@@ -807,6 +831,7 @@ cudaError_t launch_beams(const BeamArgs &a, void *workspace, cudaStream_t stream
     o.lists = static_cast<uint64_t *>(workspace);
     o.high = reinterpret_cast<float *>(o.lists + lists * a.beams);
     o.sum = o.high + lists;
+    o.mark = reinterpret_cast<uint32_t *>(o.sum + lists);
     const int groups = thread_groups(a.vocab, a.type);
     if (a.type == kRopeBf16)
         launch_slices<__nv_bfloat16>(a, groups, o, stream);
